@@ -16,8 +16,9 @@ CSRC = os.path.join(PKG, "csrc")
 OUT_DIR = os.path.join(PKG, "_lib")
 LIB = os.path.join(OUT_DIR, "libkda.so")
 SOURCES = ["kda_api.cu", "kda_chunk.cu", "kda_state.cu", "kda_recurrent.cu", "kda_noalloc.cu",
-           "kda_host.cu", "kda_status.cu", "kda_bwd.cu"]
-HEADERS = ["kda_common.cuh", "kda_kernels.cuh", "kda_tc.cuh"]
+           "kda_host.cu", "kda_status.cu", "kda_bwd.cu", "kda_latent.cu", "kda_latent_decode.cu",
+           "kda_latent_prefill.cu"]
+HEADERS = ["kda_common.cuh", "kda_kernels.cuh", "kda_tc.cuh", "kda_latent.cuh"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 NVCC_FLAGS = ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC", "-Xcompiler", "-O2",
               "--expt-relaxed-constexpr"]
@@ -35,7 +36,7 @@ def _stale() -> bool:
         return True
     t = os.path.getmtime(LIB)
     deps = [os.path.join(CSRC, f) for f in SOURCES + HEADERS]
-    deps.append(os.path.join(ROOT, "include", "kda.h"))
+    deps += [os.path.join(ROOT, "include", f) for f in ("kda.h", "kda_latent.h")]
     deps.append(os.path.abspath(__file__))
     return any(os.path.getmtime(d) > t for d in deps)
 

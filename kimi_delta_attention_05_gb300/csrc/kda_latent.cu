@@ -1,0 +1,465 @@
+// Latent attention for serving: host entry points (include/kda_latent.h), the
+// kernel that plans block tables and slot maps, and the one that writes new
+// rows into the paged cache.
+#include <algorithm>
+#include <atomic>
+#include <cmath>
+
+#include "../../include/kda_latent.h"
+#include "kda_common.cuh"
+#include "kda_kernels.cuh"
+#include "kda_latent.cuh"
+
+namespace kda {
+
+// ---- block tables and slot maps ----
+//
+// With need_b = ceil((c_b + n_b) / P) - ceil(c_b / P), request b takes the
+// entries [F_b, F_b + need_b) of free_pages, F the exclusive prefix of need,
+// and its new tokens the packed range [O_b, O_b + n_b), O that of n.  Every
+// CTA forms both prefixes for itself in shared memory (they are a few
+// kilobytes, and a second launch or a wait between CTAs would cost more than
+// the scan) and then writes its share of the tokens and pages, finding an
+// element's request by bisection of the prefix.  A token's page comes from the
+// table where the request held it before and straight from free_pages where it
+// is new, so no CTA reads what another writes.
+constexpr int kPlanThreads = 512;
+constexpr int kPlanTokens = 1024;  // tokens of slot_map per CTA
+
+struct PlanParams {
+  const int32_t *cached, *fresh;
+  int32_t* table;
+  int64_t table_stride;
+  const int32_t* free_pages;
+  int32_t* seq_lens;
+  int64_t* cu;
+  int64_t* slots;
+  int32_t* taken;
+  int B;
+  int64_t max_pages, num_free, T;
+  int page;
+  int* status;
+};
+
+__device__ __forceinline__ int64_t warp_scan(int64_t x, int lane) {
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int64_t y = __shfl_up_sync(0xffffffffu, x, o);
+    if (lane >= o) x += y;
+  }
+  return x;
+}
+
+// largest b in [0, n) with off[b] <= x (off ascending, off[0] = 0)
+__device__ __forceinline__ int find_request(const int32_t* off, int n, int x) {
+  int lo = 0, hi = n - 1;
+  while (lo < hi) {
+    const int mid = (lo + hi + 1) >> 1;
+    if (off[mid] <= x) lo = mid; else hi = mid - 1;
+  }
+  return lo;
+}
+
+__global__ void __launch_bounds__(kPlanThreads) kda_latent_plan_kernel(const PlanParams p) {
+  extern __shared__ int32_t plan_smem[];
+  int32_t* tok = plan_smem;            // [B + 1] prefix of new tokens
+  int32_t* pag = plan_smem + p.B + 1;  // [B + 1] prefix of pages taken
+  __shared__ int64_t sums[2][kPlanThreads / 32];
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int64_t P = p.page;
+  int64_t carry_t = 0, carry_p = 0;
+  int bad = 0;
+  for (int base = 0; base < p.B; base += kPlanThreads) {
+    const int b = base + tid;
+    int64_t n = 0, need = 0;
+    if (b < p.B) {
+      const int64_t c = p.cached[b];
+      n = p.fresh[b];
+      const int64_t pages = (c + n + P - 1) / P;
+      if (c < 0 || n < 0 || c + n > INT32_MAX || pages > p.max_pages) {
+        bad = 1;
+        n = 0;
+      } else {
+        need = pages - (c + P - 1) / P;
+      }
+    }
+    const int64_t st = warp_scan(n, lane), sp = warp_scan(need, lane);
+    if (lane == 31) {
+      sums[0][warp] = st;
+      sums[1][warp] = sp;
+    }
+    __syncthreads();
+    int64_t before_t = carry_t, before_p = carry_p;
+#pragma unroll
+    for (int w = 0; w < kPlanThreads / 32; ++w) {
+      const int64_t a = sums[0][w], g = sums[1][w];
+      if (w < warp) {
+        before_t += a;
+        before_p += g;
+      }
+      carry_t += a;
+      carry_p += g;
+    }
+    if (b < p.B) {  // (sums beyond 2^31 - 1 are refused below: T and num_free are below it)
+      tok[b] = (int32_t)(before_t + st - n);
+      pag[b] = (int32_t)(before_p + sp - need);
+    }
+    __syncthreads();  // sums are read
+  }
+  bad = __syncthreads_or(bad);
+  const bool no_room = carry_t > p.T, no_pages = carry_p > p.num_free;
+  const bool refused = bad || no_room || no_pages;
+  if (blockIdx.x == 0) {
+    if (tid == 0) {
+      if (refused && p.status) atomicExch(p.status, bad || no_room ? KDA_ERR_BAD_LENGTHS : KDA_ERR_NO_PAGES);
+      p.cu[p.B] = refused ? 0 : carry_t;
+      p.taken[0] = refused ? 0 : (int32_t)carry_p;
+    }
+    for (int b = tid; b < p.B; b += kPlanThreads) {
+      p.cu[b] = refused ? 0 : tok[b];
+      p.seq_lens[b] = p.cached[b] + (refused ? 0 : p.fresh[b]);
+    }
+  }
+  const int64_t total_t = refused ? 0 : carry_t, total_p = refused ? 0 : carry_p;
+  for (int64_t k = (int64_t)blockIdx.x * kPlanThreads + tid; k < total_p; k += (int64_t)gridDim.x * kPlanThreads) {
+    const int b = find_request(pag, p.B, (int)k);
+    const int64_t held = (p.cached[b] + P - 1) / P;
+    p.table[b * p.table_stride + held + (k - pag[b])] = p.free_pages[k];
+  }
+  const int64_t t1 = min(p.T, ((int64_t)blockIdx.x + 1) * kPlanTokens);
+  for (int64_t t = (int64_t)blockIdx.x * kPlanTokens + tid; t < t1; t += kPlanThreads) {
+    int64_t slot = -1;
+    if (t < total_t) {
+      const int b = find_request(tok, p.B, (int)t);
+      const int cached = p.cached[b];
+      const int pos = cached + (int)(t - tok[b]);
+      const int held = (int)(((int64_t)cached + P - 1) / P);
+      const int at = pos / p.page;
+      const int64_t page = at < held ? p.table[b * p.table_stride + at] : p.free_pages[pag[b] + at - held];
+      slot = page * P + (pos - at * p.page);
+    }
+    p.slots[t] = slot;
+  }
+}
+
+// ---- rows into the cache ----
+//
+// A warp per token: lane l holds latent values 16 l' .. in two 16-byte pieces
+// (8 l and 256 + 8 l), so the row is read and written in whole 512-byte
+// requests, the mean square is one warp reduction, and a row passes through
+// the SM once.  Bound by HBM: 2 x 1152 bytes a token.
+struct AppendParams {
+  const uint16_t *c, *pe;
+  int64_t c_st, pe_st;
+  const int64_t* slots;
+  uint16_t* cache;
+  int64_t num_pages, page_stride, token_stride;
+  int page;
+  const float* w;
+  float eps;
+  int64_t T;
+  int* status;
+};
+
+template <bool kNorm>
+__global__ void __launch_bounds__(256) kda_latent_append_kernel(const AppendParams p) {
+  const int lane = threadIdx.x & 31;
+  const int64_t warps = (int64_t)gridDim.x * 8, w0 = (int64_t)blockIdx.x * 8 + (threadIdx.x >> 5);
+  float w[16];
+  if (kNorm) {
+#pragma unroll
+    for (int i = 0; i < 16; ++i) w[i] = p.w[(i >> 3) * 256 + 8 * lane + (i & 7)];
+  }
+  for (int64_t t = w0; t < p.T; t += warps) {
+    const int64_t slot = p.slots[t];
+    const uint4* c = reinterpret_cast<const uint4*>(p.c + t * p.c_st);
+    uint4 x[2] = {c[lane], c[32 + lane]};
+    uint4 pe = make_uint4(0, 0, 0, 0);
+    if (lane < 8) pe = reinterpret_cast<const uint4*>(p.pe + t * p.pe_st)[lane];
+    if (slot < 0) continue;
+    const int64_t page = slot / p.page;
+    if (page >= p.num_pages) {
+      if (lane == 0 && p.status) atomicExch(p.status, KDA_ERR_BAD_PAGE);
+      continue;
+    }
+    if (kNorm) {
+      float f[16], sq = 0.f;
+      const uint32_t r[8] = {x[0].x, x[0].y, x[0].z, x[0].w, x[1].x, x[1].y, x[1].z, x[1].w};
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        const float2 v = unpack_bf16(r[i]);
+        f[2 * i] = v.x;
+        f[2 * i + 1] = v.y;
+        sq += v.x * v.x + v.y * v.y;
+      }
+#pragma unroll
+      for (int o = 16; o > 0; o >>= 1) sq += __shfl_xor_sync(0xffffffffu, sq, o);
+      const float rs = rsqrtf(sq * (1.0f / kLat) + p.eps);
+      uint32_t y[8];
+#pragma unroll
+      for (int i = 0; i < 8; ++i) y[i] = pack_bf16(f[2 * i] * rs * w[2 * i], f[2 * i + 1] * rs * w[2 * i + 1]);
+      x[0] = make_uint4(y[0], y[1], y[2], y[3]);
+      x[1] = make_uint4(y[4], y[5], y[6], y[7]);
+    }
+    uint4* dst = reinterpret_cast<uint4*>(p.cache + page * p.page_stride + (slot - page * p.page) * p.token_stride);
+    dst[lane] = x[0];
+    dst[32 + lane] = x[1];
+    if (lane < 8) dst[64 + lane] = pe;
+  }
+}
+
+namespace {
+
+bool al16(const void* p) { return ((uintptr_t)p & 15) == 0; }
+bool al(const void* p, uintptr_t a) { return ((uintptr_t)p & (a - 1)) == 0; }
+
+// A token stride of rows of `width` elements: whole 16-byte pieces, rows apart.
+bool stride_ok(int64_t st, int64_t width) { return st >= width && st % 8 == 0 && st <= ((int64_t)1 << 38); }
+
+int check_cache(const kda_latent_cache& c) {
+  if (!c.data && c.num_pages > 0) return KDA_ERR_NULL_ARG;
+  if (c.num_pages < 0 || c.num_pages > INT32_MAX) return KDA_ERR_SHAPE;
+  if (c.page_size <= 0 || c.page_size % 8 || c.page_size > (1 << 24)) return KDA_ERR_PAGE_SIZE;
+  if (!al16(c.data)) return KDA_ERR_ALIGNMENT;
+  if (!stride_ok(c.token_stride, kLatRow) ||
+      !stride_ok(c.page_stride, (c.page_size - 1) * c.token_stride + kLatRow))
+    return KDA_ERR_STRIDE;
+  return KDA_OK;
+}
+
+int check_decode(const kda_latent_decode_args* a) {
+  if (!a) return KDA_ERR_NULL_ARG;
+  if (a->B < 0 || a->R < 0 || a->H < 0 || a->max_pages < 0) return KDA_ERR_SHAPE;
+  if (a->B > (1 << 20) || a->R > 4096 || a->H > 4096 || a->R * a->H > (1 << 16)) return KDA_ERR_SHAPE;
+  if (a->max_pages > INT32_MAX || a->table_stride < a->max_pages) return KDA_ERR_SHAPE;
+  const int rc = check_cache(a->cache);
+  if (rc != KDA_OK) return rc;
+  if (a->max_pages * a->cache.page_size > INT32_MAX) return KDA_ERR_SHAPE;
+  if (!(a->scale > 0.f) || !std::isfinite(a->scale)) return KDA_ERR_SCALE;
+  if (a->B * a->R * a->H > 0 && (!a->q || !a->out || !a->seq_lens || (a->max_pages > 0 && !a->block_table)))
+    return KDA_ERR_NULL_ARG;
+  if (!al16(a->q) || !al16(a->out) || !al(a->lse, 4) || !al(a->block_table, 4) || !al(a->seq_lens, 4))
+    return KDA_ERR_ALIGNMENT;
+  return KDA_OK;
+}
+
+DecodeParams decode_params(const kda_latent_decode_args* a) {
+  DecodeParams p;
+  p.q = static_cast<const uint16_t*>(a->q);
+  p.cache = static_cast<const uint16_t*>(a->cache.data);
+  p.num_pages = a->cache.num_pages;
+  p.page_size = a->cache.page_size;
+  p.page_stride = a->cache.page_stride;
+  p.token_stride = a->cache.token_stride;
+  p.table = a->block_table;
+  p.table_stride = a->table_stride;
+  p.max_pages = a->max_pages;
+  p.lens = a->seq_lens;
+  p.scale_log2 = a->scale * kLog2e;
+  p.out = static_cast<uint16_t*>(a->out);
+  p.lse = a->lse;
+  p.B = (int)a->B;
+  p.R = (int)a->R;
+  p.H = (int)a->H;
+  p.ws = nullptr;
+  p.status = nullptr;
+  return p;
+}
+
+int check_prefill(const kda_latent_prefill_args* a) {
+  if (!a) return KDA_ERR_NULL_ARG;
+  if (a->B < 0 || a->Tq < 0 || a->Tk < 0 || a->H < 0 || a->N < 0 || a->H > 65535) return KDA_ERR_SHAPE;
+  if (a->flags & ~KDA_LATENT_CAUSAL) return KDA_ERR_GATE_FLAGS;
+  if ((a->cu_seqlens_q == nullptr) != (a->cu_seqlens_k == nullptr)) return KDA_ERR_NULL_ARG;
+  if (a->cu_seqlens_q) {
+    if (a->B != 1) return KDA_ERR_VARLEN_BATCH;
+  } else if (a->N != a->B) {
+    return KDA_ERR_SHAPE;
+  }
+  const int64_t most = INT32_MAX / 2;
+  if (a->N > (1 << 22) || a->Tq > most || a->Tk > most || (a->B > 0 && (a->Tq > most / a->B || a->Tk > most / a->B)))
+    return KDA_ERR_SHAPE;
+  if (!(a->scale > 0.f) || !std::isfinite(a->scale)) return KDA_ERR_SCALE;
+  const bool queries = a->B * a->Tq * a->H > 0, keys = a->B * a->Tk * a->H > 0;
+  if (queries && (!a->q || !a->out)) return KDA_ERR_NULL_ARG;
+  if (queries && keys && (!a->k || !a->k_pe || !a->v)) return KDA_ERR_NULL_ARG;
+  if (!al16(a->q) || !al16(a->k) || !al16(a->k_pe) || !al16(a->v) || !al16(a->out) || !al(a->lse, 4) ||
+      !al(a->cu_seqlens_q, 8) || !al(a->cu_seqlens_k, 8))
+    return KDA_ERR_ALIGNMENT;
+  if (queries && (!stride_ok(a->q_stride_t, kQkDim) || !stride_ok(a->q_stride_h, kQkDim))) return KDA_ERR_STRIDE;
+  if (queries && keys &&
+      (!stride_ok(a->k_stride_t, kNope) || !stride_ok(a->k_stride_h, kNope) || !stride_ok(a->k_pe_stride_t, kLatPe) ||
+       !stride_ok(a->v_stride_t, kVDim) || !stride_ok(a->v_stride_h, kVDim)))
+    return KDA_ERR_STRIDE;
+  return KDA_OK;
+}
+
+size_t prefill_workspace(const kda_latent_prefill_args* a) {
+  return a->cu_seqlens_q ? ((size_t)(a->N + 1) * 4 + 255) / 256 * 256 : 0;
+}
+
+}  // namespace
+
+// Prefix of ceil(Lq / kPrefillRows) over packed sequences, one block, after
+// checking 0 = cu[0] <= ... <= cu[N] = T of both offset arrays.  A violation
+// sets the status word and leaves no block, so nothing is written.
+__global__ void __launch_bounds__(1024) kda_latent_blocks_kernel(const int64_t* cu_q, const int64_t* cu_k, int64_t N,
+                                                                 int64_t Tq, int64_t Tk, int32_t* off, int* status) {
+  __shared__ int64_t sums[32];
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  int bad = 0;
+  for (int64_t n = tid; n <= N; n += 1024) {
+    const int64_t a = cu_q[n], b = cu_k[n];
+    bad |= (n == 0 && (a != 0 || b != 0)) || (n == N && (a != Tq || b != Tk)) || a < 0 || a > Tq || b < 0 || b > Tk;
+    if (n > 0) bad |= a < cu_q[n - 1] || b < cu_k[n - 1];
+  }
+  bad = __syncthreads_or(bad);
+  if (tid == 0 && bad && status) atomicExch(status, KDA_ERR_BAD_SEQLENS);
+  int64_t carry = 0;
+  for (int64_t base = 0; base < N; base += 1024) {
+    const int64_t n = base + tid;
+    int64_t c = 0;
+    if (n < N && !bad) c = (cu_q[n + 1] - cu_q[n] + kPrefillRows - 1) / kPrefillRows;
+    const int64_t s = warp_scan(c, lane);
+    if (lane == 31) sums[warp] = s;
+    __syncthreads();
+    int64_t before = carry;
+#pragma unroll
+    for (int w = 0; w < 32; ++w) {
+      if (w < warp) before += sums[w];
+      carry += sums[w];
+    }
+    if (n < N) off[n] = (int32_t)(before + s - c);
+    __syncthreads();
+  }
+  if (tid == 0) off[N] = (int32_t)carry;
+}
+
+}  // namespace kda
+
+using namespace kda;
+
+extern "C" int kda_latent_plan(const kda_latent_plan_args* a, void* stream) {
+  if (!a) return KDA_ERR_NULL_ARG;
+  if (a->B < 0 || a->B > kMaxPlanRequests || a->max_pages < 0 || a->max_pages > INT32_MAX || a->num_free < 0 ||
+      a->num_free > INT32_MAX || a->T < 0 || a->T > INT32_MAX || a->table_stride < a->max_pages)
+    return KDA_ERR_SHAPE;
+  if (a->page_size <= 0 || a->page_size % 8 || a->page_size > (1 << 24)) return KDA_ERR_PAGE_SIZE;
+  if (!a->cu_seqlens || !a->pages_taken || (a->T > 0 && !a->slot_map) || (a->num_free > 0 && !a->free_pages) ||
+      (a->B > 0 && (!a->cached_lens || !a->new_lens || !a->seq_lens || (a->max_pages > 0 && !a->block_table))))
+    return KDA_ERR_NULL_ARG;
+  if (!al(a->cached_lens, 4) || !al(a->new_lens, 4) || !al(a->block_table, 4) || !al(a->free_pages, 4) ||
+      !al(a->seq_lens, 4) || !al(a->cu_seqlens, 8) || !al(a->slot_map, 8) || !al(a->pages_taken, 4))
+    return KDA_ERR_ALIGNMENT;
+  cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+  int* status = status_slot(s);
+  if (!status) return KDA_ERR_LAUNCH;
+  PlanParams p{a->cached_lens, a->new_lens, a->block_table, a->table_stride, a->free_pages, a->seq_lens,
+               a->cu_seqlens, a->slot_map, a->pages_taken, (int)a->B, a->max_pages, a->num_free, a->T,
+               (int)a->page_size, status};
+  const size_t smem = (size_t)(a->B + 1) * 8;
+  if (smem > 40 * 1024) {
+    static std::atomic<int> set[64];
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return KDA_ERR_LAUNCH;
+    if (!set[dev].load()) {
+      if (cudaFuncSetAttribute(kda_latent_plan_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                               (kMaxPlanRequests + 1) * 8) != cudaSuccess)
+        return KDA_ERR_LAUNCH;
+      set[dev].store(1);
+    }
+  }
+  const int64_t ctas = std::max<int64_t>(1, (a->T + kPlanTokens - 1) / kPlanTokens);
+  kda_latent_plan_kernel<<<(unsigned)ctas, kPlanThreads, smem, s>>>(p);
+  return cudaGetLastError() == cudaSuccess ? KDA_OK : KDA_ERR_LAUNCH;
+}
+
+extern "C" int kda_latent_append(const kda_latent_append_args* a, void* stream) {
+  if (!a) return KDA_ERR_NULL_ARG;
+  if (a->T < 0 || a->T > INT32_MAX) return KDA_ERR_SHAPE;
+  const int rc = check_cache(a->cache);
+  if (rc != KDA_OK) return rc;
+  if (a->T > 0 && (!a->c || !a->k_pe || !a->slot_map)) return KDA_ERR_NULL_ARG;
+  if (!al16(a->c) || !al16(a->k_pe) || !al(a->slot_map, 8) || !al(a->norm_weight, 4)) return KDA_ERR_ALIGNMENT;
+  if (a->T > 0 && (!stride_ok(a->c_stride, kLat) || !stride_ok(a->k_pe_stride, kLatPe))) return KDA_ERR_STRIDE;
+  if (a->T == 0) return KDA_OK;
+  cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+  int* status = status_slot(s);
+  if (!status) return KDA_ERR_LAUNCH;
+  AppendParams p{static_cast<const uint16_t*>(a->c), static_cast<const uint16_t*>(a->k_pe), a->c_stride,
+                 a->k_pe_stride, a->slot_map, static_cast<uint16_t*>(a->cache.data), a->cache.num_pages,
+                 a->cache.page_stride, a->cache.token_stride, (int)a->cache.page_size, a->norm_weight, a->eps, a->T,
+                 status};
+  const unsigned ctas = (unsigned)std::min<int64_t>((a->T + 7) / 8, 152 * 8);
+  if (a->norm_weight) kda_latent_append_kernel<true><<<ctas, 256, 0, s>>>(p);
+  else kda_latent_append_kernel<false><<<ctas, 256, 0, s>>>(p);
+  return cudaGetLastError() == cudaSuccess ? KDA_OK : KDA_ERR_LAUNCH;
+}
+
+extern "C" size_t kda_latent_decode_workspace_bytes(const kda_latent_decode_args* a) {
+  if (check_decode(a) != KDA_OK || a->B * a->R * a->H == 0) return 0;
+  return decode_workspace_bytes(decode_params(a));
+}
+
+extern "C" int kda_latent_decode(const kda_latent_decode_args* a, void* workspace, size_t workspace_bytes,
+                                 void* stream) {
+  const int rc = check_decode(a);
+  if (rc != KDA_OK) return rc;
+  if (a->B * a->R * a->H == 0) return KDA_OK;
+  DecodeParams p = decode_params(a);
+  const size_t need = decode_workspace_bytes(p);
+  if (need > 0 && (!workspace || !al(workspace, 256) || workspace_bytes < need)) return KDA_ERR_WORKSPACE;
+  cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+  p.ws = static_cast<unsigned char*>(workspace);
+  p.status = status_slot(s);
+  if (!p.status || !launch_latent_decode(p, s)) return KDA_ERR_LAUNCH;
+  return cudaGetLastError() == cudaSuccess ? KDA_OK : KDA_ERR_LAUNCH;
+}
+
+extern "C" size_t kda_latent_prefill_workspace_bytes(const kda_latent_prefill_args* a) {
+  return check_prefill(a) == KDA_OK ? prefill_workspace(a) : 0;
+}
+
+extern "C" int kda_latent_prefill(const kda_latent_prefill_args* a, void* workspace, size_t workspace_bytes,
+                                  void* stream) {
+  const int rc = check_prefill(a);
+  if (rc != KDA_OK) return rc;
+  const size_t need = prefill_workspace(a);
+  if (need > 0 && (!workspace || !al(workspace, 256) || workspace_bytes < need)) return KDA_ERR_WORKSPACE;
+  if (a->N == 0 || a->H == 0 || (!a->cu_seqlens_q && a->Tq == 0)) return KDA_OK;
+  cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+  int* status = status_slot(s);
+  if (!status) return KDA_ERR_LAUNCH;
+  PrefillParams p;
+  p.q = static_cast<const uint16_t*>(a->q);
+  p.k = static_cast<const uint16_t*>(a->k);
+  p.k_pe = static_cast<const uint16_t*>(a->k_pe);
+  p.v = static_cast<const uint16_t*>(a->v);
+  p.q_st = a->q_stride_t;
+  p.q_sh = a->q_stride_h;
+  p.k_st = a->k_stride_t;
+  p.k_sh = a->k_stride_h;
+  p.pe_st = a->k_pe_stride_t;
+  p.v_st = a->v_stride_t;
+  p.v_sh = a->v_stride_h;
+  p.scale_log2 = a->scale * kLog2e;
+  p.out = static_cast<uint16_t*>(a->out);
+  p.lse = a->lse;
+  p.cu_q = a->cu_seqlens_q;
+  p.cu_k = a->cu_seqlens_k;
+  p.blk_off = nullptr;
+  p.B = a->B;
+  p.Tq = a->Tq;
+  p.Tk = a->Tk;
+  p.N = a->N;
+  p.H = (int)a->H;
+  p.causal = (a->flags & KDA_LATENT_CAUSAL) ? 1 : 0;
+  p.status = status;
+  if (a->cu_seqlens_q) {
+    int32_t* off = static_cast<int32_t*>(workspace);
+    kda_latent_blocks_kernel<<<1, 1024, 0, s>>>(a->cu_seqlens_q, a->cu_seqlens_k, a->N, a->Tq, a->Tk, off, status);
+    p.blk_off = off;
+  }
+  if (a->Tq > 0 && !launch_latent_prefill(p, s)) return KDA_ERR_LAUNCH;
+  return cudaGetLastError() == cudaSuccess ? KDA_OK : KDA_ERR_LAUNCH;
+}

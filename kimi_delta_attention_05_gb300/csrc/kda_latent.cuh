@@ -1,0 +1,55 @@
+// Parameter blocks and launch entry points of the latent-attention calls
+// (include/kda_latent.h).
+#pragma once
+#include <cuda_runtime.h>
+#include <stddef.h>
+#include <stdint.h>
+
+namespace kda {
+
+constexpr int kLat = 512;           // latent values of a cache row
+constexpr int kLatPe = 64;          // shared key values
+constexpr int kLatRow = kLat + kLatPe;
+constexpr int kQkDim = 192;         // expanded query / key channels
+constexpr int kNope = 128;          // the heads' own key channels
+constexpr int kVDim = 128;          // expanded value channels
+constexpr int kMaxPlanRequests = 16384;
+
+struct DecodeParams {
+  const uint16_t* q;                // bf16 [B, R * H, 576]
+  const uint16_t* cache;
+  int64_t num_pages, page_size, page_stride, token_stride;
+  const int32_t* table;
+  int64_t table_stride, max_pages;
+  const int32_t* lens;
+  float scale_log2;                 // scale * log2(e)
+  uint16_t* out;                    // bf16 [B, R * H, 512]
+  float* lse;                       // [B, R * H] or nullptr
+  int B, R, H;
+  unsigned char* ws;
+  int* status;
+};
+
+struct PrefillParams {
+  const uint16_t *q, *k, *k_pe, *v;
+  int64_t q_st, q_sh, k_st, k_sh, pe_st, v_st, v_sh;  // element strides: token, head
+  float scale_log2;
+  uint16_t* out;                    // bf16 [tokens, H, 128]
+  float* lse;                       // [tokens, H] or nullptr
+  const int64_t *cu_q, *cu_k;       // [N + 1] or nullptr (dense)
+  const int32_t* blk_off;           // [N + 1] prefix of query blocks (packed only)
+  int64_t B, Tq, Tk, N;
+  int H;
+  int causal;
+  int* status;
+};
+
+// Query rows of one work item of the expanded form.
+constexpr int kPrefillRows = 256;
+
+size_t decode_workspace_bytes(const DecodeParams& p);
+// false: a tensor map could not be made or a launch attribute set (nothing launched)
+bool launch_latent_decode(const DecodeParams& p, cudaStream_t s);
+bool launch_latent_prefill(const PrefillParams& p, cudaStream_t s);
+
+}  // namespace kda

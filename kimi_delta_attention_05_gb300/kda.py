@@ -25,8 +25,8 @@ HEAD_DIM = 128
 
 
 class KdaError(RuntimeError):
-    def __init__(self, code: int, msg: str):
-        super().__init__(f"kda_fwd failed with status {code}: {msg}")
+    def __init__(self, code: int, msg: str, call: str = "kda_fwd"):
+        super().__init__(f"{call} failed with status {code}: {msg}")
         self.code = code
 
 

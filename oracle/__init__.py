@@ -21,6 +21,10 @@ over a plain torch restatement of the same token recurrence
 hand through the chunk algebra (``chunk_backward.py``), pinned to the autograd
 oracle and exposing per-chunk gradient intermediates.
 
+:mod:`oracle.latent` states the latent-attention calls (plan, cache append,
+absorbed and expanded attention) in fp64 numpy; ``tests/test_latent_oracle.py``
+pins it.
+
 Parity status: every function is pinned (see ``tests/test_oracle_pins.py``,
 ``tests/test_oracle_mutations.py`` and ``tests/test_backward_oracle.py``).
 """
@@ -28,3 +32,4 @@ from .recurrence import build, kda_recurrence, gate_activation, max_threads  # n
 from .chunk_form import chunk_form  # noqa: F401
 from .backward import kda_backward, kda_forward_torch  # noqa: F401
 from .chunk_backward import chunk_backward  # noqa: F401
+from . import latent  # noqa: F401
