@@ -1,87 +1,720 @@
-// Absorbed latent attention over the paged cache, simple form: one warp a
-// query row, online softmax over groups of 32 cached rows (lane = cached row
-// for the scores, lane = 16 output values for the products).
+// Absorbed latent attention over the paged cache on the 5th-generation tensor
+// cores: split over the cache's length, joined by a second small kernel.
+//
+// Per query row (token i of a request, head h) with cached rows x_j = [c_j | pe_j]:
+//   s_j = scale q . x_j,   o = sum_j softmax(s)_j c_j,   lse = ln sum_j e^{s_j}
+// Every row of a request reads the same x_j, and c_j serves as key and value,
+// so a cached row crosses HBM once: 1152 bytes against 2 * 1088 flops a query
+// row.  Up to about 64 rows that is bound by HBM.
+//
+// Products, transposed so that the tensor core's fixed 64 / 128 rows are
+// cached tokens and value dimensions, and its free width N the query rows
+// (16, 32 or 64): few heads then cost few columns instead of empty rows.
+//   S^T [64 tokens x N]      = X (64 x 576, K-major)              . Q^T
+//   O^T [4 x 128 dims x N]  += C^T (128 x 64, the same tile read MN-major) . P^T
+// The tile of 64 cached rows lies in shared memory once, as nine 64-column
+// blocks of [64 tokens][128 bytes] with the 128-byte swizzle.  Tensor memory:
+// O^T 4 N columns, S^T twice N.
+//
+// Softmax: four warps read S^T as 16 x 8 fragments (a thread holds two tokens
+// of N / 4 rows), reduce the maximum over tokens with shuffles, and write P^T
+// as the next product's operand with transposing matrix stores.  The running
+// maximum of a row moves only when it grows by more than 2^8 (exact: the
+// result is divided by the sum taken with the same maximum), so O^T is rarely
+// rescaled; whether any row moves is one reducing barrier.
+//
+// Work: the tiles of all requests in one line, cut into equal shares, one CTA
+// a share; a CTA's share is a few pieces (request, tile range).  A piece that
+// is not its whole request writes its normalised rows and their lse in fp32 to
+// the workspace, and the join kernel weights them in the order of the tiles,
+// so results do not depend on timing.  With more than 64 query rows the CTAs
+// form groups, one a block of rows, that walk the same shares at the same
+// time, so the cache is read from HBM by one of them and from L2 by the others.
+//
+// Roles: warps 0-3 softmax and output, warp 4 copies, warp 5 products.
+// Every wait is bounded; a CTA that gives up sets the status word.
+#include <algorithm>
+#include <cstring>
+#include <numeric>
+
 #include "../../include/kda_latent.h"
-#include "kda_common.cuh"
 #include "kda_latent.cuh"
+#include "kda_latent_tc.cuh"
 
 namespace kda {
 
-__global__ void __launch_bounds__(128) kda_latent_decode_kernel(const DecodeParams p) {
-  __shared__ float qs[4][kLatRow];
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const int rows = p.R * p.H;
-  const int64_t item = (int64_t)blockIdx.x * 4 + warp;
-  if (item >= (int64_t)p.B * rows) return;
-  const int b = (int)(item / rows), i = (int)(item % rows) / p.H;
-  int64_t len = p.lens[b];
-  const int64_t cap = p.max_pages * p.page_size;
-  if (len < 0 || len > cap) {
-    if (lane == 0) atomicExch(p.status, KDA_ERR_BAD_LENGTHS);
-    len = len < 0 ? 0 : cap;
+constexpr int kDecTile = 64;                     // cached rows of a tile
+constexpr int kDecChunks = kLatRow / 64;         // 64-column blocks of a row
+constexpr int kDecStages = 2;
+constexpr int kDecBlk = kDecTile * 128;          // bytes of a 64-column block of a tile
+constexpr int kDecStage = kDecChunks * kDecBlk;  // 73728
+constexpr int kDecThreads = 192;
+constexpr float kDecSlack = 8.0f;                // log2 growth of a maximum that is let pass
+
+struct DecodeMaps {
+  CUtensorMap q, cache;
+};
+
+struct DecodePlan {
+  int row_blocks;      // groups of CTAs
+  int shares;          // CTAs of a group
+  int box_rows;        // cached rows of one tensor copy: gcd(page_size, 64)
+  int min_tiles;       // least tiles of a share
+  float* part;         // [row_blocks * shares * 2][N][512] normalised partial rows
+  float* part_lse;     // [row_blocks * shares * 2][N] their lse, log2
+  int4* split;         // [row_blocks * shares]: request that starts here and ends in another share, its last share
+};
+
+template <int N>
+struct DecCfg {
+  static constexpr int kQBufs = N <= 32 ? 2 : 1;
+  static constexpr int kQBytes = kDecChunks * N * 128;
+  static constexpr int kQ = kDecStages * kDecStage;
+  static constexpr int kP = kQ + kQBufs * kQBytes;          // [N][64 tokens] bf16
+  static constexpr int kWmax = kP + N * 128;                // fp32 [4][N]: maxima, then sums, of the warps
+  static constexpr int kFac = kWmax + 16 * N;               // fp32 [N]
+  static constexpr int kBar = kFac + 4 * N;
+  // full[2], empty[2], qfull[2], qempty[2], sfull[2], pready, pvdone
+  static constexpr int kFull = 0, kEmpty = 2, kQFull = 4, kQEmpty = 6, kSFull = 8, kPReady = 10, kPvDone = 11,
+                       kBars = 12;
+  static constexpr int kScan = kBar + 8 * kBars;            // int64 [6] warp sums, [2] first request and its prefix
+  static constexpr int kTmem = kScan + 64;
+  static constexpr int kAbort = kTmem + 8;
+  static constexpr int kSmem = kAbort + 8;
+  static constexpr uint32_t kCols = N == 16 ? 128 : N == 32 ? 256 : 512;  // 6 N rounded up
+  static_assert(kP % 1024 == 0 && kQ % 1024 == 0 && kDecStage % 1024 == 0, "operand images need 1024-byte alignment");
+  static_assert(kSmem <= 232448, "exceeds the opt-in shared memory of one CTA");
+};
+
+// A request's length, clamped to what its table can hold.
+__device__ __forceinline__ int64_t dec_len(const DecodeParams& p, int b) {
+  const int64_t len = p.lens[b], cap = p.max_pages * p.page_size;
+  return len < 0 ? 0 : (len > cap ? cap : len);
+}
+__device__ __forceinline__ int64_t dec_tiles(int64_t len) { return len > 0 ? (len + kDecTile - 1) / kDecTile : 1; }
+
+// The pieces of one share, in order.
+struct DecPieces {
+  int64_t u, u1, pre;  // next tile, end of the share, first tile of request b
+  int b;
+  // the current piece
+  int req;
+  int64_t len, t0, t1, tiles;
+  __device__ __forceinline__ bool next(const DecodeParams& p) {
+    if (u >= u1) return false;
+    req = b;
+    len = dec_len(p, b);
+    tiles = dec_tiles(len);
+    t0 = u - pre;
+    t1 = min(tiles, u1 - pre);
+    u = pre + t1;
+    pre += tiles;
+    ++b;
+    return true;
   }
-  const int64_t seen = len - (p.R - 1 - i);
-  for (int d = lane; d < kLatRow; d += 32) qs[warp][d] = bf16_to_f(p.q[item * kLatRow + d]);
-  __syncwarp();
-  float m = -INFINITY, l = 0.f, acc[16];
+  __device__ __forceinline__ int64_t count() const { return len > 0 ? t1 - t0 : 0; }
+};
+
+// A walk over the tiles of a share.
+struct DecCursor {
+  DecPieces it;
+  int64_t tile;
+  int piece;  // index of the piece among those with tiles
+  bool ok;
+  __device__ __forceinline__ void start(const DecPieces& s, const DecodeParams& p) {
+    it = s;
+    piece = -1;
+    ok = true;
+    piece_with_tiles(p);
+  }
+  __device__ __forceinline__ void piece_with_tiles(const DecodeParams& p) {
+    do {
+      ok = it.next(p);
+    } while (ok && it.count() == 0);
+    tile = it.t0;
+    ++piece;
+  }
+  __device__ __forceinline__ void advance(const DecodeParams& p) {
+    if (++tile >= it.t1) piece_with_tiles(p);
+  }
+  __device__ __forceinline__ bool first() const { return tile == it.t0; }
+  __device__ __forceinline__ bool last() const { return tile + 1 == it.t1; }
+};
+
+template <int N>
+__global__ void __launch_bounds__(kDecThreads, 1)
+    kda_latent_decode_kernel(const DecodeParams p, const DecodePlan pl, const __grid_constant__ DecodeMaps maps) {
+  using C = DecCfg<N>;
+  extern __shared__ __align__(1024) unsigned char smem[];
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int rblk = blockIdx.x % pl.row_blocks, share = blockIdx.x / pl.row_blocks;
+  const int rows = p.R * p.H, row0 = rblk * N;
+  const uint32_t sb = smem_u32(smem);
+  const uint32_t bars = sb + C::kBar;
+  auto bar = [&](int i) { return bars + 8 * i; };
+  volatile int* s_abort = reinterpret_cast<volatile int*>(smem + C::kAbort);
+  int64_t* s_scan = reinterpret_cast<int64_t*>(smem + C::kScan);
+
+  // ---- set-up: barriers, tensor memory, this CTA's share of the tiles ----
+  if (tid == 0) {
+    for (int i = 0; i < C::kBars; ++i) mbar_init(bar(i), i == C::kPReady ? 4 : 1);
+    *s_abort = (sb & 1023) ? 1 : 0;
+    s_scan[6] = 0;
+    s_scan[7] = 0;
+    asm volatile("fence.mbarrier_init.release.cluster;\n" ::: "memory");
+  }
+  if (warp == 5) {
+    asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;\n" ::"r"(sb + C::kTmem),
+                 "r"(C::kCols));
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;\n");
+  }
+  if (warp == 4 && lane == 0) {
+    prefetch_map(&maps.q);
+    prefetch_map(&maps.cache);
+  }
+  // each thread sums a run of requests; a scan over threads gives the total
+  // (hence the shares' size) and the run that holds this share's first tile
+  const int run = (p.B + kDecThreads - 1) / kDecThreads;
+  const int b0 = min(p.B, tid * run), b1 = min(p.B, b0 + run);
+  int64_t mine = 0;
+  bool odd = false;
+  for (int b = b0; b < b1; ++b) {
+    const int64_t raw = p.lens[b];
+    const int64_t len = dec_len(p, b);
+    odd |= raw != len;
+    mine += dec_tiles(len);
+  }
+  if (odd && blockIdx.x == 0) atomicExch(p.status, KDA_ERR_BAD_LENGTHS);
+  int64_t incl = mine;
 #pragma unroll
-  for (int d = 0; d < 16; ++d) acc[d] = 0.f;
-  for (int64_t j0 = 0; j0 < seen; j0 += 32) {
-    const int64_t j = j0 + lane;
-    const uint16_t* row = nullptr;
-    float s = -INFINITY;
-    if (j < seen) {
-      const int64_t page = p.table[b * p.table_stride + j / p.page_size];
-      s = 0.f;
-      if (page < 0 || page >= p.num_pages) {
-        atomicExch(p.status, KDA_ERR_BAD_PAGE);
-      } else {
-        row = p.cache + page * p.page_stride + (j % p.page_size) * p.token_stride;
-        for (int d = 0; d < kLatRow; d += 2) {
-          const float2 x = unpack_bf16(*reinterpret_cast<const uint32_t*>(row + d));
-          s += x.x * qs[warp][d] + x.y * qs[warp][d + 1];
+  for (int o = 1; o < 32; o <<= 1) {
+    const int64_t y = __shfl_up_sync(0xffffffffu, incl, o);
+    if (lane >= o) incl += y;
+  }
+  if (lane == 31) s_scan[warp] = incl;
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  int64_t before = 0, total = 0;
+#pragma unroll
+  for (int w = 0; w < kDecThreads / 32; ++w) {
+    if (w < warp) before += s_scan[w];
+    total += s_scan[w];
+  }
+  const int64_t size = max((int64_t)pl.min_tiles, (total + pl.shares - 1) / pl.shares);
+  const int64_t u0 = min(total, share * size), u1 = min(total, u0 + size);
+  before += incl - mine;
+  if (u0 < u1 && u0 >= before && u0 < before + mine) {
+    int64_t pre = before;
+    for (int b = b0; b < b1; ++b) {
+      const int64_t t = dec_tiles(dec_len(p, b));
+      if (u0 < pre + t) {
+        s_scan[6] = b;
+        s_scan[7] = pre;
+        break;
+      }
+      pre += t;
+    }
+  }
+  __syncthreads();
+  DecPieces pieces;
+  pieces.u = u0;
+  pieces.u1 = u1;
+  pieces.b = (int)s_scan[6];
+  pieces.pre = s_scan[7];
+  const uint32_t tmem = *reinterpret_cast<volatile uint32_t*>(smem + C::kTmem);
+  if (*s_abort && tid == 0) atomicExch(p.status, KDA_ERR_DEVICE_TIMEOUT);
+  asm volatile("griddepcontrol.launch_dependents;\n" ::: "memory");
+
+  auto wait = [&](uint32_t b, uint32_t parity) {
+    if (*s_abort) return;
+    if (!mbar_wait_bounded(b, parity)) {
+      atomicExch(p.status, KDA_ERR_DEVICE_TIMEOUT);
+      *s_abort = 1;
+    }
+  };
+
+  if (warp == 4) {
+    // ---- copies: the tiles of the share into the stages, the query rows of each piece ----
+    const int box = pl.box_rows;
+    DecCursor c;
+    c.start(pieces, p);
+    int64_t it = 0;
+    int qi = 0;  // query blocks issued
+    while (c.ok) {
+      const int s = (int)(it & 1);
+      const int64_t j0 = c.tile * kDecTile;
+      const int valid = (int)min((int64_t)kDecTile, c.it.len - j0);
+      const int segs = (valid + box - 1) / box;
+      // page of this lane's run of box rows (lanes below segs), fetched before the wait
+      int page = 0, off = 0;
+      if (lane < segs) {
+        const int64_t j = j0 + (int64_t)lane * box;
+        page = p.table[c.it.req * p.table_stride + j / p.page_size];
+        off = (int)(j % p.page_size);
+        if (page < 0 || page >= p.num_pages) {
+          atomicExch(p.status, KDA_ERR_BAD_PAGE);
+          page = (int)p.num_pages;  // past the map: reads as zeros
         }
       }
-      s *= p.scale_log2;
+      if (it >= kDecStages) wait(bar(C::kEmpty + s), (uint32_t)(((it >> 1) & 1) ^ 1));
+      __syncwarp();
+      if (*s_abort) break;
+      const uint32_t full = bar(C::kFull + s), dst = sb + s * kDecStage;
+      if (lane == 0) mbar_expect_tx(full, (uint32_t)(segs * box * 128 * kDecChunks));
+      __syncwarp();
+      if (box == kDecTile) {
+        if (lane == 0) tma_load_4d(dst, &maps.cache, 0, off, 0, page, full);
+      } else {
+        for (int i0 = 0; i0 < segs * kDecChunks; i0 += 32) {
+          const int i = i0 + lane, seg = i / kDecChunks, ch = i - seg * kDecChunks;
+          const int pg = __shfl_sync(0xffffffffu, page, seg & 31), of = __shfl_sync(0xffffffffu, off, seg & 31);
+          if (i < segs * kDecChunks)
+            tma_load_4d(dst + ch * kDecBlk + seg * box * 128, &maps.cache, 0, of, ch, pg, full);
+        }
+      }
+      if (c.first()) {
+        const int qb = qi % C::kQBufs;
+        if (qi >= C::kQBufs) wait(bar(C::kQEmpty + qb), (uint32_t)(((qi / C::kQBufs) & 1) ^ 1));
+        __syncwarp();
+        if (*s_abort) {
+          ++it;
+          break;
+        }
+        if (lane == 0) {
+          mbar_expect_tx(bar(C::kQFull + qb), C::kQBytes);
+          tma_load_4d(sb + C::kQ + qb * C::kQBytes, &maps.q, 0, row0, 0, c.it.req, bar(C::kQFull + qb));
+        }
+        ++qi;
+      }
+      ++it;
+      c.advance(p);
     }
-    float mt = s;
+    // After a timeout: let the copies still in flight land before leaving.
+    if (*s_abort && lane == 0) {
+      for (int64_t t = it > kDecStages ? it - kDecStages : 0; t < it; ++t)
+        mbar_wait_bounded(bar(C::kFull + (int)(t & 1)), (uint32_t)((t >> 1) & 1));
+      for (int t = qi > C::kQBufs ? qi - C::kQBufs : 0; t < qi; ++t)
+        mbar_wait_bounded(bar(C::kQFull + t % C::kQBufs), (uint32_t)((t / C::kQBufs) & 1));
+    }
+  } else if (warp == 5) {
+    // ---- products ----
+    const uint32_t id_s = idesc_bf16(64, N, false, false), id_o = idesc_bf16(128, N, true, false);
+    const uint64_t d_x = smem_desc(sb, 16, 1024), d_c = smem_desc(sb, kDecBlk, 1024);
+    const uint64_t d_q = smem_desc(sb + C::kQ, 16, 1024), d_p = smem_desc(sb + C::kP, 16, 1024);
+    const uint32_t t_s = tmem + 4 * N;
+    DecCursor cs, co;
+    cs.start(pieces, p);
+    co = cs;
+    int64_t is = 0, io = 0;
+    auto scores_ready = [&]() {
+      bool r = mbar_test(bar(C::kFull + (int)(is & 1)), (uint32_t)((is >> 1) & 1));
+      if (cs.first()) r = r && mbar_test(bar(C::kQFull + cs.piece % C::kQBufs), (uint32_t)((cs.piece / C::kQBufs) & 1));
+      return __all_sync(0xffffffffu, r);
+    };
+    auto scores = [&]() {  // S^T of tile `is` into its half of the score columns
+      const int s = (int)(is & 1), qb = cs.piece % C::kQBufs;
+      if (cs.first()) wait(bar(C::kQFull + qb), (uint32_t)((cs.piece / C::kQBufs) & 1));
+      wait(bar(C::kFull + s), (uint32_t)((is >> 1) & 1));
+      __syncwarp();
+      tc_fence_after();
+      const uint64_t a = d_x + (uint64_t)((s * kDecStage) >> 4), b = d_q + (uint64_t)((qb * C::kQBytes) >> 4);
 #pragma unroll
-    for (int o = 16; o > 0; o >>= 1) mt = fmaxf(mt, __shfl_xor_sync(0xffffffffu, mt, o));
-    const float mn = fmaxf(m, mt), f = ex2(m - mn);
-    const float e = ex2(s - mn);
-    m = mn;
-    l = l * f + e;
+      for (int ch = 0; ch < kDecChunks; ++ch)
 #pragma unroll
-    for (int d = 0; d < 16; ++d) acc[d] *= f;
-    const int cnt = (int)min((int64_t)32, seen - j0);
-    for (int jj = 0; jj < cnt; ++jj) {
-      const float w = __shfl_sync(0xffffffffu, e, jj);
-      const uint64_t r = __shfl_sync(0xffffffffu, (unsigned long long)row, jj);
-      if (!r) continue;
-      const uint32_t* v = reinterpret_cast<const uint32_t*>(r) + lane;
+        for (int ks = 0; ks < 4; ++ks)
+          tc_mma(t_s + N * s, a + (uint64_t)((ch * kDecBlk + ks * 32) >> 4), b + (uint64_t)((ch * N * 128 + ks * 32) >> 4),
+                 id_s, ch + ks > 0);
+      tc_commit(bar(C::kSFull + s));
+      if (cs.last()) tc_commit(bar(C::kQEmpty + qb));
+      ++is;
+      cs.advance(p);
+    };
+    if (cs.ok) scores();
+    while (co.ok) {
+      const int s = (int)(io & 1);
+      // the next tile's scores first if it has landed, so that the softmax of one
+      // tile overlaps the products of the other; else do not wait for it here
+      if (is == io + 1 && cs.ok && scores_ready()) scores();
+      wait(bar(C::kPReady), (uint32_t)(io & 1));
+      const int valid = (int)min((int64_t)kDecTile, co.it.len - co.tile * kDecTile);
+      if (valid < kDecTile) {
+        // what lies behind the length takes part in the product with weight 0: it has to be finite
+        const int n16 = (kDecTile - valid) * 8;
+        for (int ch = 0; ch < kLat / 64; ++ch)
+          for (int i = lane; i < n16; i += 32)
+            reinterpret_cast<uint4*>(smem + s * kDecStage + ch * kDecBlk + valid * 128)[i] = make_uint4(0, 0, 0, 0);
+        fence_proxy_async_smem();
+      }
+      __syncwarp();
+      tc_fence_after();
+      const uint64_t a = d_c + (uint64_t)((s * kDecStage) >> 4);
+      const uint32_t start = co.first() ? 0u : 1u;
 #pragma unroll
-      for (int d = 0; d < 8; ++d) {
-        const float2 x = unpack_bf16(v[32 * d]);
-        acc[2 * d] += w * x.x;
-        acc[2 * d + 1] += w * x.y;
+      for (int mt = 0; mt < 4; ++mt)
+#pragma unroll
+        for (int ks = 0; ks < 4; ++ks)
+          tc_mma(tmem + mt * N, a + (uint64_t)((mt * 2 * kDecBlk + ks * 2048) >> 4), d_p + (uint64_t)((ks * 32) >> 4),
+                 id_o, ks > 0 ? 1u : start);
+      tc_commit(bar(C::kEmpty + s));
+      tc_commit(bar(C::kPvDone));
+      if (is == io + 1 && cs.ok) scores();
+      ++io;
+      co.advance(p);
+    }
+    if (io > 0) mbar_wait_bounded(bar(C::kPvDone), (uint32_t)((io - 1) & 1));  // before tensor memory is freed
+  } else {
+    // ---- softmax and output: warp w holds tokens 16 w .. 16 w + 15 of a tile, then
+    //      value dimensions 32 w .. of each 128 ----
+    constexpr int kV = N / 2;  // scores of a thread: 8-column group g, v[4 g + 2 r + e] = row 8 g + 2 (lane % 4) + e
+    constexpr int kM = N / 4;  //   of token lane / 4 + 8 r; maxima and sums m[2 g + e]
+    float* wmax = reinterpret_cast<float*>(smem + C::kWmax);
+    float* fac = reinterpret_cast<float*>(smem + C::kFac);
+    const uint32_t lane_base = (uint32_t)(warp * 32) << 16;
+    const int tok = 16 * warp + (lane >> 2);
+    const int c0 = 2 * (lane & 3);
+    // this lane's address for the transposing stores: matrix lane / 8, row lane % 8
+    const int st_head = 8 * (lane >> 4) + (lane & 7), st_chunk = 2 * warp + ((lane >> 3) & 1);
+    const uint32_t st_addr = sb + C::kP + st_head * 128 + ((st_chunk ^ (lane & 7)) << 4);
+    int64_t it = 0;
+    while (pieces.next(p)) {
+      const int64_t nt = pieces.count();
+      const bool whole = pieces.t0 == 0 && pieces.t1 == pieces.tiles;
+      float m[kM], l[kM];
+#pragma unroll
+      for (int i = 0; i < kM; ++i) {
+        m[i] = -INFINITY;
+        l[i] = 0.f;
+      }
+      for (int64_t tile = pieces.t0; tile < pieces.t0 + nt; ++tile, ++it) {
+        const int s = (int)(it & 1);
+        wait(bar(C::kSFull + s), (uint32_t)((it >> 1) & 1));
+        __syncwarp();
+        tc_fence_after();
+        float v[kV];
+        tc_ld16x256(tmem + lane_base + 4 * N + N * s, v);
+#pragma unroll
+        for (int i = 0; i < kV; ++i) v[i] *= p.scale_log2;
+        const int64_t j = tile * kDecTile + tok;
+        if ((tile + 1) * kDecTile > pieces.len - (p.R - 1)) {
+          // the last tiles: row (token i, head) sees j < len - (R - 1 - i)
+#pragma unroll
+          for (int i = 0; i < kM; ++i) {
+            const int row = row0 + 8 * (i >> 1) + c0 + (i & 1);
+            const int64_t seen = pieces.len - max(0, p.R - 1 - row / p.H);
+            if (j >= seen) v[4 * (i >> 1) + (i & 1)] = -INFINITY;
+            if (j + 8 >= seen) v[4 * (i >> 1) + 2 + (i & 1)] = -INFINITY;
+          }
+        }
+        float mx[kM];
+        bool grow = false;
+#pragma unroll
+        for (int i = 0; i < kM; ++i) {
+          float x = fmaxf(v[4 * (i >> 1) + (i & 1)], v[4 * (i >> 1) + 2 + (i & 1)]);
+          x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 4));
+          x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 8));
+          x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 16));
+          mx[i] = x;
+          grow |= x > m[i] + kDecSlack;
+        }
+        const bool first = tile == pieces.t0;
+        if (named_bar_or(1, 128, grow)) {
+          if (lane < 4) {
+#pragma unroll
+            for (int i = 0; i < kM; ++i) wmax[warp * N + 8 * (i >> 1) + c0 + (i & 1)] = mx[i];
+          }
+          named_bar(1, 128);
+          float f[kM];
+#pragma unroll
+          for (int i = 0; i < kM; ++i) {
+            const int c = 8 * (i >> 1) + c0 + (i & 1);
+            const float x = fmaxf(fmaxf(wmax[c], wmax[N + c]), fmaxf(wmax[2 * N + c], wmax[3 * N + c]));
+            f[i] = 1.0f;
+            if (x > m[i] + kDecSlack) {
+              f[i] = ex2(m[i] - x);
+              m[i] = x;
+              l[i] *= f[i];
+            }
+          }
+          if (!first) {  // O^T of the tiles so far to the new maxima
+            if (warp == 0 && lane < 4) {
+#pragma unroll
+              for (int i = 0; i < kM; ++i) fac[8 * (i >> 1) + c0 + (i & 1)] = f[i];
+            }
+            wait(bar(C::kPvDone), (uint32_t)((it - 1) & 1));
+            named_bar(1, 128);
+            tc_fence_after();
+#pragma unroll 1
+            for (int cc = 0; cc < 4 * N; cc += 16) {
+              float o[16];
+              tc_ld16(tmem + lane_base + cc, o);
+#pragma unroll
+              for (int i = 0; i < 16; ++i) o[i] *= fac[(cc % N) + i];
+              tc_st16(tmem + lane_base + cc, o);
+            }
+            tc_st_wait();
+          }
+        }
+#pragma unroll
+        for (int i = 0; i < kM; ++i) {
+          const float base = m[i] == -INFINITY ? 0.f : m[i];
+          float& x = v[4 * (i >> 1) + (i & 1)];
+          float& y = v[4 * (i >> 1) + 2 + (i & 1)];
+          x = ex2(x - base);
+          y = ex2(y - base);
+          l[i] += x + y;
+        }
+        if (it > 0) wait(bar(C::kPvDone), (uint32_t)((it - 1) & 1));  // P^T of the tile before is read
+        __syncwarp();
+        // weights rounded to bf16, the operands' type: 2^-9 of each on average, and the sum is taken before it
+#pragma unroll
+        for (int g = 0; g < N / 8; g += 2)
+          stsm_x4_t(st_addr + g * 1024, pack_bf16(v[4 * g], v[4 * g + 1]), pack_bf16(v[4 * g + 2], v[4 * g + 3]),
+                    pack_bf16(v[4 * g + 4], v[4 * g + 5]), pack_bf16(v[4 * g + 6], v[4 * g + 7]));
+        fence_proxy_async_smem();
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(bar(C::kPReady));
+      }
+      // ---- the piece's rows ----
+      named_bar(1, 128);  // wmax and fac of the last tile are read
+#pragma unroll
+      for (int i = 0; i < kM; ++i) {
+        l[i] += __shfl_xor_sync(0xffffffffu, l[i], 4);
+        l[i] += __shfl_xor_sync(0xffffffffu, l[i], 8);
+        l[i] += __shfl_xor_sync(0xffffffffu, l[i], 16);
+        if (lane < 4) wmax[warp * N + 8 * (i >> 1) + c0 + (i & 1)] = l[i];
+      }
+      named_bar(1, 128);
+      const int slot = 2 * blockIdx.x + (pieces.t0 > 0 ? 0 : 1);
+      if (warp == 0 && lane < 4) {
+#pragma unroll
+        for (int i = 0; i < kM; ++i) {
+          const int c = 8 * (i >> 1) + c0 + (i & 1);
+          const float sum = (wmax[c] + wmax[N + c]) + (wmax[2 * N + c] + wmax[3 * N + c]);
+          fac[c] = sum > 0.f ? 1.0f / sum : (sum == 0.f ? 0.f : sum);
+          const float lse2 = sum == 0.f ? -INFINITY : m[i] + __log2f(sum);
+          if (!whole) {
+            pl.part_lse[(int64_t)slot * N + c] = lse2;
+          } else if (p.lse && row0 + c < rows) {
+            p.lse[(int64_t)pieces.req * rows + row0 + c] = lse2 * 0.6931471805599453f;
+          }
+        }
+      }
+      if (nt > 0) {
+        wait(bar(C::kPvDone), (uint32_t)((it - 1) & 1));
+        __syncwarp();
+      }
+      named_bar(1, 128);
+      tc_fence_after();
+#pragma unroll 1
+      for (int cc = 0; cc < 4 * N; cc += 16) {
+        const int dim = (cc / N) * 128 + warp * 32;  // this warp's 32 dimensions of the block of 128
+        const int r0 = cc % N;
+        float o[16];
+        if (nt > 0) {
+          tc_ld16(tmem + lane_base + cc, o);
+        } else {
+#pragma unroll
+          for (int i = 0; i < 16; ++i) o[i] = 0.f;
+        }
+#pragma unroll
+        for (int i = 0; i < 16; ++i) o[i] = fac[r0 + i] == 0.f ? 0.f : o[i] * fac[r0 + i];
+        if (!whole) {
+          float* dst = pl.part + ((int64_t)slot * N + r0) * kLat + dim + lane;
+#pragma unroll
+          for (int i = 0; i < 16; ++i) dst[i * kLat] = o[i];
+        } else {
+          // two rows at a time: even lanes store two dimensions of the first, odd lanes of the second
+#pragma unroll
+          for (int i = 0; i < 16; i += 2) {
+            const float other = __shfl_xor_sync(0xffffffffu, (lane & 1) ? o[i] : o[i + 1], 1);
+            const uint32_t w = (lane & 1) ? pack_bf16(other, o[i + 1]) : pack_bf16(o[i], other);
+            const int row = row0 + r0 + i + (lane & 1);
+            if (row < rows)
+              *reinterpret_cast<uint32_t*>(p.out + ((int64_t)pieces.req * rows + row) * kLat + dim + (lane & ~1)) = w;
+          }
+        }
+      }
+      named_bar(1, 128);  // fac is read
+    }
+    tc_fence_before();
+  }
+  if (tid == 0) {
+    // the request that starts in this share and ends in a later one
+    int4 info = make_int4(-1, 0, 0, 0);
+    if (u0 < u1) {
+      DecPieces last = pieces;
+      last.u = u0;
+      last.u1 = u1;
+      last.b = (int)s_scan[6];
+      last.pre = s_scan[7];
+      while (last.next(p)) {
+      }
+      if (last.t0 == 0 && last.t1 < last.tiles) {
+        info.x = last.req;
+        info.y = (int)((last.pre - 1) / size);  // share of the request's last tile
       }
     }
+    pl.split[blockIdx.x] = info;
   }
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) l += __shfl_xor_sync(0xffffffffu, l, o);
-  const float inv = l > 0.f ? 1.0f / l : 0.f;
-  uint32_t* out = reinterpret_cast<uint32_t*>(p.out + item * kLat) + lane;
-#pragma unroll
-  for (int d = 0; d < 8; ++d) out[32 * d] = pack_bf16(acc[2 * d] * inv, acc[2 * d + 1] * inv);
-  if (lane == 0 && p.lse) p.lse[item] = seen > 0 ? m / kLog2e + logf(l) : -INFINITY;
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  if (warp == 5)
+    asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;\n" ::"r"(tmem), "r"(C::kCols));
 }
 
-size_t decode_workspace_bytes(const DecodeParams&) { return 0; }
+// Joins the parts of a request that several shares hold: out = sum_k w_k o_k,
+// w_k = 2^(lse_k - lse), in the shares' order.  A CTA a row of one split
+// request: 128 threads x 4 dimensions, four quarters of the parts side by side.
+__global__ void __launch_bounds__(512) kda_latent_join_kernel(const DecodeParams p, const DecodePlan pl, int n) {
+  __shared__ float part[4][kLat];
+  __shared__ float wts[4];
+  asm volatile("griddepcontrol.wait;\n" ::: "memory");
+  const int4 info = pl.split[blockIdx.x];
+  if (info.x < 0) return;
+  const int rblk = blockIdx.x % pl.row_blocks, first = blockIdx.x / pl.row_blocks;
+  const int rows = p.R * p.H, row = rblk * n + blockIdx.y;
+  if (row >= rows) return;
+  const int parts = info.y - first + 1;
+  const int tid = threadIdx.x, quarter = tid >> 7, t = tid & 127;
+  auto slot = [&](int k) {  // the first part is its share's second slot, the others their shares' first
+    return (int64_t)(2 * ((first + k) * pl.row_blocks + rblk) + (k == 0 ? 1 : 0)) * n + blockIdx.y;
+  };
+  float top = -INFINITY;
+  for (int k = 0; k < parts; ++k) top = fmaxf(top, pl.part_lse[slot(k)]);
+  const float base = top == -INFINITY ? 0.f : top;
+  const int k0 = parts * quarter / 4, k1 = parts * (quarter + 1) / 4;
+  float acc[4] = {0.f, 0.f, 0.f, 0.f}, sum = 0.f;
+#pragma unroll 4
+  for (int k = k0; k < k1; ++k) {
+    const int64_t at = slot(k);
+    const float w = ex2(pl.part_lse[at] - base);
+    const float4 x = reinterpret_cast<const float4*>(pl.part + at * kLat)[t];
+    sum += w;
+    if (w != 0.f) {
+      acc[0] += w * x.x;
+      acc[1] += w * x.y;
+      acc[2] += w * x.z;
+      acc[3] += w * x.w;
+    }
+  }
+  reinterpret_cast<float4*>(part[quarter])[t] = make_float4(acc[0], acc[1], acc[2], acc[3]);
+  if (t == 0) wts[quarter] = sum;
+  __syncthreads();
+  const float total = (wts[0] + wts[1]) + (wts[2] + wts[3]);
+  const float inv = total > 0.f ? 1.0f / total : (total == 0.f ? 0.f : total);
+  const float o = (part[0][tid] + part[1][tid]) + (part[2][tid] + part[3][tid]);
+  const int64_t at = (int64_t)info.x * rows + row;
+  __nv_bfloat16 r = __float2bfloat16_rn(o * inv);
+  reinterpret_cast<__nv_bfloat16*>(p.out)[at * kLat + tid] = r;
+  if (tid == 0 && p.lse) p.lse[at] = total == 0.f ? -INFINITY : (top + __log2f(total)) * 0.6931471805599453f;
+}
 
-bool launch_latent_decode(const DecodeParams& p, cudaStream_t s) {
-  const int64_t items = (int64_t)p.B * p.R * p.H;
-  kda_latent_decode_kernel<<<(unsigned)((items + 3) / 4), 128, 0, s>>>(p);
-  return true;
+namespace {
+
+int device_sm_count() {
+  int dev = 0, sms = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess ||
+      cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess) {
+    cudaGetLastError();
+    return 0;
+  }
+  return sms;
+}
+
+// Columns of the products: the query rows of a request rounded up to 16, 32 or
+// 64; blocks of 64 beyond that.
+int dec_width(const DecodeParams& p) {
+  const int rows = p.R * p.H;
+  return rows <= 16 ? 16 : rows <= 32 ? 32 : 64;
+}
+
+struct DecLayout {
+  DecodePlan plan;
+  int n;
+  size_t lse_at, split_at, bytes;
+};
+
+DecLayout dec_layout(const DecodeParams& p) {
+  DecLayout d;
+  memset(&d, 0, sizeof(d));
+  d.n = dec_width(p);
+  const int sms = std::max(1, device_sm_count());
+  const int rows = p.R * p.H;
+  d.plan.row_blocks = (rows + d.n - 1) / d.n;
+  const int64_t most = (int64_t)p.B * std::max<int64_t>(1, (p.max_pages * p.page_size + kDecTile - 1) / kDecTile);
+  d.plan.min_tiles = 2;
+  d.plan.shares = (int)std::max<int64_t>(1, std::min<int64_t>(sms / d.plan.row_blocks,
+                                                              (most + d.plan.min_tiles - 1) / d.plan.min_tiles));
+  d.plan.box_rows = (int)std::gcd<int64_t, int64_t>(p.page_size, kDecTile);
+  const size_t ctas = (size_t)d.plan.row_blocks * d.plan.shares;
+  d.lse_at = ctas * 2 * d.n * kLat * 4;
+  d.split_at = d.lse_at + ctas * 2 * d.n * 4;
+  d.bytes = (d.split_at + ctas * sizeof(int4) + 255) / 256 * 256;
+  return d;
+}
+
+template <int N>
+bool launch_dec(const DecodeParams& p, const DecLayout& d, const DecodeMaps& maps, cudaStream_t s) {
+  const unsigned ctas = (unsigned)(d.plan.row_blocks * d.plan.shares);
+  static std::once_flag once[64];
+  static cudaError_t rc[64];
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return false;
+  std::call_once(once[dev], [&] {
+    rc[dev] = cudaFuncSetAttribute(kda_latent_decode_kernel<N>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                   DecCfg<N>::kSmem);
+  });
+  if (rc[dev] != cudaSuccess) return false;
+  kda_latent_decode_kernel<N><<<ctas, kDecThreads, DecCfg<N>::kSmem, s>>>(p, d.plan, maps);
+  if (d.plan.shares == 1) return true;  // no request is split
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(ctas, (unsigned)std::min(N, p.R * p.H));
+  cfg.blockDim = dim3(512);
+  cfg.stream = s;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kda_latent_join_kernel, p, d.plan, N) == cudaSuccess;
+}
+
+}  // namespace
+
+size_t decode_workspace_bytes(const DecodeParams& p) { return dec_layout(p).bytes; }
+
+bool launch_latent_decode(const DecodeParams& args, cudaStream_t s) {
+  DecodeParams p = args;
+  DecLayout d = dec_layout(p);
+  d.plan.part = reinterpret_cast<float*>(p.ws);
+  d.plan.part_lse = reinterpret_cast<float*>(p.ws + d.lse_at);
+  d.plan.split = reinterpret_cast<int4*>(p.ws + d.split_at);
+  DecodeMaps maps;
+  memset(&maps, 0, sizeof(maps));
+  const int rows = p.R * p.H;
+  {  // query rows [B][rows][576] as [64 values][rows][9 blocks][B]: one copy brings N rows of a request
+    const cuuint64_t dims[4] = {64, (cuuint64_t)rows, (cuuint64_t)kDecChunks, (cuuint64_t)p.B};
+    const cuuint64_t strides[3] = {kLatRow * 2, 128, (cuuint64_t)rows * kLatRow * 2};
+    const cuuint32_t box[4] = {64, (cuuint32_t)d.n, (cuuint32_t)kDecChunks, 1};
+    if (!encode_map_bf16(&maps.q, p.q, 4, dims, strides, box)) return false;
+  }
+  if (p.num_pages == 0) {
+    p.max_pages = 0;  // no cache: every length is taken as 0, and nothing is copied
+  } else {  // the cache as [64 values][page rows][9 blocks][pages]
+    const cuuint64_t dims[4] = {64, (cuuint64_t)p.page_size, (cuuint64_t)kDecChunks, (cuuint64_t)p.num_pages};
+    const cuuint64_t strides[3] = {(cuuint64_t)p.token_stride * 2, 128, (cuuint64_t)p.page_stride * 2};
+    const cuuint32_t box[4] = {64, (cuuint32_t)d.plan.box_rows,
+                               (cuuint32_t)(d.plan.box_rows == kDecTile ? kDecChunks : 1), 1};
+    if (!encode_map_bf16(&maps.cache, p.cache, 4, dims, strides, box)) return false;
+  }
+  switch (d.n) {
+    case 16: return launch_dec<16>(p, d, maps, s);
+    case 32: return launch_dec<32>(p, d, maps, s);
+    default: return launch_dec<64>(p, d, maps, s);
+  }
 }
 
 }  // namespace kda
