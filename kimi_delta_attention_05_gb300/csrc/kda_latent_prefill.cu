@@ -1,16 +1,101 @@
-// Expanded latent attention, simple form: a CTA per (block of 256 query rows,
-// head), one warp a query row at a time, online softmax over groups of 32 keys.
+// Expanded latent attention on the 5th-generation tensor cores: one CTA a
+// (block of 256 query rows, head), two 128-row tiles in turn.
+//
+//   s_ij = scale (q_i . [k_j | pe_j]),  o_i = sum_j softmax(s_i)_j v_j
+// over the keys a row sees (causal: j <= i + Lk - Lq).  The 64 shared key
+// channels are loaded from k_pe for every head; nothing is expanded in memory.
+//
+// Per tile of 128 keys and each of the two query tiles:
+//   S [128 x 128]  = Q (128 x 192, shared memory) . [K | pe]^T
+//   O [128 x 128] += P (128 x 128, bf16 in tensor memory, over S) . V
+// 2 (192 + 128) flops a (row, key) pair: bound by the tensor cores, so the aim
+// is that they never wait.  While one tile's softmax runs, the other tile's
+// products do: the issue order is S0(i), O1(i-1), S1(i), O0(i).  A thread owns
+// a row of S (32x32b loads), so row maximum and sum need no exchange; the
+// running maximum moves only when it grows by more than 2^8 (exact: the result
+// is divided by the sum taken with the same maximum), so O is rarely rescaled.
+//
+// Shared memory: Q 96 KB, and a ring of eight 16 KB slots ([128 keys][64
+// channels], 128-byte swizzle) that takes a tile's three key blocks and two
+// value blocks in the order they are used, each with its own barriers, so a
+// slot is refilled as soon as its products are done.  Tensor memory: S0, S1,
+// O0, O1, 128 columns each.
+//
+// Roles: warps 0-3 and 4-7 softmax and output of the two tiles, warp 8 copies,
+// warp 9 products.  Every wait is bounded; a CTA that gives up sets the status
+// word.
+#include <algorithm>
+#include <cstring>
+
 #include "../../include/kda_latent.h"
-#include "kda_common.cuh"
 #include "kda_latent.cuh"
+#include "kda_latent_tc.cuh"
 
 namespace kda {
 
-__global__ void __launch_bounds__(256) kda_latent_prefill_kernel(const PrefillParams p, int64_t blocks_per_row) {
-  __shared__ float qs[8][kQkDim];
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, h = blockIdx.y;
-  const int64_t blk = blockIdx.x;
-  int64_t q0, k0, lq, lk, r0;
+constexpr int kPreRows = 128;                    // query rows of a tile
+constexpr int kPreKeys = 128;                    // keys of a tile
+constexpr int kPreSlots = 8;
+constexpr int kPreSlot = kPreKeys * 128;         // [128 keys][64 channels] bf16
+constexpr int kPreQ = 0;                         // two tiles of three [128 rows][64 channels] blocks
+constexpr int kPreQTile = 3 * kPreRows * 128;
+constexpr int kPreRing = 2 * kPreQTile;
+constexpr int kPreBar = kPreRing + kPreSlots * kPreSlot;
+// full[8], empty[8], q, sfull[2], pready[2], pvdone[2]
+constexpr int kPbFull = 0, kPbEmpty = 8, kPbQ = 16, kPbS = 17, kPbP = 19, kPbPv = 21, kPbars = 23;
+constexpr int kPreTmem = kPreBar + 8 * kPbars;
+constexpr int kPreAbort = kPreTmem + 8;
+constexpr int kPreSmem = kPreAbort + 8;
+constexpr int kPreThreads = 320;
+constexpr float kPreSlack = 8.0f;                // log2 growth of a maximum that is let pass
+static_assert(kPreRing % 1024 == 0 && kPreSmem <= 232448, "shared memory");
+
+struct PrefillMaps {
+  CUtensorMap q, k, pe, v;
+};
+
+// D += A B with A (bf16) in tensor memory; issue as tc_mma.
+__device__ __forceinline__ void tc_mma_ts(uint32_t d_tmem, uint32_t a_tmem, uint64_t b, uint32_t idesc,
+                                          uint32_t accumulate) {
+  asm volatile(
+      "{\n .reg .pred p, e;\n elect.sync _|e, 0xffffffff;\n setp.ne.u32 p, %4, 0;\n"
+      " @e tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n}\n" ::"r"(d_tmem),
+      "r"(a_tmem), "l"(b), "r"(idesc), "r"(accumulate));
+}
+// 32 columns of this thread's lane, without waiting for the data.
+__device__ __forceinline__ void tc_ld32_nowait(uint32_t taddr, float* v) {
+  uint32_t* r = reinterpret_cast<uint32_t*>(v);
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,"
+      "%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];\n"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
+        "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]), "=r"(r[16]),
+        "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]),
+        "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
+      : "r"(taddr));
+}
+__device__ __forceinline__ void tc_ld_wait() { asm volatile("tcgen05.wait::ld.sync.aligned;\n" ::: "memory"); }
+__device__ __forceinline__ f32x2 fma2(f32x2 a, f32x2 b, f32x2 c) {
+  f32x2 d;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(a), "l"(b), "l"(c));
+  return d;
+}
+__device__ __forceinline__ float max3(float a, float b, float c) {
+  float d;
+  asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
+  return d;
+}
+
+__global__ void __launch_bounds__(kPreThreads, 1)
+    kda_latent_prefill_kernel(const PrefillParams p, int64_t blocks_per_row, const __grid_constant__ PrefillMaps maps) {
+  extern __shared__ __align__(1024) unsigned char smem[];
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int h = blockIdx.x % p.H;
+  // blocks with more keys (later rows of a causal sequence) go first
+  const int64_t nblk = gridDim.x / p.H;
+  int64_t blk = nblk - 1 - blockIdx.x / p.H;
+  int64_t q0, k0;       // first query and key of the sequence
+  int lq, lk, r0;       // its lengths, this block's first row
   if (p.cu_q) {
     if (blk >= p.blk_off[p.N]) return;
     int64_t lo = 0, hi = p.N - 1;
@@ -19,72 +104,323 @@ __global__ void __launch_bounds__(256) kda_latent_prefill_kernel(const PrefillPa
       if (p.blk_off[mid] <= blk) lo = mid; else hi = mid - 1;
     }
     q0 = p.cu_q[lo];
-    lq = p.cu_q[lo + 1] - q0;
+    lq = (int)(p.cu_q[lo + 1] - q0);
     k0 = p.cu_k[lo];
-    lk = p.cu_k[lo + 1] - k0;
-    r0 = (blk - p.blk_off[lo]) * kPrefillRows;
+    lk = (int)(p.cu_k[lo + 1] - k0);
+    r0 = (int)(blk - p.blk_off[lo]) * kPrefillRows;
   } else {
     const int64_t n = blk / blocks_per_row;
     q0 = n * p.Tq;
-    lq = p.Tq;
+    lq = (int)p.Tq;
     k0 = n * p.Tk;
-    lk = p.Tk;
-    r0 = (blk - n * blocks_per_row) * kPrefillRows;
+    lk = (int)p.Tk;
+    r0 = (int)(blk - n * blocks_per_row) * kPrefillRows;
   }
-  const int64_t r1 = min(lq, r0 + kPrefillRows);
-  for (int64_t i = r0 + warp; i < r1; i += 8) {
-    const uint16_t* q = p.q + (q0 + i) * p.q_st + h * p.q_sh;
-    for (int d = lane; d < kQkDim; d += 32) qs[warp][d] = bf16_to_f(q[d]);
-    __syncwarp();
-    const int64_t seen = p.causal ? min(lk, i + lk - lq + 1) : lk;
-    float m = -INFINITY, l = 0.f, acc[4] = {0.f, 0.f, 0.f, 0.f};
-    for (int64_t j0 = 0; j0 < seen; j0 += 32) {
-      const int64_t j = j0 + lane;
-      float s = -INFINITY;
-      if (j < seen) {
-        const uint32_t* k = reinterpret_cast<const uint32_t*>(p.k + (k0 + j) * p.k_st + h * p.k_sh);
-        const uint32_t* pe = reinterpret_cast<const uint32_t*>(p.k_pe + (k0 + j) * p.pe_st);
-        s = 0.f;
-        for (int d = 0; d < kQkDim / 2; ++d) {
-          const float2 x = unpack_bf16(d < kNope / 2 ? k[d] : pe[d - kNope / 2]);
-          s += x.x * qs[warp][2 * d] + x.y * qs[warp][2 * d + 1];
+  // key tiles of the two query tiles (0 where it has no row or its rows see nothing)
+  auto tiles_of = [&](int t) {
+    const int first = r0 + t * kPreRows;
+    if (first >= lq) return 0;
+    const int last = min(lq, first + kPreRows) - 1;
+    const int seen = p.causal ? min(lk, last + lk - lq + 1) : lk;
+    return seen > 0 ? (seen + kPreKeys - 1) / kPreKeys : 0;
+  };
+  const int n0 = tiles_of(0), n1 = tiles_of(1), nt = max(n0, n1);
+
+  const uint32_t sb = smem_u32(smem), bars = sb + kPreBar;
+  auto bar = [&](int i) { return bars + 8 * i; };
+  volatile int* s_abort = reinterpret_cast<volatile int*>(smem + kPreAbort);
+  if (tid == 0) {
+    for (int i = 0; i < kPbars; ++i) mbar_init(bar(i), (i == kPbP || i == kPbP + 1) ? 4 : 1);
+    *s_abort = (sb & 1023) ? 1 : 0;
+    if (sb & 1023) atomicExch(p.status, KDA_ERR_DEVICE_TIMEOUT);
+    asm volatile("fence.mbarrier_init.release.cluster;\n" ::: "memory");
+  }
+  if (warp == 9) {
+    asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;\n" ::"r"(sb + kPreTmem), "r"(512u));
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;\n");
+  }
+  if (warp == 8 && lane == 0) {
+    prefetch_map(&maps.q);
+    prefetch_map(&maps.k);
+    prefetch_map(&maps.pe);
+    prefetch_map(&maps.v);
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = *reinterpret_cast<volatile uint32_t*>(smem + kPreTmem);
+  auto wait = [&](uint32_t b, uint32_t parity) {
+    if (*s_abort) return;
+    if (!mbar_wait_bounded(b, parity)) {
+      atomicExch(p.status, KDA_ERR_DEVICE_TIMEOUT);
+      *s_abort = 1;
+    }
+  };
+
+  if (warp == 8) {
+    // ---- copies: Q, then per key tile K (two blocks), pe, V (two blocks) ----
+    int slot = 0, done = 0;   // next slot of the ring, copies issued
+    uint32_t ph = 1;          // parity of the slots' previous use
+    bool q_sent = false;
+    for (int i = 0; i < nt && !*s_abort; ++i) {
+      const int key = (int)(k0 + (int64_t)i * kPreKeys);
+      for (int c = 0; c < 5; ++c) {
+        if (done >= kPreSlots) wait(bar(kPbEmpty + slot), ph);
+        __syncwarp();
+        if (*s_abort) break;
+        if (lane == 0) {
+          const uint32_t full = bar(kPbFull + slot), dst = sb + kPreRing + slot * kPreSlot;
+          mbar_expect_tx(full, kPreSlot);
+          if (c < 2) tma_load_3d(dst, &maps.k, 64 * c, h, key, full);
+          else if (c == 2) tma_load_2d(dst, &maps.pe, 0, key, full);
+          else tma_load_3d(dst, &maps.v, 64 * (c - 3), h, key, full);
+          if (!q_sent) {
+            mbar_expect_tx(bar(kPbQ), 2 * kPreQTile);
+            for (int t = 0; t < 2; ++t)
+              for (int b = 0; b < 3; ++b)
+                tma_load_3d(sb + kPreQ + t * kPreQTile + b * kPreRows * 128, &maps.q, 64 * b, h,
+                            (int)(q0 + r0 + t * kPreRows), bar(kPbQ));
+          }
         }
-        s *= p.scale_log2;
-      }
-      float mt = s;
-#pragma unroll
-      for (int o = 16; o > 0; o >>= 1) mt = fmaxf(mt, __shfl_xor_sync(0xffffffffu, mt, o));
-      const float mn = fmaxf(m, mt), f = ex2(m - mn), e = ex2(s - mn);
-      m = mn;
-      l = l * f + e;
-#pragma unroll
-      for (int d = 0; d < 4; ++d) acc[d] *= f;
-      const int cnt = (int)min((int64_t)32, seen - j0);
-      for (int jj = 0; jj < cnt; ++jj) {
-        const float w = __shfl_sync(0xffffffffu, e, jj);
-        const uint2 r = reinterpret_cast<const uint2*>(p.v + (k0 + j0 + jj) * p.v_st + h * p.v_sh)[lane];
-        const float2 x = unpack_bf16(r.x), y = unpack_bf16(r.y);
-        acc[0] += w * x.x;
-        acc[1] += w * x.y;
-        acc[2] += w * y.x;
-        acc[3] += w * y.y;
+        q_sent = true;
+        ++done;
+        if (++slot == kPreSlots) {
+          slot = 0;
+          ph ^= 1u;
+        }
       }
     }
+    // After a timeout: let the copies still in flight land before leaving.
+    if (*s_abort && lane == 0) {
+      for (int c = max(0, done - kPreSlots); c < done; ++c)
+        mbar_wait_bounded(bar(kPbFull + c % kPreSlots), (uint32_t)((c / kPreSlots) & 1));
+      if (q_sent) mbar_wait_bounded(bar(kPbQ), 0);
+    }
+  } else if (warp == 9) {
+    // ---- products ----
+    const uint32_t id_s = idesc_bf16(kPreRows, kPreKeys, false, false);
+    const uint32_t id_o = idesc_bf16(kPreRows, kVDim, false, true), id_o64 = idesc_bf16(kPreRows, 64, false, true);
+    const uint64_t d_q = smem_desc(sb + kPreQ, 16, 1024), d_k = smem_desc(sb + kPreRing, 16, 1024);
+    const uint64_t d_v = smem_desc(sb + kPreRing, kPreSlot, 1024);
+    if (nt > 0) {
+      wait(bar(kPbQ), 0);
+      __syncwarp();
+    }
+    auto slot_of = [&](int i, int c) { return (5 * i + c) % kPreSlots; };
+    auto full_wait = [&](int i, int c) {
+      wait(bar(kPbFull + slot_of(i, c)), (uint32_t)(((5 * i + c) / kPreSlots) & 1));
+      __syncwarp();
+      tc_fence_after();
+    };
+    auto scores = [&](int t, int i, bool fresh) {
 #pragma unroll
-    for (int o = 16; o > 0; o >>= 1) l += __shfl_xor_sync(0xffffffffu, l, o);
-    const float inv = l > 0.f ? 1.0f / l : 0.f;
-    const int64_t row = (q0 + i) * p.H + h;
-    reinterpret_cast<uint2*>(p.out + row * kVDim)[lane] =
-        make_uint2(pack_bf16(acc[0] * inv, acc[1] * inv), pack_bf16(acc[2] * inv, acc[3] * inv));
-    if (lane == 0 && p.lse) p.lse[row] = seen > 0 ? m / kLog2e + logf(l) : -INFINITY;
-    __syncwarp();
+      for (int c = 0; c < 3; ++c) {
+        if (fresh) full_wait(i, c);
+        const uint64_t a = d_q + (uint64_t)((t * kPreQTile + c * kPreRows * 128) >> 4);
+        const uint64_t b = d_k + (uint64_t)((slot_of(i, c) * kPreSlot) >> 4);
+#pragma unroll
+        for (int ks = 0; ks < 4; ++ks)
+          tc_mma(tmem + 128 * t, a + 2 * ks, b + 2 * ks, id_s, c + ks > 0);
+      }
+      tc_commit(bar(kPbS + t));
+    };
+    auto values = [&](int t, int i) {
+      wait(bar(kPbP + t), (uint32_t)(i & 1));
+      __syncwarp();
+      tc_fence_after();
+      const int s0 = slot_of(i, 3), s1 = slot_of(i, 4);
+      const uint32_t o = tmem + 256 + 128 * t, a = tmem + 128 * t;
+      const uint64_t b0 = d_v + (uint64_t)((s0 * kPreSlot) >> 4), b1 = d_v + (uint64_t)((s1 * kPreSlot) >> 4);
+      if (s1 == s0 + 1) {  // the two 64-column blocks lie one slot apart: one operand of 128 columns
+#pragma unroll
+        for (int ks = 0; ks < 8; ++ks)
+          tc_mma_ts(o, a + 8 * ks, b0 + (uint64_t)((ks * 2048) >> 4), id_o, i > 0 || ks > 0);
+      } else {
+#pragma unroll
+        for (int ks = 0; ks < 8; ++ks) {
+          tc_mma_ts(o, a + 8 * ks, b0 + (uint64_t)((ks * 2048) >> 4), id_o64, i > 0 || ks > 0);
+          tc_mma_ts(o + 64, a + 8 * ks, b1 + (uint64_t)((ks * 2048) >> 4), id_o64, i > 0 || ks > 0);
+        }
+      }
+      tc_commit(bar(kPbPv + t));
+    };
+    for (int i = 0; i < nt; ++i) {
+      // (the copies of a tile that only the second query tile uses are waited for all the same)
+      if (i < n0) scores(0, i, true);
+      if (i > 0) {
+        if (i - 1 < n1) values(1, i - 1);
+        tc_commit(bar(kPbEmpty + slot_of(i - 1, 3)));
+        tc_commit(bar(kPbEmpty + slot_of(i - 1, 4)));
+      }
+      if (i < n1) scores(1, i, i >= n0);
+      for (int c = 0; c < 3; ++c) tc_commit(bar(kPbEmpty + slot_of(i, c)));
+      full_wait(i, 3);
+      full_wait(i, 4);
+      const int valid = lk - i * kPreKeys;
+      if (valid < kPreKeys) {
+        // rows behind the sequence take part with weight 0: they have to be finite
+        for (int c = 3; c < 5; ++c)
+          for (int x = lane; x < (kPreKeys - valid) * 8; x += 32)
+            reinterpret_cast<uint4*>(smem + kPreRing + slot_of(i, c) * kPreSlot + valid * 128)[x] = make_uint4(0, 0, 0, 0);
+        fence_proxy_async_smem();
+        __syncwarp();
+      }
+      if (i < n0) values(0, i);
+    }
+    if (nt > 0 && nt - 1 < n1) values(1, nt - 1);
+    // the last products complete before tensor memory is freed
+    if (n0 > 0) mbar_wait_bounded(bar(kPbPv), (uint32_t)((n0 - 1) & 1));
+    if (n1 > 0) mbar_wait_bounded(bar(kPbPv + 1), (uint32_t)((n1 - 1) & 1));
+  } else {
+    // ---- softmax and output: thread = row of tile t ----
+    const int t = warp >> 2, q = warp & 3;
+    const int n = t == 0 ? n0 : n1;
+    const int row = r0 + t * kPreRows + q * 32 + lane;  // query within the sequence
+    const int lim = p.causal ? min(lk, row + lk - lq + 1) : lk;
+    const int lim_first = p.causal ? min(lk, row - lane + lk - lq + 1) : lk;  // the warp's first row's
+    const uint32_t lane_base = (uint32_t)(q * 32) << 16;
+    const uint32_t t_s = tmem + lane_base + 128 * t, t_o = tmem + lane_base + 256 + 128 * t;
+    const float sl = p.scale_log2;
+    const f32x2 sl2 = f2(sl, sl);
+    float m = -INFINITY, l = 0.f;  // maximum (times scale, log2) and sum
+    for (int i = 0; i < n; ++i) {
+      wait(bar(kPbS + t), (uint32_t)(i & 1));
+      __syncwarp();
+      tc_fence_after();
+      float s[128];
+#pragma unroll
+      for (int c = 0; c < 4; ++c) tc_ld32_nowait(t_s + 32 * c, s + 32 * c);
+      tc_ld_wait();
+      if ((i + 1) * kPreKeys > lim_first) {
+        const int rem = lim - i * kPreKeys;
+#pragma unroll
+        for (int c = 0; c < 128; ++c)
+          if (c >= rem) s[c] = -INFINITY;
+      }
+      float mx[4] = {s[0], s[1], s[2], s[3]};
+#pragma unroll
+      for (int c = 4; c < 124; c += 8)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) mx[e] = max3(mx[e], s[c + 2 * e], s[c + 2 * e + 1]);
+      mx[0] = max3(mx[0], s[124], s[125]);
+      mx[1] = max3(mx[1], s[126], s[127]);
+      const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * sl;
+      if (__any_sync(0xffffffffu, top > m + kPreSlack)) {
+        float f = 1.0f;
+        if (top > m + kPreSlack) {
+          f = ex2(m - top);
+          m = top;
+          l *= f;
+        }
+        if (i > 0) {
+          wait(bar(kPbPv + t), (uint32_t)((i - 1) & 1));
+          __syncwarp();
+          tc_fence_after();
+#pragma unroll 1
+          for (int c = 0; c < 128; c += 16) {
+            float o[16];
+            tc_ld16(t_o + c, o);
+#pragma unroll
+            for (int e = 0; e < 16; ++e) o[e] *= f;
+            tc_st16(t_o + c, o);
+          }
+        }
+      }
+      const float base = m == -INFINITY ? 0.f : -m;
+      const f32x2 base2 = f2(base, base);
+      f32x2 sum[2] = {f2(0.f, 0.f), f2(0.f, 0.f)};
+#pragma unroll
+      for (int c = 0; c < 128; c += 32) {
+        float w[16];  // 32 weights as bf16 pairs (the operand type; the sum is taken before the rounding)
+#pragma unroll
+        for (int e = 0; e < 16; ++e) {
+          const float2 x = f2u(fma2(f2(s[c + 2 * e], s[c + 2 * e + 1]), sl2, base2));
+          const float a = ex2(x.x), b = ex2(x.y);
+          sum[e & 1] = add2(sum[e & 1], f2(a, b));
+          w[e] = __uint_as_float(pack_bf16(a, b));
+        }
+        tc_st16(t_s + c / 2, w);
+      }
+      tc_st_wait();
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(bar(kPbP + t));
+      const float2 z = f2u(add2(sum[0], sum[1]));
+      l += z.x + z.y;
+    }
+    // ---- this row ----
+    if (n > 0) {
+      wait(bar(kPbPv + t), (uint32_t)((n - 1) & 1));
+      __syncwarp();
+      tc_fence_after();
+    }
+    const float inv = l > 0.f ? 1.0f / l : (l == 0.f ? 0.f : l);
+    const int64_t at = (q0 + row) * p.H + h;
+#pragma unroll 1
+    for (int c = 0; c < 128; c += 32) {
+      float o[32];
+      if (n > 0) {
+        tc_ld32(t_o + c, o);
+      } else {
+#pragma unroll
+        for (int e = 0; e < 32; ++e) o[e] = 0.f;
+      }
+      if (row < lq) {
+        uint4* dst = reinterpret_cast<uint4*>(p.out + at * kVDim + c);
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+          dst[e] = make_uint4(pack_bf16(o[8 * e] * inv, o[8 * e + 1] * inv), pack_bf16(o[8 * e + 2] * inv, o[8 * e + 3] * inv),
+                              pack_bf16(o[8 * e + 4] * inv, o[8 * e + 5] * inv),
+                              pack_bf16(o[8 * e + 6] * inv, o[8 * e + 7] * inv));
+      }
+    }
+    if (p.lse && row < lq) p.lse[at] = l == 0.f ? -INFINITY : (m + __log2f(l)) * 0.6931471805599453f;
+    tc_fence_before();
   }
+  __syncthreads();
+  tc_fence_after();
+  if (warp == 9)
+    asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;\n" ::"r"(tmem), "r"(512u));
 }
 
+namespace {
+
+// [tokens][H][d] with token / head strides: 64 x 1 x `rows` boxes
+bool head_map(CUtensorMap* m, const uint16_t* base, int d, int64_t H, int64_t tokens, int64_t st, int64_t sh, int rows) {
+  const cuuint64_t dims[3] = {(cuuint64_t)d, (cuuint64_t)H, (cuuint64_t)tokens};
+  const cuuint64_t strides[2] = {(cuuint64_t)sh * 2, (cuuint64_t)st * 2};
+  const cuuint32_t box[3] = {64, 1, (cuuint32_t)rows};
+  return encode_map_bf16(m, base, 3, dims, strides, box);
+}
+
+}  // namespace
+
 bool launch_latent_prefill(const PrefillParams& p, cudaStream_t s) {
+  static std::once_flag once[64];
+  static cudaError_t rc[64];
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return false;
+  std::call_once(once[dev], [&] {
+    rc[dev] = cudaFuncSetAttribute(kda_latent_prefill_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kPreSmem);
+  });
+  if (rc[dev] != cudaSuccess) return false;
   const int64_t per = (p.Tq + kPrefillRows - 1) / kPrefillRows;
-  const int64_t blocks = p.cu_q ? p.Tq / kPrefillRows + p.N : p.B * per;
-  kda_latent_prefill_kernel<<<dim3((unsigned)blocks, (unsigned)p.H), 256, 0, s>>>(p, per);
+  const int64_t blocks = (p.cu_q ? p.Tq / kPrefillRows + p.N : p.B * per) * p.H;
+  if (blocks > INT32_MAX) return false;
+  PrefillMaps maps;
+  memset(&maps, 0, sizeof(maps));
+  if (!head_map(&maps.q, p.q, kQkDim, p.H, p.B * p.Tq, p.q_st, p.q_sh, kPreRows)) return false;
+  const int64_t keys = p.B * p.Tk;
+  if (keys > 0) {  // (without keys no key tile exists and nothing is copied)
+    const cuuint64_t dims[2] = {kLatPe, (cuuint64_t)keys};
+    const cuuint64_t strides[1] = {(cuuint64_t)p.pe_st * 2};
+    const cuuint32_t box[2] = {64, kPreKeys};
+    if (!head_map(&maps.k, p.k, kNope, p.H, keys, p.k_st, p.k_sh, kPreKeys) ||
+        !head_map(&maps.v, p.v, kVDim, p.H, keys, p.v_st, p.v_sh, kPreKeys) ||
+        !encode_map_bf16(&maps.pe, p.k_pe, 2, dims, strides, box))
+      return false;
+  }
+  kda_latent_prefill_kernel<<<(unsigned)blocks, kPreThreads, kPreSmem, s>>>(p, per, maps);
   return true;
 }
 
