@@ -78,26 +78,22 @@ def _library():
     return _fns
 
 
+_bf16, _f32, _i32, _i64 = torch.bfloat16, torch.float32, torch.int32, torch.int64
+_empty, _byref = torch.empty, ctypes.byref
+
+
 def _raise(call, rc):
     raise KdaError(rc, _library().kda_error_string(rc).decode(), call)
 
 
-def _need(ok, what):
-    if not ok:
-        raise ValueError(what)
-
+# A serving step makes these calls every few microseconds, so the checks are
+# plain comparisons in line and the messages are put together only on failure.
 
 def _on(t, dtype, ndim, device, name):
     """A CUDA tensor of this type and rank on `device`."""
-    if t.dtype is not dtype or t.dim() != ndim or t.device != device:
+    if t.dtype is not dtype or t.ndim != ndim or t.device != device:
         raise ValueError(f"{name}: a {ndim}-d {dtype} tensor on {device} is needed, "
                          f"got {t.dim()}-d {t.dtype} on {t.device}")
-
-
-def _rows(t, name):
-    """Innermost dimension contiguous."""
-    if t.stride(-1) != 1 and t.numel() > 0:
-        raise ValueError(f"{name}: the last dimension has to be contiguous")
 
 
 def _dense(t, name):
@@ -111,33 +107,41 @@ def _gpu(t, name):
     return t.device
 
 
-class _Call:
-    """The stream of a call, and allocation on it.  The tensor's device has to
-    be the current one, as for every launch of the library."""
+def _last(strides, t, name):
+    if strides[-1] != 1 and t.numel() > 0:
+        raise ValueError(f"{name}: the last dimension has to be contiguous")
 
-    __slots__ = ("stream", "handle", "side")
 
-    def __init__(self, device, stream):
-        current = torch.cuda.current_stream(device)
-        self.side = stream is not None and stream != current
-        self.stream = stream if self.side else current
-        self.handle = self.stream.cuda_stream
+# The handle of the current stream without the Stream object around it, where
+# this PyTorch has the call (2 us less on the host).
+_current = getattr(torch._C, "_cuda_getCurrentRawStream", None)
 
-    def empty(self, shape, dtype, device):
-        if not self.side:
-            return torch.empty(shape, dtype=dtype, device=device)
-        with torch.cuda.stream(self.stream):
-            return torch.empty(shape, dtype=dtype, device=device)
+
+def _handle(device, stream):
+    if stream is not None:
+        return stream.cuda_stream
+    if _current is not None:
+        return _current(device.index)
+    return torch.cuda.current_stream(device).cuda_stream
+
+
+def _new(shape, dtype, device, stream):
+    """Memory allocated on the stream that uses it."""
+    if stream is None:
+        return _empty(shape, dtype=dtype, device=device)
+    with torch.cuda.stream(stream):
+        return _empty(shape, dtype=dtype, device=device)
 
 
 def _cache_block(cache, device):
-    _on(cache, torch.bfloat16, 3, device, "cache")
-    _need(cache.shape[2] == LATENT_ROW, f"cache: rows of {LATENT_ROW} values are needed")
-    _rows(cache, "cache")
-    pages, page, _ = cache.shape
-    token_stride = cache.stride(1)
-    page_stride = cache.stride(0) if pages > 1 else (page - 1) * token_stride + LATENT_ROW + (-LATENT_ROW) % 8
-    return kda_latent_cache(cache.data_ptr(), pages, page, page_stride, token_stride)
+    _on(cache, _bf16, 3, device, "cache")
+    pages, page, row = cache.shape
+    strides = cache.stride()
+    if row != LATENT_ROW:
+        raise ValueError(f"cache: rows of {LATENT_ROW} values are needed")
+    _last(strides, cache, "cache")
+    page_stride = strides[0] if pages > 1 else (page - 1) * strides[1] + LATENT_ROW
+    return kda_latent_cache(cache.data_ptr(), pages, page, page_stride, strides[1])
 
 
 def latent_plan(cached_lens, new_lens, block_table, free_pages, page_size, num_tokens, *, stream=None):
@@ -151,24 +155,26 @@ def latent_plan(cached_lens, new_lens, block_table, free_pages, page_size, num_t
     do not fit, or too few free pages, plan nothing and show in
     :func:`get_status` (18 / 19)."""
     dev = _gpu(cached_lens, "cached_lens")
-    for t, name in ((cached_lens, "cached_lens"), (new_lens, "new_lens"), (free_pages, "free_pages")):
-        _on(t, torch.int32, 1, dev, name)
-        _dense(t, name)
-    _on(block_table, torch.int32, 2, dev, "block_table")
-    _rows(block_table, "block_table")
-    B = cached_lens.shape[0]
-    _need(new_lens.shape[0] == B and block_table.shape[0] == B, "cached_lens, new_lens and block_table: one row a request")
-    c = _Call(dev, stream)
-    T, width = int(num_tokens), block_table.shape[1]
-    lens = c.empty((B,), torch.int32, dev)
-    cu = c.empty((B + 1,), torch.int64, dev)
-    slots = c.empty((max(T, 0),), torch.int64, dev)
-    taken = c.empty((1,), torch.int32, dev)
+    _on(cached_lens, _i32, 1, dev, "cached_lens")
+    _on(new_lens, _i32, 1, dev, "new_lens")
+    _on(free_pages, _i32, 1, dev, "free_pages")
+    _on(block_table, _i32, 2, dev, "block_table")
+    if not (cached_lens.is_contiguous() and new_lens.is_contiguous() and free_pages.is_contiguous()):
+        raise ValueError("cached_lens, new_lens and free_pages: contiguous tensors are needed")
+    B, width = block_table.shape
+    strides = block_table.stride()
+    _last(strides, block_table, "block_table")
+    if cached_lens.shape[0] != B or new_lens.shape[0] != B:
+        raise ValueError("cached_lens, new_lens and block_table: one row a request")
+    T = int(num_tokens)
+    lens = _new(B, _i32, dev, stream)
+    cu = _new(B + 1, _i64, dev, stream)
+    slots = _new(max(T, 0), _i64, dev, stream)
+    taken = _new(1, _i32, dev, stream)
     a = kda_latent_plan_args(cached_lens.data_ptr(), new_lens.data_ptr(), block_table.data_ptr(),
-                             block_table.stride(0) if B > 1 else width, free_pages.data_ptr(), lens.data_ptr(),
-                             cu.data_ptr(), slots.data_ptr(), taken.data_ptr(), B, width, free_pages.shape[0],
-                             int(page_size), T)
-    rc = _library().kda_latent_plan(ctypes.byref(a), c.handle)
+                             strides[0] if B > 1 else width, free_pages.data_ptr(), lens.data_ptr(), cu.data_ptr(),
+                             slots.data_ptr(), taken.data_ptr(), B, width, free_pages.shape[0], int(page_size), T)
+    rc = _library().kda_latent_plan(_byref(a), _handle(dev, stream))
     if rc != 0:
         _raise("kda_latent_plan", rc)
     return {"seq_lens": lens, "cu_seqlens": cu, "slot_map": slots, "pages_taken": taken}
@@ -182,24 +188,26 @@ def latent_append(c, k_pe, slot_map, cache, norm_weight=None, eps=1e-6, *, strea
     576]; norm_weight fp32 [512]: the latents are RMS-normalised with ``eps``
     and scaled on the way."""
     dev = _gpu(cache, "cache")
-    _on(c, torch.bfloat16, 2, dev, "c")
-    _on(k_pe, torch.bfloat16, 2, dev, "k_pe")
-    _on(slot_map, torch.int64, 1, dev, "slot_map")
-    T = c.shape[0]
-    _need(c.shape[1] == LATENT_DIM and k_pe.shape[1] == LATENT_PE_DIM and k_pe.shape[0] == T and slot_map.shape[0] == T,
-          "c [T, 512], k_pe [T, 64] and slot_map [T] are needed")
-    _rows(c, "c")
-    _rows(k_pe, "k_pe")
+    _on(c, _bf16, 2, dev, "c")
+    _on(k_pe, _bf16, 2, dev, "k_pe")
+    _on(slot_map, _i64, 1, dev, "slot_map")
+    T, width = c.shape
+    if width != LATENT_DIM or k_pe.shape != (T, LATENT_PE_DIM) or slot_map.shape[0] != T:
+        raise ValueError("c [T, 512], k_pe [T, 64] and slot_map [T] are needed")
+    c_strides, pe_strides = c.stride(), k_pe.stride()
+    _last(c_strides, c, "c")
+    _last(pe_strides, k_pe, "k_pe")
     _dense(slot_map, "slot_map")
     if norm_weight is not None:
-        _on(norm_weight, torch.float32, 1, dev, "norm_weight")
-        _need(norm_weight.shape[0] == LATENT_DIM, "norm_weight [512] is needed")
+        _on(norm_weight, _f32, 1, dev, "norm_weight")
         _dense(norm_weight, "norm_weight")
-    a = kda_latent_append_args(c.data_ptr(), k_pe.data_ptr(), c.stride(0) if T > 1 else LATENT_DIM,
-                               k_pe.stride(0) if T > 1 else LATENT_PE_DIM, slot_map.data_ptr(),
+        if norm_weight.shape[0] != LATENT_DIM:
+            raise ValueError("norm_weight [512] is needed")
+    a = kda_latent_append_args(c.data_ptr(), k_pe.data_ptr(), c_strides[0] if T > 1 else LATENT_DIM,
+                               pe_strides[0] if T > 1 else LATENT_PE_DIM, slot_map.data_ptr(),
                                _cache_block(cache, dev), None if norm_weight is None else norm_weight.data_ptr(),
-                               float(eps), T)
-    rc = _library().kda_latent_append(ctypes.byref(a), _Call(dev, stream).handle)
+                               eps, T)
+    rc = _library().kda_latent_append(_byref(a), _handle(dev, stream))
     if rc != 0:
         _raise("kda_latent_append", rc)
     return cache
@@ -215,36 +223,40 @@ def latent_decode(q, cache, block_table, seq_lens, scale, out=None, lse=None, *,
     optional fp32 [B, R, H] tensor to be written.  ``workspace``: an optional
     uint8 tensor of at least :func:`latent_decode_workspace_bytes` bytes."""
     dev = _gpu(q, "q")
-    _on(q, torch.bfloat16, 4, dev, "q")
+    _on(q, _bf16, 4, dev, "q")
     B, R, H, D = q.shape
-    _need(D == LATENT_ROW, f"q: heads of {LATENT_ROW} values are needed")
+    if D != LATENT_ROW:
+        raise ValueError(f"q: heads of {LATENT_ROW} values are needed")
     _dense(q, "q")
-    _on(block_table, torch.int32, 2, dev, "block_table")
-    _rows(block_table, "block_table")
-    _on(seq_lens, torch.int32, 1, dev, "seq_lens")
+    _on(block_table, _i32, 2, dev, "block_table")
+    rows, width = block_table.shape
+    strides = block_table.stride()
+    _last(strides, block_table, "block_table")
+    _on(seq_lens, _i32, 1, dev, "seq_lens")
     _dense(seq_lens, "seq_lens")
-    _need(block_table.shape[0] == B and seq_lens.shape[0] == B, "block_table and seq_lens: one row a request")
-    c = _Call(dev, stream)
+    if rows != B or seq_lens.shape[0] != B:
+        raise ValueError("block_table and seq_lens: one row a request")
     if out is None:
-        out = c.empty((B, R, H, LATENT_DIM), torch.bfloat16, dev)
+        out = _new((B, R, H, LATENT_DIM), _bf16, dev, stream)
     else:
-        _on(out, torch.bfloat16, 4, dev, "out")
-        _need(out.shape == (B, R, H, LATENT_DIM), "out [B, R, H, 512] is needed")
+        _on(out, _bf16, 4, dev, "out")
         _dense(out, "out")
+        if out.shape != (B, R, H, LATENT_DIM):
+            raise ValueError("out [B, R, H, 512] is needed")
     if lse is not None:
-        _on(lse, torch.float32, 3, dev, "lse")
-        _need(lse.shape == (B, R, H), "lse [B, R, H] is needed")
+        _on(lse, _f32, 3, dev, "lse")
         _dense(lse, "lse")
-    width = block_table.shape[1]
+        if lse.shape != (B, R, H):
+            raise ValueError("lse [B, R, H] is needed")
     a = kda_latent_decode_args(q.data_ptr(), _cache_block(cache, dev), block_table.data_ptr(),
-                               block_table.stride(0) if B > 1 else width, width, seq_lens.data_ptr(), float(scale),
+                               strides[0] if B > 1 else width, width, seq_lens.data_ptr(), scale,
                                out.data_ptr(), None if lse is None else lse.data_ptr(), B, R, H)
-    lib, ref = _library(), ctypes.byref(a)
-    need = lib.kda_latent_decode_workspace_bytes(ref)
-    if workspace is None and need:
-        workspace = c.empty((need,), torch.uint8, dev)
-    rc = lib.kda_latent_decode(ref, workspace.data_ptr() if workspace is not None else None,
-                               workspace.numel() if workspace is not None else 0, c.handle)
+    lib, ref = _library(), _byref(a)
+    if workspace is None:
+        need = lib.kda_latent_decode_workspace_bytes(ref)
+        workspace = _new(need, torch.uint8, dev, stream) if need else None
+    rc = lib.kda_latent_decode(ref, None if workspace is None else workspace.data_ptr(),
+                               0 if workspace is None else workspace.numel(), _handle(dev, stream))
     if rc != 0:
         _raise("kda_latent_decode", rc)
     return out
@@ -257,17 +269,14 @@ def latent_decode_workspace_bytes(B, R, H, cache, block_table):
     return int(_library().kda_latent_decode_workspace_bytes(ctypes.byref(a)))
 
 
-def _tokens(t, name, heads):
-    """Token and head strides of a [B, T, H, .] (or [B, T, .]) tensor whose batch rows follow one another."""
-    _rows(t, name)
-    B, T = t.shape[0], t.shape[1]
-    st = t.stride(1) if T > 1 else (t.stride(0) if B > 1 else None)
-    if B > 1 and T > 0 and t.stride(0) != T * st:
-        raise ValueError(f"{name}: batch rows have to follow one another")
-    if not heads:
-        return st if st is not None else t.shape[2]
-    sh = t.stride(2) if t.shape[2] > 1 else t.shape[3]
-    return (st if st is not None else max(sh * t.shape[2], t.shape[3])), sh
+def _token_stride(shape, strides, row, name):
+    """Token stride of a [B, T, ...] tensor whose batch rows follow one another; `row` where it has one token."""
+    B, T = shape[0], shape[1]
+    if B > 1:
+        if T > 1 and strides[0] != T * strides[1]:
+            raise ValueError(f"{name}: batch rows have to follow one another")
+        return strides[0] if T == 1 else strides[1]
+    return strides[1] if T > 1 else row
 
 
 def latent_prefill(q, k, k_pe, v, scale, out=None, lse=None, cu_seqlens=None, cu_seqlens_k=None, *, causal=True,
@@ -282,50 +291,60 @@ def latent_prefill(q, k, k_pe, v, scale, out=None, lse=None, cu_seqlens=None, cu
     keys j <= i + Lk - Lq, or all with ``causal=False``.  out bf16 [B, Tq, H,
     128]; lse an optional fp32 [B, Tq, H] tensor to be written."""
     dev = _gpu(q, "q")
-    for t, d, name in ((q, 4, "q"), (k, 4, "k"), (k_pe, 3, "k_pe"), (v, 4, "v")):
-        _on(t, torch.bfloat16, d, dev, name)
-    B, Tq, H, D = q.shape
-    Tk = k.shape[1]
-    _need(D == LATENT_QK_DIM and k.shape == (B, Tk, H, 128) and v.shape == (B, Tk, H, LATENT_V_DIM)
-          and k_pe.shape == (B, Tk, LATENT_PE_DIM),
-          "q [B, Tq, H, 192], k and v [B, Tk, H, 128] and k_pe [B, Tk, 64] are needed")
-    c = _Call(dev, stream)
+    _on(q, _bf16, 4, dev, "q")
+    _on(k, _bf16, 4, dev, "k")
+    _on(k_pe, _bf16, 3, dev, "k_pe")
+    _on(v, _bf16, 4, dev, "v")
+    B, Tq, H, D = shape = q.shape
+    k_shape = k.shape
+    Tk = k_shape[1]
+    if (D != LATENT_QK_DIM or k_shape != (B, Tk, H, 128) or v.shape != k_shape
+            or k_pe.shape != (B, Tk, LATENT_PE_DIM)):
+        raise ValueError("q [B, Tq, H, 192], k and v [B, Tk, H, 128] and k_pe [B, Tk, 64] are needed")
+    qs, ks, ps, vs = q.stride(), k.stride(), k_pe.stride(), v.stride()
+    _last(qs, q, "q")
+    _last(ks, k, "k")
+    _last(ps, k_pe, "k_pe")
+    _last(vs, v, "v")
     if out is None:
-        out = c.empty((B, Tq, H, LATENT_V_DIM), torch.bfloat16, dev)
+        out = _new((B, Tq, H, LATENT_V_DIM), _bf16, dev, stream)
     else:
-        _on(out, torch.bfloat16, 4, dev, "out")
-        _need(out.shape == (B, Tq, H, LATENT_V_DIM), "out [B, Tq, H, 128] is needed")
+        _on(out, _bf16, 4, dev, "out")
         _dense(out, "out")
+        if out.shape != (B, Tq, H, LATENT_V_DIM):
+            raise ValueError("out [B, Tq, H, 128] is needed")
     if lse is not None:
-        _on(lse, torch.float32, 3, dev, "lse")
-        _need(lse.shape == (B, Tq, H), "lse [B, Tq, H] is needed")
+        _on(lse, _f32, 3, dev, "lse")
         _dense(lse, "lse")
-    N = B
+        if lse.shape != (B, Tq, H):
+            raise ValueError("lse [B, Tq, H] is needed")
+    N, cu_q, cu_k = B, None, None
     if cu_seqlens is not None:
         if cu_seqlens_k is None:
             cu_seqlens_k = cu_seqlens
-        for t, name in ((cu_seqlens, "cu_seqlens"), (cu_seqlens_k, "cu_seqlens_k")):
-            _on(t, torch.int64, 1, dev, name)
-            _dense(t, name)
+        _on(cu_seqlens, _i64, 1, dev, "cu_seqlens")
+        _on(cu_seqlens_k, _i64, 1, dev, "cu_seqlens_k")
+        _dense(cu_seqlens, "cu_seqlens")
+        _dense(cu_seqlens_k, "cu_seqlens_k")
         N = cu_seqlens.shape[0] - 1
-        _need(N >= 0 and cu_seqlens_k.shape[0] == N + 1, "cu_seqlens and cu_seqlens_k: [N + 1] each")
-    else:
-        _need(cu_seqlens_k is None, "cu_seqlens_k needs cu_seqlens")
-    q_st, q_sh = _tokens(q, "q", True)
-    k_st, k_sh = _tokens(k, "k", True)
-    v_st, v_sh = _tokens(v, "v", True)
+        if N < 0 or cu_seqlens_k.shape[0] != N + 1:
+            raise ValueError("cu_seqlens and cu_seqlens_k: [N + 1] each")
+        cu_q, cu_k = cu_seqlens.data_ptr(), cu_seqlens_k.data_ptr()
+    elif cu_seqlens_k is not None:
+        raise ValueError("cu_seqlens_k needs cu_seqlens")
+    # (a dimension of one has no stride of its own)
+    qh, kh, vh = (qs[2], ks[2], vs[2]) if H > 1 else (LATENT_QK_DIM, 128, LATENT_V_DIM)
     a = kda_latent_prefill_args(
-        q.data_ptr(), k.data_ptr(), k_pe.data_ptr(), v.data_ptr(), q_st, q_sh, k_st, k_sh,
-        _tokens(k_pe, "k_pe", False), v_st, v_sh, float(scale), out.data_ptr(),
-        None if lse is None else lse.data_ptr(), None if cu_seqlens is None else cu_seqlens.data_ptr(),
-        None if cu_seqlens is None else cu_seqlens_k.data_ptr(), B, Tq, Tk, H, N,
-        KDA_LATENT_CAUSAL if causal else 0)
-    lib, ref = _library(), ctypes.byref(a)
-    need = lib.kda_latent_prefill_workspace_bytes(ref)
-    if workspace is None and need:
-        workspace = c.empty((need,), torch.uint8, dev)
-    rc = lib.kda_latent_prefill(ref, workspace.data_ptr() if workspace is not None else None,
-                                workspace.numel() if workspace is not None else 0, c.handle)
+        q.data_ptr(), k.data_ptr(), k_pe.data_ptr(), v.data_ptr(), _token_stride(shape, qs, H * qh, "q"), qh,
+        _token_stride(k_shape, ks, H * kh, "k"), kh, _token_stride(k_shape, ps, LATENT_PE_DIM, "k_pe"),
+        _token_stride(k_shape, vs, H * vh, "v"), vh, scale, out.data_ptr(), None if lse is None else lse.data_ptr(),
+        cu_q, cu_k, B, Tq, Tk, H, N, KDA_LATENT_CAUSAL if causal else 0)
+    lib, ref = _library(), _byref(a)
+    if workspace is None and cu_q is not None:
+        need = lib.kda_latent_prefill_workspace_bytes(ref)
+        workspace = _new(need, torch.uint8, dev, stream) if need else None
+    rc = lib.kda_latent_prefill(ref, None if workspace is None else workspace.data_ptr(),
+                                0 if workspace is None else workspace.numel(), _handle(dev, stream))
     if rc != 0:
         _raise("kda_latent_prefill", rc)
     return out
