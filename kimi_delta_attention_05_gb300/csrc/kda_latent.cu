@@ -234,7 +234,7 @@ int check_decode(const kda_latent_decode_args* a) {
   if (a->max_pages > INT32_MAX || a->table_stride < a->max_pages) return KDA_ERR_SHAPE;
   const int rc = check_cache(a->cache);
   if (rc != KDA_OK) return rc;
-  if (a->max_pages * a->cache.page_size > INT32_MAX) return KDA_ERR_SHAPE;
+  if (a->max_pages * a->cache.page_size > INT32_MAX - 127) return KDA_ERR_SHAPE;  // tile ends stay in 32 bits
   if (!(a->scale > 0.f) || !std::isfinite(a->scale)) return KDA_ERR_SCALE;
   if (a->B * a->R * a->H > 0 && (!a->q || !a->out || !a->seq_lens || (a->max_pages > 0 && !a->block_table)))
     return KDA_ERR_NULL_ARG;

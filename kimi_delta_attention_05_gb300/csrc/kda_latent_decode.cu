@@ -16,8 +16,8 @@
 // blocks of [64 tokens][128 bytes] with the 128-byte swizzle.  Tensor memory:
 // O^T 4 N columns, S^T twice N.
 //
-// Softmax: four warps read S^T as 16 x 8 fragments (a thread holds two tokens
-// of N / 4 rows), reduce the maximum over tokens with shuffles, and write P^T
+// Softmax: four warps for each half of the query rows read S^T as 16 x 8
+// fragments (a thread holds two tokens of N / 8 rows), reduce the maximum over tokens with shuffles, and write P^T
 // as the next product's operand with transposing matrix stores.  The running
 // maximum of a row moves only when it grows by more than 2^8 (exact: the
 // result is divided by the sum taken with the same maximum), so O^T is rarely
@@ -31,7 +31,7 @@
 // form groups, one a block of rows, that walk the same shares at the same
 // time, so the cache is read from HBM by one of them and from L2 by the others.
 //
-// Roles: warps 0-3 softmax and output, warp 4 copies, warp 5 products.
+// Roles: warps 0-7 softmax and output, warp 8 copies, warp 9 products.
 // Every wait is bounded; a CTA that gives up sets the status word.
 #include <algorithm>
 #include <cstring>
@@ -46,9 +46,14 @@ namespace kda {
 constexpr int kDecTile = 64;                     // cached rows of a tile
 constexpr int kDecChunks = kLatRow / 64;         // 64-column blocks of a row
 constexpr int kDecStages = 2;
+constexpr int kDecGroups = 3;                    // the blocks of a tile arrive three by three
 constexpr int kDecBlk = kDecTile * 128;          // bytes of a 64-column block of a tile
 constexpr int kDecStage = kDecChunks * kDecBlk;  // 73728
-constexpr int kDecThreads = 192;
+constexpr int kDecThreads = 320;
+constexpr int kDecCopyWarp = 8, kDecMmaWarp = 9;
+// A share's cost: 4 a tile and 4 a request (query block, first wait, output),
+// which together are about one tile's time.
+constexpr int kDecTileCost = 4, kDecReqCost = 4;
 constexpr float kDecSlack = 8.0f;                // log2 growth of a maximum that is let pass
 
 struct DecodeMaps {
@@ -62,7 +67,8 @@ struct DecodePlan {
   int min_tiles;       // least tiles of a share
   float* part;         // [row_blocks * shares * 2][N][512] normalised partial rows
   float* part_lse;     // [row_blocks * shares * 2][N] their lse, log2
-  int4* split;         // [row_blocks * shares]: request that starts here and ends in another share, its last share
+  int by_request;      // the join works by request (fewer than shares), else by share
+  int4* split;         // [requests or shares][row_blocks]: (request or -1, first share, last share)
 };
 
 template <int N>
@@ -74,11 +80,11 @@ struct DecCfg {
   static constexpr int kWmax = kP + N * 128;                // fp32 [4][N]: maxima, then sums, of the warps
   static constexpr int kFac = kWmax + 16 * N;               // fp32 [N]
   static constexpr int kBar = kFac + 4 * N;
-  // full[2], empty[2], qfull[2], qempty[2], sfull[2], pready, pvdone
-  static constexpr int kFull = 0, kEmpty = 2, kQFull = 4, kQEmpty = 6, kSFull = 8, kPReady = 10, kPvDone = 11,
-                       kBars = 12;
-  static constexpr int kScan = kBar + 8 * kBars;            // int64 [6] warp sums, [2] first request and its prefix
-  static constexpr int kTmem = kScan + 64;
+  // full[2][3] (stage, group), empty[2], qfull[2], qempty[2], sfull[2], pready, pvdone
+  static constexpr int kFull = 0, kEmpty = 6, kQFull = 8, kQEmpty = 10, kSFull = 12, kPReady = 14, kPvDone = 15,
+                       kBars = 16;
+  static constexpr int kScan = kBar + 8 * kBars;            // int64 [10] sums of the warps, [2] first request and its start
+  static constexpr int kTmem = kScan + 96;
   static constexpr int kAbort = kTmem + 8;
   static constexpr int kSmem = kAbort + 8;
   static constexpr uint32_t kCols = N == 16 ? 128 : N == 32 ? 256 : 512;  // 6 N rounded up
@@ -87,38 +93,48 @@ struct DecCfg {
 };
 
 // A request's length, clamped to what its table can hold.
-__device__ __forceinline__ int64_t dec_len(const DecodeParams& p, int b) {
+__device__ __forceinline__ int dec_len(const DecodeParams& p, int b) {
   const int64_t len = p.lens[b], cap = p.max_pages * p.page_size;
-  return len < 0 ? 0 : (len > cap ? cap : len);
+  return (int)(len < 0 ? 0 : (len > cap ? cap : len));
 }
-__device__ __forceinline__ int64_t dec_tiles(int64_t len) { return len > 0 ? (len + kDecTile - 1) / kDecTile : 1; }
+__device__ __forceinline__ int dec_tiles(int len) { return len > 0 ? (len - 1) / kDecTile + 1 : 0; }
+__device__ __forceinline__ int64_t dec_cost(int tiles) { return (int64_t)tiles * kDecTileCost + kDecReqCost; }
 
-// The pieces of one share, in order.
+// The pieces of one share [u0, u1) of the line of costs, in order.  Request b
+// takes [pre, pre + cost) of it; its tile k starts at pre + kDecReqCost + k
+// kDecTileCost and belongs to the share that holds that point; a request
+// without tiles belongs to the share that holds pre.
 struct DecPieces {
-  int64_t u, u1, pre;  // next tile, end of the share, first tile of request b
+  int64_t u0, u1, pre;  // the share; start of request b
   int b;
-  // the current piece
-  int req;
-  int64_t len, t0, t1, tiles;
-  __device__ __forceinline__ bool next(const DecodeParams& p) {
-    if (u >= u1) return false;
-    req = b;
-    len = dec_len(p, b);
-    tiles = dec_tiles(len);
-    t0 = u - pre;
-    t1 = min(tiles, u1 - pre);
-    u = pre + t1;
-    pre += tiles;
-    ++b;
-    return true;
+  // the current piece: request, its length, tiles [t0, t1) of its `tiles`
+  int req, len, t0, t1, tiles;
+  __device__ __forceinline__ int tiles_before(int64_t u) const {
+    const int64_t d = u - pre - kDecReqCost;
+    return d <= 0 ? 0 : (int)min((int64_t)tiles, (d + kDecTileCost - 1) / kDecTileCost);
   }
-  __device__ __forceinline__ int64_t count() const { return len > 0 ? t1 - t0 : 0; }
+  __device__ __forceinline__ bool next(const DecodeParams& p) {
+    while (b < p.B && pre < u1) {
+      req = b;
+      len = dec_len(p, b);
+      tiles = dec_tiles(len);
+      t0 = tiles_before(u0);
+      t1 = tiles_before(u1);
+      const bool mine = tiles > 0 ? t0 < t1 : pre >= u0;
+      pre += dec_cost(tiles);
+      ++b;
+      if (mine) return true;
+    }
+    return false;
+  }
+  __device__ __forceinline__ int count() const { return t1 - t0; }
+  __device__ __forceinline__ bool whole() const { return t1 - t0 == tiles; }
 };
 
 // A walk over the tiles of a share.
 struct DecCursor {
   DecPieces it;
-  int64_t tile;
+  int tile;
   int piece;  // index of the piece among those with tiles
   bool ok;
   __device__ __forceinline__ void start(const DecPieces& s, const DecodeParams& p) {
@@ -157,18 +173,18 @@ __global__ void __launch_bounds__(kDecThreads, 1)
 
   // ---- set-up: barriers, tensor memory, this CTA's share of the tiles ----
   if (tid == 0) {
-    for (int i = 0; i < C::kBars; ++i) mbar_init(bar(i), i == C::kPReady ? 4 : 1);
+    for (int i = 0; i < C::kBars; ++i) mbar_init(bar(i), i == C::kPReady ? 8 : 1);
     *s_abort = (sb & 1023) ? 1 : 0;
-    s_scan[6] = 0;
-    s_scan[7] = 0;
+    s_scan[10] = 0;
+    s_scan[11] = 0;
     asm volatile("fence.mbarrier_init.release.cluster;\n" ::: "memory");
   }
-  if (warp == 5) {
+  if (warp == kDecMmaWarp) {
     asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;\n" ::"r"(sb + C::kTmem),
                  "r"(C::kCols));
     asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;\n");
   }
-  if (warp == 4 && lane == 0) {
+  if (warp == kDecCopyWarp && lane == 0) {
     prefetch_map(&maps.q);
     prefetch_map(&maps.cache);
   }
@@ -179,10 +195,9 @@ __global__ void __launch_bounds__(kDecThreads, 1)
   int64_t mine = 0;
   bool odd = false;
   for (int b = b0; b < b1; ++b) {
-    const int64_t raw = p.lens[b];
-    const int64_t len = dec_len(p, b);
+    const int raw = p.lens[b], len = dec_len(p, b);
     odd |= raw != len;
-    mine += dec_tiles(len);
+    mine += dec_cost(dec_tiles(len));
   }
   if (odd && blockIdx.x == 0) atomicExch(p.status, KDA_ERR_BAD_LENGTHS);
   int64_t incl = mine;
@@ -201,16 +216,16 @@ __global__ void __launch_bounds__(kDecThreads, 1)
     if (w < warp) before += s_scan[w];
     total += s_scan[w];
   }
-  const int64_t size = max((int64_t)pl.min_tiles, (total + pl.shares - 1) / pl.shares);
+  const int64_t size = max((int64_t)pl.min_tiles * kDecTileCost, (total + pl.shares - 1) / pl.shares);
   const int64_t u0 = min(total, share * size), u1 = min(total, u0 + size);
   before += incl - mine;
   if (u0 < u1 && u0 >= before && u0 < before + mine) {
     int64_t pre = before;
     for (int b = b0; b < b1; ++b) {
-      const int64_t t = dec_tiles(dec_len(p, b));
+      const int64_t t = dec_cost(dec_tiles(dec_len(p, b)));
       if (u0 < pre + t) {
-        s_scan[6] = b;
-        s_scan[7] = pre;
+        s_scan[10] = b;
+        s_scan[11] = pre;
         break;
       }
       pre += t;
@@ -218,86 +233,86 @@ __global__ void __launch_bounds__(kDecThreads, 1)
   }
   __syncthreads();
   DecPieces pieces;
-  pieces.u = u0;
+  pieces.u0 = u0;
   pieces.u1 = u1;
-  pieces.b = (int)s_scan[6];
-  pieces.pre = s_scan[7];
+  pieces.b = u0 < u1 ? (int)s_scan[10] : p.B;
+  pieces.pre = s_scan[11];
   const uint32_t tmem = *reinterpret_cast<volatile uint32_t*>(smem + C::kTmem);
   if (*s_abort && tid == 0) atomicExch(p.status, KDA_ERR_DEVICE_TIMEOUT);
   asm volatile("griddepcontrol.launch_dependents;\n" ::: "memory");
 
   auto wait = [&](uint32_t b, uint32_t parity) {
-    if (*s_abort) return;
+    if (mbar_try_wait(b, parity) || *s_abort) return;
     if (!mbar_wait_bounded(b, parity)) {
       atomicExch(p.status, KDA_ERR_DEVICE_TIMEOUT);
       *s_abort = 1;
     }
   };
 
-  if (warp == 4) {
+  if (warp == kDecCopyWarp) {
     // ---- copies: the tiles of the share into the stages, the query rows of each piece ----
     const int box = pl.box_rows;
     DecCursor c;
     c.start(pieces, p);
-    int64_t it = 0;
-    int qi = 0;  // query blocks issued
-    while (c.ok) {
-      const int s = (int)(it & 1);
-      const int64_t j0 = c.tile * kDecTile;
-      const int valid = (int)min((int64_t)kDecTile, c.it.len - j0);
+    int it = 0, qi = 0;  // tiles and query blocks issued
+    bool gone = false;
+    while (c.ok && !gone) {
+      const int s = it & 1;
+      const int valid = min(kDecTile, c.it.len - c.tile * kDecTile);
       const int segs = (valid + box - 1) / box;
       // page of this lane's run of box rows (lanes below segs), fetched before the wait
       int page = 0, off = 0;
       if (lane < segs) {
-        const int64_t j = j0 + (int64_t)lane * box;
-        page = p.table[c.it.req * p.table_stride + j / p.page_size];
-        off = (int)(j % p.page_size);
+        const uint32_t j = (uint32_t)(c.tile * kDecTile + lane * box), in_table = j / (uint32_t)p.page_size;
+        page = p.table[c.it.req * p.table_stride + in_table];
+        off = (int)(j - in_table * (uint32_t)p.page_size);
         if (page < 0 || page >= p.num_pages) {
           atomicExch(p.status, KDA_ERR_BAD_PAGE);
           page = (int)p.num_pages;  // past the map: reads as zeros
         }
       }
+      const uint32_t dst = sb + s * kDecStage, full = bar(C::kFull + kDecGroups * s);
       if (it >= kDecStages) wait(bar(C::kEmpty + s), (uint32_t)(((it >> 1) & 1) ^ 1));
       __syncwarp();
-      if (*s_abort) break;
-      const uint32_t full = bar(C::kFull + s), dst = sb + s * kDecStage;
-      if (lane == 0) mbar_expect_tx(full, (uint32_t)(segs * box * 128 * kDecChunks));
-      __syncwarp();
-      if (box == kDecTile) {
-        if (lane == 0) tma_load_4d(dst, &maps.cache, 0, off, 0, page, full);
-      } else {
+      gone = __any_sync(0xffffffffu, *s_abort != 0);
+      if (gone) break;
+      if (lane < kDecGroups) mbar_expect_tx(full + 8 * lane, (uint32_t)(segs * box * 128 * 3));
+      if (box == kDecTile) {  // lane = group
+        const int pg = __shfl_sync(0xffffffffu, page, 0), of = __shfl_sync(0xffffffffu, off, 0);
+        if (lane < kDecGroups)
+          tma_load_4d(dst + 3 * lane * kDecBlk, &maps.cache, 0, of, 3 * lane, pg, full + 8 * lane);
+      } else {                // lane = (run, block)
+        __syncwarp();
         for (int i0 = 0; i0 < segs * kDecChunks; i0 += 32) {
-          const int i = i0 + lane, seg = i / kDecChunks, ch = i - seg * kDecChunks;
-          const int pg = __shfl_sync(0xffffffffu, page, seg & 31), of = __shfl_sync(0xffffffffu, off, seg & 31);
-          if (i < segs * kDecChunks)
-            tma_load_4d(dst + ch * kDecBlk + seg * box * 128, &maps.cache, 0, of, ch, pg, full);
+          const int i = i0 + lane, ch = i / segs, seg = i - ch * segs;
+          const int pg = __shfl_sync(0xffffffffu, page, seg), of = __shfl_sync(0xffffffffu, off, seg);
+          if (ch < kDecChunks)
+            tma_load_4d(dst + ch * kDecBlk + seg * box * 128, &maps.cache, 0, of, ch, pg, full + 8 * (ch / 3));
         }
       }
       if (c.first()) {
         const int qb = qi % C::kQBufs;
         if (qi >= C::kQBufs) wait(bar(C::kQEmpty + qb), (uint32_t)(((qi / C::kQBufs) & 1) ^ 1));
         __syncwarp();
-        if (*s_abort) {
-          ++it;
-          break;
-        }
-        if (lane == 0) {
+        gone = __any_sync(0xffffffffu, *s_abort != 0);
+        if (!gone && lane == 0) {
           mbar_expect_tx(bar(C::kQFull + qb), C::kQBytes);
           tma_load_4d(sb + C::kQ + qb * C::kQBytes, &maps.q, 0, row0, 0, c.it.req, bar(C::kQFull + qb));
         }
-        ++qi;
+        if (!gone) ++qi;
       }
-      ++it;
+      ++it;  // (also where the query block was given up: the tile's copies are in flight)
       c.advance(p);
     }
     // After a timeout: let the copies still in flight land before leaving.
-    if (*s_abort && lane == 0) {
-      for (int64_t t = it > kDecStages ? it - kDecStages : 0; t < it; ++t)
-        mbar_wait_bounded(bar(C::kFull + (int)(t & 1)), (uint32_t)((t >> 1) & 1));
-      for (int t = qi > C::kQBufs ? qi - C::kQBufs : 0; t < qi; ++t)
+    if (gone && lane == 0) {
+      for (int t = max(0, it - kDecStages); t < it; ++t)
+        for (int g = 0; g < kDecGroups; ++g)
+          mbar_wait_bounded(bar(C::kFull + kDecGroups * (t & 1) + g), (uint32_t)((t >> 1) & 1));
+      for (int t = max(0, qi - C::kQBufs); t < qi; ++t)
         mbar_wait_bounded(bar(C::kQFull + t % C::kQBufs), (uint32_t)((t / C::kQBufs) & 1));
     }
-  } else if (warp == 5) {
+  } else if (warp == kDecMmaWarp) {
     // ---- products ----
     const uint32_t id_s = idesc_bf16(64, N, false, false), id_o = idesc_bf16(128, N, true, false);
     const uint64_t d_x = smem_desc(sb, 16, 1024), d_c = smem_desc(sb, kDecBlk, 1024);
@@ -306,38 +321,46 @@ __global__ void __launch_bounds__(kDecThreads, 1)
     DecCursor cs, co;
     cs.start(pieces, p);
     co = cs;
-    int64_t is = 0, io = 0;
-    auto scores_ready = [&]() {
-      bool r = mbar_test(bar(C::kFull + (int)(is & 1)), (uint32_t)((is >> 1) & 1));
-      if (cs.first()) r = r && mbar_test(bar(C::kQFull + cs.piece % C::kQBufs), (uint32_t)((cs.piece / C::kQBufs) & 1));
-      return __all_sync(0xffffffffu, r);
-    };
-    auto scores = [&]() {  // S^T of tile `is` into its half of the score columns
-      const int s = (int)(is & 1), qb = cs.piece % C::kQBufs;
-      if (cs.first()) wait(bar(C::kQFull + qb), (uint32_t)((cs.piece / C::kQBufs) & 1));
-      wait(bar(C::kFull + s), (uint32_t)((is >> 1) & 1));
-      __syncwarp();
-      tc_fence_after();
-      const uint64_t a = d_x + (uint64_t)((s * kDecStage) >> 4), b = d_q + (uint64_t)((qb * C::kQBytes) >> 4);
+    int is = 0, io = 0;  // tiles of the scores and of the values
+    // One place each for the two products (a second copy of the unrolled issue
+    // loops costs microseconds of instruction fetches on a cold start), written
+    // out in full (with a block index of run time the operands leave the uniform
+    // registers and an issue costs 120 cycles instead of 35).  The next tile's
+    // scores go first if it has landed, so that the softmax of one tile overlaps
+    // the products of the other; else they follow this tile's values.  Barriers
+    // are read as seldom as possible: while the tensor core streams its operands
+    // a shared-memory access takes some 250 cycles.
+    for (;;) {
+      bool go = cs.ok && is == io;
+      if (cs.ok && is == io + 1)
+        go = __all_sync(0xffffffffu, mbar_test(bar(C::kFull + kDecGroups * (is & 1) + 2), (uint32_t)((is >> 1) & 1)));
+      if (go) {  // S^T of tile `is` into its half of the score columns
+        const int s = is & 1, qb = cs.piece % C::kQBufs;
+        const uint64_t a = d_x + (uint64_t)((s * kDecStage) >> 4), b = d_q + (uint64_t)((qb * C::kQBytes) >> 4);
+        if (cs.first()) wait(bar(C::kQFull + qb), (uint32_t)((cs.piece / C::kQBufs) & 1));
 #pragma unroll
-      for (int ch = 0; ch < kDecChunks; ++ch)
+        for (int ch = 0; ch < kDecChunks; ++ch) {
+          if (ch % 3 == 0) {
+            wait(bar(C::kFull + kDecGroups * s + ch / 3), (uint32_t)((is >> 1) & 1));
+            __syncwarp();
+            tc_fence_after();
+          }
 #pragma unroll
-        for (int ks = 0; ks < 4; ++ks)
-          tc_mma(t_s + N * s, a + (uint64_t)((ch * kDecBlk + ks * 32) >> 4), b + (uint64_t)((ch * N * 128 + ks * 32) >> 4),
-                 id_s, ch + ks > 0);
-      tc_commit(bar(C::kSFull + s));
-      if (cs.last()) tc_commit(bar(C::kQEmpty + qb));
-      ++is;
-      cs.advance(p);
-    };
-    if (cs.ok) scores();
-    while (co.ok) {
-      const int s = (int)(io & 1);
-      // the next tile's scores first if it has landed, so that the softmax of one
-      // tile overlaps the products of the other; else do not wait for it here
-      if (is == io + 1 && cs.ok && scores_ready()) scores();
+          for (int ks = 0; ks < 4; ++ks)
+            tc_mma(t_s + N * s, a + (uint64_t)((ch * kDecBlk + ks * 32) >> 4), b + (uint64_t)((ch * N * 128 + ks * 32) >> 4),
+                   id_s, ch + ks > 0);
+        }
+        tc_commit(bar(C::kSFull + s));
+        if (cs.last()) tc_commit(bar(C::kQEmpty + qb));
+        ++is;
+        cs.advance(p);
+        continue;
+      }
+      if (!co.ok) break;
+      // O^T += C^T P^T of tile `io`
+      const int s = io & 1;
       wait(bar(C::kPReady), (uint32_t)(io & 1));
-      const int valid = (int)min((int64_t)kDecTile, co.it.len - co.tile * kDecTile);
+      const int valid = min(kDecTile, co.it.len - co.tile * kDecTile);
       if (valid < kDecTile) {
         // what lies behind the length takes part in the product with weight 0: it has to be finite
         const int n16 = (kDecTile - valid) * 8;
@@ -358,36 +381,38 @@ __global__ void __launch_bounds__(kDecThreads, 1)
                  id_o, ks > 0 ? 1u : start);
       tc_commit(bar(C::kEmpty + s));
       tc_commit(bar(C::kPvDone));
-      if (is == io + 1 && cs.ok) scores();
       ++io;
       co.advance(p);
     }
     if (io > 0) mbar_wait_bounded(bar(C::kPvDone), (uint32_t)((io - 1) & 1));  // before tensor memory is freed
   } else {
-    // ---- softmax and output: warp w holds tokens 16 w .. 16 w + 15 of a tile, then
-    //      value dimensions 32 w .. of each 128 ----
-    constexpr int kV = N / 2;  // scores of a thread: 8-column group g, v[4 g + 2 r + e] = row 8 g + 2 (lane % 4) + e
-    constexpr int kM = N / 4;  //   of token lane / 4 + 8 r; maxima and sums m[2 g + e]
-    float* wmax = reinterpret_cast<float*>(smem + C::kWmax);
-    float* fac = reinterpret_cast<float*>(smem + C::kFac);
-    const uint32_t lane_base = (uint32_t)(warp * 32) << 16;
-    const int tok = 16 * warp + (lane >> 2);
+    // ---- softmax and output: warps 0-3 the first half of the query rows, 4-7 the
+    //      second; warp w of the four holds tokens 16 w .. 16 w + 15 of a tile, then value
+    //      dimensions 32 w .. of each 128 ----
+    constexpr int kH = N / 2;   // query rows of this half
+    constexpr int kV = kH / 2;  // scores of a thread: 8-column group g, v[4 g + 2 r + e] = row 8 g + 2 (lane % 4) + e
+    constexpr int kM = kH / 4;  //   of token lane / 4 + 8 r; maxima and sums m[2 g + e]
+    const int half = warp >> 2, w4 = warp & 3, h0 = half * kH, bar_id = 1 + half;
+    float* wmax = reinterpret_cast<float*>(smem + C::kWmax) + h0;
+    float* fac = reinterpret_cast<float*>(smem + C::kFac) + h0;
+    const uint32_t lane_base = ((uint32_t)(w4 * 32) << 16) + h0;
+    const int tok = 16 * w4 + (lane >> 2);
     const int c0 = 2 * (lane & 3);
     // this lane's address for the transposing stores: matrix lane / 8, row lane % 8
-    const int st_head = 8 * (lane >> 4) + (lane & 7), st_chunk = 2 * warp + ((lane >> 3) & 1);
+    const int st_head = h0 + 8 * (lane >> 4) + (lane & 7), st_chunk = 2 * w4 + ((lane >> 3) & 1);
     const uint32_t st_addr = sb + C::kP + st_head * 128 + ((st_chunk ^ (lane & 7)) << 4);
-    int64_t it = 0;
+    int it = 0;
     while (pieces.next(p)) {
-      const int64_t nt = pieces.count();
-      const bool whole = pieces.t0 == 0 && pieces.t1 == pieces.tiles;
+      const int nt = pieces.count();
+      const bool whole = pieces.whole();
       float m[kM], l[kM];
 #pragma unroll
       for (int i = 0; i < kM; ++i) {
         m[i] = -INFINITY;
         l[i] = 0.f;
       }
-      for (int64_t tile = pieces.t0; tile < pieces.t0 + nt; ++tile, ++it) {
-        const int s = (int)(it & 1);
+      for (int tile = pieces.t0; tile < pieces.t0 + nt; ++tile, ++it) {
+        const int s = it & 1;
         wait(bar(C::kSFull + s), (uint32_t)((it >> 1) & 1));
         __syncwarp();
         tc_fence_after();
@@ -395,13 +420,13 @@ __global__ void __launch_bounds__(kDecThreads, 1)
         tc_ld16x256(tmem + lane_base + 4 * N + N * s, v);
 #pragma unroll
         for (int i = 0; i < kV; ++i) v[i] *= p.scale_log2;
-        const int64_t j = tile * kDecTile + tok;
+        const int j = tile * kDecTile + tok;
         if ((tile + 1) * kDecTile > pieces.len - (p.R - 1)) {
           // the last tiles: row (token i, head) sees j < len - (R - 1 - i)
 #pragma unroll
           for (int i = 0; i < kM; ++i) {
-            const int row = row0 + 8 * (i >> 1) + c0 + (i & 1);
-            const int64_t seen = pieces.len - max(0, p.R - 1 - row / p.H);
+            const int row = row0 + h0 + 8 * (i >> 1) + c0 + (i & 1);
+            const int seen = pieces.len - max(0, p.R - 1 - row / p.H);
             if (j >= seen) v[4 * (i >> 1) + (i & 1)] = -INFINITY;
             if (j + 8 >= seen) v[4 * (i >> 1) + 2 + (i & 1)] = -INFINITY;
           }
@@ -418,12 +443,12 @@ __global__ void __launch_bounds__(kDecThreads, 1)
           grow |= x > m[i] + kDecSlack;
         }
         const bool first = tile == pieces.t0;
-        if (named_bar_or(1, 128, grow)) {
+        if (named_bar_or(bar_id, 128, grow)) {
           if (lane < 4) {
 #pragma unroll
-            for (int i = 0; i < kM; ++i) wmax[warp * N + 8 * (i >> 1) + c0 + (i & 1)] = mx[i];
+            for (int i = 0; i < kM; ++i) wmax[w4 * N + 8 * (i >> 1) + c0 + (i & 1)] = mx[i];
           }
-          named_bar(1, 128);
+          named_bar(bar_id, 128);
           float f[kM];
 #pragma unroll
           for (int i = 0; i < kM; ++i) {
@@ -437,20 +462,24 @@ __global__ void __launch_bounds__(kDecThreads, 1)
             }
           }
           if (!first) {  // O^T of the tiles so far to the new maxima
-            if (warp == 0 && lane < 4) {
+            if (w4 == 0 && lane < 4) {
 #pragma unroll
               for (int i = 0; i < kM; ++i) fac[8 * (i >> 1) + c0 + (i & 1)] = f[i];
             }
             wait(bar(C::kPvDone), (uint32_t)((it - 1) & 1));
-            named_bar(1, 128);
+            named_bar(bar_id, 128);
             tc_fence_after();
 #pragma unroll 1
-            for (int cc = 0; cc < 4 * N; cc += 16) {
-              float o[16];
-              tc_ld16(tmem + lane_base + cc, o);
+            for (int mt = 0; mt < 4; ++mt) {
 #pragma unroll
-              for (int i = 0; i < 16; ++i) o[i] *= fac[(cc % N) + i];
-              tc_st16(tmem + lane_base + cc, o);
+              for (int r = 0; r < kH; r += 8) {
+                float o[8];
+                tc_ld8_nowait(tmem + lane_base + mt * N + r, o);
+                tc_ld_wait();
+#pragma unroll
+                for (int i = 0; i < 8; ++i) o[i] *= fac[r + i];
+                tc_st8(tmem + lane_base + mt * N + r, o);
+              }
             }
             tc_st_wait();
           }
@@ -466,28 +495,32 @@ __global__ void __launch_bounds__(kDecThreads, 1)
         }
         if (it > 0) wait(bar(C::kPvDone), (uint32_t)((it - 1) & 1));  // P^T of the tile before is read
         __syncwarp();
-        // weights rounded to bf16, the operands' type: 2^-9 of each on average, and the sum is taken before it
+        // weights rounded to bf16, the operands' type; the sums are taken before it
+        if constexpr (kH == 8) {
+          stsm_x2_t(st_addr, pack_bf16(v[0], v[1]), pack_bf16(v[2], v[3]));
+        } else {
 #pragma unroll
-        for (int g = 0; g < N / 8; g += 2)
-          stsm_x4_t(st_addr + g * 1024, pack_bf16(v[4 * g], v[4 * g + 1]), pack_bf16(v[4 * g + 2], v[4 * g + 3]),
-                    pack_bf16(v[4 * g + 4], v[4 * g + 5]), pack_bf16(v[4 * g + 6], v[4 * g + 7]));
+          for (int g = 0; g < kH / 8; g += 2)
+            stsm_x4_t(st_addr + g * 1024, pack_bf16(v[4 * g], v[4 * g + 1]), pack_bf16(v[4 * g + 2], v[4 * g + 3]),
+                      pack_bf16(v[4 * g + 4], v[4 * g + 5]), pack_bf16(v[4 * g + 6], v[4 * g + 7]));
+        }
         fence_proxy_async_smem();
         tc_fence_before();
         __syncwarp();
         if (lane == 0) mbar_arrive(bar(C::kPReady));
       }
       // ---- the piece's rows ----
-      named_bar(1, 128);  // wmax and fac of the last tile are read
+      named_bar(bar_id, 128);  // wmax and fac of the last tile are read
 #pragma unroll
       for (int i = 0; i < kM; ++i) {
         l[i] += __shfl_xor_sync(0xffffffffu, l[i], 4);
         l[i] += __shfl_xor_sync(0xffffffffu, l[i], 8);
         l[i] += __shfl_xor_sync(0xffffffffu, l[i], 16);
-        if (lane < 4) wmax[warp * N + 8 * (i >> 1) + c0 + (i & 1)] = l[i];
+        if (lane < 4) wmax[w4 * N + 8 * (i >> 1) + c0 + (i & 1)] = l[i];
       }
-      named_bar(1, 128);
+      named_bar(bar_id, 128);
       const int slot = 2 * blockIdx.x + (pieces.t0 > 0 ? 0 : 1);
-      if (warp == 0 && lane < 4) {
+      if (w4 == 0 && lane < 4) {
 #pragma unroll
         for (int i = 0; i < kM; ++i) {
           const int c = 8 * (i >> 1) + c0 + (i & 1);
@@ -495,9 +528,9 @@ __global__ void __launch_bounds__(kDecThreads, 1)
           fac[c] = sum > 0.f ? 1.0f / sum : (sum == 0.f ? 0.f : sum);
           const float lse2 = sum == 0.f ? -INFINITY : m[i] + __log2f(sum);
           if (!whole) {
-            pl.part_lse[(int64_t)slot * N + c] = lse2;
-          } else if (p.lse && row0 + c < rows) {
-            p.lse[(int64_t)pieces.req * rows + row0 + c] = lse2 * 0.6931471805599453f;
+            pl.part_lse[(int64_t)slot * N + h0 + c] = lse2;
+          } else if (p.lse && row0 + h0 + c < rows) {
+            p.lse[(int64_t)pieces.req * rows + row0 + h0 + c] = lse2 * 0.6931471805599453f;
           }
         }
       }
@@ -505,111 +538,152 @@ __global__ void __launch_bounds__(kDecThreads, 1)
         wait(bar(C::kPvDone), (uint32_t)((it - 1) & 1));
         __syncwarp();
       }
-      named_bar(1, 128);
+      named_bar(bar_id, 128);
       tc_fence_after();
 #pragma unroll 1
-      for (int cc = 0; cc < 4 * N; cc += 16) {
-        const int dim = (cc / N) * 128 + warp * 32;  // this warp's 32 dimensions of the block of 128
-        const int r0 = cc % N;
-        float o[16];
+      for (int mt = 0; mt < 4; ++mt) {
+        const int dim = mt * 128 + w4 * 32;  // this warp's 32 dimensions of the block of 128
+        float o[kH];
         if (nt > 0) {
-          tc_ld16(tmem + lane_base + cc, o);
+#pragma unroll
+          for (int r = 0; r < kH; r += 8) tc_ld8_nowait(tmem + lane_base + mt * N + r, o + r);
+          tc_ld_wait();
         } else {
 #pragma unroll
-          for (int i = 0; i < 16; ++i) o[i] = 0.f;
+          for (int r = 0; r < kH; ++r) o[r] = 0.f;
         }
 #pragma unroll
-        for (int i = 0; i < 16; ++i) o[i] = fac[r0 + i] == 0.f ? 0.f : o[i] * fac[r0 + i];
+        for (int r = 0; r < kH; r += 4) {
+          const float4 f = *reinterpret_cast<const float4*>(fac + r);
+          o[r] = f.x == 0.f ? 0.f : o[r] * f.x;
+          o[r + 1] = f.y == 0.f ? 0.f : o[r + 1] * f.y;
+          o[r + 2] = f.z == 0.f ? 0.f : o[r + 2] * f.z;
+          o[r + 3] = f.w == 0.f ? 0.f : o[r + 3] * f.w;
+        }
+        const int left = rows - row0 - h0;  // query rows there are from this half's first
         if (!whole) {
-          float* dst = pl.part + ((int64_t)slot * N + r0) * kLat + dim + lane;
+          float* dst = pl.part + ((int64_t)slot * N + h0) * kLat + dim + lane;
 #pragma unroll
-          for (int i = 0; i < 16; ++i) dst[i * kLat] = o[i];
+          for (int r = 0; r < kH; ++r)
+            if (r < left) dst[r * kLat] = o[r];
         } else {
           // two rows at a time: even lanes store two dimensions of the first, odd lanes of the second
+          uint16_t* dst = p.out + ((int64_t)pieces.req * rows + row0 + h0) * kLat + dim + (lane & ~1);
 #pragma unroll
-          for (int i = 0; i < 16; i += 2) {
-            const float other = __shfl_xor_sync(0xffffffffu, (lane & 1) ? o[i] : o[i + 1], 1);
-            const uint32_t w = (lane & 1) ? pack_bf16(other, o[i + 1]) : pack_bf16(o[i], other);
-            const int row = row0 + r0 + i + (lane & 1);
-            if (row < rows)
-              *reinterpret_cast<uint32_t*>(p.out + ((int64_t)pieces.req * rows + row) * kLat + dim + (lane & ~1)) = w;
+          for (int r = 0; r < kH; r += 2) {
+            const float other = __shfl_xor_sync(0xffffffffu, (lane & 1) ? o[r] : o[r + 1], 1);
+            const uint32_t w = (lane & 1) ? pack_bf16(other, o[r + 1]) : pack_bf16(o[r], other);
+            const int at = r + (lane & 1);
+            if (at < left) *reinterpret_cast<uint32_t*>(dst + at * kLat) = w;
           }
         }
       }
-      named_bar(1, 128);  // fac is read
+      named_bar(bar_id, 128);  // fac is read
     }
     tc_fence_before();
   }
   if (tid == 0) {
-    // the request that starts in this share and ends in a later one
-    int4 info = make_int4(-1, 0, 0, 0);
-    if (u0 < u1) {
-      DecPieces last = pieces;
-      last.u = u0;
-      last.u1 = u1;
-      last.b = (int)s_scan[6];
-      last.pre = s_scan[7];
-      while (last.next(p)) {
-      }
-      if (last.t0 == 0 && last.t1 < last.tiles) {
-        info.x = last.req;
-        info.y = (int)((last.pre - 1) / size);  // share of the request's last tile
-      }
+    // what the join kernel has to do, by request or by the share a request starts in
+    if (!pl.by_request) pl.split[blockIdx.x] = make_int4(-1, 0, 0, 0);
+    DecPieces each = pieces;
+    each.b = u0 < u1 ? (int)s_scan[10] : p.B;
+    each.pre = s_scan[11];
+    while (each.next(p)) {
+      if (each.t0 > 0) continue;
+      // (the request's last tile starts kDecTileCost before the next request)
+      const int4 info = each.whole() ? make_int4(-1, 0, 0, 0)
+                                     : make_int4(each.req, share, (int)((each.pre - kDecTileCost) / size), 0);
+      if (pl.by_request) pl.split[each.req * pl.row_blocks + rblk] = info;
+      else if (!each.whole()) pl.split[blockIdx.x] = info;
     }
-    pl.split[blockIdx.x] = info;
   }
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  if (warp == 5)
+  if (warp == kDecMmaWarp)
     asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;\n" ::"r"(tmem), "r"(C::kCols));
 }
 
 // Joins the parts of a request that several shares hold: out = sum_k w_k o_k,
-// w_k = 2^(lse_k - lse), in the shares' order.  A CTA a row of one split
-// request: 128 threads x 4 dimensions, four quarters of the parts side by side.
+// w_k = 2^(lse_k - lse), in the shares' order.  kWide: a CTA a row, four groups
+// of 128 threads (4 dimensions each) over quarters of the parts, for few
+// requests in many parts; else a warp a row (16 dimensions a lane).
+template <bool kWide>
 __global__ void __launch_bounds__(512) kda_latent_join_kernel(const DecodeParams p, const DecodePlan pl, int n) {
-  __shared__ float part[4][kLat];
-  __shared__ float wts[4];
   asm volatile("griddepcontrol.wait;\n" ::: "memory");
   const int4 info = pl.split[blockIdx.x];
   if (info.x < 0) return;
-  const int rblk = blockIdx.x % pl.row_blocks, first = blockIdx.x / pl.row_blocks;
-  const int rows = p.R * p.H, row = rblk * n + blockIdx.y;
-  if (row >= rows) return;
-  const int parts = info.y - first + 1;
-  const int tid = threadIdx.x, quarter = tid >> 7, t = tid & 127;
-  auto slot = [&](int k) {  // the first part is its share's second slot, the others their shares' first
-    return (int64_t)(2 * ((first + k) * pl.row_blocks + rblk) + (k == 0 ? 1 : 0)) * n + blockIdx.y;
-  };
-  float top = -INFINITY;
-  for (int k = 0; k < parts; ++k) top = fmaxf(top, pl.part_lse[slot(k)]);
-  const float base = top == -INFINITY ? 0.f : top;
-  const int k0 = parts * quarter / 4, k1 = parts * (quarter + 1) / 4;
-  float acc[4] = {0.f, 0.f, 0.f, 0.f}, sum = 0.f;
-#pragma unroll 4
-  for (int k = k0; k < k1; ++k) {
-    const int64_t at = slot(k);
-    const float w = ex2(pl.part_lse[at] - base);
-    const float4 x = reinterpret_cast<const float4*>(pl.part + at * kLat)[t];
-    sum += w;
-    if (w != 0.f) {
-      acc[0] += w * x.x;
-      acc[1] += w * x.y;
-      acc[2] += w * x.z;
-      acc[3] += w * x.w;
-    }
-  }
-  reinterpret_cast<float4*>(part[quarter])[t] = make_float4(acc[0], acc[1], acc[2], acc[3]);
-  if (t == 0) wts[quarter] = sum;
-  __syncthreads();
-  const float total = (wts[0] + wts[1]) + (wts[2] + wts[3]);
-  const float inv = total > 0.f ? 1.0f / total : (total == 0.f ? 0.f : total);
-  const float o = (part[0][tid] + part[1][tid]) + (part[2][tid] + part[3][tid]);
+  const int tid = threadIdx.x, lane = tid & 31, rblk = blockIdx.x % pl.row_blocks, first = info.y;
+  const int r = kWide ? blockIdx.y : blockIdx.y * 16 + (tid >> 5);  // row of the block of n
+  const int rows = p.R * p.H, row = rblk * n + r;
+  if (r >= n || row >= rows) return;  // (kWide: the whole CTA)
+  const int parts = info.z - first + 1;
   const int64_t at = (int64_t)info.x * rows + row;
-  __nv_bfloat16 r = __float2bfloat16_rn(o * inv);
-  reinterpret_cast<__nv_bfloat16*>(p.out)[at * kLat + tid] = r;
-  if (tid == 0 && p.lse) p.lse[at] = total == 0.f ? -INFINITY : (top + __log2f(total)) * 0.6931471805599453f;
+  auto slot = [&](int k) {  // the first part is its share's second slot, the others their shares' first
+    return (int64_t)(2 * ((first + k) * pl.row_blocks + rblk) + (k == 0 ? 1 : 0)) * n + r;
+  };
+  // every warp takes the maximum over all parts for itself
+  float top = -INFINITY;
+  for (int k = lane; k < parts; k += 32) top = fmaxf(top, pl.part_lse[slot(k)]);
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+  const float base = top == -INFINITY ? 0.f : top;
+  if constexpr (kWide) {
+    __shared__ float part[4][kLat];
+    __shared__ float wts[4];
+    const int quarter = tid >> 7, t = tid & 127;
+    const int k0 = parts * quarter / 4, k1 = parts * (quarter + 1) / 4;
+    float acc[4] = {0.f, 0.f, 0.f, 0.f}, sum = 0.f;
+#pragma unroll 8
+    for (int k = k0; k < k1; ++k) {
+      const int64_t from = slot(k);
+      const float w = ex2(pl.part_lse[from] - base);
+      const float4 x = reinterpret_cast<const float4*>(pl.part + from * kLat)[t];
+      sum += w;
+      if (w != 0.f) {
+        acc[0] += w * x.x;
+        acc[1] += w * x.y;
+        acc[2] += w * x.z;
+        acc[3] += w * x.w;
+      }
+    }
+    reinterpret_cast<float4*>(part[quarter])[t] = make_float4(acc[0], acc[1], acc[2], acc[3]);
+    if (t == 0) wts[quarter] = sum;
+    __syncthreads();
+    const float total = (wts[0] + wts[1]) + (wts[2] + wts[3]);
+    const float inv = total > 0.f ? 1.0f / total : (total == 0.f ? 0.f : total);
+    const float o = (part[0][tid] + part[1][tid]) + (part[2][tid] + part[3][tid]);
+    reinterpret_cast<__nv_bfloat16*>(p.out)[at * kLat + tid] = __float2bfloat16_rn(o * inv);
+    if (tid == 0 && p.lse) p.lse[at] = total == 0.f ? -INFINITY : (top + __log2f(total)) * 0.6931471805599453f;
+  } else {
+    float acc[16], sum = 0.f;
+#pragma unroll
+    for (int i = 0; i < 16; ++i) acc[i] = 0.f;
+#pragma unroll 2
+    for (int k = 0; k < parts; ++k) {
+      const int64_t from = slot(k);
+      const float w = ex2(pl.part_lse[from] - base);
+      const float4* src = reinterpret_cast<const float4*>(pl.part + from * kLat) + lane;
+      sum += w;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const float4 x = src[32 * i];
+        if (w != 0.f) {
+          acc[4 * i] += w * x.x;
+          acc[4 * i + 1] += w * x.y;
+          acc[4 * i + 2] += w * x.z;
+          acc[4 * i + 3] += w * x.w;
+        }
+      }
+    }
+    const float inv = sum > 0.f ? 1.0f / sum : (sum == 0.f ? 0.f : sum);
+    uint2* dst = reinterpret_cast<uint2*>(p.out + at * kLat) + lane;
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      dst[32 * i] = make_uint2(pack_bf16(acc[4 * i] * inv, acc[4 * i + 1] * inv),
+                               pack_bf16(acc[4 * i + 2] * inv, acc[4 * i + 3] * inv));
+    if (lane == 0 && p.lse) p.lse[at] = sum == 0.f ? -INFINITY : (top + __log2f(sum)) * 0.6931471805599453f;
+  }
 }
 
 namespace {
@@ -633,7 +707,7 @@ int dec_width(const DecodeParams& p) {
 
 struct DecLayout {
   DecodePlan plan;
-  int n;
+  int n, joins;
   size_t lse_at, split_at, bytes;
 };
 
@@ -644,7 +718,7 @@ DecLayout dec_layout(const DecodeParams& p) {
   const int sms = std::max(1, device_sm_count());
   const int rows = p.R * p.H;
   d.plan.row_blocks = (rows + d.n - 1) / d.n;
-  const int64_t most = (int64_t)p.B * std::max<int64_t>(1, (p.max_pages * p.page_size + kDecTile - 1) / kDecTile);
+  const int64_t most = (int64_t)p.B * ((p.max_pages * p.page_size + kDecTile - 1) / kDecTile + 1);
   d.plan.min_tiles = 2;
   d.plan.shares = (int)std::max<int64_t>(1, std::min<int64_t>(sms / d.plan.row_blocks,
                                                               (most + d.plan.min_tiles - 1) / d.plan.min_tiles));
@@ -652,7 +726,9 @@ DecLayout dec_layout(const DecodeParams& p) {
   const size_t ctas = (size_t)d.plan.row_blocks * d.plan.shares;
   d.lse_at = ctas * 2 * d.n * kLat * 4;
   d.split_at = d.lse_at + ctas * 2 * d.n * 4;
-  d.bytes = (d.split_at + ctas * sizeof(int4) + 255) / 256 * 256;
+  d.plan.by_request = p.B <= d.plan.shares;
+  d.joins = (int)(std::min<int64_t>(p.B, d.plan.shares) * d.plan.row_blocks);
+  d.bytes = (d.split_at + (size_t)d.joins * sizeof(int4) + 255) / 256 * 256;
   return d;
 }
 
@@ -671,7 +747,10 @@ bool launch_dec(const DecodeParams& p, const DecLayout& d, const DecodeMaps& map
   kda_latent_decode_kernel<N><<<ctas, kDecThreads, DecCfg<N>::kSmem, s>>>(p, d.plan, maps);
   if (d.plan.shares == 1) return true;  // no request is split
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(ctas, (unsigned)std::min(N, p.R * p.H));
+  // a row a CTA where a request is in more than four parts on average, else a row a warp
+  const bool wide = (int64_t)p.B * 4 < d.plan.shares;
+  const int most = std::min(N, p.R * p.H);
+  cfg.gridDim = dim3((unsigned)d.joins, (unsigned)(wide ? most : (most + 15) / 16));
   cfg.blockDim = dim3(512);
   cfg.stream = s;
   cudaLaunchAttribute attr[1];
@@ -679,7 +758,8 @@ bool launch_dec(const DecodeParams& p, const DecLayout& d, const DecodeMaps& map
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, kda_latent_join_kernel, p, d.plan, N) == cudaSuccess;
+  return cudaLaunchKernelEx(&cfg, wide ? kda_latent_join_kernel<true> : kda_latent_join_kernel<false>, p, d.plan, N) ==
+         cudaSuccess;
 }
 
 }  // namespace
@@ -706,8 +786,7 @@ bool launch_latent_decode(const DecodeParams& args, cudaStream_t s) {
   } else {  // the cache as [64 values][page rows][9 blocks][pages]
     const cuuint64_t dims[4] = {64, (cuuint64_t)p.page_size, (cuuint64_t)kDecChunks, (cuuint64_t)p.num_pages};
     const cuuint64_t strides[3] = {(cuuint64_t)p.token_stride * 2, 128, (cuuint64_t)p.page_stride * 2};
-    const cuuint32_t box[4] = {64, (cuuint32_t)d.plan.box_rows,
-                               (cuuint32_t)(d.plan.box_rows == kDecTile ? kDecChunks : 1), 1};
+    const cuuint32_t box[4] = {64, (cuuint32_t)d.plan.box_rows, (cuuint32_t)(d.plan.box_rows == kDecTile ? 3 : 1), 1};
     if (!encode_map_bf16(&maps.cache, p.cache, 4, dims, strides, box)) return false;
   }
   switch (d.n) {
