@@ -12,8 +12,10 @@
 // (16, 32 or 64): few heads then cost few columns instead of empty rows.
 //   S^T [64 tokens x N]      = X (64 x 576, K-major)              . Q^T
 //   O^T [4 x 128 dims x N]  += C^T (128 x 64, the same tile read MN-major) . P^T
-// The tile of 64 cached rows lies in shared memory once, as nine 64-column
-// blocks of [64 tokens][128 bytes] with the 128-byte swizzle.  Tensor memory:
+// The tile of 64 cached rows lies in shared memory once, as [8 groups of 8
+// tokens][9 blocks of 64 columns][8 tokens][128 bytes] with the 128-byte
+// swizzle: pages of any multiple of 8 tokens arrive in whole rows, as one
+// copy a run of gcd(page_size, 64) tokens.  Tensor memory:
 // O^T 4 N columns, S^T twice N.
 //
 // Softmax: four warps for each half of the query rows read S^T as 16 x 8
@@ -46,9 +48,9 @@ namespace kda {
 constexpr int kDecTile = 64;                     // cached rows of a tile
 constexpr int kDecChunks = kLatRow / 64;         // 64-column blocks of a row
 constexpr int kDecStages = 2;
-constexpr int kDecGroups = 3;                    // the blocks of a tile arrive three by three
-constexpr int kDecBlk = kDecTile * 128;          // bytes of a 64-column block of a tile
-constexpr int kDecStage = kDecChunks * kDecBlk;  // 73728
+constexpr int kDecAtom = 8 * 128;                // 8 tokens of a 64-column block
+constexpr int kDecGroup = kDecChunks * kDecAtom; // 8 tokens: 9216 bytes
+constexpr int kDecStage = 8 * kDecGroup;         // 73728
 constexpr int kDecThreads = 320;
 constexpr int kDecCopyWarp = 8, kDecMmaWarp = 9;
 // A share's cost: 4 a tile and 4 a request (query block, first wait, output),
@@ -80,9 +82,9 @@ struct DecCfg {
   static constexpr int kWmax = kP + N * 128;                // fp32 [4][N]: maxima, then sums, of the warps
   static constexpr int kFac = kWmax + 16 * N;               // fp32 [N]
   static constexpr int kBar = kFac + 4 * N;
-  // full[2][3] (stage, group), empty[2], qfull[2], qempty[2], sfull[2], pready, pvdone
-  static constexpr int kFull = 0, kEmpty = 6, kQFull = 8, kQEmpty = 10, kSFull = 12, kPReady = 14, kPvDone = 15,
-                       kBars = 16;
+  // full[2], empty[2], qfull[2], qempty[2], sfull[2], pready, pvdone
+  static constexpr int kFull = 0, kEmpty = 2, kQFull = 4, kQEmpty = 6, kSFull = 8, kPReady = 10, kPvDone = 11,
+                       kBars = 12;
   static constexpr int kScan = kBar + 8 * kBars;            // int64 [10] sums of the warps, [2] first request and its start
   static constexpr int kTmem = kScan + 96;
   static constexpr int kAbort = kTmem + 8;
@@ -271,25 +273,15 @@ __global__ void __launch_bounds__(kDecThreads, 1)
           page = (int)p.num_pages;  // past the map: reads as zeros
         }
       }
-      const uint32_t dst = sb + s * kDecStage, full = bar(C::kFull + kDecGroups * s);
+      const uint32_t dst = sb + s * kDecStage, full = bar(C::kFull + s);
       if (it >= kDecStages) wait(bar(C::kEmpty + s), (uint32_t)(((it >> 1) & 1) ^ 1));
       __syncwarp();
       gone = __any_sync(0xffffffffu, *s_abort != 0);
       if (gone) break;
-      if (lane < kDecGroups) mbar_expect_tx(full + 8 * lane, (uint32_t)(segs * box * 128 * 3));
-      if (box == kDecTile) {  // lane = group
-        const int pg = __shfl_sync(0xffffffffu, page, 0), of = __shfl_sync(0xffffffffu, off, 0);
-        if (lane < kDecGroups)
-          tma_load_4d(dst + 3 * lane * kDecBlk, &maps.cache, 0, of, 3 * lane, pg, full + 8 * lane);
-      } else {                // lane = (run, block)
-        __syncwarp();
-        for (int i0 = 0; i0 < segs * kDecChunks; i0 += 32) {
-          const int i = i0 + lane, ch = i / segs, seg = i - ch * segs;
-          const int pg = __shfl_sync(0xffffffffu, page, seg), of = __shfl_sync(0xffffffffu, off, seg);
-          if (ch < kDecChunks)
-            tma_load_4d(dst + ch * kDecBlk + seg * box * 128, &maps.cache, 0, of, ch, pg, full + 8 * (ch / 3));
-        }
-      }
+      if (lane == 0) mbar_expect_tx(full, (uint32_t)(segs * box * (kDecGroup / 8)));
+      __syncwarp();
+      if (lane < segs)
+        tma_load_5d(dst + lane * box * (kDecGroup / 8), &maps.cache, 0, 0, 0, off >> 3, page, full);
       if (c.first()) {
         const int qb = qi % C::kQBufs;
         if (qi >= C::kQBufs) wait(bar(C::kQEmpty + qb), (uint32_t)(((qi / C::kQBufs) & 1) ^ 1));
@@ -307,15 +299,14 @@ __global__ void __launch_bounds__(kDecThreads, 1)
     // After a timeout: let the copies still in flight land before leaving.
     if (gone && lane == 0) {
       for (int t = max(0, it - kDecStages); t < it; ++t)
-        for (int g = 0; g < kDecGroups; ++g)
-          mbar_wait_bounded(bar(C::kFull + kDecGroups * (t & 1) + g), (uint32_t)((t >> 1) & 1));
+        mbar_wait_bounded(bar(C::kFull + (t & 1)), (uint32_t)((t >> 1) & 1));
       for (int t = max(0, qi - C::kQBufs); t < qi; ++t)
         mbar_wait_bounded(bar(C::kQFull + t % C::kQBufs), (uint32_t)((t / C::kQBufs) & 1));
     }
   } else if (warp == kDecMmaWarp) {
     // ---- products ----
     const uint32_t id_s = idesc_bf16(64, N, false, false), id_o = idesc_bf16(128, N, true, false);
-    const uint64_t d_x = smem_desc(sb, 16, 1024), d_c = smem_desc(sb, kDecBlk, 1024);
+    const uint64_t d_x = smem_desc(sb, 16, kDecGroup), d_c = smem_desc(sb, kDecAtom, kDecGroup);
     const uint64_t d_q = smem_desc(sb + C::kQ, 16, 1024), d_p = smem_desc(sb + C::kP, 16, 1024);
     const uint32_t t_s = tmem + 4 * N;
     DecCursor cs, co;
@@ -333,23 +324,20 @@ __global__ void __launch_bounds__(kDecThreads, 1)
     for (;;) {
       bool go = cs.ok && is == io;
       if (cs.ok && is == io + 1)
-        go = __all_sync(0xffffffffu, mbar_test(bar(C::kFull + kDecGroups * (is & 1) + 2), (uint32_t)((is >> 1) & 1)));
+        go = __all_sync(0xffffffffu, mbar_test(bar(C::kFull + (is & 1)), (uint32_t)((is >> 1) & 1)));
       if (go) {  // S^T of tile `is` into its half of the score columns
         const int s = is & 1, qb = cs.piece % C::kQBufs;
         const uint64_t a = d_x + (uint64_t)((s * kDecStage) >> 4), b = d_q + (uint64_t)((qb * C::kQBytes) >> 4);
         if (cs.first()) wait(bar(C::kQFull + qb), (uint32_t)((cs.piece / C::kQBufs) & 1));
+        wait(bar(C::kFull + s), (uint32_t)((is >> 1) & 1));
+        __syncwarp();
+        tc_fence_after();
 #pragma unroll
-        for (int ch = 0; ch < kDecChunks; ++ch) {
-          if (ch % 3 == 0) {
-            wait(bar(C::kFull + kDecGroups * s + ch / 3), (uint32_t)((is >> 1) & 1));
-            __syncwarp();
-            tc_fence_after();
-          }
+        for (int ch = 0; ch < kDecChunks; ++ch)
 #pragma unroll
           for (int ks = 0; ks < 4; ++ks)
-            tc_mma(t_s + N * s, a + (uint64_t)((ch * kDecBlk + ks * 32) >> 4), b + (uint64_t)((ch * N * 128 + ks * 32) >> 4),
+            tc_mma(t_s + N * s, a + (uint64_t)((ch * kDecAtom + ks * 32) >> 4), b + (uint64_t)((ch * N * 128 + ks * 32) >> 4),
                    id_s, ch + ks > 0);
-        }
         tc_commit(bar(C::kSFull + s));
         if (cs.last()) tc_commit(bar(C::kQEmpty + qb));
         ++is;
@@ -363,10 +351,10 @@ __global__ void __launch_bounds__(kDecThreads, 1)
       const int valid = min(kDecTile, co.it.len - co.tile * kDecTile);
       if (valid < kDecTile) {
         // what lies behind the length takes part in the product with weight 0: it has to be finite
-        const int n16 = (kDecTile - valid) * 8;
-        for (int ch = 0; ch < kLat / 64; ++ch)
-          for (int i = lane; i < n16; i += 32)
-            reinterpret_cast<uint4*>(smem + s * kDecStage + ch * kDecBlk + valid * 128)[i] = make_uint4(0, 0, 0, 0);
+        for (int t = valid; t < kDecTile; ++t)
+          for (int i = lane; i < kLat / 8; i += 32)
+            *reinterpret_cast<uint4*>(smem + s * kDecStage + (t >> 3) * kDecGroup + (i >> 3) * kDecAtom + (t & 7) * 128 +
+                                      (i & 7) * 16) = make_uint4(0, 0, 0, 0);
         fence_proxy_async_smem();
       }
       __syncwarp();
@@ -377,7 +365,7 @@ __global__ void __launch_bounds__(kDecThreads, 1)
       for (int mt = 0; mt < 4; ++mt)
 #pragma unroll
         for (int ks = 0; ks < 4; ++ks)
-          tc_mma(tmem + mt * N, a + (uint64_t)((mt * 2 * kDecBlk + ks * 2048) >> 4), d_p + (uint64_t)((ks * 32) >> 4),
+          tc_mma(tmem + mt * N, a + (uint64_t)((mt * 2 * kDecAtom + ks * 2 * kDecGroup) >> 4), d_p + (uint64_t)((ks * 32) >> 4),
                  id_o, ks > 0 ? 1u : start);
       tc_commit(bar(C::kEmpty + s));
       tc_commit(bar(C::kPvDone));
@@ -783,11 +771,12 @@ bool launch_latent_decode(const DecodeParams& args, cudaStream_t s) {
   }
   if (p.num_pages == 0) {
     p.max_pages = 0;  // no cache: every length is taken as 0, and nothing is copied
-  } else {  // the cache as [64 values][page rows][9 blocks][pages]
-    const cuuint64_t dims[4] = {64, (cuuint64_t)p.page_size, (cuuint64_t)kDecChunks, (cuuint64_t)p.num_pages};
-    const cuuint64_t strides[3] = {(cuuint64_t)p.token_stride * 2, 128, (cuuint64_t)p.page_stride * 2};
-    const cuuint32_t box[4] = {64, (cuuint32_t)d.plan.box_rows, (cuuint32_t)(d.plan.box_rows == kDecTile ? 3 : 1), 1};
-    if (!encode_map_bf16(&maps.cache, p.cache, 4, dims, strides, box)) return false;
+  } else {  // the cache as [64 values][8 tokens][9 blocks][8-token groups of a page][pages]
+    const cuuint64_t dims[5] = {64, 8, (cuuint64_t)kDecChunks, (cuuint64_t)p.page_size / 8, (cuuint64_t)p.num_pages};
+    const cuuint64_t strides[4] = {(cuuint64_t)p.token_stride * 2, 128, (cuuint64_t)p.token_stride * 16,
+                                   (cuuint64_t)p.page_stride * 2};
+    const cuuint32_t box[5] = {64, 8, (cuuint32_t)kDecChunks, (cuuint32_t)d.plan.box_rows / 8, 1};
+    if (!encode_map_bf16(&maps.cache, p.cache, 5, dims, strides, box)) return false;
   }
   switch (d.n) {
     case 16: return launch_dec<16>(p, d, maps, s);
