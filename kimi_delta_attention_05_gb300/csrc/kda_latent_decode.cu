@@ -53,9 +53,11 @@ constexpr int kDecGroup = kDecChunks * kDecAtom; // 8 tokens: 9216 bytes
 constexpr int kDecStage = 8 * kDecGroup;         // 73728
 constexpr int kDecThreads = 320;
 constexpr int kDecCopyWarp = 8, kDecMmaWarp = 9;
-// A share's cost: 4 a tile and 4 a request (query block, first wait, output),
-// which together are about one tile's time.
-constexpr int kDecTileCost = 4, kDecReqCost = 4;
+// A share's cost: 4 a tile and 6 a request (query block, first wait, output),
+// which together are about one and a half tiles' time (2, 4 and 6 measured: 121.2,
+// 120.7 and 120.3 us on 256 requests of up to 4096 tokens, 53.4, 52.9 and 50.0 on 203 of up to 1400).
+constexpr int kDecTileCost = 4, kDecReqCost = 6;
+static_assert(kDecTileCost == 4, "tiles_before shifts by it");
 constexpr float kDecSlack = 8.0f;                // log2 growth of a maximum that is let pass
 
 struct DecodeMaps {
@@ -102,6 +104,11 @@ __device__ __forceinline__ int dec_len(const DecodeParams& p, int b) {
 __device__ __forceinline__ int dec_tiles(int len) { return len > 0 ? (len - 1) / kDecTile + 1 : 0; }
 __device__ __forceinline__ int64_t dec_cost(int tiles) { return (int64_t)tiles * kDecTileCost + kDecReqCost; }
 
+// a / b of non-negative numbers, in 32 bits where they fit
+__device__ __forceinline__ int64_t div_fast(int64_t a, int64_t b) {
+  return ((a | b) >> 32) == 0 ? (int64_t)((uint32_t)a / (uint32_t)b) : a / b;
+}
+
 // The pieces of one share [u0, u1) of the line of costs, in order.  Request b
 // takes [pre, pre + cost) of it; its tile k starts at pre + kDecReqCost + k
 // kDecTileCost and belongs to the share that holds that point; a request
@@ -113,7 +120,7 @@ struct DecPieces {
   int req, len, t0, t1, tiles;
   __device__ __forceinline__ int tiles_before(int64_t u) const {
     const int64_t d = u - pre - kDecReqCost;
-    return d <= 0 ? 0 : (int)min((int64_t)tiles, (d + kDecTileCost - 1) / kDecTileCost);
+    return d <= 0 ? 0 : (int)min((int64_t)tiles, (d + kDecTileCost - 1) >> 2);
   }
   __device__ __forceinline__ bool next(const DecodeParams& p) {
     while (b < p.B && pre < u1) {
@@ -174,7 +181,8 @@ __global__ void __launch_bounds__(kDecThreads, 1)
   int64_t* s_scan = reinterpret_cast<int64_t*>(smem + C::kScan);
 
   // ---- set-up: barriers, tensor memory, this CTA's share of the tiles ----
-  if (tid == 0) {
+  // (by the last warps: the first ones fetch the lengths meanwhile)
+  if (warp == kDecCopyWarp && lane == 0) {
     for (int i = 0; i < C::kBars; ++i) mbar_init(bar(i), i == C::kPReady ? 8 : 1);
     *s_abort = (sb & 1023) ? 1 : 0;
     s_scan[10] = 0;
@@ -218,7 +226,7 @@ __global__ void __launch_bounds__(kDecThreads, 1)
     if (w < warp) before += s_scan[w];
     total += s_scan[w];
   }
-  const int64_t size = max((int64_t)pl.min_tiles * kDecTileCost, (total + pl.shares - 1) / pl.shares);
+  const int64_t size = max((int64_t)pl.min_tiles * kDecTileCost, div_fast(total + pl.shares - 1, pl.shares));
   const int64_t u0 = min(total, share * size), u1 = min(total, u0 + size);
   before += incl - mine;
   if (u0 < u1 && u0 >= before && u0 < before + mine) {
@@ -580,7 +588,7 @@ __global__ void __launch_bounds__(kDecThreads, 1)
       if (each.t0 > 0) continue;
       // (the request's last tile starts kDecTileCost before the next request)
       const int4 info = each.whole() ? make_int4(-1, 0, 0, 0)
-                                     : make_int4(each.req, share, (int)((each.pre - kDecTileCost) / size), 0);
+                                     : make_int4(each.req, share, (int)div_fast(each.pre - kDecTileCost, size), 0);
       if (pl.by_request) pl.split[each.req * pl.row_blocks + rblk] = info;
       else if (!each.whole()) pl.split[blockIdx.x] = info;
     }
