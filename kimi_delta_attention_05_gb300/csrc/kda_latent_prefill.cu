@@ -17,8 +17,11 @@
 //
 // Shared memory: Q 96 KB, and a ring of eight 16 KB slots ([128 keys][64
 // channels], 128-byte swizzle) that takes a tile's three key blocks and two
-// value blocks in the order they are used, each with its own barriers, so a
-// slot is refilled as soon as its products are done.  Tensor memory: S0, S1,
+// value blocks in the order they are used and is refilled as soon as their
+// products are done.  Keys and values of a tile have one barrier each: while
+// the tensor core streams its operands a shared-memory access takes some 150
+// to 300 cycles, and the issuing warp has about 400 cycles of queued products
+// to spend on waits (one barrier a slot: 528 us on the 8192-token prompt).  Tensor memory: S0, S1,
 // O0, O1, 128 columns each.
 //
 // Roles: warps 0-3 and 4-7 softmax and output of the two tiles, warp 8 copies,
@@ -41,8 +44,9 @@ constexpr int kPreQ = 0;                         // two tiles of three [128 rows
 constexpr int kPreQTile = 3 * kPreRows * 128;
 constexpr int kPreRing = 2 * kPreQTile;
 constexpr int kPreBar = kPreRing + kPreSlots * kPreSlot;
-// full[8], empty[8], q, sfull[2], pready[2], pvdone[2]
-constexpr int kPbFull = 0, kPbEmpty = 8, kPbQ = 16, kPbS = 17, kPbP = 19, kPbPv = 21, kPbars = 23;
+// full and empty of the key and value blocks (by the tile's parity), q, sfull[2], pready[2], pvdone[2]
+constexpr int kPbFullK = 0, kPbFullV = 2, kPbEmptyK = 4, kPbEmptyV = 6, kPbQ = 8, kPbS = 9, kPbP = 11, kPbPv = 13,
+              kPbars = 15;
 constexpr int kPreTmem = kPreBar + 8 * kPbars;
 constexpr int kPreAbort = kPreTmem + 8;
 constexpr int kPreSmem = kPreAbort + 8;
@@ -149,7 +153,7 @@ __global__ void __launch_bounds__(kPreThreads, 1)
   tc_fence_after();
   const uint32_t tmem = *reinterpret_cast<volatile uint32_t*>(smem + kPreTmem);
   auto wait = [&](uint32_t b, uint32_t parity) {
-    if (*s_abort) return;
+    if (mbar_try_wait(b, parity) || *s_abort) return;
     if (!mbar_wait_bounded(b, parity)) {
       atomicExch(p.status, KDA_ERR_DEVICE_TIMEOUT);
       *s_abort = 1;
@@ -157,43 +161,53 @@ __global__ void __launch_bounds__(kPreThreads, 1)
   };
 
   if (warp == 8) {
-    // ---- copies: Q, then per key tile K (two blocks), pe, V (two blocks) ----
-    int slot = 0, done = 0;   // next slot of the ring, copies issued
-    uint32_t ph = 1;          // parity of the slots' previous use
-    bool q_sent = false;
-    for (int i = 0; i < nt && !*s_abort; ++i) {
+    // ---- copies: Q, then per key tile K (two blocks) and pe, V (two blocks).  Tile i's
+    //      five slots start at slot 5 i % 8, so its keys follow the values of tile i - 2
+    //      (and the last key block of i - 2), its values the keys of tile i - 1 ----
+    bool gone = false;
+    int keys = 0, values = 0;  // tiles whose keys / values are on the way
+    for (int i = 0; i < nt && !gone; ++i) {
       const int key = (int)(k0 + (int64_t)i * kPreKeys);
-      for (int c = 0; c < 5; ++c) {
-        if (done >= kPreSlots) wait(bar(kPbEmpty + slot), ph);
-        __syncwarp();
-        if (*s_abort) break;
-        if (lane == 0) {
-          const uint32_t full = bar(kPbFull + slot), dst = sb + kPreRing + slot * kPreSlot;
-          mbar_expect_tx(full, kPreSlot);
-          if (c < 2) tma_load_3d(dst, &maps.k, 64 * c, h, key, full);
-          else if (c == 2) tma_load_2d(dst, &maps.pe, 0, key, full);
-          else tma_load_3d(dst, &maps.v, 64 * (c - 3), h, key, full);
-          if (!q_sent) {
-            mbar_expect_tx(bar(kPbQ), 2 * kPreQTile);
-            for (int t = 0; t < 2; ++t)
-              for (int b = 0; b < 3; ++b)
-                tma_load_3d(sb + kPreQ + t * kPreQTile + b * kPreRows * 128, &maps.q, 64 * b, h,
-                            (int)(q0 + r0 + t * kPreRows), bar(kPbQ));
-          }
+      auto dst = [&](int c) { return sb + kPreRing + ((5 * i + c) % kPreSlots) * kPreSlot; };
+      if (i >= 2) wait(bar(kPbEmptyV + (i & 1)), (uint32_t)(((i - 2) >> 1) & 1));
+      __syncwarp();
+      gone = __any_sync(0xffffffffu, *s_abort != 0);
+      if (gone) break;
+      if (lane == 0) {
+        const uint32_t full = bar(kPbFullK + (i & 1));
+        mbar_expect_tx(full, 3 * kPreSlot);
+        if (i == 0) {
+          mbar_expect_tx(bar(kPbQ), 2 * kPreQTile);
+          for (int b = 0; b < 3; ++b)
+            tma_load_3d(sb + kPreQ + b * kPreRows * 128, &maps.q, 64 * b, h, (int)(q0 + r0), bar(kPbQ));
         }
-        q_sent = true;
-        ++done;
-        if (++slot == kPreSlots) {
-          slot = 0;
-          ph ^= 1u;
-        }
+        tma_load_3d(dst(0), &maps.k, 0, h, key, full);
+        tma_load_3d(dst(1), &maps.k, 64, h, key, full);
+        tma_load_2d(dst(2), &maps.pe, 0, key, full);
+        if (i == 0)
+          for (int b = 0; b < 3; ++b)
+            tma_load_3d(sb + kPreQ + kPreQTile + b * kPreRows * 128, &maps.q, 64 * b, h, (int)(q0 + r0 + kPreRows),
+                        bar(kPbQ));
       }
+      ++keys;
+      if (i >= 1) wait(bar(kPbEmptyK + ((i - 1) & 1)), (uint32_t)(((i - 1) >> 1) & 1));
+      __syncwarp();
+      gone = __any_sync(0xffffffffu, *s_abort != 0);
+      if (gone) break;
+      if (lane == 0) {
+        const uint32_t full = bar(kPbFullV + (i & 1));
+        mbar_expect_tx(full, 2 * kPreSlot);
+        tma_load_3d(dst(3), &maps.v, 0, h, key, full);
+        tma_load_3d(dst(4), &maps.v, 64, h, key, full);
+      }
+      ++values;
     }
     // After a timeout: let the copies still in flight land before leaving.
-    if (*s_abort && lane == 0) {
-      for (int c = max(0, done - kPreSlots); c < done; ++c)
-        mbar_wait_bounded(bar(kPbFull + c % kPreSlots), (uint32_t)((c / kPreSlots) & 1));
-      if (q_sent) mbar_wait_bounded(bar(kPbQ), 0);
+    if (gone && lane == 0) {
+      for (int i = max(0, keys - 2); i < keys; ++i) mbar_wait_bounded(bar(kPbFullK + (i & 1)), (uint32_t)((i >> 1) & 1));
+      for (int i = max(0, values - 2); i < values; ++i)
+        mbar_wait_bounded(bar(kPbFullV + (i & 1)), (uint32_t)((i >> 1) & 1));
+      if (keys > 0) mbar_wait_bounded(bar(kPbQ), 0);
     }
   } else if (warp == 9) {
     // ---- products ----
@@ -206,15 +220,14 @@ __global__ void __launch_bounds__(kPreThreads, 1)
       __syncwarp();
     }
     auto slot_of = [&](int i, int c) { return (5 * i + c) % kPreSlots; };
-    auto full_wait = [&](int i, int c) {
-      wait(bar(kPbFull + slot_of(i, c)), (uint32_t)(((5 * i + c) / kPreSlots) & 1));
+    auto full_wait = [&](int b, int i) {
+      wait(bar(b + (i & 1)), (uint32_t)((i >> 1) & 1));
       __syncwarp();
       tc_fence_after();
     };
-    auto scores = [&](int t, int i, bool fresh) {
+    auto scores = [&](int t, int i) {
 #pragma unroll
       for (int c = 0; c < 3; ++c) {
-        if (fresh) full_wait(i, c);
         const uint64_t a = d_q + (uint64_t)((t * kPreQTile + c * kPreRows * 128) >> 4);
         const uint64_t b = d_k + (uint64_t)((slot_of(i, c) * kPreSlot) >> 4);
 #pragma unroll
@@ -244,17 +257,15 @@ __global__ void __launch_bounds__(kPreThreads, 1)
       tc_commit(bar(kPbPv + t));
     };
     for (int i = 0; i < nt; ++i) {
-      // (the copies of a tile that only the second query tile uses are waited for all the same)
-      if (i < n0) scores(0, i, true);
+      full_wait(kPbFullK, i);
+      if (i < n0) scores(0, i);
       if (i > 0) {
         if (i - 1 < n1) values(1, i - 1);
-        tc_commit(bar(kPbEmpty + slot_of(i - 1, 3)));
-        tc_commit(bar(kPbEmpty + slot_of(i - 1, 4)));
+        tc_commit(bar(kPbEmptyV + ((i - 1) & 1)));
       }
-      if (i < n1) scores(1, i, i >= n0);
-      for (int c = 0; c < 3; ++c) tc_commit(bar(kPbEmpty + slot_of(i, c)));
-      full_wait(i, 3);
-      full_wait(i, 4);
+      if (i < n1) scores(1, i);
+      tc_commit(bar(kPbEmptyK + (i & 1)));
+      full_wait(kPbFullV, i);
       const int valid = lk - i * kPreKeys;
       if (valid < kPreKeys) {
         // rows behind the sequence take part with weight 0: they have to be finite
