@@ -294,19 +294,35 @@ int check_prefill(const kda_latent_prefill_args* a) {
   return KDA_OK;
 }
 
+// Query blocks of packed sequences: at most one a sequence more than the rows fill.
+int64_t prefill_blocks(const kda_latent_prefill_args* a) { return a->Tq / kPrefillRows + a->N; }
+
 size_t prefill_workspace(const kda_latent_prefill_args* a) {
-  return a->cu_seqlens_q ? ((size_t)(a->N + 1) * 4 + 255) / 256 * 256 : 0;
+  return a->cu_seqlens_q ? 256 + ((size_t)prefill_blocks(a) * sizeof(PrefillItem) + 255) / 256 * 256 : 0;
 }
 
 }  // namespace
 
-// Prefix of ceil(Lq / kPrefillRows) over packed sequences, one block, after
-// checking 0 = cu[0] <= ... <= cu[N] = T of both offset arrays.  A violation
-// sets the status word and leaves no block, so nothing is written.
+// The query blocks of packed sequences, those with most work first (so that
+// the persistent attention kernel ends evenly), by a counting sort over classes
+// of equal work (a sixteenth of an octave from 32 key tiles on).  Checks 0 =
+// cu[0] <= ... <= cu[N] = T of both offset arrays first: a violation sets the
+// status word and leaves no block, so nothing is written.  One block; the order
+// within a class is that of the atomics, and no result depends on it.
+constexpr int kWorkClasses = 352;
+__device__ __forceinline__ int work_class(int tiles) {
+  if (tiles < 32) return kWorkClasses - 1 - tiles;
+  const int e = 31 - __clz(tiles);
+  return kWorkClasses - 1 - (32 + (e - 5) * 16 + ((tiles >> (e - 4)) & 15));
+}
+
 __global__ void __launch_bounds__(1024) kda_latent_blocks_kernel(const int64_t* cu_q, const int64_t* cu_k, int64_t N,
-                                                                 int64_t Tq, int64_t Tk, int32_t* off, int* status) {
-  __shared__ int64_t sums[32];
+                                                                 int64_t Tq, int64_t Tk, int causal, PrefillItem* items,
+                                                                 int32_t* count, int* status) {
+  __shared__ int32_t at[kWorkClasses];
+  asm volatile("griddepcontrol.launch_dependents;\n" ::: "memory");
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  for (int i = tid; i < kWorkClasses; i += 1024) at[i] = 0;
   int bad = 0;
   for (int64_t n = tid; n <= N; n += 1024) {
     const int64_t a = cu_q[n], b = cu_k[n];
@@ -315,24 +331,38 @@ __global__ void __launch_bounds__(1024) kda_latent_blocks_kernel(const int64_t* 
   }
   bad = __syncthreads_or(bad);
   if (tid == 0 && bad && status) atomicExch(status, KDA_ERR_BAD_SEQLENS);
-  int64_t carry = 0;
-  for (int64_t base = 0; base < N; base += 1024) {
-    const int64_t n = base + tid;
-    int64_t c = 0;
-    if (n < N && !bad) c = (cu_q[n + 1] - cu_q[n] + kPrefillRows - 1) / kPrefillRows;
-    const int64_t s = warp_scan(c, lane);
-    if (lane == 31) sums[warp] = s;
-    __syncthreads();
-    int64_t before = carry;
-#pragma unroll
-    for (int w = 0; w < 32; ++w) {
-      if (w < warp) before += sums[w];
-      carry += sums[w];
+  // a warp a sequence, a lane a block: first counted, then placed
+  for (int pass = 0; pass < 2; ++pass) {
+    for (int64_t n = warp; n < N && !bad; n += 32) {
+      PrefillItem it;
+      it.q0 = (int)cu_q[n];
+      it.lq = (int)(cu_q[n + 1] - cu_q[n]);
+      it.k0 = (int)cu_k[n];
+      it.lk = (int)(cu_k[n + 1] - cu_k[n]);
+      it.pad[0] = it.pad[1] = it.pad[2] = 0;
+      for (int64_t r = (int64_t)lane * kPrefillRows; r < it.lq; r += 32 * kPrefillRows) {
+        it.r0 = (int)r;
+        int tiles = 0;
+        for (int t = 0; t < 2; ++t) {
+          const int first = it.r0 + t * (kPrefillRows / 2), last = min(it.lq, first + kPrefillRows / 2) - 1;
+          if (first < it.lq) tiles += (max(0, causal ? min(it.lk, last + it.lk - it.lq + 1) : it.lk) + 127) / 128;
+        }
+        const int where = atomicAdd(&at[work_class(tiles)], 1);
+        if (pass == 1) items[where] = it;
+      }
     }
-    if (n < N) off[n] = (int32_t)(before + s - c);
+    __syncthreads();
+    if (pass == 0 && warp == 0) {  // counts to first places
+      int carry = 0;
+      for (int i = lane; i < kWorkClasses; i += 32) {
+        const int c = at[i], s = (int)warp_scan(c, lane);
+        at[i] = carry + s - c;
+        carry += __shfl_sync(0xffffffffu, s, 31);
+      }
+      if (lane == 0) *count = carry;
+    }
     __syncthreads();
   }
-  if (tid == 0) off[N] = (int32_t)carry;
 }
 
 }  // namespace kda
@@ -447,7 +477,8 @@ extern "C" int kda_latent_prefill(const kda_latent_prefill_args* a, void* worksp
   p.lse = a->lse;
   p.cu_q = a->cu_seqlens_q;
   p.cu_k = a->cu_seqlens_k;
-  p.blk_off = nullptr;
+  p.items = nullptr;
+  p.count = nullptr;
   p.B = a->B;
   p.Tq = a->Tq;
   p.Tk = a->Tk;
@@ -456,9 +487,12 @@ extern "C" int kda_latent_prefill(const kda_latent_prefill_args* a, void* worksp
   p.causal = (a->flags & KDA_LATENT_CAUSAL) ? 1 : 0;
   p.status = status;
   if (a->cu_seqlens_q) {
-    int32_t* off = static_cast<int32_t*>(workspace);
-    kda_latent_blocks_kernel<<<1, 1024, 0, s>>>(a->cu_seqlens_q, a->cu_seqlens_k, a->N, a->Tq, a->Tk, off, status);
-    p.blk_off = off;
+    int32_t* count = static_cast<int32_t*>(workspace);
+    PrefillItem* items = reinterpret_cast<PrefillItem*>(static_cast<unsigned char*>(workspace) + 256);
+    kda_latent_blocks_kernel<<<1, 1024, 0, s>>>(a->cu_seqlens_q, a->cu_seqlens_k, a->N, a->Tq, a->Tk, p.causal, items,
+                                                count, status);
+    p.items = items;
+    p.count = count;
   }
   if (a->Tq > 0 && !launch_latent_prefill(p, s)) return KDA_ERR_LAUNCH;
   return cudaGetLastError() == cudaSuccess ? KDA_OK : KDA_ERR_LAUNCH;

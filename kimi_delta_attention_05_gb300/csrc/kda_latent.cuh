@@ -30,6 +30,15 @@ struct DecodeParams {
   int* status;
 };
 
+// A block of query rows of a packed sequence.
+struct PrefillItem {
+  int q0, k0;                       // first query and key of the sequence
+  int lq, lk;                       // its lengths
+  int r0;                           // first row of the block within it
+  int pad[3];
+};
+static_assert(sizeof(PrefillItem) == 32, "read as two 16-byte pieces");
+
 struct PrefillParams {
   const uint16_t *q, *k, *k_pe, *v;
   int64_t q_st, q_sh, k_st, k_sh, pe_st, v_st, v_sh;  // element strides: token, head
@@ -37,7 +46,8 @@ struct PrefillParams {
   uint16_t* out;                    // bf16 [tokens, H, 128]
   float* lse;                       // [tokens, H] or nullptr
   const int64_t *cu_q, *cu_k;       // [N + 1] or nullptr (dense)
-  const int32_t* blk_off;           // [N + 1] prefix of query blocks (packed only)
+  const PrefillItem* items;         // query blocks, most work first (packed only)
+  const int32_t* count;             // their number (packed only)
   int64_t B, Tq, Tk, N;
   int H;
   int causal;

@@ -1,5 +1,5 @@
-// Expanded latent attention on the 5th-generation tensor cores: one CTA a
-// (block of 256 query rows, head), two 128-row tiles in turn.
+// Expanded latent attention on the 5th-generation tensor cores: persistent
+// CTAs walk (block of 256 query rows, head) items, two 128-row tiles in turn.
 //
 //   s_ij = scale (q_i . [k_j | pe_j]),  o_i = sum_j softmax(s_i)_j v_j
 // over the keys a row sees (causal: j <= i + Lk - Lq).  The 64 shared key
@@ -21,7 +21,9 @@
 // products are done.  Keys and values of a tile have one barrier each: while
 // the tensor core streams its operands a shared-memory access takes some 150
 // to 300 cycles, and the issuing warp has about 400 cycles of queued products
-// to spend on waits (one barrier a slot: 528 us on the 8192-token prompt).  Tensor memory: S0, S1,
+// to spend on waits (one barrier a slot: 528 us on the 8192-token prompt, 454
+// with one for the keys and one for the values).  The first key block has its
+// own, as its slot is free a product earlier than the others'.  Tensor memory: S0, S1,
 // O0, O1, 128 columns each.
 //
 // Roles: warps 0-3 and 4-7 softmax and output of the two tiles, warp 8 copies,
@@ -44,9 +46,10 @@ constexpr int kPreQ = 0;                         // two tiles of three [128 rows
 constexpr int kPreQTile = 3 * kPreRows * 128;
 constexpr int kPreRing = 2 * kPreQTile;
 constexpr int kPreBar = kPreRing + kPreSlots * kPreSlot;
-// full and empty of the key and value blocks (by the tile's parity), q, sfull[2], pready[2], pvdone[2]
-constexpr int kPbFullK = 0, kPbFullV = 2, kPbEmptyK = 4, kPbEmptyV = 6, kPbQ = 8, kPbS = 9, kPbP = 11, kPbPv = 13,
-              kPbars = 15;
+// full and empty of a tile's first key block, other key blocks and value blocks
+// (by the tile's parity), q full and empty, sfull[2], pready[2], pvdone[2]
+constexpr int kPbFullK0 = 0, kPbFullK = 2, kPbFullV = 4, kPbEmptyK = 6, kPbEmptyV = 8, kPbQ = 10, kPbQEmpty = 11,
+              kPbS = 12, kPbP = 14, kPbPv = 16, kPbars = 18;
 constexpr int kPreTmem = kPreBar + 8 * kPbars;
 constexpr int kPreAbort = kPreTmem + 8;
 constexpr int kPreSmem = kPreAbort + 8;
@@ -89,46 +92,63 @@ __device__ __forceinline__ float max3(float a, float b, float c) {
   return d;
 }
 
+// One item as every role sees it: a block of rows of a sequence and a head.
+struct PreItem {
+  int64_t q0, k0;    // first query and key of the sequence
+  int lq, lk, r0, h;  // its lengths, the block's first row, head
+  int n0, n1, nt;    // key tiles of the two query tiles (0 where a tile has no row or its rows see nothing)
+};
+
+// The items of a CTA: every grid-th of the list (most work first), each second
+// round backwards, so that the work of all CTAs is nearly the same.
+struct PreWalk {
+  int64_t round, total;
+  __device__ __forceinline__ void start(const PrefillParams& p, int64_t blocks) {
+    round = 0;
+    total = (p.items ? (int64_t)*p.count : blocks) * p.H;
+  }
+  __device__ __forceinline__ bool next(const PrefillParams& p, int64_t per, PreItem& it) {
+    const int64_t base = round * gridDim.x;
+    const int64_t idx = base + ((round & 1) ? gridDim.x - 1 - blockIdx.x : blockIdx.x);
+    ++round;
+    if (base >= total || idx >= total) return false;  // (only the last round is not full)
+    if (p.items) {
+      const uint32_t e = (uint32_t)idx / (uint32_t)p.H;
+      it.h = (int)((uint32_t)idx - e * (uint32_t)p.H);
+      const int4 a = __ldg(reinterpret_cast<const int4*>(p.items + e));
+      it.q0 = a.x;
+      it.k0 = a.y;
+      it.lq = a.z;
+      it.lk = a.w;
+      it.r0 = __ldg(&p.items[e].r0);
+    } else {  // later blocks of a causal sequence see more keys: they go first
+      const uint32_t bh = (uint32_t)(p.B * p.H), back = (uint32_t)idx / bh, x = (uint32_t)idx - back * bh;
+      const uint32_t n = x / (uint32_t)p.H;
+      it.h = (int)(x - n * (uint32_t)p.H);
+      it.q0 = (int64_t)n * p.Tq;
+      it.k0 = (int64_t)n * p.Tk;
+      it.lq = (int)p.Tq;
+      it.lk = (int)p.Tk;
+      it.r0 = (int)(per - 1 - back) * kPrefillRows;
+    }
+    auto tiles_of = [&](int t) {
+      const int first = it.r0 + t * kPreRows;
+      if (first >= it.lq) return 0;
+      const int last = min(it.lq, first + kPreRows) - 1;
+      const int seen = p.causal ? min(it.lk, last + it.lk - it.lq + 1) : it.lk;
+      return seen > 0 ? (seen + kPreKeys - 1) / kPreKeys : 0;
+    };
+    it.n0 = tiles_of(0);
+    it.n1 = tiles_of(1);
+    it.nt = max(it.n0, it.n1);
+    return true;
+  }
+};
+
 __global__ void __launch_bounds__(kPreThreads, 1)
-    kda_latent_prefill_kernel(const PrefillParams p, int64_t blocks_per_row, const __grid_constant__ PrefillMaps maps) {
+    kda_latent_prefill_kernel(const PrefillParams p, int64_t per, const __grid_constant__ PrefillMaps maps) {
   extern __shared__ __align__(1024) unsigned char smem[];
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  const int h = blockIdx.x % p.H;
-  // blocks with more keys (later rows of a causal sequence) go first
-  const int64_t nblk = gridDim.x / p.H;
-  int64_t blk = nblk - 1 - blockIdx.x / p.H;
-  int64_t q0, k0;       // first query and key of the sequence
-  int lq, lk, r0;       // its lengths, this block's first row
-  if (p.cu_q) {
-    if (blk >= p.blk_off[p.N]) return;
-    int64_t lo = 0, hi = p.N - 1;
-    while (lo < hi) {
-      const int64_t mid = (lo + hi + 1) >> 1;
-      if (p.blk_off[mid] <= blk) lo = mid; else hi = mid - 1;
-    }
-    q0 = p.cu_q[lo];
-    lq = (int)(p.cu_q[lo + 1] - q0);
-    k0 = p.cu_k[lo];
-    lk = (int)(p.cu_k[lo + 1] - k0);
-    r0 = (int)(blk - p.blk_off[lo]) * kPrefillRows;
-  } else {
-    const int64_t n = blk / blocks_per_row;
-    q0 = n * p.Tq;
-    lq = (int)p.Tq;
-    k0 = n * p.Tk;
-    lk = (int)p.Tk;
-    r0 = (int)(blk - n * blocks_per_row) * kPrefillRows;
-  }
-  // key tiles of the two query tiles (0 where it has no row or its rows see nothing)
-  auto tiles_of = [&](int t) {
-    const int first = r0 + t * kPreRows;
-    if (first >= lq) return 0;
-    const int last = min(lq, first + kPreRows) - 1;
-    const int seen = p.causal ? min(lk, last + lk - lq + 1) : lk;
-    return seen > 0 ? (seen + kPreKeys - 1) / kPreKeys : 0;
-  };
-  const int n0 = tiles_of(0), n1 = tiles_of(1), nt = max(n0, n1);
-
   const uint32_t sb = smem_u32(smem), bars = sb + kPreBar;
   auto bar = [&](int i) { return bars + 8 * i; };
   volatile int* s_abort = reinterpret_cast<volatile int*>(smem + kPreAbort);
@@ -148,6 +168,7 @@ __global__ void __launch_bounds__(kPreThreads, 1)
     prefetch_map(&maps.pe);
     prefetch_map(&maps.v);
   }
+  asm volatile("griddepcontrol.wait;\n" ::: "memory");  // (packed: the list of blocks)
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
@@ -159,55 +180,71 @@ __global__ void __launch_bounds__(kPreThreads, 1)
       *s_abort = 1;
     }
   };
+  PreWalk walk;
+  walk.start(p, p.B * per);
+  PreItem it;
+  int g = 0;  // key tiles so far, over all items
 
   if (warp == 8) {
-    // ---- copies: Q, then per key tile K (two blocks) and pe, V (two blocks).  Tile i's
-    //      five slots start at slot 5 i % 8, so its keys follow the values of tile i - 2
-    //      (and the last key block of i - 2), its values the keys of tile i - 1 ----
+    // ---- copies.  Key tile g's five slots (two key blocks, pe, two value blocks) start at
+    //      slot 5 g % 8: its first key block follows the last one of tile g - 2 (free where the
+    //      values of g - 1 could be sent), its other two the values of g - 2, its values the keys
+    //      of g - 1 ----
     bool gone = false;
-    int keys = 0, values = 0;  // tiles whose keys / values are on the way
-    for (int i = 0; i < nt && !gone; ++i) {
-      const int key = (int)(k0 + (int64_t)i * kPreKeys);
-      auto dst = [&](int c) { return sb + kPreRing + ((5 * i + c) % kPreSlots) * kPreSlot; };
-      if (i >= 2) wait(bar(kPbEmptyV + (i & 1)), (uint32_t)(((i - 2) >> 1) & 1));
+    int keys0 = 0, keys = 0, values = 0, q = 0;  // tiles whose parts, and items whose queries, are on the way
+    auto stop = [&]() {
       __syncwarp();
       gone = __any_sync(0xffffffffu, *s_abort != 0);
-      if (gone) break;
-      if (lane == 0) {
-        const uint32_t full = bar(kPbFullK + (i & 1));
-        mbar_expect_tx(full, 3 * kPreSlot);
-        if (i == 0) {
-          mbar_expect_tx(bar(kPbQ), 2 * kPreQTile);
-          for (int b = 0; b < 3; ++b)
-            tma_load_3d(sb + kPreQ + b * kPreRows * 128, &maps.q, 64 * b, h, (int)(q0 + r0), bar(kPbQ));
+      return gone;
+    };
+    while (!gone && walk.next(p, per, it)) {
+      for (int i = 0; i < it.nt && !gone; ++i, ++g) {
+        const int key = (int)(it.k0 + (int64_t)i * kPreKeys), s = g & 1;
+        auto dst = [&](int c) { return sb + kPreRing + ((5 * g + c) % kPreSlots) * kPreSlot; };
+        if (lane == 0) {
+          mbar_expect_tx(bar(kPbFullK0 + s), kPreSlot);
+          tma_load_3d(dst(0), &maps.k, 0, it.h, key, bar(kPbFullK0 + s));
         }
-        tma_load_3d(dst(0), &maps.k, 0, h, key, full);
-        tma_load_3d(dst(1), &maps.k, 64, h, key, full);
-        tma_load_2d(dst(2), &maps.pe, 0, key, full);
-        if (i == 0)
-          for (int b = 0; b < 3; ++b)
-            tma_load_3d(sb + kPreQ + kPreQTile + b * kPreRows * 128, &maps.q, 64 * b, h, (int)(q0 + r0 + kPreRows),
-                        bar(kPbQ));
+        ++keys0;
+        if (g >= 2) wait(bar(kPbEmptyV + s), (uint32_t)(((g - 2) >> 1) & 1));
+        if (stop()) break;
+        if (lane == 0) {
+          mbar_expect_tx(bar(kPbFullK + s), 2 * kPreSlot);
+          tma_load_3d(dst(1), &maps.k, 64, it.h, key, bar(kPbFullK + s));
+          tma_load_2d(dst(2), &maps.pe, 0, key, bar(kPbFullK + s));
+        }
+        ++keys;
+        if (i == 0) {
+          if (q > 0) wait(bar(kPbQEmpty), (uint32_t)((q - 1) & 1));
+          if (stop()) break;
+          if (lane == 0) {
+            mbar_expect_tx(bar(kPbQ), 2 * kPreQTile);
+            for (int t = 0; t < 2; ++t)
+              for (int b = 0; b < 3; ++b)
+                tma_load_3d(sb + kPreQ + t * kPreQTile + b * kPreRows * 128, &maps.q, 64 * b, it.h,
+                            (int)(it.q0 + it.r0 + t * kPreRows), bar(kPbQ));
+          }
+          ++q;
+        }
+        if (g >= 1) wait(bar(kPbEmptyK + (s ^ 1)), (uint32_t)(((g - 1) >> 1) & 1));
+        if (stop()) break;
+        if (lane == 0) {
+          mbar_expect_tx(bar(kPbFullV + s), 2 * kPreSlot);
+          tma_load_3d(dst(3), &maps.v, 0, it.h, key, bar(kPbFullV + s));
+          tma_load_3d(dst(4), &maps.v, 64, it.h, key, bar(kPbFullV + s));
+        }
+        ++values;
       }
-      ++keys;
-      if (i >= 1) wait(bar(kPbEmptyK + ((i - 1) & 1)), (uint32_t)(((i - 1) >> 1) & 1));
-      __syncwarp();
-      gone = __any_sync(0xffffffffu, *s_abort != 0);
-      if (gone) break;
-      if (lane == 0) {
-        const uint32_t full = bar(kPbFullV + (i & 1));
-        mbar_expect_tx(full, 2 * kPreSlot);
-        tma_load_3d(dst(3), &maps.v, 0, h, key, full);
-        tma_load_3d(dst(4), &maps.v, 64, h, key, full);
-      }
-      ++values;
     }
     // After a timeout: let the copies still in flight land before leaving.
     if (gone && lane == 0) {
-      for (int i = max(0, keys - 2); i < keys; ++i) mbar_wait_bounded(bar(kPbFullK + (i & 1)), (uint32_t)((i >> 1) & 1));
-      for (int i = max(0, values - 2); i < values; ++i)
-        mbar_wait_bounded(bar(kPbFullV + (i & 1)), (uint32_t)((i >> 1) & 1));
-      if (keys > 0) mbar_wait_bounded(bar(kPbQ), 0);
+      auto drain = [&](int b, int n) {
+        for (int i = max(0, n - 2); i < n; ++i) mbar_wait_bounded(bar(b + (i & 1)), (uint32_t)((i >> 1) & 1));
+      };
+      drain(kPbFullK0, keys0);
+      drain(kPbFullK, keys);
+      drain(kPbFullV, values);
+      if (q > 0) mbar_wait_bounded(bar(kPbQ), (uint32_t)((q - 1) & 1));
     }
   } else if (warp == 9) {
     // ---- products ----
@@ -215,178 +252,201 @@ __global__ void __launch_bounds__(kPreThreads, 1)
     const uint32_t id_o = idesc_bf16(kPreRows, kVDim, false, true), id_o64 = idesc_bf16(kPreRows, 64, false, true);
     const uint64_t d_q = smem_desc(sb + kPreQ, 16, 1024), d_k = smem_desc(sb + kPreRing, 16, 1024);
     const uint64_t d_v = smem_desc(sb + kPreRing, kPreSlot, 1024);
-    if (nt > 0) {
-      wait(bar(kPbQ), 0);
-      __syncwarp();
-    }
-    auto slot_of = [&](int i, int c) { return (5 * i + c) % kPreSlots; };
-    auto full_wait = [&](int b, int i) {
-      wait(bar(b + (i & 1)), (uint32_t)((i >> 1) & 1));
+    int q = 0, done0 = 0, done1 = 0;  // items; weights used of the two query tiles
+    auto slot_of = [&](int tile, int c) { return (5 * tile + c) % kPreSlots; };
+    auto full_wait = [&](int b, int tile) {
+      wait(bar(b + (tile & 1)), (uint32_t)((tile >> 1) & 1));
       __syncwarp();
       tc_fence_after();
     };
-    auto scores = [&](int t, int i) {
+    // S of query tile t against key tile `tile`; `fresh`: the first product to read these keys
+    auto scores = [&](int t, int tile, bool fresh) {
 #pragma unroll
       for (int c = 0; c < 3; ++c) {
+        if (fresh && c < 2) full_wait(c == 0 ? kPbFullK0 : kPbFullK, tile);
         const uint64_t a = d_q + (uint64_t)((t * kPreQTile + c * kPreRows * 128) >> 4);
-        const uint64_t b = d_k + (uint64_t)((slot_of(i, c) * kPreSlot) >> 4);
+        const uint64_t b = d_k + (uint64_t)((slot_of(tile, c) * kPreSlot) >> 4);
 #pragma unroll
         for (int ks = 0; ks < 4; ++ks)
           tc_mma(tmem + 128 * t, a + 2 * ks, b + 2 * ks, id_s, c + ks > 0);
       }
       tc_commit(bar(kPbS + t));
     };
-    auto values = [&](int t, int i) {
-      wait(bar(kPbP + t), (uint32_t)(i & 1));
+    // O of query tile t += its weights times the values of key tile `tile`
+    auto values = [&](int t, int tile, int& done, bool first) {
+      wait(bar(kPbP + t), (uint32_t)(done & 1));
+      ++done;
       __syncwarp();
       tc_fence_after();
-      const int s0 = slot_of(i, 3), s1 = slot_of(i, 4);
-      const uint32_t o = tmem + 256 + 128 * t, a = tmem + 128 * t;
+      const int s0 = slot_of(tile, 3), s1 = slot_of(tile, 4);
+      const uint32_t o = tmem + 256 + 128 * t, a = tmem + 128 * t, more = first ? 0u : 1u;
       const uint64_t b0 = d_v + (uint64_t)((s0 * kPreSlot) >> 4), b1 = d_v + (uint64_t)((s1 * kPreSlot) >> 4);
       if (s1 == s0 + 1) {  // the two 64-column blocks lie one slot apart: one operand of 128 columns
 #pragma unroll
         for (int ks = 0; ks < 8; ++ks)
-          tc_mma_ts(o, a + 8 * ks, b0 + (uint64_t)((ks * 2048) >> 4), id_o, i > 0 || ks > 0);
+          tc_mma_ts(o, a + 8 * ks, b0 + (uint64_t)((ks * 2048) >> 4), id_o, ks > 0 ? 1u : more);
       } else {
 #pragma unroll
         for (int ks = 0; ks < 8; ++ks) {
-          tc_mma_ts(o, a + 8 * ks, b0 + (uint64_t)((ks * 2048) >> 4), id_o64, i > 0 || ks > 0);
-          tc_mma_ts(o + 64, a + 8 * ks, b1 + (uint64_t)((ks * 2048) >> 4), id_o64, i > 0 || ks > 0);
+          tc_mma_ts(o, a + 8 * ks, b0 + (uint64_t)((ks * 2048) >> 4), id_o64, ks > 0 ? 1u : more);
+          tc_mma_ts(o + 64, a + 8 * ks, b1 + (uint64_t)((ks * 2048) >> 4), id_o64, ks > 0 ? 1u : more);
         }
       }
       tc_commit(bar(kPbPv + t));
     };
-    for (int i = 0; i < nt; ++i) {
-      full_wait(kPbFullK, i);
-      if (i < n0) scores(0, i);
-      if (i > 0) {
-        if (i - 1 < n1) values(1, i - 1);
-        tc_commit(bar(kPbEmptyV + ((i - 1) & 1)));
+    while (walk.next(p, per, it)) {
+      if (it.nt == 0) continue;
+      wait(bar(kPbQ), (uint32_t)(q & 1));
+      ++q;
+      __syncwarp();
+      for (int i = 0; i < it.nt; ++i) {
+        const int tile = g + i;
+        if (i < it.n0) scores(0, tile, true);
+        if (i > 0) {
+          if (i - 1 < it.n1) values(1, tile - 1, done1, i == 1);
+          tc_commit(bar(kPbEmptyV + ((tile - 1) & 1)));
+        }
+        if (i < it.n1) scores(1, tile, i >= it.n0);
+        tc_commit(bar(kPbEmptyK + (tile & 1)));
+        if (i + 1 == it.nt) tc_commit(bar(kPbQEmpty));
+        full_wait(kPbFullV, tile);
+        const int valid = it.lk - i * kPreKeys;
+        if (valid < kPreKeys) {
+          // rows behind the sequence take part with weight 0: they have to be finite
+          for (int c = 3; c < 5; ++c) {
+            unsigned char* rows = smem + kPreRing + slot_of(tile, c) * kPreSlot + valid * 128;
+            for (int x = lane; x < (kPreKeys - valid) * 8; x += 32)
+              reinterpret_cast<uint4*>(rows)[x] = make_uint4(0, 0, 0, 0);
+          }
+          fence_proxy_async_smem();
+          __syncwarp();
+        }
+        if (i < it.n0) values(0, tile, done0, i == 0);
       }
-      if (i < n1) scores(1, i);
-      tc_commit(bar(kPbEmptyK + (i & 1)));
-      full_wait(kPbFullV, i);
-      const int valid = lk - i * kPreKeys;
-      if (valid < kPreKeys) {
-        // rows behind the sequence take part with weight 0: they have to be finite
-        for (int c = 3; c < 5; ++c)
-          for (int x = lane; x < (kPreKeys - valid) * 8; x += 32)
-            reinterpret_cast<uint4*>(smem + kPreRing + slot_of(i, c) * kPreSlot + valid * 128)[x] = make_uint4(0, 0, 0, 0);
-        fence_proxy_async_smem();
-        __syncwarp();
-      }
-      if (i < n0) values(0, i);
+      g += it.nt;
+      if (it.nt - 1 < it.n1) values(1, g - 1, done1, it.nt == 1);
+      tc_commit(bar(kPbEmptyV + ((g - 1) & 1)));
     }
-    if (nt > 0 && nt - 1 < n1) values(1, nt - 1);
     // the last products complete before tensor memory is freed
-    if (n0 > 0) mbar_wait_bounded(bar(kPbPv), (uint32_t)((n0 - 1) & 1));
-    if (n1 > 0) mbar_wait_bounded(bar(kPbPv + 1), (uint32_t)((n1 - 1) & 1));
+    if (done0 > 0) mbar_wait_bounded(bar(kPbPv), (uint32_t)((done0 - 1) & 1));
+    if (done1 > 0) mbar_wait_bounded(bar(kPbPv + 1), (uint32_t)((done1 - 1) & 1));
   } else {
     // ---- softmax and output: thread = row of tile t ----
     const int t = warp >> 2, q = warp & 3;
-    const int n = t == 0 ? n0 : n1;
-    const int row = r0 + t * kPreRows + q * 32 + lane;  // query within the sequence
-    const int lim = p.causal ? min(lk, row + lk - lq + 1) : lk;
-    const int lim_first = p.causal ? min(lk, row - lane + lk - lq + 1) : lk;  // the warp's first row's
     const uint32_t lane_base = (uint32_t)(q * 32) << 16;
     const uint32_t t_s = tmem + lane_base + 128 * t, t_o = tmem + lane_base + 256 + 128 * t;
     const float sl = p.scale_log2;
     const f32x2 sl2 = f2(sl, sl);
-    float m = -INFINITY, l = 0.f;  // maximum (times scale, log2) and sum
-    for (int i = 0; i < n; ++i) {
-      wait(bar(kPbS + t), (uint32_t)(i & 1));
-      __syncwarp();
-      tc_fence_after();
-      float s[128];
+    int done = 0;  // scores used
+    while (walk.next(p, per, it)) {
+      const int n = t == 0 ? it.n0 : it.n1;
+      const int row = it.r0 + t * kPreRows + q * 32 + lane;  // query within the sequence
+      const int lim = p.causal ? min(it.lk, row + it.lk - it.lq + 1) : it.lk;
+      const int lim_first = p.causal ? min(it.lk, row - lane + it.lk - it.lq + 1) : it.lk;  // the warp's first row's
+      float m = -INFINITY, l = 0.f;  // maximum (times scale, log2) and sum
+      for (int i = 0; i < n; ++i, ++done) {
+        wait(bar(kPbS + t), (uint32_t)(done & 1));
+        __syncwarp();
+        tc_fence_after();
+        float s[128];
 #pragma unroll
-      for (int c = 0; c < 4; ++c) tc_ld32_nowait(t_s + 32 * c, s + 32 * c);
-      tc_ld_wait();
-      if ((i + 1) * kPreKeys > lim_first) {
-        const int rem = lim - i * kPreKeys;
+        for (int c = 0; c < 4; ++c) tc_ld32_nowait(t_s + 32 * c, s + 32 * c);
+        tc_ld_wait();
+        if ((i + 1) * kPreKeys > lim_first) {
+          const int rem = lim - i * kPreKeys;
 #pragma unroll
-        for (int c = 0; c < 128; ++c)
-          if (c >= rem) s[c] = -INFINITY;
-      }
-      float mx[4] = {s[0], s[1], s[2], s[3]};
-#pragma unroll
-      for (int c = 4; c < 124; c += 8)
-#pragma unroll
-        for (int e = 0; e < 4; ++e) mx[e] = max3(mx[e], s[c + 2 * e], s[c + 2 * e + 1]);
-      mx[0] = max3(mx[0], s[124], s[125]);
-      mx[1] = max3(mx[1], s[126], s[127]);
-      const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * sl;
-      if (__any_sync(0xffffffffu, top > m + kPreSlack)) {
-        float f = 1.0f;
-        if (top > m + kPreSlack) {
-          f = ex2(m - top);
-          m = top;
-          l *= f;
+          for (int c = 0; c < 128; ++c)
+            if (c >= rem) s[c] = -INFINITY;
         }
-        if (i > 0) {
-          wait(bar(kPbPv + t), (uint32_t)((i - 1) & 1));
-          __syncwarp();
-          tc_fence_after();
-#pragma unroll 1
-          for (int c = 0; c < 128; c += 16) {
-            float o[16];
-            tc_ld16(t_o + c, o);
+        float mx[4] = {s[0], s[1], s[2], s[3]};
 #pragma unroll
-            for (int e = 0; e < 16; ++e) o[e] *= f;
-            tc_st16(t_o + c, o);
+        for (int c = 4; c < 124; c += 8)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) mx[e] = max3(mx[e], s[c + 2 * e], s[c + 2 * e + 1]);
+        mx[0] = max3(mx[0], s[124], s[125]);
+        mx[1] = max3(mx[1], s[126], s[127]);
+        const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * sl;
+        if (__any_sync(0xffffffffu, top > m + kPreSlack)) {
+          float f = 1.0f;
+          if (top > m + kPreSlack) {
+            f = ex2(m - top);
+            m = top;
+            l *= f;
+          }
+          if (i > 0) {
+            wait(bar(kPbPv + t), (uint32_t)((done - 1) & 1));
+            __syncwarp();
+            tc_fence_after();
+#pragma unroll 1
+            for (int c = 0; c < 128; c += 16) {
+              float o[16];
+              tc_ld16(t_o + c, o);
+#pragma unroll
+              for (int e = 0; e < 16; ++e) o[e] *= f;
+              tc_st16(t_o + c, o);
+            }
+          }
+        }
+        const float base = m == -INFINITY ? 0.f : -m;
+        const f32x2 base2 = f2(base, base);
+        f32x2 sum[2] = {f2(0.f, 0.f), f2(0.f, 0.f)};
+#pragma unroll
+        for (int c = 0; c < 128; c += 32) {
+          float w[16];  // 32 weights as bf16 pairs (the operand type; the sum is taken before the rounding)
+#pragma unroll
+          for (int e = 0; e < 16; ++e) {
+            const float2 x = f2u(fma2(f2(s[c + 2 * e], s[c + 2 * e + 1]), sl2, base2));
+            const float a = ex2(x.x), b = ex2(x.y);
+            sum[e & 1] = add2(sum[e & 1], f2(a, b));
+            w[e] = __uint_as_float(pack_bf16(a, b));
+          }
+          tc_st16(t_s + c / 2, w);
+        }
+        tc_st_wait();
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(bar(kPbP + t));
+        const float2 z = f2u(add2(sum[0], sum[1]));
+        l += z.x + z.y;
+      }
+      // ---- this row ----
+      if (n > 0) {
+        wait(bar(kPbPv + t), (uint32_t)((done - 1) & 1));
+        __syncwarp();
+        tc_fence_after();
+      }
+      const float inv = l > 0.f ? 1.0f / l : (l == 0.f ? 0.f : l);
+      const int64_t at = (it.q0 + row) * p.H + it.h;
+#pragma unroll 1
+      for (int c = 0; c < 128; c += 64) {
+        float o[64];
+        if (n > 0) {
+          tc_ld32_nowait(t_o + c, o);
+          tc_ld32_nowait(t_o + c + 32, o + 32);
+          tc_ld_wait();
+        } else {
+#pragma unroll
+          for (int e = 0; e < 64; ++e) o[e] = 0.f;
+        }
+        if (row < it.lq) {
+          // whole 32-byte sectors: a 16-byte store of a row alone would write halves of them
+          uint16_t* dst = p.out + at * kVDim + c;
+#pragma unroll
+          for (int e = 0; e < 64; e += 16) {
+            uint32_t w[8];
+#pragma unroll
+            for (int x = 0; x < 8; ++x) w[x] = pack_bf16(o[e + 2 * x] * inv, o[e + 2 * x + 1] * inv);
+            asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};\n" ::"l"(dst + e), "r"(w[0]),
+                         "r"(w[1]), "r"(w[2]), "r"(w[3]), "r"(w[4]), "r"(w[5]), "r"(w[6]), "r"(w[7])
+                         : "memory");
           }
         }
       }
-      const float base = m == -INFINITY ? 0.f : -m;
-      const f32x2 base2 = f2(base, base);
-      f32x2 sum[2] = {f2(0.f, 0.f), f2(0.f, 0.f)};
-#pragma unroll
-      for (int c = 0; c < 128; c += 32) {
-        float w[16];  // 32 weights as bf16 pairs (the operand type; the sum is taken before the rounding)
-#pragma unroll
-        for (int e = 0; e < 16; ++e) {
-          const float2 x = f2u(fma2(f2(s[c + 2 * e], s[c + 2 * e + 1]), sl2, base2));
-          const float a = ex2(x.x), b = ex2(x.y);
-          sum[e & 1] = add2(sum[e & 1], f2(a, b));
-          w[e] = __uint_as_float(pack_bf16(a, b));
-        }
-        tc_st16(t_s + c / 2, w);
-      }
-      tc_st_wait();
+      if (p.lse && row < it.lq) p.lse[at] = l == 0.f ? -INFINITY : (m + __log2f(l)) * 0.6931471805599453f;
       tc_fence_before();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(bar(kPbP + t));
-      const float2 z = f2u(add2(sum[0], sum[1]));
-      l += z.x + z.y;
     }
-    // ---- this row ----
-    if (n > 0) {
-      wait(bar(kPbPv + t), (uint32_t)((n - 1) & 1));
-      __syncwarp();
-      tc_fence_after();
-    }
-    const float inv = l > 0.f ? 1.0f / l : (l == 0.f ? 0.f : l);
-    const int64_t at = (q0 + row) * p.H + h;
-#pragma unroll 1
-    for (int c = 0; c < 128; c += 32) {
-      float o[32];
-      if (n > 0) {
-        tc_ld32(t_o + c, o);
-      } else {
-#pragma unroll
-        for (int e = 0; e < 32; ++e) o[e] = 0.f;
-      }
-      if (row < lq) {
-        uint4* dst = reinterpret_cast<uint4*>(p.out + at * kVDim + c);
-#pragma unroll
-        for (int e = 0; e < 4; ++e)
-          dst[e] = make_uint4(pack_bf16(o[8 * e] * inv, o[8 * e + 1] * inv), pack_bf16(o[8 * e + 2] * inv, o[8 * e + 3] * inv),
-                              pack_bf16(o[8 * e + 4] * inv, o[8 * e + 5] * inv),
-                              pack_bf16(o[8 * e + 6] * inv, o[8 * e + 7] * inv));
-      }
-    }
-    if (p.lse && row < lq) p.lse[at] = l == 0.f ? -INFINITY : (m + __log2f(l)) * 0.6931471805599453f;
-    tc_fence_before();
   }
+  tc_fence_before();
   __syncthreads();
   tc_fence_after();
   if (warp == 9)
@@ -415,8 +475,10 @@ bool launch_latent_prefill(const PrefillParams& p, cudaStream_t s) {
   });
   if (rc[dev] != cudaSuccess) return false;
   const int64_t per = (p.Tq + kPrefillRows - 1) / kPrefillRows;
-  const int64_t blocks = (p.cu_q ? p.Tq / kPrefillRows + p.N : p.B * per) * p.H;
-  if (blocks > INT32_MAX) return false;
+  const int64_t items = (p.items ? p.Tq / kPrefillRows + p.N : p.B * per) * p.H;
+  if (items > INT32_MAX) return false;
+  int sms = 0;
+  if (cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess || sms < 1) return false;
   PrefillMaps maps;
   memset(&maps, 0, sizeof(maps));
   if (!head_map(&maps.q, p.q, kQkDim, p.H, p.B * p.Tq, p.q_st, p.q_sh, kPreRows)) return false;
@@ -430,8 +492,18 @@ bool launch_latent_prefill(const PrefillParams& p, cudaStream_t s) {
         !encode_map_bf16(&maps.pe, p.k_pe, 2, dims, strides, box))
       return false;
   }
-  kda_latent_prefill_kernel<<<(unsigned)blocks, kPreThreads, kPreSmem, s>>>(p, per, maps);
-  return true;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)std::min<int64_t>(items, sms));
+  cfg.blockDim = dim3(kPreThreads);
+  cfg.dynamicSmemBytes = kPreSmem;
+  cfg.stream = s;
+  // packed: set up while the list of blocks is made
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = p.items ? 1 : 0;
+  return cudaLaunchKernelEx(&cfg, kda_latent_prefill_kernel, p, per, maps) == cudaSuccess;
 }
 
 }  // namespace kda
