@@ -317,7 +317,8 @@ __device__ __forceinline__ int work_class(int tiles) {
 }
 
 __global__ void __launch_bounds__(1024) kda_latent_blocks_kernel(const int64_t* cu_q, const int64_t* cu_k, int64_t N,
-                                                                 int64_t Tq, int64_t Tk, int causal, PrefillItem* items,
+                                                                 int64_t Tq, int64_t Tk, int causal, int rows,
+                                                                 PrefillItem* items,
                                                                  int32_t* count, int* status) {
   __shared__ int32_t at[kWorkClasses];
   asm volatile("griddepcontrol.launch_dependents;\n" ::: "memory");
@@ -340,11 +341,11 @@ __global__ void __launch_bounds__(1024) kda_latent_blocks_kernel(const int64_t* 
       it.k0 = (int)cu_k[n];
       it.lk = (int)(cu_k[n + 1] - cu_k[n]);
       it.pad[0] = it.pad[1] = it.pad[2] = 0;
-      for (int64_t r = (int64_t)lane * kPrefillRows; r < it.lq; r += 32 * kPrefillRows) {
+      for (int64_t r = (int64_t)lane * rows; r < it.lq; r += 32 * rows) {
         it.r0 = (int)r;
         int tiles = 0;
         for (int t = 0; t < 2; ++t) {
-          const int first = it.r0 + t * (kPrefillRows / 2), last = min(it.lq, first + kPrefillRows / 2) - 1;
+          const int first = it.r0 + t * (rows / 2), last = min(it.lq, first + rows / 2) - 1;
           if (first < it.lq) tiles += (max(0, causal ? min(it.lk, last + it.lk - it.lq + 1) : it.lk) + 127) / 128;
         }
         const int where = atomicAdd(&at[work_class(tiles)], 1);
@@ -485,12 +486,13 @@ extern "C" int kda_latent_prefill(const kda_latent_prefill_args* a, void* worksp
   p.N = a->N;
   p.H = (int)a->H;
   p.causal = (a->flags & KDA_LATENT_CAUSAL) ? 1 : 0;
+  p.pairs = prefill_pairs(a->B * a->Tq, a->N) ? 1 : 0;
   p.status = status;
   if (a->cu_seqlens_q) {
     int32_t* count = static_cast<int32_t*>(workspace);
     PrefillItem* items = reinterpret_cast<PrefillItem*>(static_cast<unsigned char*>(workspace) + 256);
-    kda_latent_blocks_kernel<<<1, 1024, 0, s>>>(a->cu_seqlens_q, a->cu_seqlens_k, a->N, a->Tq, a->Tk, p.causal, items,
-                                                count, status);
+    kda_latent_blocks_kernel<<<1, 1024, 0, s>>>(a->cu_seqlens_q, a->cu_seqlens_k, a->N, a->Tq, a->Tk, p.causal,
+                                                p.pairs ? 2 * kPrefillRows : kPrefillRows, items, count, status);
     p.items = items;
     p.count = count;
   }

@@ -51,10 +51,14 @@ struct PrefillParams {
   int64_t B, Tq, Tk, N;
   int H;
   int causal;
+  int pairs;                        // CTA pairs and items of 2 kPrefillRows rows
   int* status;
 };
 
-// Query rows of one work item of the expanded form.
+// Whether `rows` queries of `sequences` sequences go to CTA pairs.
+bool prefill_pairs(int64_t rows, int64_t sequences);
+
+// Query rows of one work item of the expanded form (of single CTAs).
 constexpr int kPrefillRows = 256;
 
 size_t decode_workspace_bytes(const DecodeParams& p);

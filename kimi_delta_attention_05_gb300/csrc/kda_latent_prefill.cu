@@ -26,9 +26,17 @@
 // own, as its slot is free a product earlier than the others'.  Tensor memory: S0, S1,
 // O0, O1, 128 columns each.
 //
+// What bounds this is shared memory: each 128 x 128 x 16 product of S reads 8 KB
+// of operands, about 78 cycles of its bandwidth against 64 of arithmetic.  So
+// long sequences go to the paired form: two CTAs on neighbouring SMs share one
+// product of 256 rows (cta_group::2), each holds its own 128 query rows of a
+// tile and half of every key and value tile, and an operand of 6 KB is read in
+// its place; loads from L2 halve too.  Items are then 512 rows, whose causal
+// edge wastes more, so short sequences keep single CTAs.
+//
 // Roles: warps 0-3 and 4-7 softmax and output of the two tiles, warp 8 copies,
-// warp 9 products.  Every wait is bounded; a CTA that gives up sets the status
-// word.
+// warp 9 products (of the pair: in its first CTA).  Every wait is bounded; a CTA
+// that gives up sets the status word.
 #include <algorithm>
 #include <cstring>
 
@@ -38,24 +46,32 @@
 
 namespace kda {
 
-constexpr int kPreRows = 128;                    // query rows of a tile
+constexpr int kPreRows = 128;                    // query rows of a tile in one CTA
 constexpr int kPreKeys = 128;                    // keys of a tile
-constexpr int kPreSlots = 8;
-constexpr int kPreSlot = kPreKeys * 128;         // [128 keys][64 channels] bf16
 constexpr int kPreQ = 0;                         // two tiles of three [128 rows][64 channels] blocks
 constexpr int kPreQTile = 3 * kPreRows * 128;
-constexpr int kPreRing = 2 * kPreQTile;
-constexpr int kPreBar = kPreRing + kPreSlots * kPreSlot;
+constexpr int kPreRing = 2 * kPreQTile;          // key and value blocks
+constexpr int kPreThreads = 320;
+constexpr float kPreSlack = 8.0f;                // log2 growth of a maximum that is let pass
+// single CTAs: ring of [128 keys][64 channels] slots
+constexpr int kPreSlots = 8;
+constexpr int kPreSlot = kPreKeys * 128;
+// pairs: stages of this CTA's 64 keys (three blocks) and its 64 value channels of 128 keys
+constexpr int kPairStages = 3;
+constexpr int kPairK = 64 * 128;                 // a key block
+constexpr int kPairStage = 3 * kPairK + kPreSlot;
+constexpr int kPreBar = kPreRing + (kPreSlots * kPreSlot > kPairStages * kPairStage ? kPreSlots * kPreSlot
+                                                                                    : kPairStages * kPairStage);
 // full and empty of a tile's first key block, other key blocks and value blocks
 // (by the tile's parity), q full and empty, sfull[2], pready[2], pvdone[2]
 constexpr int kPbFullK0 = 0, kPbFullK = 2, kPbFullV = 4, kPbEmptyK = 6, kPbEmptyV = 8, kPbQ = 10, kPbQEmpty = 11,
-              kPbS = 12, kPbP = 14, kPbPv = 16, kPbars = 18;
+              kPbS = 12, kPbP = 14, kPbPv = 16;
+// pairs: by stage; then a barrier for value tiles that end behind the sequence
+constexpr int kPpFullK = 18, kPpFullV = 21, kPpEmptyK = 24, kPpEmptyV = 27, kPpTail = 30, kPbars = 31;
 constexpr int kPreTmem = kPreBar + 8 * kPbars;
 constexpr int kPreAbort = kPreTmem + 8;
 constexpr int kPreSmem = kPreAbort + 8;
-constexpr int kPreThreads = 320;
-constexpr float kPreSlack = 8.0f;                // log2 growth of a maximum that is let pass
-static_assert(kPreRing % 1024 == 0 && kPreSmem <= 232448, "shared memory");
+static_assert(kPreRing % 1024 == 0 && kPairStage % 1024 == 0 && kPreSmem <= 232448, "shared memory");
 
 struct PrefillMaps {
   CUtensorMap q, k, pe, v;
@@ -99,17 +115,20 @@ struct PreItem {
   int n0, n1, nt;    // key tiles of the two query tiles (0 where a tile has no row or its rows see nothing)
 };
 
-// The items of a CTA: every grid-th of the list (most work first), each second
-// round backwards, so that the work of all CTAs is nearly the same.
+// The items of a CTA or pair: every grid-th of the list (most work first), each
+// second round backwards, so that the work of all is nearly the same.
+template <bool kPair>
 struct PreWalk {
+  static constexpr int kTileRows = kPair ? 2 * kPreRows : kPreRows;
   int64_t round, total;
   __device__ __forceinline__ void start(const PrefillParams& p, int64_t blocks) {
     round = 0;
     total = (p.items ? (int64_t)*p.count : blocks) * p.H;
   }
   __device__ __forceinline__ bool next(const PrefillParams& p, int64_t per, PreItem& it) {
-    const int64_t base = round * gridDim.x;
-    const int64_t idx = base + ((round & 1) ? gridDim.x - 1 - blockIdx.x : blockIdx.x);
+    const int64_t wide = kPair ? gridDim.x >> 1 : gridDim.x, mine = kPair ? blockIdx.x >> 1 : blockIdx.x;
+    const int64_t base = round * wide;
+    const int64_t idx = base + ((round & 1) ? wide - 1 - mine : mine);
     ++round;
     if (base >= total || idx >= total) return false;  // (only the last round is not full)
     if (p.items) {
@@ -129,12 +148,12 @@ struct PreWalk {
       it.k0 = (int64_t)n * p.Tk;
       it.lq = (int)p.Tq;
       it.lk = (int)p.Tk;
-      it.r0 = (int)(per - 1 - back) * kPrefillRows;
+      it.r0 = (int)(per - 1 - back) * 2 * kTileRows;
     }
     auto tiles_of = [&](int t) {
-      const int first = it.r0 + t * kPreRows;
+      const int first = it.r0 + t * kTileRows;
       if (first >= it.lq) return 0;
-      const int last = min(it.lq, first + kPreRows) - 1;
+      const int last = min(it.lq, first + kTileRows) - 1;
       const int seen = p.causal ? min(it.lk, last + it.lk - it.lq + 1) : it.lk;
       return seen > 0 ? (seen + kPreKeys - 1) / kPreKeys : 0;
     };
@@ -145,6 +164,7 @@ struct PreWalk {
   }
 };
 
+template <bool kPair>
 __global__ void __launch_bounds__(kPreThreads, 1)
     kda_latent_prefill_kernel(const PrefillParams p, int64_t per, const __grid_constant__ PrefillMaps maps) {
   extern __shared__ __align__(1024) unsigned char smem[];
@@ -152,15 +172,26 @@ __global__ void __launch_bounds__(kPreThreads, 1)
   const uint32_t sb = smem_u32(smem), bars = sb + kPreBar;
   auto bar = [&](int i) { return bars + 8 * i; };
   volatile int* s_abort = reinterpret_cast<volatile int*>(smem + kPreAbort);
+  const uint32_t rank = kPair ? cta_rank() : 0;
   if (tid == 0) {
-    for (int i = 0; i < kPbars; ++i) mbar_init(bar(i), (i == kPbP || i == kPbP + 1) ? 4 : 1);
+    for (int i = 0; i < kPbars; ++i) {
+      uint32_t n = 1;
+      if (i == kPbP || i == kPbP + 1) n = kPair ? 8 : 4;                             // the softmax warps of a tile
+      if (kPair && (i == kPbQ || (i >= kPpFullK && i < kPpFullK + 2 * kPairStages))) n = 2;  // both CTAs' copies
+      mbar_init(bar(i), n);
+    }
     *s_abort = (sb & 1023) ? 1 : 0;
     if (sb & 1023) atomicExch(p.status, KDA_ERR_DEVICE_TIMEOUT);
     asm volatile("fence.mbarrier_init.release.cluster;\n" ::: "memory");
   }
   if (warp == 9) {
-    asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;\n" ::"r"(sb + kPreTmem), "r"(512u));
-    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;\n");
+    if constexpr (kPair) {
+      asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;\n" ::"r"(sb + kPreTmem), "r"(512u));
+      asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;\n");
+    } else {
+      asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;\n" ::"r"(sb + kPreTmem), "r"(512u));
+      asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;\n");
+    }
   }
   if (warp == 8 && lane == 0) {
     prefetch_map(&maps.q);
@@ -171,6 +202,7 @@ __global__ void __launch_bounds__(kPreThreads, 1)
   asm volatile("griddepcontrol.wait;\n" ::: "memory");  // (packed: the list of blocks)
   tc_fence_before();
   __syncthreads();
+  if (kPair) cluster_sync();  // the other CTA's barriers are ready too
   tc_fence_after();
   const uint32_t tmem = *reinterpret_cast<volatile uint32_t*>(smem + kPreTmem);
   auto wait = [&](uint32_t b, uint32_t parity) {
@@ -180,12 +212,164 @@ __global__ void __launch_bounds__(kPreThreads, 1)
       *s_abort = 1;
     }
   };
-  PreWalk walk;
+  // barriers that the issuing CTA waits on, as both CTAs' copies and warps reach them
+  auto lead = [&](int i) { return kPair ? map_rank(bar(i), 0) : bar(i); };
+  PreWalk<kPair> walk;
   walk.start(p, p.B * per);
   PreItem it;
   int g = 0;  // key tiles so far, over all items
 
-  if (warp == 8) {
+  if (kPair && warp == 8) {
+    // ---- copies of a pair: this CTA's half of the keys and of the value channels, its query rows ----
+    bool gone = false;
+    int keys = 0, values = 0, tails = 0, q = 0;  // tiles and items on the way
+    auto stop = [&]() {
+      __syncwarp();
+      gone = __any_sync(0xffffffffu, *s_abort != 0);
+      return gone;
+    };
+    int s = 0;
+    uint32_t ph = 1;  // parity of the stage's use before
+    while (!gone && walk.next(p, per, it)) {
+      for (int i = 0; i < it.nt && !gone; ++i, ++g) {
+        const int key = (int)(it.k0 + (int64_t)i * kPreKeys);
+        const uint32_t dst = sb + kPreRing + s * kPairStage;
+        if (g >= kPairStages) wait(bar(kPpEmptyK + s), ph);
+        if (stop()) break;
+        if (lane == 0) {
+          const uint32_t full = lead(kPpFullK + s);
+          const int own = key + 64 * (int)rank;
+          mbar_expect_tx_cluster(full, 3 * kPairK);
+          tma_pair_3d(dst, &maps.k, 0, it.h, own, full);
+          tma_pair_3d(dst + kPairK, &maps.k, 64, it.h, own, full);
+          tma_pair_2d(dst + 2 * kPairK, &maps.pe, 0, own, full);
+        }
+        ++keys;
+        if (i == 0) {
+          if (q > 0) wait(bar(kPbQEmpty), (uint32_t)((q - 1) & 1));
+          if (stop()) break;
+          if (lane == 0) {
+            const uint32_t full = lead(kPbQ);
+            mbar_expect_tx_cluster(full, 2 * kPreQTile);
+            for (int t = 0; t < 2; ++t)
+              for (int b = 0; b < 3; ++b)
+                tma_pair_3d(sb + kPreQ + t * kPreQTile + b * kPreRows * 128, &maps.q, 64 * b, it.h,
+                            (int)(it.q0 + it.r0 + (2 * t + (int)rank) * kPreRows), full);
+          }
+          ++q;
+        }
+        if (g >= kPairStages) wait(bar(kPpEmptyV + s), ph);
+        if (stop()) break;
+        const int valid = it.lk - i * kPreKeys;
+        const uint32_t full = lead(kPpFullV + s);
+        if (valid >= kPreKeys) {
+          if (lane == 0) {
+            mbar_expect_tx_cluster(full, kPreSlot);
+            tma_pair_3d(dst + 3 * kPairK, &maps.v, 64 * (int)rank, it.h, key, full);
+          }
+        } else {
+          // rows behind the sequence take part with weight 0: they have to be finite.  The tile
+          // lands on a barrier of this CTA's own, is cleared, and only then handed over
+          if (lane == 0) {
+            mbar_expect_tx(bar(kPpTail), kPreSlot);
+            tma_load_3d(dst + 3 * kPairK, &maps.v, 64 * (int)rank, it.h, key, bar(kPpTail));
+          }
+          ++tails;
+          wait(bar(kPpTail), (uint32_t)((tails - 1) & 1));
+          if (stop()) break;
+          unsigned char* rows = smem + kPreRing + s * kPairStage + 3 * kPairK + valid * 128;
+          for (int x = lane; x < (kPreKeys - valid) * 8; x += 32)
+            reinterpret_cast<uint4*>(rows)[x] = make_uint4(0, 0, 0, 0);
+          fence_proxy_async_smem();
+          __syncwarp();
+          if (lane == 0) mbar_arrive_cluster(full);
+        }
+        ++values;
+        if (++s == kPairStages) {
+          s = 0;
+          ph ^= 1u;
+        }
+      }
+    }
+    // After a timeout: copies still in flight land in memory of this CTA, which stays until
+    // the cluster's last barrier; they are few and unconditional, so a bounded pause is enough.
+    if (gone && lane == 0) {
+      if (tails > 0) mbar_wait_bounded(bar(kPpTail), (uint32_t)((tails - 1) & 1));
+      const long long t0 = clock64();
+      while (clock64() - t0 < (1LL << 22)) {
+      }
+    }
+  } else if (kPair && warp == 9) {
+    // ---- products of the pair, issued by its first CTA ----
+    if (rank == 0) {
+      const uint32_t id_s = idesc_bf16(2 * kPreRows, kPreKeys, false, false);
+      const uint32_t id_o = idesc_bf16(2 * kPreRows, kVDim, false, true);
+      const uint64_t d_q = smem_desc(sb + kPreQ, 16, 1024), d_k = smem_desc(sb + kPreRing, 16, 1024);
+      const uint64_t d_v = smem_desc(sb + kPreRing + 3 * kPairK, 16, 1024);
+      auto wait_pair = [&](uint32_t b, uint32_t parity) {  // (acquires the other CTA's writes too)
+        if (!mbar_try_wait_cluster(b, parity)) {
+          const long long t0 = clock64();
+          while (!*s_abort && !mbar_try_wait_cluster(b, parity))
+            if (clock64() - t0 > (1LL << 31)) {
+              atomicExch(p.status, KDA_ERR_DEVICE_TIMEOUT);
+              *s_abort = 1;
+            }
+        }
+        __syncwarp();
+        tc_fence_after();
+      };
+      int q = 0, done0 = 0, done1 = 0;
+      int s = 0, s_prev = 0;     // stage of this key tile and of the one before
+      uint32_t ph = 0;
+      auto scores = [&](int t) {
+        const uint64_t a = d_q + (uint64_t)((t * kPreQTile) >> 4), b = d_k + (uint64_t)((s * kPairStage) >> 4);
+#pragma unroll
+        for (int c = 0; c < 3; ++c)
+#pragma unroll
+          for (int ks = 0; ks < 4; ++ks)
+            tc_mma_pair(tmem + 128 * t, a + (uint64_t)((c * kPreRows * 128 + ks * 32) >> 4),
+                        b + (uint64_t)((c * kPairK + ks * 32) >> 4), id_s, c + ks > 0);
+        tc_commit_pair(bar(kPbS + t));
+      };
+      auto values = [&](int t, int stage, int& done, bool first) {
+        wait_pair(bar(kPbP + t), (uint32_t)(done & 1));
+        ++done;
+        const uint64_t b = d_v + (uint64_t)((stage * kPairStage) >> 4);
+        const uint32_t o = tmem + 256 + 128 * t, a = tmem + 128 * t, more = first ? 0u : 1u;
+#pragma unroll
+        for (int ks = 0; ks < 8; ++ks)
+          tc_mma_ts_pair(o, a + 8 * ks, b + (uint64_t)((ks * 2048) >> 4), id_o, ks > 0 ? 1u : more);
+        tc_commit_pair(bar(kPbPv + t));
+      };
+      while (walk.next(p, per, it)) {
+        if (it.nt == 0) continue;
+        wait_pair(bar(kPbQ), (uint32_t)(q & 1));
+        ++q;
+        for (int i = 0; i < it.nt; ++i) {
+          wait_pair(bar(kPpFullK + s), ph);
+          if (i < it.n0) scores(0);
+          if (i > 0) {
+            if (i - 1 < it.n1) values(1, s_prev, done1, i == 1);
+            tc_commit_pair(bar(kPpEmptyV + s_prev));
+          }
+          if (i < it.n1) scores(1);
+          tc_commit_pair(bar(kPpEmptyK + s));
+          if (i + 1 == it.nt) tc_commit_pair(bar(kPbQEmpty));
+          wait_pair(bar(kPpFullV + s), ph);
+          if (i < it.n0) values(0, s, done0, i == 0);
+          s_prev = s;
+          if (++s == kPairStages) {
+            s = 0;
+            ph ^= 1u;
+          }
+        }
+        if (it.nt - 1 < it.n1) values(1, s_prev, done1, it.nt == 1);
+        tc_commit_pair(bar(kPpEmptyV + s_prev));
+      }
+      if (done0 > 0) mbar_wait_bounded(bar(kPbPv), (uint32_t)((done0 - 1) & 1));
+      if (done1 > 0) mbar_wait_bounded(bar(kPbPv + 1), (uint32_t)((done1 - 1) & 1));
+    }
+  } else if (warp == 8) {
     // ---- copies.  Key tile g's five slots (two key blocks, pe, two value blocks) start at
     //      slot 5 g % 8: its first key block follows the last one of tile g - 2 (free where the
     //      values of g - 1 could be sent), its other two the values of g - 2, its values the keys
@@ -340,7 +524,7 @@ __global__ void __launch_bounds__(kPreThreads, 1)
     int done = 0;  // scores used
     while (walk.next(p, per, it)) {
       const int n = t == 0 ? it.n0 : it.n1;
-      const int row = it.r0 + t * kPreRows + q * 32 + lane;  // query within the sequence
+      const int row = it.r0 + (kPair ? 2 * t + (int)rank : t) * kPreRows + q * 32 + lane;  // query within the sequence
       const int lim = p.causal ? min(it.lk, row + it.lk - it.lq + 1) : it.lk;
       const int lim_first = p.causal ? min(it.lk, row - lane + it.lk - it.lq + 1) : it.lk;  // the warp's first row's
       float m = -INFINITY, l = 0.f;  // maximum (times scale, log2) and sum
@@ -405,7 +589,10 @@ __global__ void __launch_bounds__(kPreThreads, 1)
         tc_st_wait();
         tc_fence_before();
         __syncwarp();
-        if (lane == 0) mbar_arrive(bar(kPbP + t));
+        if (lane == 0) {
+          if (kPair) mbar_arrive_cluster(lead(kPbP + t));
+          else mbar_arrive(bar(kPbP + t));
+        }
         const float2 z = f2u(add2(sum[0], sum[1]));
         l += z.x + z.y;
       }
@@ -448,9 +635,14 @@ __global__ void __launch_bounds__(kPreThreads, 1)
   }
   tc_fence_before();
   __syncthreads();
+  if (kPair) cluster_sync();  // nothing of this pair reaches a CTA that has left
   tc_fence_after();
-  if (warp == 9)
-    asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;\n" ::"r"(tmem), "r"(512u));
+  if (warp == 9) {
+    if constexpr (kPair)
+      asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;\n" ::"r"(tmem), "r"(512u));
+    else
+      asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;\n" ::"r"(tmem), "r"(512u));
+  }
 }
 
 namespace {
@@ -463,47 +655,63 @@ bool head_map(CUtensorMap* m, const uint16_t* base, int d, int64_t H, int64_t to
   return encode_map_bf16(m, base, 3, dims, strides, box);
 }
 
-}  // namespace
-
-bool launch_latent_prefill(const PrefillParams& p, cudaStream_t s) {
+template <bool kPair>
+bool launch_prefill(const PrefillParams& p, cudaStream_t s) {
   static std::once_flag once[64];
   static cudaError_t rc[64];
-  int dev = 0;
+  int dev = 0, sms = 0;
   if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return false;
   std::call_once(once[dev], [&] {
-    rc[dev] = cudaFuncSetAttribute(kda_latent_prefill_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kPreSmem);
+    rc[dev] = cudaFuncSetAttribute(kda_latent_prefill_kernel<kPair>, cudaFuncAttributeMaxDynamicSharedMemorySize, kPreSmem);
   });
   if (rc[dev] != cudaSuccess) return false;
-  const int64_t per = (p.Tq + kPrefillRows - 1) / kPrefillRows;
-  const int64_t items = (p.items ? p.Tq / kPrefillRows + p.N : p.B * per) * p.H;
+  if (cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess || sms < 2) return false;
+  const int rows = kPair ? 2 * kPrefillRows : kPrefillRows;
+  const int64_t per = (p.Tq + rows - 1) / rows;
+  const int64_t items = (p.items ? p.Tq / rows + p.N : p.B * per) * p.H;
   if (items > INT32_MAX) return false;
-  int sms = 0;
-  if (cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess || sms < 1) return false;
   PrefillMaps maps;
   memset(&maps, 0, sizeof(maps));
   if (!head_map(&maps.q, p.q, kQkDim, p.H, p.B * p.Tq, p.q_st, p.q_sh, kPreRows)) return false;
   const int64_t keys = p.B * p.Tk;
   if (keys > 0) {  // (without keys no key tile exists and nothing is copied)
+    const int box_keys = kPair ? kPreKeys / 2 : kPreKeys;
     const cuuint64_t dims[2] = {kLatPe, (cuuint64_t)keys};
     const cuuint64_t strides[1] = {(cuuint64_t)p.pe_st * 2};
-    const cuuint32_t box[2] = {64, kPreKeys};
-    if (!head_map(&maps.k, p.k, kNope, p.H, keys, p.k_st, p.k_sh, kPreKeys) ||
+    const cuuint32_t box[2] = {64, (cuuint32_t)box_keys};
+    if (!head_map(&maps.k, p.k, kNope, p.H, keys, p.k_st, p.k_sh, box_keys) ||
         !head_map(&maps.v, p.v, kVDim, p.H, keys, p.v_st, p.v_sh, kPreKeys) ||
         !encode_map_bf16(&maps.pe, p.k_pe, 2, dims, strides, box))
       return false;
   }
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((unsigned)std::min<int64_t>(items, sms));
+  cfg.gridDim = dim3((unsigned)(kPair ? 2 * std::min<int64_t>(items, sms / 2) : std::min<int64_t>(items, sms)));
   cfg.blockDim = dim3(kPreThreads);
   cfg.dynamicSmemBytes = kPreSmem;
   cfg.stream = s;
-  // packed: set up while the list of blocks is made
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cudaLaunchAttribute attr[2];
+  int n = 0;
+  if (p.items) {  // packed: set up while the list of blocks is made
+    attr[n].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[n++].val.programmaticStreamSerializationAllowed = 1;
+  }
+  if (kPair) {
+    attr[n].id = cudaLaunchAttributeClusterDimension;
+    attr[n].val.clusterDim.x = 2;
+    attr[n].val.clusterDim.y = 1;
+    attr[n++].val.clusterDim.z = 1;
+  }
   cfg.attrs = attr;
-  cfg.numAttrs = p.items ? 1 : 0;
-  return cudaLaunchKernelEx(&cfg, kda_latent_prefill_kernel, p, per, maps) == cudaSuccess;
+  cfg.numAttrs = n;
+  return cudaLaunchKernelEx(&cfg, kda_latent_prefill_kernel<kPair>, p, per, maps) == cudaSuccess;
+}
+
+}  // namespace
+
+bool prefill_pairs(int64_t rows, int64_t sequences) { return rows >= 1024 * sequences; }
+
+bool launch_latent_prefill(const PrefillParams& p, cudaStream_t s) {
+  return p.pairs ? launch_prefill<true>(p, s) : launch_prefill<false>(p, s);
 }
 
 }  // namespace kda

@@ -373,25 +373,39 @@ def test_prefill_dense_batch_contiguous_and_large_scores():
     _prefill([150] * 2, [280] * 2, 2, True, False, std=40.0)
 
 
+@pytest.mark.parametrize("lq,lk", [(1024, 1024), (1100, 1100), (1537, 1537), (1030, 2000), (1280, 700), (1040, 1)])
+@pytest.mark.parametrize("causal", [True, False])
+def test_prefill_long(lq, lk, causal):
+    """Long enough for the form in which two CTAs share a tile: whole and ragged blocks, keys that
+    end inside a tile, context before and fewer keys than queries."""
+    _prefill([lq], [lk], 1, causal, False, seed=lq)
+
+
+def test_prefill_long_packed_and_batched():
+    _prefill([1500, 0, 2100, 700], [1500, 0, 2200, 650], 1, True, True, seed=5)
+    _prefill([1060] * 2, [1200] * 2, 2, True, False, seed=6, std=20.0)
+
+
 def test_prefill_without_keys():
     _prefill([40], [0], 2, True, False)
 
 
-def test_prefill_neighbours_do_not_touch():
+@pytest.mark.parametrize("a,b,n", [(70, 220, 310), (700, 2750, 3450)])
+def test_prefill_neighbours_do_not_touch(a, b, n):
     """NaN and Inf in the sequence before and after (queries, keys, values) stay there."""
     gen = torch.Generator().manual_seed(3)
-    H, lens = 2, [70, 150, 90]
-    q, kv, pe = (_rand(gen, 1, 310, *x).cuda() for x in ((H, 192), (H, 256), (64,)))
-    cu = torch.tensor([0, 70, 220, 310], device="cuda")
-    lse = torch.empty(1, 310, H, device="cuda")
-    clean = M.latent_prefill(q, kv[..., :128], pe, kv[..., 128:], 0.07, lse=lse, cu_seqlens=cu)[:, 70:220].clone()
-    clean_lse = lse[:, 70:220].clone()
+    H = 2
+    q, kv, pe = (_rand(gen, 1, n, *x).cuda() for x in ((H, 192), (H, 256), (64,)))
+    cu = torch.tensor([0, a, b, n], device="cuda")
+    lse = torch.empty(1, n, H, device="cuda")
+    clean = M.latent_prefill(q, kv[..., :128], pe, kv[..., 128:], 0.07, lse=lse, cu_seqlens=cu)[:, a:b].clone()
+    clean_lse = lse[:, a:b].clone()
     for bad in (NAN, float("inf")):
         for t in (q, kv, pe):
-            t[:, :70] = bad
-            t[:, 220:] = bad
+            t[:, :a] = bad
+            t[:, b:] = bad
         out = M.latent_prefill(q, kv[..., :128], pe, kv[..., 128:], 0.07, lse=lse, cu_seqlens=cu)
-        assert torch.equal(out[:, 70:220], clean) and torch.equal(lse[:, 70:220], clean_lse)
+        assert torch.equal(out[:, a:b], clean) and torch.equal(lse[:, a:b], clean_lse)
     assert np.isfinite(_f64(clean)).all()
 
 
