@@ -282,7 +282,7 @@ __global__ void __launch_bounds__(kPreThreads, 1)
             reinterpret_cast<uint4*>(rows)[x] = make_uint4(0, 0, 0, 0);
           fence_proxy_async_smem();
           __syncwarp();
-          if (lane == 0) mbar_arrive_cluster(full);
+          if (lane == 0) mbar_release_cluster(full);
         }
         ++values;
         if (++s == kPairStages) {
@@ -306,15 +306,8 @@ __global__ void __launch_bounds__(kPreThreads, 1)
       const uint32_t id_o = idesc_bf16(2 * kPreRows, kVDim, false, true);
       const uint64_t d_q = smem_desc(sb + kPreQ, 16, 1024), d_k = smem_desc(sb + kPreRing, 16, 1024);
       const uint64_t d_v = smem_desc(sb + kPreRing + 3 * kPairK, 16, 1024);
-      auto wait_pair = [&](uint32_t b, uint32_t parity) {  // (acquires the other CTA's writes too)
-        if (!mbar_try_wait_cluster(b, parity)) {
-          const long long t0 = clock64();
-          while (!*s_abort && !mbar_try_wait_cluster(b, parity))
-            if (clock64() - t0 > (1LL << 31)) {
-              atomicExch(p.status, KDA_ERR_DEVICE_TIMEOUT);
-              *s_abort = 1;
-            }
-        }
+      auto wait_pair = [&](uint32_t b, uint32_t parity) {
+        wait(b, parity);
         __syncwarp();
         tc_fence_after();
       };
@@ -356,6 +349,7 @@ __global__ void __launch_bounds__(kPreThreads, 1)
           tc_commit_pair(bar(kPpEmptyK + s));
           if (i + 1 == it.nt) tc_commit_pair(bar(kPbQEmpty));
           wait_pair(bar(kPpFullV + s), ph);
+          if (it.lk < (i + 1) * kPreKeys) mbar_try_wait_cluster(bar(kPpFullV + s), ph);  // acquires the cleared rows
           if (i < it.n0) values(0, s, done0, i == 0);
           s_prev = s;
           if (++s == kPairStages) {
