@@ -35,8 +35,8 @@
 // edge wastes more, so short sequences keep single CTAs.
 //
 // Roles: warps 0-3 and 4-7 softmax and output of the two tiles, warp 8 copies,
-// warp 9 products (of the pair: in its first CTA).  Every wait is bounded; a CTA
-// that gives up sets the status word.
+// warp 9 products (of the pair: in its first CTA), two more only fill their
+// warpgroup.  Every wait is bounded; a CTA that gives up sets the status word.
 #include <algorithm>
 #include <cstring>
 
@@ -51,7 +51,12 @@ constexpr int kPreKeys = 128;                    // keys of a tile
 constexpr int kPreQ = 0;                         // two tiles of three [128 rows][64 channels] blocks
 constexpr int kPreQTile = 3 * kPreRows * 128;
 constexpr int kPreRing = 2 * kPreQTile;          // key and value blocks
-constexpr int kPreThreads = 320;
+constexpr int kPreThreads = 384;
+// Registers: 168 a thread at launch; the warpgroup of copies and products gives
+// up 64 of its share, the two of the softmax take 32 each (a row of scores and
+// its weights in registers): 128 (104 + 2 x 200) = 384 x 168.
+constexpr int kPreRegsFew = 104, kPreRegsMany = 200;
+static_assert(128 * (kPreRegsFew + 2 * kPreRegsMany) == kPreThreads * 168, "register split");
 constexpr float kPreSlack = 8.0f;                // log2 growth of a maximum that is let pass
 // single CTAs: ring of [128 keys][64 channels] slots
 constexpr int kPreSlots = 8;
@@ -219,6 +224,8 @@ __global__ void __launch_bounds__(kPreThreads, 1)
   PreItem it;
   int g = 0;  // key tiles so far, over all items
 
+  if (warp >= 8) {
+  asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;\n" ::"n"(kPreRegsFew));
   if (kPair && warp == 8) {
     // ---- copies of a pair: this CTA's half of the keys and of the value channels, its query rows ----
     bool gone = false;
@@ -508,7 +515,9 @@ __global__ void __launch_bounds__(kPreThreads, 1)
     // the last products complete before tensor memory is freed
     if (done0 > 0) mbar_wait_bounded(bar(kPbPv), (uint32_t)((done0 - 1) & 1));
     if (done1 > 0) mbar_wait_bounded(bar(kPbPv + 1), (uint32_t)((done1 - 1) & 1));
+  }
   } else {
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;\n" ::"n"(kPreRegsMany));
     // ---- softmax and output: thread = row of tile t ----
     const int t = warp >> 2, q = warp & 3;
     const uint32_t lane_base = (uint32_t)(q * 32) << 16;
