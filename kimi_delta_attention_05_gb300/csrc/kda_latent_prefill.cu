@@ -57,6 +57,11 @@ constexpr int kPreThreads = 384;
 // its weights in registers): 128 (104 + 2 x 200) = 384 x 168.
 constexpr int kPreRegsFew = 104, kPreRegsMany = 200;
 static_assert(128 * (kPreRegsFew + 2 * kPreRegsMany) == kPreThreads * 168, "register split");
+// Keys of a tile whose weights a pair hands over first: its round from scores to
+// values is the longer one, and the products of these keys start meanwhile (none,
+// 64 and 96 of the 128 measured: 391, 380 and 395 us on the 8192-token prompt;
+// single CTAs gain nothing).
+constexpr int kPreFirst = 64;
 constexpr float kPreSlack = 8.0f;                // log2 growth of a maximum that is let pass
 // single CTAs: ring of [128 keys][64 channels] slots
 constexpr int kPreSlots = 8;
@@ -71,8 +76,8 @@ constexpr int kPreBar = kPreRing + (kPreSlots * kPreSlot > kPairStages * kPairSt
 // (by the tile's parity), q full and empty, sfull[2], pready[2], pvdone[2]
 constexpr int kPbFullK0 = 0, kPbFullK = 2, kPbFullV = 4, kPbEmptyK = 6, kPbEmptyV = 8, kPbQ = 10, kPbQEmpty = 11,
               kPbS = 12, kPbP = 14, kPbPv = 16;
-// pairs: by stage; then a barrier for value tiles that end behind the sequence
-constexpr int kPpFullK = 18, kPpFullV = 21, kPpEmptyK = 24, kPpEmptyV = 27, kPpTail = 30, kPbars = 31;
+// pairs: by stage; then a barrier for value tiles that end behind the sequence, and for the other weights
+constexpr int kPpFullK = 18, kPpFullV = 21, kPpEmptyK = 24, kPpEmptyV = 27, kPpTail = 30, kPbP2 = 31, kPbars = 33;
 constexpr int kPreTmem = kPreBar + 8 * kPbars;
 constexpr int kPreAbort = kPreTmem + 8;
 constexpr int kPreSmem = kPreAbort + 8;
@@ -181,7 +186,7 @@ __global__ void __launch_bounds__(kPreThreads, 1)
   if (tid == 0) {
     for (int i = 0; i < kPbars; ++i) {
       uint32_t n = 1;
-      if (i == kPbP || i == kPbP + 1) n = kPair ? 8 : 4;                             // the softmax warps of a tile
+      if (i == kPbP || i == kPbP + 1 || i >= kPbP2) n = kPair ? 8 : 4;               // the softmax warps of a tile
       if (kPair && (i == kPbQ || (i >= kPpFullK && i < kPpFullK + 2 * kPairStages))) n = 2;  // both CTAs' copies
       mbar_init(bar(i), n);
     }
@@ -333,12 +338,14 @@ __global__ void __launch_bounds__(kPreThreads, 1)
       };
       auto values = [&](int t, int stage, int& done, bool first) {
         wait_pair(bar(kPbP + t), (uint32_t)(done & 1));
-        ++done;
         const uint64_t b = d_v + (uint64_t)((stage * kPairStage) >> 4);
         const uint32_t o = tmem + 256 + 128 * t, a = tmem + 128 * t, more = first ? 0u : 1u;
 #pragma unroll
-        for (int ks = 0; ks < 8; ++ks)
+        for (int ks = 0; ks < 8; ++ks) {
+          if (ks == kPreFirst / 16) wait_pair(bar(kPbP2 + t), (uint32_t)(done & 1));
           tc_mma_ts_pair(o, a + 8 * ks, b + (uint64_t)((ks * 2048) >> 4), id_o, ks > 0 ? 1u : more);
+        }
+        ++done;
         tc_commit_pair(bar(kPbPv + t));
       };
       while (walk.next(p, per, it)) {
@@ -525,6 +532,15 @@ __global__ void __launch_bounds__(kPreThreads, 1)
     const float sl = p.scale_log2;
     const f32x2 sl2 = f2(sl, sl);
     int done = 0;  // scores used
+    auto hand_over = [&](int b) {  // the weights stored so far, to the products
+      tc_st_wait();
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) {
+        if (kPair) mbar_arrive_cluster(lead(b));
+        else mbar_arrive(bar(b));
+      }
+    };
     while (walk.next(p, per, it)) {
       const int n = t == 0 ? it.n0 : it.n1;
       const int row = it.r0 + (kPair ? 2 * t + (int)rank : t) * kPreRows + q * 32 + lane;  // query within the sequence
@@ -588,14 +604,9 @@ __global__ void __launch_bounds__(kPreThreads, 1)
             w[e] = __uint_as_float(pack_bf16(a, b));
           }
           tc_st16(t_s + c / 2, w);
+          if (kPair && c == kPreFirst - 32) hand_over(kPbP + t);
         }
-        tc_st_wait();
-        tc_fence_before();
-        __syncwarp();
-        if (lane == 0) {
-          if (kPair) mbar_arrive_cluster(lead(kPbP + t));
-          else mbar_arrive(bar(kPbP + t));
-        }
+        hand_over((kPair ? kPbP2 : kPbP) + t);
         const float2 z = f2u(add2(sum[0], sum[1]));
         l += z.x + z.y;
       }
