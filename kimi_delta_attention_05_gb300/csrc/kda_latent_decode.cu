@@ -340,14 +340,17 @@ __global__ void __launch_bounds__(kDecThreads, 1)
         wait(bar(C::kFull + s), (uint32_t)((is >> 1) & 1));
         __syncwarp();
         tc_fence_after();
+        if (elect_one()) {
 #pragma unroll
-        for (int ch = 0; ch < kDecChunks; ++ch)
+          for (int ch = 0; ch < kDecChunks; ++ch)
 #pragma unroll
-          for (int ks = 0; ks < 4; ++ks)
-            tc_mma(t_s + N * s, a + (uint64_t)((ch * kDecAtom + ks * 32) >> 4), b + (uint64_t)((ch * N * 128 + ks * 32) >> 4),
-                   id_s, ch + ks > 0);
-        tc_commit(bar(C::kSFull + s));
-        if (cs.last()) tc_commit(bar(C::kQEmpty + qb));
+            for (int ks = 0; ks < 4; ++ks)
+              mma_ss<false>(t_s + N * s, a + (uint64_t)((ch * kDecAtom + ks * 32) >> 4),
+                            b + (uint64_t)((ch * N * 128 + ks * 32) >> 4), id_s, ch + ks > 0);
+          mma_commit<false>(bar(C::kSFull + s));
+          if (cs.last()) mma_commit<false>(bar(C::kQEmpty + qb));
+        }
+        __syncwarp();
         ++is;
         cs.advance(p);
         continue;
@@ -369,14 +372,17 @@ __global__ void __launch_bounds__(kDecThreads, 1)
       tc_fence_after();
       const uint64_t a = d_c + (uint64_t)((s * kDecStage) >> 4);
       const uint32_t start = co.first() ? 0u : 1u;
+      if (elect_one()) {
 #pragma unroll
-      for (int mt = 0; mt < 4; ++mt)
+        for (int mt = 0; mt < 4; ++mt)
 #pragma unroll
-        for (int ks = 0; ks < 4; ++ks)
-          tc_mma(tmem + mt * N, a + (uint64_t)((mt * 2 * kDecAtom + ks * 2 * kDecGroup) >> 4), d_p + (uint64_t)((ks * 32) >> 4),
-                 id_o, ks > 0 ? 1u : start);
-      tc_commit(bar(C::kEmpty + s));
-      tc_commit(bar(C::kPvDone));
+          for (int ks = 0; ks < 4; ++ks)
+            mma_ss<false>(tmem + mt * N, a + (uint64_t)((mt * 2 * kDecAtom + ks * 2 * kDecGroup) >> 4),
+                          d_p + (uint64_t)((ks * 32) >> 4), id_o, ks > 0 ? 1u : start);
+        mma_commit<false>(bar(C::kEmpty + s));
+        mma_commit<false>(bar(C::kPvDone));
+      }
+      __syncwarp();
       ++io;
       co.advance(p);
     }

@@ -87,14 +87,6 @@ struct PrefillMaps {
   CUtensorMap q, k, pe, v;
 };
 
-// D += A B with A (bf16) in tensor memory; issue as tc_mma.
-__device__ __forceinline__ void tc_mma_ts(uint32_t d_tmem, uint32_t a_tmem, uint64_t b, uint32_t idesc,
-                                          uint32_t accumulate) {
-  asm volatile(
-      "{\n .reg .pred p, e;\n elect.sync _|e, 0xffffffff;\n setp.ne.u32 p, %4, 0;\n"
-      " @e tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n}\n" ::"r"(d_tmem),
-      "r"(a_tmem), "l"(b), "r"(idesc), "r"(accumulate));
-}
 // 32 columns of this thread's lane, without waiting for the data.
 __device__ __forceinline__ void tc_ld32_nowait(uint32_t taddr, float* v) {
   uint32_t* r = reinterpret_cast<uint32_t*>(v);
@@ -326,42 +318,63 @@ __global__ void __launch_bounds__(kPreThreads, 1)
       int q = 0, done0 = 0, done1 = 0;
       int s = 0, s_prev = 0;     // stage of this key tile and of the one before
       uint32_t ph = 0;
+      // One place each for the products of every query tile: a copy of them for the last step
+      // would run once an item, from cold instruction caches.
       auto scores = [&](int t) {
         const uint64_t a = d_q + (uint64_t)((t * kPreQTile) >> 4), b = d_k + (uint64_t)((s * kPairStage) >> 4);
+        if (elect_one()) {
 #pragma unroll
-        for (int c = 0; c < 3; ++c)
+          for (int c = 0; c < 3; ++c)
 #pragma unroll
-          for (int ks = 0; ks < 4; ++ks)
-            tc_mma_pair(tmem + 128 * t, a + (uint64_t)((c * kPreRows * 128 + ks * 32) >> 4),
-                        b + (uint64_t)((c * kPairK + ks * 32) >> 4), id_s, c + ks > 0);
-        tc_commit_pair(bar(kPbS + t));
+            for (int ks = 0; ks < 4; ++ks)
+              mma_ss<true>(tmem + 128 * t, a + (uint64_t)((c * kPreRows * 128 + ks * 32) >> 4),
+                           b + (uint64_t)((c * kPairK + ks * 32) >> 4), id_s, c + ks > 0);
+          mma_commit<true>(bar(kPbS + t));
+        }
+        __syncwarp();
       };
       auto values = [&](int t, int stage, int& done, bool first) {
-        wait_pair(bar(kPbP + t), (uint32_t)(done & 1));
         const uint64_t b = d_v + (uint64_t)((stage * kPairStage) >> 4);
         const uint32_t o = tmem + 256 + 128 * t, a = tmem + 128 * t, more = first ? 0u : 1u;
+        wait_pair(bar(kPbP + t), (uint32_t)(done & 1));
+        if (elect_one()) {
 #pragma unroll
-        for (int ks = 0; ks < 8; ++ks) {
-          if (ks == kPreFirst / 16) wait_pair(bar(kPbP2 + t), (uint32_t)(done & 1));
-          tc_mma_ts_pair(o, a + 8 * ks, b + (uint64_t)((ks * 2048) >> 4), id_o, ks > 0 ? 1u : more);
+          for (int ks = 0; ks < kPreFirst / 16; ++ks)
+            mma_ts<true>(o, a + 8 * ks, b + (uint64_t)((ks * 2048) >> 4), id_o, ks > 0 ? 1u : more);
         }
+        __syncwarp();
+        wait_pair(bar(kPbP2 + t), (uint32_t)(done & 1));
         ++done;
-        tc_commit_pair(bar(kPbPv + t));
+        if (elect_one()) {
+#pragma unroll
+          for (int ks = kPreFirst / 16; ks < 8; ++ks)
+            mma_ts<true>(o, a + 8 * ks, b + (uint64_t)((ks * 2048) >> 4), id_o, 1u);
+          mma_commit<true>(bar(kPbPv + t));
+        }
+        __syncwarp();
+      };
+      auto done_with = [&](int b) {
+        if (elect_one()) mma_commit<true>(bar(b));
+        __syncwarp();
       };
       while (walk.next(p, per, it)) {
         if (it.nt == 0) continue;
         wait_pair(bar(kPbQ), (uint32_t)(q & 1));
         ++q;
-        for (int i = 0; i < it.nt; ++i) {
-          wait_pair(bar(kPpFullK + s), ph);
-          if (i < it.n0) scores(0);
+        for (int i = 0; i <= it.nt; ++i) {
+          const bool more = i < it.nt;
+          if (more) {
+            wait_pair(bar(kPpFullK + s), ph);
+            if (i < it.n0) scores(0);
+          }
           if (i > 0) {
             if (i - 1 < it.n1) values(1, s_prev, done1, i == 1);
-            tc_commit_pair(bar(kPpEmptyV + s_prev));
+            done_with(kPpEmptyV + s_prev);
           }
+          if (!more) break;
           if (i < it.n1) scores(1);
-          tc_commit_pair(bar(kPpEmptyK + s));
-          if (i + 1 == it.nt) tc_commit_pair(bar(kPbQEmpty));
+          done_with(kPpEmptyK + s);
+          if (i + 1 == it.nt) done_with(kPbQEmpty);
           wait_pair(bar(kPpFullV + s), ph);
           if (it.lk < (i + 1) * kPreKeys) mbar_try_wait_cluster(bar(kPpFullV + s), ph);  // acquires the cleared rows
           if (i < it.n0) values(0, s, done0, i == 0);
@@ -371,8 +384,6 @@ __global__ void __launch_bounds__(kPreThreads, 1)
             ph ^= 1u;
           }
         }
-        if (it.nt - 1 < it.n1) values(1, s_prev, done1, it.nt == 1);
-        tc_commit_pair(bar(kPpEmptyV + s_prev));
       }
       if (done0 > 0) mbar_wait_bounded(bar(kPbPv), (uint32_t)((done0 - 1) & 1));
       if (done1 > 0) mbar_wait_bounded(bar(kPbPv + 1), (uint32_t)((done1 - 1) & 1));
@@ -453,16 +464,23 @@ __global__ void __launch_bounds__(kPreThreads, 1)
     };
     // S of query tile t against key tile `tile`; `fresh`: the first product to read these keys
     auto scores = [&](int t, int tile, bool fresh) {
-#pragma unroll
-      for (int c = 0; c < 3; ++c) {
-        if (fresh && c < 2) full_wait(c == 0 ? kPbFullK0 : kPbFullK, tile);
-        const uint64_t a = d_q + (uint64_t)((t * kPreQTile + c * kPreRows * 128) >> 4);
+      const uint64_t a = d_q + (uint64_t)((t * kPreQTile) >> 4);
+      auto part = [&](int c) {
         const uint64_t b = d_k + (uint64_t)((slot_of(tile, c) * kPreSlot) >> 4);
 #pragma unroll
         for (int ks = 0; ks < 4; ++ks)
-          tc_mma(tmem + 128 * t, a + 2 * ks, b + 2 * ks, id_s, c + ks > 0);
+          mma_ss<false>(tmem + 128 * t, a + (uint64_t)((c * kPreRows * 128 + ks * 32) >> 4), b + 2 * ks, id_s, c + ks > 0);
+      };
+      if (fresh) full_wait(kPbFullK0, tile);
+      if (elect_one()) part(0);
+      __syncwarp();
+      if (fresh) full_wait(kPbFullK, tile);
+      if (elect_one()) {
+        part(1);
+        part(2);
+        mma_commit<false>(bar(kPbS + t));
       }
-      tc_commit(bar(kPbS + t));
+      __syncwarp();
     };
     // O of query tile t += its weights times the values of key tile `tile`
     auto values = [&](int t, int tile, int& done, bool first) {
@@ -473,34 +491,43 @@ __global__ void __launch_bounds__(kPreThreads, 1)
       const int s0 = slot_of(tile, 3), s1 = slot_of(tile, 4);
       const uint32_t o = tmem + 256 + 128 * t, a = tmem + 128 * t, more = first ? 0u : 1u;
       const uint64_t b0 = d_v + (uint64_t)((s0 * kPreSlot) >> 4), b1 = d_v + (uint64_t)((s1 * kPreSlot) >> 4);
-      if (s1 == s0 + 1) {  // the two 64-column blocks lie one slot apart: one operand of 128 columns
+      if (elect_one()) {
+        if (s1 == s0 + 1) {  // the two 64-column blocks lie one slot apart: one operand of 128 columns
 #pragma unroll
-        for (int ks = 0; ks < 8; ++ks)
-          tc_mma_ts(o, a + 8 * ks, b0 + (uint64_t)((ks * 2048) >> 4), id_o, ks > 0 ? 1u : more);
-      } else {
+          for (int ks = 0; ks < 8; ++ks)
+            mma_ts<false>(o, a + 8 * ks, b0 + (uint64_t)((ks * 2048) >> 4), id_o, ks > 0 ? 1u : more);
+        } else {
 #pragma unroll
-        for (int ks = 0; ks < 8; ++ks) {
-          tc_mma_ts(o, a + 8 * ks, b0 + (uint64_t)((ks * 2048) >> 4), id_o64, ks > 0 ? 1u : more);
-          tc_mma_ts(o + 64, a + 8 * ks, b1 + (uint64_t)((ks * 2048) >> 4), id_o64, ks > 0 ? 1u : more);
+          for (int ks = 0; ks < 8; ++ks) {
+            mma_ts<false>(o, a + 8 * ks, b0 + (uint64_t)((ks * 2048) >> 4), id_o64, ks > 0 ? 1u : more);
+            mma_ts<false>(o + 64, a + 8 * ks, b1 + (uint64_t)((ks * 2048) >> 4), id_o64, ks > 0 ? 1u : more);
+          }
         }
+        mma_commit<false>(bar(kPbPv + t));
       }
-      tc_commit(bar(kPbPv + t));
+      __syncwarp();
+    };
+    auto done_with = [&](int b) {
+      if (elect_one()) mma_commit<false>(bar(b));
+      __syncwarp();
     };
     while (walk.next(p, per, it)) {
       if (it.nt == 0) continue;
       wait(bar(kPbQ), (uint32_t)(q & 1));
       ++q;
       __syncwarp();
-      for (int i = 0; i < it.nt; ++i) {
+      for (int i = 0; i <= it.nt; ++i) {
         const int tile = g + i;
-        if (i < it.n0) scores(0, tile, true);
+        const bool more = i < it.nt;
+        if (more && i < it.n0) scores(0, tile, true);
         if (i > 0) {
           if (i - 1 < it.n1) values(1, tile - 1, done1, i == 1);
-          tc_commit(bar(kPbEmptyV + ((tile - 1) & 1)));
+          done_with(kPbEmptyV + ((tile - 1) & 1));
         }
+        if (!more) break;
         if (i < it.n1) scores(1, tile, i >= it.n0);
-        tc_commit(bar(kPbEmptyK + (tile & 1)));
-        if (i + 1 == it.nt) tc_commit(bar(kPbQEmpty));
+        done_with(kPbEmptyK + (tile & 1));
+        if (i + 1 == it.nt) done_with(kPbQEmpty);
         full_wait(kPbFullV, tile);
         const int valid = it.lk - i * kPreKeys;
         if (valid < kPreKeys) {
@@ -516,8 +543,6 @@ __global__ void __launch_bounds__(kPreThreads, 1)
         if (i < it.n0) values(0, tile, done0, i == 0);
       }
       g += it.nt;
-      if (it.nt - 1 < it.n1) values(1, g - 1, done1, it.nt == 1);
-      tc_commit(bar(kPbEmptyV + ((g - 1) & 1)));
     }
     // the last products complete before tensor memory is freed
     if (done0 > 0) mbar_wait_bounded(bar(kPbPv), (uint32_t)((done0 - 1) & 1));
