@@ -69,6 +69,7 @@ struct DecodePlan {
   int shares;          // CTAs of a group
   int box_rows;        // cached rows of one tensor copy: gcd(page_size, 64)
   int min_tiles;       // least tiles of a share
+  int whole;           // requests are not split: the share that holds a request's start has all of it
   float* part;         // [row_blocks * shares * 2][N][512] normalised partial rows
   float* part_lse;     // [row_blocks * shares * 2][N] their lse, log2
   int by_request;      // the join works by request (fewer than shares), else by share
@@ -112,8 +113,9 @@ __device__ __forceinline__ int64_t div_fast(int64_t a, int64_t b) {
 // The pieces of one share [u0, u1) of the line of costs, in order.  Request b
 // takes [pre, pre + cost) of it; its tile k starts at pre + kDecReqCost + k
 // kDecTileCost and belongs to the share that holds that point; a request
-// without tiles belongs to the share that holds pre.
+// without tiles, or one that is not split, belongs to the share that holds pre.
 struct DecPieces {
+  int unsplit;
   int64_t u0, u1, pre;  // the share; start of request b
   int b;
   // the current piece: request, its length, tiles [t0, t1) of its `tiles`
@@ -129,7 +131,8 @@ struct DecPieces {
       tiles = dec_tiles(len);
       t0 = tiles_before(u0);
       t1 = tiles_before(u1);
-      const bool mine = tiles > 0 ? t0 < t1 : pre >= u0;
+      if (unsplit && pre >= u0) t1 = tiles;  // (and t0 is 0)
+      const bool mine = tiles > 0 && !unsplit ? t0 < t1 : pre >= u0;
       pre += dec_cost(tiles);
       ++b;
       if (mine) return true;
@@ -243,6 +246,7 @@ __global__ void __launch_bounds__(kDecThreads, 1)
   }
   __syncthreads();
   DecPieces pieces;
+  pieces.unsplit = pl.whole;
   pieces.u0 = u0;
   pieces.u1 = u1;
   pieces.b = u0 < u1 ? (int)s_scan[10] : p.B;
@@ -584,7 +588,7 @@ __global__ void __launch_bounds__(kDecThreads, 1)
     }
     tc_fence_before();
   }
-  if (tid == 0) {
+  if (tid == 0 && !pl.whole) {
     // what the join kernel has to do, by request or by the share a request starts in
     if (!pl.by_request) pl.split[blockIdx.x] = make_int4(-1, 0, 0, 0);
     DecPieces each = pieces;
@@ -722,9 +726,13 @@ DecLayout dec_layout(const DecodeParams& p) {
   d.plan.row_blocks = (rows + d.n - 1) / d.n;
   const int64_t most = (int64_t)p.B * ((p.max_pages * p.page_size + kDecTile - 1) / kDecTile + 1);
   d.plan.min_tiles = 2;
-  d.plan.shares = (int)std::max<int64_t>(1, std::min<int64_t>(sms / d.plan.row_blocks,
-                                                              (most + d.plan.min_tiles - 1) / d.plan.min_tiles));
+  // Tables of up to four tiles: a split and its join cost more than they
+  // save (TIME_S us split, TIME_W whole, for one request of 256 tokens and 32 rows).
+  d.plan.whole = p.max_pages * p.page_size <= 4 * kDecTile;
+  const int64_t units = d.plan.whole ? p.B : (most + d.plan.min_tiles - 1) / d.plan.min_tiles;
+  d.plan.shares = (int)std::max<int64_t>(1, std::min<int64_t>(sms / d.plan.row_blocks, units));
   d.plan.box_rows = (int)std::gcd<int64_t, int64_t>(p.page_size, kDecTile);
+  if (d.plan.whole) return d;  // no parts: no workspace
   const size_t ctas = (size_t)d.plan.row_blocks * d.plan.shares;
   d.lse_at = ctas * 2 * d.n * kLat * 4;
   d.split_at = d.lse_at + ctas * 2 * d.n * 4;
@@ -747,7 +755,7 @@ bool launch_dec(const DecodeParams& p, const DecLayout& d, const DecodeMaps& map
   });
   if (rc[dev] != cudaSuccess) return false;
   kda_latent_decode_kernel<N><<<ctas, kDecThreads, DecCfg<N>::kSmem, s>>>(p, d.plan, maps);
-  if (d.plan.shares == 1) return true;  // no request is split
+  if (d.plan.whole) return true;  // nothing to join
   cudaLaunchConfig_t cfg = {};
   // a row a CTA where a request is in more than four parts on average, else a row a warp
   const bool wide = (int64_t)p.B * 4 < d.plan.shares;

@@ -79,6 +79,16 @@ def test_decode_workspace_is_checked():
         assert _call("decode", a, (FAKE + 16, need)) == 10
 
 
+def test_decode_workspace_of_long_tables_is_checked():
+    """Tables that one CTA does not walk alone hold parts to be joined."""
+    a = M.kda_latent_decode_args(FAKE, _cache(), FAKE, 400, 400, FAKE, 0.07, FAKE, None, 2, 1, 32)
+    need = M._library().kda_latent_decode_workspace_bytes(ctypes.byref(a))
+    assert need > 0
+    assert _call("decode", a, (None, need)) == 10
+    assert _call("decode", a, (FAKE, need - 1)) == 10
+    assert _call("decode", a, (FAKE + 16, need)) == 10
+
+
 def test_decode_of_nothing_is_nothing():
     a = M.kda_latent_decode_args(None, _cache(), None, 0, 0, None, 0.07, None, None, 0, 1, 32)
     assert _call("decode", a, (None, 0)) == 0
