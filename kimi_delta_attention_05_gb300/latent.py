@@ -10,6 +10,7 @@ from :func:`get_status`.
 from __future__ import annotations
 
 import ctypes
+import struct
 
 import torch
 
@@ -56,6 +57,22 @@ class kda_latent_prefill_args(ctypes.Structure):
                 ("B", _I), ("Tq", _I), ("Tk", _I), ("H", _I), ("N", _I), ("flags", ctypes.c_uint32)]
 
 
+def _packer(block):
+    """Packs the fields of an argument block, nested ones in place, into its bytes: one call
+    where filling the ctypes structure takes three times as long."""
+    codes = {_P: "P", _I: "q", _F: "f", ctypes.c_uint32: "I"}
+
+    def fields(cls):
+        return "".join(codes[t] if t in codes else fields(t) for _, t in cls._fields_)
+
+    layout = struct.Struct("@" + fields(block) + "0q")
+    assert layout.size == ctypes.sizeof(block)
+    return layout.pack
+
+
+_plan_block, _append_block = _packer(kda_latent_plan_args), _packer(kda_latent_append_args)
+_decode_block, _prefill_block = _packer(kda_latent_decode_args), _packer(kda_latent_prefill_args)
+
 _fns = None
 
 
@@ -63,31 +80,30 @@ def _library():
     global _fns
     if _fns is None:
         lib = load_library()
-        lib.kda_latent_plan.restype = ctypes.c_int
-        lib.kda_latent_plan.argtypes = [ctypes.POINTER(kda_latent_plan_args), _P]
-        lib.kda_latent_append.restype = ctypes.c_int
-        lib.kda_latent_append.argtypes = [ctypes.POINTER(kda_latent_append_args), _P]
-        for name, args in (("decode", kda_latent_decode_args), ("prefill", kda_latent_prefill_args)):
+        for name in ("plan", "append", "decode", "prefill"):
             fn = getattr(lib, f"kda_latent_{name}")
             fn.restype = ctypes.c_int
-            fn.argtypes = [ctypes.POINTER(args), _P, ctypes.c_size_t, _P]
+            if name in ("plan", "append"):  # the block (its bytes or a reference), the stream
+                fn.argtypes = [_P, _P]
+                continue
+            fn.argtypes = [_P, _P, ctypes.c_size_t, _P]
             size = getattr(lib, f"kda_latent_{name}_workspace_bytes")
             size.restype = ctypes.c_size_t
-            size.argtypes = [ctypes.POINTER(args)]
+            size.argtypes = [_P]
         _fns = lib
     return _fns
 
 
 _bf16, _f32, _i32, _i64 = torch.bfloat16, torch.float32, torch.int32, torch.int64
-_empty, _byref = torch.empty, ctypes.byref
+_empty = torch.empty
 
 
 def _raise(call, rc):
     raise KdaError(rc, _library().kda_error_string(rc).decode(), call)
 
 
-# A serving step makes these calls every few microseconds, so the checks are
-# plain comparisons in line and the messages are put together only on failure.
+# A serving step makes these calls every few microseconds: the checks are plain
+# comparisons, and the messages are put together only on failure.
 
 def _on(t, dtype, ndim, device, name):
     """A CUDA tensor of this type and rank on `device`."""
@@ -108,7 +124,7 @@ def _gpu(t, name):
 
 
 def _last(strides, t, name):
-    if strides[-1] != 1 and t.numel() > 0:
+    if strides[-1] != 1 and t.shape[-1] > 1 and t.numel() > 0:
         raise ValueError(f"{name}: the last dimension has to be contiguous")
 
 
@@ -141,7 +157,7 @@ def _cache_block(cache, device):
         raise ValueError(f"cache: rows of {LATENT_ROW} values are needed")
     _last(strides, cache, "cache")
     page_stride = strides[0] if pages > 1 else (page - 1) * strides[1] + LATENT_ROW
-    return kda_latent_cache(cache.data_ptr(), pages, page, page_stride, strides[1])
+    return cache.data_ptr(), pages, page, page_stride, strides[1]
 
 
 def latent_plan(cached_lens, new_lens, block_table, free_pages, page_size, num_tokens, *, stream=None):
@@ -171,10 +187,10 @@ def latent_plan(cached_lens, new_lens, block_table, free_pages, page_size, num_t
     cu = _new(B + 1, _i64, dev, stream)
     slots = _new(max(T, 0), _i64, dev, stream)
     taken = _new(1, _i32, dev, stream)
-    a = kda_latent_plan_args(cached_lens.data_ptr(), new_lens.data_ptr(), block_table.data_ptr(),
-                             strides[0] if B > 1 else width, free_pages.data_ptr(), lens.data_ptr(), cu.data_ptr(),
-                             slots.data_ptr(), taken.data_ptr(), B, width, free_pages.shape[0], int(page_size), T)
-    rc = _library().kda_latent_plan(_byref(a), _handle(dev, stream))
+    a = _plan_block(cached_lens.data_ptr(), new_lens.data_ptr(), block_table.data_ptr(), strides[0] if B > 1 else width,
+                    free_pages.data_ptr(), lens.data_ptr(), cu.data_ptr(), slots.data_ptr(), taken.data_ptr(), B, width,
+                    free_pages.shape[0], int(page_size), T)
+    rc = _library().kda_latent_plan(a, _handle(dev, stream))
     if rc != 0:
         _raise("kda_latent_plan", rc)
     return {"seq_lens": lens, "cu_seqlens": cu, "slot_map": slots, "pages_taken": taken}
@@ -203,11 +219,10 @@ def latent_append(c, k_pe, slot_map, cache, norm_weight=None, eps=1e-6, *, strea
         _dense(norm_weight, "norm_weight")
         if norm_weight.shape[0] != LATENT_DIM:
             raise ValueError("norm_weight [512] is needed")
-    a = kda_latent_append_args(c.data_ptr(), k_pe.data_ptr(), c_strides[0] if T > 1 else LATENT_DIM,
-                               pe_strides[0] if T > 1 else LATENT_PE_DIM, slot_map.data_ptr(),
-                               _cache_block(cache, dev), None if norm_weight is None else norm_weight.data_ptr(),
-                               eps, T)
-    rc = _library().kda_latent_append(_byref(a), _handle(dev, stream))
+    a = _append_block(c.data_ptr(), k_pe.data_ptr(), c_strides[0] if T > 1 else LATENT_DIM,
+                      pe_strides[0] if T > 1 else LATENT_PE_DIM, slot_map.data_ptr(), *_cache_block(cache, dev),
+                      0 if norm_weight is None else norm_weight.data_ptr(), eps, T)
+    rc = _library().kda_latent_append(a, _handle(dev, stream))
     if rc != 0:
         _raise("kda_latent_append", rc)
     return cache
@@ -248,14 +263,13 @@ def latent_decode(q, cache, block_table, seq_lens, scale, out=None, lse=None, *,
         _dense(lse, "lse")
         if lse.shape != (B, R, H):
             raise ValueError("lse [B, R, H] is needed")
-    a = kda_latent_decode_args(q.data_ptr(), _cache_block(cache, dev), block_table.data_ptr(),
-                               strides[0] if B > 1 else width, width, seq_lens.data_ptr(), scale,
-                               out.data_ptr(), None if lse is None else lse.data_ptr(), B, R, H)
-    lib, ref = _library(), _byref(a)
+    a = _decode_block(q.data_ptr(), *_cache_block(cache, dev), block_table.data_ptr(), strides[0] if B > 1 else width,
+                      width, seq_lens.data_ptr(), scale, out.data_ptr(), 0 if lse is None else lse.data_ptr(), B, R, H)
+    lib = _library()
     if workspace is None:
-        need = lib.kda_latent_decode_workspace_bytes(ref)
+        need = lib.kda_latent_decode_workspace_bytes(a)
         workspace = _new(need, torch.uint8, dev, stream) if need else None
-    rc = lib.kda_latent_decode(ref, None if workspace is None else workspace.data_ptr(),
+    rc = lib.kda_latent_decode(a, None if workspace is None else workspace.data_ptr(),
                                0 if workspace is None else workspace.numel(), _handle(dev, stream))
     if rc != 0:
         _raise("kda_latent_decode", rc)
@@ -264,9 +278,9 @@ def latent_decode(q, cache, block_table, seq_lens, scale, out=None, lse=None, *,
 
 def latent_decode_workspace_bytes(B, R, H, cache, block_table):
     """Workspace bytes of :func:`latent_decode` for these sizes on the current device."""
-    a = kda_latent_decode_args(16, _cache_block(cache, cache.device), 16, block_table.shape[1], block_table.shape[1], 16,
-                               1.0, 16, None, B, R, H)
-    return int(_library().kda_latent_decode_workspace_bytes(ctypes.byref(a)))
+    width = block_table.shape[1]
+    return int(_library().kda_latent_decode_workspace_bytes(
+        _decode_block(16, *_cache_block(cache, cache.device), 16, width, width, 16, 1.0, 16, 0, B, R, H)))
 
 
 def _token_stride(shape, strides, row, name):
@@ -318,7 +332,7 @@ def latent_prefill(q, k, k_pe, v, scale, out=None, lse=None, cu_seqlens=None, cu
         _dense(lse, "lse")
         if lse.shape != (B, Tq, H):
             raise ValueError("lse [B, Tq, H] is needed")
-    N, cu_q, cu_k = B, None, None
+    N, cu_q, cu_k = B, 0, 0
     if cu_seqlens is not None:
         if cu_seqlens_k is None:
             cu_seqlens_k = cu_seqlens
@@ -334,16 +348,16 @@ def latent_prefill(q, k, k_pe, v, scale, out=None, lse=None, cu_seqlens=None, cu
         raise ValueError("cu_seqlens_k needs cu_seqlens")
     # (a dimension of one has no stride of its own)
     qh, kh, vh = (qs[2], ks[2], vs[2]) if H > 1 else (LATENT_QK_DIM, 128, LATENT_V_DIM)
-    a = kda_latent_prefill_args(
+    a = _prefill_block(
         q.data_ptr(), k.data_ptr(), k_pe.data_ptr(), v.data_ptr(), _token_stride(shape, qs, H * qh, "q"), qh,
         _token_stride(k_shape, ks, H * kh, "k"), kh, _token_stride(k_shape, ps, LATENT_PE_DIM, "k_pe"),
-        _token_stride(k_shape, vs, H * vh, "v"), vh, scale, out.data_ptr(), None if lse is None else lse.data_ptr(),
+        _token_stride(k_shape, vs, H * vh, "v"), vh, scale, out.data_ptr(), 0 if lse is None else lse.data_ptr(),
         cu_q, cu_k, B, Tq, Tk, H, N, KDA_LATENT_CAUSAL if causal else 0)
-    lib, ref = _library(), _byref(a)
-    if workspace is None and cu_q is not None:
-        need = lib.kda_latent_prefill_workspace_bytes(ref)
+    lib = _library()
+    if workspace is None and cu_seqlens is not None:
+        need = lib.kda_latent_prefill_workspace_bytes(a)
         workspace = _new(need, torch.uint8, dev, stream) if need else None
-    rc = lib.kda_latent_prefill(ref, None if workspace is None else workspace.data_ptr(),
+    rc = lib.kda_latent_prefill(a, None if workspace is None else workspace.data_ptr(),
                                 0 if workspace is None else workspace.numel(), _handle(dev, stream))
     if rc != 0:
         _raise("kda_latent_prefill", rc)
