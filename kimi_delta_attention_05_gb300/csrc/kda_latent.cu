@@ -67,6 +67,7 @@ __global__ void __launch_bounds__(kPlanThreads) kda_latent_plan_kernel(const Pla
   __shared__ int64_t sums[2][kPlanThreads / 32];
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int64_t P = p.page;
+  asm volatile("griddepcontrol.wait;\n" ::: "memory");
   int64_t carry_t = 0, carry_p = 0;
   int bad = 0;
   for (int base = 0; base < p.B; base += kPlanThreads) {
@@ -162,8 +163,9 @@ struct AppendParams {
 };
 
 template <bool kNorm, int kAppendTokens>
-__global__ void __launch_bounds__(256) kda_latent_append_kernel(const AppendParams p) {
+__global__ void __launch_bounds__(256) kda_latent_append_kernel(AppendParams p) {
   __shared__ __align__(16) float w[kLat];
+  asm volatile("griddepcontrol.wait;\n" ::: "memory");
   if (kNorm) {
     for (int i = threadIdx.x; i < kLat; i += 256) w[i] = p.w[i];
     __syncthreads();
@@ -337,6 +339,7 @@ __global__ void __launch_bounds__(1024) kda_latent_blocks_kernel(const int64_t* 
                                                                  int32_t* count, int* status) {
   __shared__ int32_t at[kWorkClasses];
   asm volatile("griddepcontrol.launch_dependents;\n" ::: "memory");
+  asm volatile("griddepcontrol.wait;\n" ::: "memory");
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   for (int i = tid; i < kWorkClasses; i += 1024) at[i] = 0;
   int bad = 0;
@@ -416,8 +419,8 @@ extern "C" int kda_latent_plan(const kda_latent_plan_args* a, void* stream) {
     }
   }
   const int64_t ctas = std::max<int64_t>(1, (a->T + kPlanTokens - 1) / kPlanTokens);
-  kda_latent_plan_kernel<<<(unsigned)ctas, kPlanThreads, smem, s>>>(p);
-  return cudaGetLastError() == cudaSuccess ? KDA_OK : KDA_ERR_LAUNCH;
+  return launch_overlapped(kda_latent_plan_kernel, dim3((unsigned)ctas), kPlanThreads, smem, s, 1, p) ? KDA_OK
+                                                                                                     : KDA_ERR_LAUNCH;
 }
 
 extern "C" int kda_latent_append(const kda_latent_append_args* a, void* stream) {
@@ -440,14 +443,10 @@ extern "C" int kda_latent_append(const kda_latent_append_args* a, void* stream) 
   // with one, 52.9 with two, 57.1 with four); few tokens spread over more warps.
   const int per = a->T > 8 * 152 * 4 ? 2 : 1;
   const unsigned ctas = (unsigned)std::min<int64_t>((a->T + 8 * per - 1) / (8 * per), 152 * 6);
-  if (a->norm_weight) {
-    if (per == 2) kda_latent_append_kernel<true, 2><<<ctas, 256, 0, s>>>(p);
-    else kda_latent_append_kernel<true, 1><<<ctas, 256, 0, s>>>(p);
-  } else {
-    if (per == 2) kda_latent_append_kernel<false, 2><<<ctas, 256, 0, s>>>(p);
-    else kda_latent_append_kernel<false, 1><<<ctas, 256, 0, s>>>(p);
-  }
-  return cudaGetLastError() == cudaSuccess ? KDA_OK : KDA_ERR_LAUNCH;
+  void (*kernel)(AppendParams) =
+      a->norm_weight ? (per == 2 ? kda_latent_append_kernel<true, 2> : kda_latent_append_kernel<true, 1>)
+                     : (per == 2 ? kda_latent_append_kernel<false, 2> : kda_latent_append_kernel<false, 1>);
+  return launch_overlapped(kernel, dim3(ctas), 256, 0, s, 1, p) ? KDA_OK : KDA_ERR_LAUNCH;
 }
 
 extern "C" size_t kda_latent_decode_workspace_bytes(const kda_latent_decode_args* a) {
@@ -514,8 +513,9 @@ extern "C" int kda_latent_prefill(const kda_latent_prefill_args* a, void* worksp
   if (a->cu_seqlens_q) {
     int32_t* count = static_cast<int32_t*>(workspace);
     PrefillItem* items = reinterpret_cast<PrefillItem*>(static_cast<unsigned char*>(workspace) + 256);
-    kda_latent_blocks_kernel<<<1, 1024, 0, s>>>(a->cu_seqlens_q, a->cu_seqlens_k, a->N, a->Tq, a->Tk, p.causal,
-                                                p.pairs ? 2 * kPrefillRows : kPrefillRows, items, count, status);
+    if (!launch_overlapped(kda_latent_blocks_kernel, dim3(1), 1024, 0, s, 1, a->cu_seqlens_q, a->cu_seqlens_k, a->N, a->Tq,
+                           a->Tk, p.causal, p.pairs ? 2 * kPrefillRows : kPrefillRows, items, count, status))
+      return KDA_ERR_LAUNCH;
     p.items = items;
     p.count = count;
   }

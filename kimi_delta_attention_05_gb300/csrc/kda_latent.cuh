@@ -61,6 +61,29 @@ bool prefill_pairs(int64_t rows, int64_t sequences);
 // Query rows of one work item of the expanded form (of single CTAs).
 constexpr int kPrefillRows = 256;
 
+// Launches a kernel whose set-up may overlap the end of the kernel before it in
+// the stream; it waits (griddepcontrol.wait) before it touches memory.
+// cluster: CTAs of a cluster.
+template <class... P, class... A>
+bool launch_overlapped(void (*kernel)(P...), dim3 grid, unsigned threads, size_t smem, cudaStream_t s, unsigned cluster,
+                       A&&... args) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = grid;
+  cfg.blockDim = dim3(threads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = s;
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = cluster;
+  attr[1].val.clusterDim.y = 1;
+  attr[1].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = cluster > 1 ? 2 : 1;
+  return cudaLaunchKernelEx(&cfg, kernel, static_cast<P>(args)...) == cudaSuccess;
+}
+
 size_t decode_workspace_bytes(const DecodeParams& p);
 // false: a tensor map could not be made or a launch attribute set (nothing launched)
 bool launch_latent_decode(const DecodeParams& p, cudaStream_t s);

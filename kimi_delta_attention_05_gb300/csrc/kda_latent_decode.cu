@@ -201,6 +201,8 @@ __global__ void __launch_bounds__(kDecThreads, 1)
     prefetch_map(&maps.q);
     prefetch_map(&maps.cache);
   }
+  // (set up while the kernel before this one ends; nothing it wrote is read until here)
+  asm volatile("griddepcontrol.wait;\n" ::: "memory");
   // each thread sums a run of requests; a scan over threads gives the total
   // (hence the shares' size) and the run that holds this share's first tile
   const int run = (p.B + kDecThreads - 1) / kDecThreads;
@@ -616,6 +618,7 @@ __global__ void __launch_bounds__(kDecThreads, 1)
 // requests in many parts; else a warp a row (16 dimensions a lane).
 template <bool kWide>
 __global__ void __launch_bounds__(512) kda_latent_join_kernel(const DecodeParams p, const DecodePlan pl, int n) {
+  asm volatile("griddepcontrol.launch_dependents;\n" ::: "memory");
   asm volatile("griddepcontrol.wait;\n" ::: "memory");
   const int4 info = pl.split[blockIdx.x];
   if (info.x < 0) return;
@@ -754,22 +757,15 @@ bool launch_dec(const DecodeParams& p, const DecLayout& d, const DecodeMaps& map
                                    DecCfg<N>::kSmem);
   });
   if (rc[dev] != cudaSuccess) return false;
-  kda_latent_decode_kernel<N><<<ctas, kDecThreads, DecCfg<N>::kSmem, s>>>(p, d.plan, maps);
+  if (!launch_overlapped(kda_latent_decode_kernel<N>, dim3(ctas), kDecThreads, DecCfg<N>::kSmem, s, 1, p, d.plan, maps))
+    return false;
   if (d.plan.whole) return true;  // nothing to join
-  cudaLaunchConfig_t cfg = {};
   // a row a CTA where a request is in more than four parts on average, else a row a warp
   const bool wide = (int64_t)p.B * 4 < d.plan.shares;
   const int most = std::min(N, p.R * p.H);
-  cfg.gridDim = dim3((unsigned)d.joins, (unsigned)(wide ? most : (most + 15) / 16));
-  cfg.blockDim = dim3(512);
-  cfg.stream = s;
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[0].val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = attr;
-  cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, wide ? kda_latent_join_kernel<true> : kda_latent_join_kernel<false>, p, d.plan, N) ==
-         cudaSuccess;
+  const dim3 grid((unsigned)d.joins, (unsigned)(wide ? most : (most + 15) / 16));
+  return launch_overlapped(wide ? kda_latent_join_kernel<true> : kda_latent_join_kernel<false>, grid, 512, 0, s, 1, p,
+                           d.plan, N);
 }
 
 }  // namespace

@@ -201,7 +201,8 @@ __global__ void __launch_bounds__(kPreThreads, 1)
     prefetch_map(&maps.pe);
     prefetch_map(&maps.v);
   }
-  asm volatile("griddepcontrol.wait;\n" ::: "memory");  // (packed: the list of blocks)
+  // (set up while the kernel before this one ends; packed, that is the one that lists the blocks)
+  asm volatile("griddepcontrol.wait;\n" ::: "memory");
   tc_fence_before();
   __syncthreads();
   if (kPair) cluster_sync();  // the other CTA's barriers are ready too
@@ -723,26 +724,9 @@ bool launch_prefill(const PrefillParams& p, cudaStream_t s) {
         !encode_map_bf16(&maps.pe, p.k_pe, 2, dims, strides, box))
       return false;
   }
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((unsigned)(kPair ? 2 * std::min<int64_t>(items, sms / 2) : std::min<int64_t>(items, sms)));
-  cfg.blockDim = dim3(kPreThreads);
-  cfg.dynamicSmemBytes = kPreSmem;
-  cfg.stream = s;
-  cudaLaunchAttribute attr[2];
-  int n = 0;
-  if (p.items) {  // packed: set up while the list of blocks is made
-    attr[n].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr[n++].val.programmaticStreamSerializationAllowed = 1;
-  }
-  if (kPair) {
-    attr[n].id = cudaLaunchAttributeClusterDimension;
-    attr[n].val.clusterDim.x = 2;
-    attr[n].val.clusterDim.y = 1;
-    attr[n++].val.clusterDim.z = 1;
-  }
-  cfg.attrs = attr;
-  cfg.numAttrs = n;
-  return cudaLaunchKernelEx(&cfg, kda_latent_prefill_kernel<kPair>, p, per, maps) == cudaSuccess;
+  const unsigned ctas = (unsigned)(kPair ? 2 * std::min<int64_t>(items, sms / 2) : std::min<int64_t>(items, sms));
+  return launch_overlapped(kda_latent_prefill_kernel<kPair>, dim3(ctas), kPreThreads, kPreSmem, s, kPair ? 2 : 1, p, per,
+                           maps);
 }
 
 }  // namespace
