@@ -378,7 +378,10 @@ __global__ void __launch_bounds__(1024) kda_latent_blocks_kernel(const int64_t* 
         at[i] = carry + s - c;
         carry += __shfl_sync(0xffffffffu, s, 31);
       }
-      if (lane == 0) *count = carry;
+      if (lane == 0) {
+        count[0] = carry;
+        count[1] = 0;
+      }
     }
     __syncthreads();
   }

@@ -47,7 +47,7 @@ struct PrefillParams {
   float* lse;                       // [tokens, H] or nullptr
   const int64_t *cu_q, *cu_k;       // [N + 1] or nullptr (dense)
   const PrefillItem* items;         // query blocks, most work first (packed only)
-  const int32_t* count;             // their number (packed only)
+  int32_t* count;                   // their number, and how many were taken by counter (packed only)
   int64_t B, Tq, Tk, N;
   int H;
   int causal;

@@ -35,8 +35,8 @@
 // edge wastes more, so short sequences keep single CTAs.
 //
 // Roles: warps 0-3 and 4-7 softmax and output of the two tiles, warp 8 copies,
-// warp 9 products (of the pair: in its first CTA), two more only fill their
-// warpgroup.  Every wait is bounded; a CTA that gives up sets the status word.
+// warp 9 products (of the pair: in its first CTA), warp 10 the list of items, one
+// more only fills its warpgroup.  Every wait is bounded; a CTA that gives up sets the status word.
 #include <algorithm>
 #include <cstring>
 
@@ -77,8 +77,11 @@ constexpr int kPreBar = kPreRing + (kPreSlots * kPreSlot > kPairStages * kPairSt
 constexpr int kPbFullK0 = 0, kPbFullK = 2, kPbFullV = 4, kPbEmptyK = 6, kPbEmptyV = 8, kPbQ = 10, kPbQEmpty = 11,
               kPbS = 12, kPbP = 14, kPbPv = 16;
 // pairs: by stage; then a barrier for value tiles that end behind the sequence, and for the other weights
-constexpr int kPpFullK = 18, kPpFullV = 21, kPpEmptyK = 24, kPpEmptyV = 27, kPpTail = 30, kPbP2 = 31, kPbars = 33;
-constexpr int kPreTmem = kPreBar + 8 * kPbars;
+constexpr int kPpFullK = 18, kPpFullV = 21, kPpEmptyK = 24, kPpEmptyV = 27, kPpTail = 30, kPbP2 = 31;
+// the next item: written, and read by every role
+constexpr int kPbItem = 33, kPbItemRead = 34, kPbars = 35;
+constexpr int kPreItem = (kPreBar + 8 * kPbars + 15) / 16 * 16;
+constexpr int kPreTmem = kPreItem + 32;
 constexpr int kPreAbort = kPreTmem + 8;
 constexpr int kPreSmem = kPreAbort + 8;
 static_assert(kPreRing % 1024 == 0 && kPairStage % 1024 == 0 && kPreSmem <= 232448, "shared memory");
@@ -112,13 +115,18 @@ __device__ __forceinline__ float max3(float a, float b, float c) {
 
 // One item as every role sees it: a block of rows of a sequence and a head.
 struct PreItem {
-  int64_t q0, k0;    // first query and key of the sequence
-  int lq, lk, r0, h;  // its lengths, the block's first row, head
-  int n0, n1, nt;    // key tiles of the two query tiles (0 where a tile has no row or its rows see nothing)
+  int q0, k0, lq, lk;  // first query and key of the sequence, its lengths
+  int r0, h;           // the block's first row; head, or -1 behind the last item
+  int n0, n1;          // key tiles of the two query tiles (0 where a tile has no row or its rows see nothing)
+  __device__ __forceinline__ int nt() const { return max(n0, n1); }
 };
 
-// The items of a CTA or pair: every grid-th of the list (most work first), each
-// second round backwards, so that the work of all is nearly the same.
+// The items of a CTA or pair, most work first: every grid-th of the list, each
+// second round backwards, so that the work of all is nearly the same.  Packed
+// sequences' single CTAs take them as they come instead, by a counter behind the
+// list's length: an item's time is its tiles' and about two tiles' more, which the
+// order does not know, and the CTAs ended 20% apart (24 sequences of up to 2048
+// tokens, 16 heads: 186 us in the fixed order, 167 by the counter).
 template <bool kPair>
 struct PreWalk {
   static constexpr int kTileRows = kPair ? 2 * kPreRows : kPreRows;
@@ -130,24 +138,29 @@ struct PreWalk {
   __device__ __forceinline__ bool next(const PrefillParams& p, int64_t per, PreItem& it) {
     const int64_t wide = kPair ? gridDim.x >> 1 : gridDim.x, mine = kPair ? blockIdx.x >> 1 : blockIdx.x;
     const int64_t base = round * wide;
-    const int64_t idx = base + ((round & 1) ? wide - 1 - mine : mine);
+    int64_t idx = base + ((round & 1) ? wide - 1 - mine : mine);
+    if (!kPair && p.items && round > 0) {  // (all lanes of a warp are here)
+      int next = 0;
+      if ((threadIdx.x & 31) == 0) next = atomicAdd(p.count + 1, 1);
+      idx = wide + __shfl_sync(0xffffffffu, next, 0);
+    }
     ++round;
-    if (base >= total || idx >= total) return false;  // (only the last round is not full)
+    if (idx >= total) return false;
     if (p.items) {
       const uint32_t e = (uint32_t)idx / (uint32_t)p.H;
       it.h = (int)((uint32_t)idx - e * (uint32_t)p.H);
-      const int4 a = __ldg(reinterpret_cast<const int4*>(p.items + e));
+      const int4 a = *reinterpret_cast<const int4*>(p.items + e);
       it.q0 = a.x;
       it.k0 = a.y;
       it.lq = a.z;
       it.lk = a.w;
-      it.r0 = __ldg(&p.items[e].r0);
+      it.r0 = p.items[e].r0;
     } else {  // later blocks of a causal sequence see more keys: they go first
       const uint32_t bh = (uint32_t)(p.B * p.H), back = (uint32_t)idx / bh, x = (uint32_t)idx - back * bh;
       const uint32_t n = x / (uint32_t)p.H;
       it.h = (int)(x - n * (uint32_t)p.H);
-      it.q0 = (int64_t)n * p.Tq;
-      it.k0 = (int64_t)n * p.Tk;
+      it.q0 = (int)(n * p.Tq);
+      it.k0 = (int)(n * p.Tk);
       it.lq = (int)p.Tq;
       it.lk = (int)p.Tk;
       it.r0 = (int)(per - 1 - back) * 2 * kTileRows;
@@ -161,7 +174,6 @@ struct PreWalk {
     };
     it.n0 = tiles_of(0);
     it.n1 = tiles_of(1);
-    it.nt = max(it.n0, it.n1);
     return true;
   }
 };
@@ -178,8 +190,9 @@ __global__ void __launch_bounds__(kPreThreads, 1)
   if (tid == 0) {
     for (int i = 0; i < kPbars; ++i) {
       uint32_t n = 1;
-      if (i == kPbP || i == kPbP + 1 || i >= kPbP2) n = kPair ? 8 : 4;               // the softmax warps of a tile
+      if (i == kPbP || i == kPbP + 1 || i == kPbP2 || i == kPbP2 + 1) n = kPair ? 8 : 4;               // the softmax warps of a tile
       if (kPair && (i == kPbQ || (i >= kPpFullK && i < kPpFullK + 2 * kPairStages))) n = 2;  // both CTAs' copies
+      if (i == kPbItemRead) n = kPair && rank ? 9 : 10;  // warps of softmax, copies and, where it issues, products
       mbar_init(bar(i), n);
     }
     *s_abort = (sb & 1023) ? 1 : 0;
@@ -217,8 +230,25 @@ __global__ void __launch_bounds__(kPreThreads, 1)
   };
   // barriers that the issuing CTA waits on, as both CTAs' copies and warps reach them
   auto lead = [&](int i) { return kPair ? map_rank(bar(i), 0) : bar(i); };
-  PreWalk<kPair> walk;
-  walk.start(p, p.B * per);
+  // These waits last as long as an item, which may be longer than one wait is
+  // allowed to; a timeout of another ends them.
+  auto wait_long = [&](uint32_t b, uint32_t parity) {
+    bool there = mbar_try_wait(b, parity);
+    for (int k = 0; k < 512 && !there && !*s_abort; ++k) there = mbar_wait_bounded(b, parity);
+    return __all_sync(0xffffffffu, there) != 0;
+  };
+  // The next item, for all lanes of a warp; false behind the last one or after a timeout.
+  uint32_t taken = 0;
+  auto take = [&](PreItem& it) {
+    if (!wait_long(bar(kPbItem), taken & 1)) return false;
+    ++taken;
+    const int4* from = reinterpret_cast<const int4*>(smem + kPreItem);
+    const int4 a = from[0], b = from[1];
+    __syncwarp();
+    if (lane == 0) mbar_arrive(bar(kPbItemRead));
+    it = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
+    return it.h >= 0;
+  };
   PreItem it;
   int g = 0;  // key tiles so far, over all items
 
@@ -235,9 +265,10 @@ __global__ void __launch_bounds__(kPreThreads, 1)
     };
     int s = 0;
     uint32_t ph = 1;  // parity of the stage's use before
-    while (!gone && walk.next(p, per, it)) {
-      for (int i = 0; i < it.nt && !gone; ++i, ++g) {
-        const int key = (int)(it.k0 + (int64_t)i * kPreKeys);
+    while (!gone && take(it)) {
+      const int nt = it.nt();
+      for (int i = 0; i < nt && !gone; ++i, ++g) {
+        const int key = it.k0 + i * kPreKeys;
         const uint32_t dst = sb + kPreRing + s * kPairStage;
         if (g >= kPairStages) wait(bar(kPpEmptyK + s), ph);
         if (stop()) break;
@@ -296,6 +327,7 @@ __global__ void __launch_bounds__(kPreThreads, 1)
         }
       }
     }
+    stop();
     // After a timeout: copies still in flight land in memory of this CTA, which stays until
     // the cluster's last barrier; they are few and unconditional, so a bounded pause is enough.
     if (gone && lane == 0) {
@@ -358,13 +390,14 @@ __global__ void __launch_bounds__(kPreThreads, 1)
         if (elect_one()) mma_commit<true>(bar(b));
         __syncwarp();
       };
-      while (walk.next(p, per, it)) {
-        if (it.nt == 0) continue;
+      while (take(it)) {
+        const int nt = it.nt();
+        if (nt == 0) continue;
         wait_pair(bar(kPbQ), (uint32_t)(q & 1));
         ++q;
-        for (int i = 0; i <= it.nt; ++i) {
-          const bool more = i < it.nt;
-          if (more) {
+        for (int i = 0; i <= nt; ++i) {
+          const bool keys = i < nt;
+          if (keys) {
             wait_pair(bar(kPpFullK + s), ph);
             if (i < it.n0) scores(0);
           }
@@ -372,10 +405,10 @@ __global__ void __launch_bounds__(kPreThreads, 1)
             if (i - 1 < it.n1) values(1, s_prev, done1, i == 1);
             done_with(kPpEmptyV + s_prev);
           }
-          if (!more) break;
+          if (!keys) break;
           if (i < it.n1) scores(1);
           done_with(kPpEmptyK + s);
-          if (i + 1 == it.nt) done_with(kPbQEmpty);
+          if (i + 1 == nt) done_with(kPbQEmpty);
           wait_pair(bar(kPpFullV + s), ph);
           if (it.lk < (i + 1) * kPreKeys) mbar_try_wait_cluster(bar(kPpFullV + s), ph);  // acquires the cleared rows
           if (i < it.n0) values(0, s, done0, i == 0);
@@ -401,9 +434,10 @@ __global__ void __launch_bounds__(kPreThreads, 1)
       gone = __any_sync(0xffffffffu, *s_abort != 0);
       return gone;
     };
-    while (!gone && walk.next(p, per, it)) {
-      for (int i = 0; i < it.nt && !gone; ++i, ++g) {
-        const int key = (int)(it.k0 + (int64_t)i * kPreKeys), s = g & 1;
+    while (!gone && take(it)) {
+      const int nt = it.nt();
+      for (int i = 0; i < nt && !gone; ++i, ++g) {
+        const int key = it.k0 + i * kPreKeys, s = g & 1;
         auto dst = [&](int c) { return sb + kPreRing + ((5 * g + c) % kPreSlots) * kPreSlot; };
         if (lane == 0) {
           mbar_expect_tx(bar(kPbFullK0 + s), kPreSlot);
@@ -440,6 +474,7 @@ __global__ void __launch_bounds__(kPreThreads, 1)
         ++values;
       }
     }
+    stop();
     // After a timeout: let the copies still in flight land before leaving.
     if (gone && lane == 0) {
       auto drain = [&](int b, int n) {
@@ -512,23 +547,24 @@ __global__ void __launch_bounds__(kPreThreads, 1)
       if (elect_one()) mma_commit<false>(bar(b));
       __syncwarp();
     };
-    while (walk.next(p, per, it)) {
-      if (it.nt == 0) continue;
+    while (take(it)) {
+      const int nt = it.nt();
+      if (nt == 0) continue;
       wait(bar(kPbQ), (uint32_t)(q & 1));
       ++q;
       __syncwarp();
-      for (int i = 0; i <= it.nt; ++i) {
+      for (int i = 0; i <= nt; ++i) {
         const int tile = g + i;
-        const bool more = i < it.nt;
-        if (more && i < it.n0) scores(0, tile, true);
+        const bool keys = i < nt;
+        if (keys && i < it.n0) scores(0, tile, true);
         if (i > 0) {
           if (i - 1 < it.n1) values(1, tile - 1, done1, i == 1);
           done_with(kPbEmptyV + ((tile - 1) & 1));
         }
-        if (!more) break;
+        if (!keys) break;
         if (i < it.n1) scores(1, tile, i >= it.n0);
         done_with(kPbEmptyK + (tile & 1));
-        if (i + 1 == it.nt) done_with(kPbQEmpty);
+        if (i + 1 == nt) done_with(kPbQEmpty);
         full_wait(kPbFullV, tile);
         const int valid = it.lk - i * kPreKeys;
         if (valid < kPreKeys) {
@@ -543,11 +579,29 @@ __global__ void __launch_bounds__(kPreThreads, 1)
         }
         if (i < it.n0) values(0, tile, done0, i == 0);
       }
-      g += it.nt;
+      g += nt;
     }
     // the last products complete before tensor memory is freed
     if (done0 > 0) mbar_wait_bounded(bar(kPbPv), (uint32_t)((done0 - 1) & 1));
     if (done1 > 0) mbar_wait_bounded(bar(kPbPv + 1), (uint32_t)((done1 - 1) & 1));
+  } else if (warp == 10) {
+    // ---- the items: the next one is found while the others work on theirs (found by each
+    //      role for itself, it cost the products some 3000 cycles between two items) ----
+    PreWalk<kPair> walk;
+    walk.start(p, p.B * per);
+    bool have = true;
+    for (uint32_t n = 0; have; ++n) {
+      have = walk.next(p, per, it);
+      if (!have) it.h = -1;
+      if (n > 0 && !wait_long(bar(kPbItemRead), (n - 1) & 1)) break;
+      if (lane == 0) {
+        int4* to = reinterpret_cast<int4*>(smem + kPreItem);
+        to[0] = make_int4(it.q0, it.k0, it.lq, it.lk);
+        to[1] = make_int4(it.r0, it.h, it.n0, it.n1);
+        mbar_arrive(bar(kPbItem));
+      }
+      __syncwarp();
+    }
   }
   } else {
     asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;\n" ::"n"(kPreRegsMany));
@@ -567,7 +621,7 @@ __global__ void __launch_bounds__(kPreThreads, 1)
         else mbar_arrive(bar(b));
       }
     };
-    while (walk.next(p, per, it)) {
+    while (take(it)) {
       const int n = t == 0 ? it.n0 : it.n1;
       const int row = it.r0 + (kPair ? 2 * t + (int)rank : t) * kPreRows + q * 32 + lane;  // query within the sequence
       const int lim = p.causal ? min(it.lk, row + it.lk - it.lq + 1) : it.lk;
@@ -643,7 +697,7 @@ __global__ void __launch_bounds__(kPreThreads, 1)
         tc_fence_after();
       }
       const float inv = l > 0.f ? 1.0f / l : (l == 0.f ? 0.f : l);
-      const int64_t at = (it.q0 + row) * p.H + it.h;
+      const int64_t at = ((int64_t)it.q0 + row) * p.H + it.h;
 #pragma unroll 1
       for (int c = 0; c < 128; c += 64) {
         float o[64];
