@@ -239,6 +239,8 @@ __global__ void __launch_bounds__(kPreThreads, 1)
   };
   // The next item, for all lanes of a warp; false behind the last one or after a timeout.
   uint32_t taken = 0;
+  // Broadcast, so that the compiler knows the values as uniform (the products are then issued without moves to
+  // uniform registers: 368 -> 361 us on the 8192-token prompt, 191 -> 185 on two pieces of 1024 behind 15360).
   auto take = [&](PreItem& it) {
     if (!wait_long(bar(kPbItem), taken & 1)) return false;
     ++taken;
@@ -246,7 +248,8 @@ __global__ void __launch_bounds__(kPreThreads, 1)
     const int4 a = from[0], b = from[1];
     __syncwarp();
     if (lane == 0) mbar_arrive(bar(kPbItemRead));
-    it = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
+    auto same = [](int x) { return __shfl_sync(0xffffffffu, x, 0); };
+    it = {same(a.x), same(a.y), same(a.z), same(a.w), same(b.x), same(b.y), same(b.z), same(b.w)};
     return it.h >= 0;
   };
   PreItem it;
