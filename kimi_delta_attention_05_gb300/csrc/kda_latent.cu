@@ -320,9 +320,12 @@ size_t prefill_workspace(const kda_latent_prefill_args* a) {
 
 }  // namespace
 
-// The query blocks of packed sequences, those with most work first (so that
-// the persistent attention kernel ends evenly), by a counting sort over classes
-// of equal work (a sixteenth of an octave from 32 key tiles on).  Checks 0 =
+// The query blocks of packed sequences, by a counting sort over classes of equal
+// work (a sixteenth of an octave from 32 key tiles on).  Single CTAs take them as
+// they come: the sequences with most keys first, the blocks of each together, last
+// block first (keys and values are then found in L2: 24 sequences of up to 2048
+// tokens, 16 heads, 161 us against 165 with single blocks by their work).  Pairs take
+// every grid-th: blocks with most work first, so that all end evenly.  Checks 0 =
 // cu[0] <= ... <= cu[N] = T of both offset arrays first: a violation sets the
 // status word and leaves no block, so nothing is written.  One block; the order
 // within a class is that of the atomics, and no result depends on it.
@@ -335,8 +338,8 @@ __device__ __forceinline__ int work_class(int tiles) {
 
 __global__ void __launch_bounds__(1024) kda_latent_blocks_kernel(const int64_t* cu_q, const int64_t* cu_k, int64_t N,
                                                                  int64_t Tq, int64_t Tk, int causal, int rows,
-                                                                 PrefillItem* items,
-                                                                 int32_t* count, int* status) {
+                                                                 int together, PrefillItem* items, int32_t* count,
+                                                                 int* status) {
   __shared__ int32_t at[kWorkClasses];
   asm volatile("griddepcontrol.launch_dependents;\n" ::: "memory");
   asm volatile("griddepcontrol.wait;\n" ::: "memory");
@@ -359,6 +362,19 @@ __global__ void __launch_bounds__(1024) kda_latent_blocks_kernel(const int64_t* 
       it.k0 = (int)cu_k[n];
       it.lk = (int)(cu_k[n + 1] - cu_k[n]);
       it.pad[0] = it.pad[1] = it.pad[2] = 0;
+      if (together) {
+        const int blocks = (int)(((int64_t)it.lq + rows - 1) / rows);
+        int* place = &at[work_class(it.lk / 64)];
+        int first = 0;
+        if (lane == 0) first = atomicAdd(place, blocks);
+        if (pass == 0) continue;
+        first = __shfl_sync(0xffffffffu, first, 0);
+        for (int j = lane; j < blocks; j += 32) {
+          it.r0 = (blocks - 1 - j) * rows;
+          items[first + j] = it;
+        }
+        continue;
+      }
       for (int64_t r = (int64_t)lane * rows; r < it.lq; r += 32 * rows) {
         it.r0 = (int)r;
         int tiles = 0;
@@ -511,13 +527,13 @@ extern "C" int kda_latent_prefill(const kda_latent_prefill_args* a, void* worksp
   p.N = a->N;
   p.H = (int)a->H;
   p.causal = (a->flags & KDA_LATENT_CAUSAL) ? 1 : 0;
-  p.pairs = prefill_pairs(a->B * a->Tq, a->N) ? 1 : 0;
+  p.pairs = prefill_pairs(a->B * a->Tq, a->N, a->cu_seqlens_q != nullptr) ? 1 : 0;
   p.status = status;
   if (a->cu_seqlens_q) {
     int32_t* count = static_cast<int32_t*>(workspace);
     PrefillItem* items = reinterpret_cast<PrefillItem*>(static_cast<unsigned char*>(workspace) + 256);
     if (!launch_overlapped(kda_latent_blocks_kernel, dim3(1), 1024, 0, s, 1, a->cu_seqlens_q, a->cu_seqlens_k, a->N, a->Tq,
-                           a->Tk, p.causal, p.pairs ? 2 * kPrefillRows : kPrefillRows, items, count, status))
+                           a->Tk, p.causal, p.pairs ? 2 * kPrefillRows : kPrefillRows, !p.pairs, items, count, status))
       return KDA_ERR_LAUNCH;
     p.items = items;
     p.count = count;

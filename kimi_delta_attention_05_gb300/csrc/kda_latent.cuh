@@ -46,7 +46,7 @@ struct PrefillParams {
   uint16_t* out;                    // bf16 [tokens, H, 128]
   float* lse;                       // [tokens, H] or nullptr
   const int64_t *cu_q, *cu_k;       // [N + 1] or nullptr (dense)
-  const PrefillItem* items;         // query blocks, most work first (packed only)
+  const PrefillItem* items;         // query blocks in the order of their work (packed only)
   int32_t* count;                   // their number, and how many were taken by counter (packed only)
   int64_t B, Tq, Tk, N;
   int H;
@@ -56,7 +56,7 @@ struct PrefillParams {
 };
 
 // Whether `rows` queries of `sequences` sequences go to CTA pairs.
-bool prefill_pairs(int64_t rows, int64_t sequences);
+bool prefill_pairs(int64_t rows, int64_t sequences, bool packed);
 
 // Query rows of one work item of the expanded form (of single CTAs).
 constexpr int kPrefillRows = 256;

@@ -386,11 +386,20 @@ def test_prefill_long_packed_and_batched():
     _prefill([1060] * 2, [1200] * 2, 2, True, False, seed=6, std=20.0)
 
 
+@pytest.mark.parametrize("lq,lk,heads,causal", [([700, 30, 300, 0, 513, 256], [720, 30, 40, 0, 513, 256], 24, True),
+                                                ([300, 30, 300, 0, 256], [300, 30, 40, 0, 513], 24, False),
+                                                ([2300, 1900, 2100], [2400, 300, 2100], 6, True)])
+def test_prefill_packed_in_many_blocks(lq, lk, heads, causal):
+    """More blocks of rows and heads than the GPU has SMs (or pairs of them), so that each works on several in
+    turn; some blocks in between see no key."""
+    _prefill(lq, lk, heads, causal, True, seed=7)
+
+
 def test_prefill_without_keys():
     _prefill([40], [0], 2, True, False)
 
 
-@pytest.mark.parametrize("a,b,n", [(70, 220, 310), (700, 2750, 3450)])
+@pytest.mark.parametrize("a,b,n", [(70, 220, 310), (700, 2750, 3450), (900, 4200, 6300)])
 def test_prefill_neighbours_do_not_touch(a, b, n):
     """NaN and Inf in the sequence before and after (queries, keys, values) stay there."""
     gen = torch.Generator().manual_seed(3)
