@@ -387,7 +387,7 @@ def test_prefill_long_packed_and_batched():
 
 
 @pytest.mark.parametrize("lq,lk,heads,causal", [([700, 30, 300, 0, 513, 256], [720, 30, 40, 0, 513, 256], 24, True),
-                                                ([300, 30, 300, 0, 256], [300, 30, 40, 0, 513], 24, False),
+                                                ([300, 30, 300, 0, 256], [300, 30, 40, 0, 513], 32, False),
                                                 ([2300, 1900, 2100], [2400, 300, 2100], 6, True)])
 def test_prefill_packed_in_many_blocks(lq, lk, heads, causal):
     """More blocks of rows and heads than the GPU has SMs (or pairs of them), so that each works on several in
