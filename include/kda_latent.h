@@ -166,6 +166,10 @@ int kda_latent_decode(const kda_latent_decode_args *args, void *workspace, size_
  *         a violation of either sets KDA_ERR_BAD_SEQLENS and nothing is written.
  * Rows of other sequences (and past the tensors) never touch a result; within a
  * sequence, keys and values have to be finite.
+ *
+ * workspace: kda_latent_prefill_workspace_bytes bytes, aligned to 256.  A dense call
+ * with few blocks of queries and many keys has its keys split over the SMs and the
+ * parts joined, for which it needs some; with workspace NULL it is not split.
  */
 #define KDA_LATENT_CAUSAL 0x1u
 typedef struct kda_latent_prefill_args {

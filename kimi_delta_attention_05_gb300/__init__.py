@@ -8,7 +8,7 @@ workload generator.
 from .kda import (kda_bwd, kda_fwd, kda_fwd_host, kda_fwd_recurrent, get_status, load_library,  # noqa: F401
                   KdaError, workspace_bytes)
 from .latent import (latent_append, latent_decode, latent_decode_workspace_bytes, latent_plan,  # noqa: F401
-                     latent_prefill)
+                     latent_prefill, latent_prefill_workspace_bytes)
 from . import workloads  # noqa: F401
 
 __version__ = "0.1.0"

@@ -314,8 +314,24 @@ int check_prefill(const kda_latent_prefill_args* a) {
 // Query blocks of packed sequences: at most one a sequence more than the rows fill.
 int64_t prefill_blocks(const kda_latent_prefill_args* a) { return a->Tq / kPrefillRows + a->N; }
 
+// The sizes and the form of a call.
+PrefillParams prefill_shape(const kda_latent_prefill_args* a) {
+  PrefillParams p = {};
+  p.cu_q = a->cu_seqlens_q;
+  p.cu_k = a->cu_seqlens_k;
+  p.B = a->B;
+  p.Tq = a->Tq;
+  p.Tk = a->Tk;
+  p.N = a->N;
+  p.H = (int)a->H;
+  p.causal = (a->flags & KDA_LATENT_CAUSAL) ? 1 : 0;
+  p.pairs = prefill_pairs(a->B * a->Tq, a->N, a->cu_seqlens_q != nullptr) ? 1 : 0;
+  return p;
+}
+
 size_t prefill_workspace(const kda_latent_prefill_args* a) {
-  return a->cu_seqlens_q ? 256 + ((size_t)prefill_blocks(a) * sizeof(PrefillItem) + 255) / 256 * 256 : 0;
+  if (!a->cu_seqlens_q) return prefill_split_bytes(prefill_shape(a));
+  return 256 + ((size_t)prefill_blocks(a) * sizeof(PrefillItem) + 255) / 256 * 256;
 }
 
 }  // namespace
@@ -497,12 +513,14 @@ extern "C" int kda_latent_prefill(const kda_latent_prefill_args* a, void* worksp
   const int rc = check_prefill(a);
   if (rc != KDA_OK) return rc;
   const size_t need = prefill_workspace(a);
-  if (need > 0 && (!workspace || !al(workspace, 256) || workspace_bytes < need)) return KDA_ERR_WORKSPACE;
+  // (a dense call without one is not split)
+  const bool given = a->cu_seqlens_q || workspace;
+  if (given && need > 0 && (!workspace || !al(workspace, 256) || workspace_bytes < need)) return KDA_ERR_WORKSPACE;
   if (a->N == 0 || a->H == 0 || (!a->cu_seqlens_q && a->Tq == 0)) return KDA_OK;
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
   int* status = status_slot(s);
   if (!status) return KDA_ERR_LAUNCH;
-  PrefillParams p;
+  PrefillParams p = prefill_shape(a);
   p.q = static_cast<const uint16_t*>(a->q);
   p.k = static_cast<const uint16_t*>(a->k);
   p.k_pe = static_cast<const uint16_t*>(a->k_pe);
@@ -517,18 +535,8 @@ extern "C" int kda_latent_prefill(const kda_latent_prefill_args* a, void* worksp
   p.scale_log2 = a->scale * kLog2e;
   p.out = static_cast<uint16_t*>(a->out);
   p.lse = a->lse;
-  p.cu_q = a->cu_seqlens_q;
-  p.cu_k = a->cu_seqlens_k;
-  p.items = nullptr;
-  p.count = nullptr;
-  p.B = a->B;
-  p.Tq = a->Tq;
-  p.Tk = a->Tk;
-  p.N = a->N;
-  p.H = (int)a->H;
-  p.causal = (a->flags & KDA_LATENT_CAUSAL) ? 1 : 0;
-  p.pairs = prefill_pairs(a->B * a->Tq, a->N, a->cu_seqlens_q != nullptr) ? 1 : 0;
   p.status = status;
+  if (!a->cu_seqlens_q && need > 0) p.part = static_cast<float*>(workspace);
   if (a->cu_seqlens_q) {
     int32_t* count = static_cast<int32_t*>(workspace);
     PrefillItem* items = reinterpret_cast<PrefillItem*>(static_cast<unsigned char*>(workspace) + 256);

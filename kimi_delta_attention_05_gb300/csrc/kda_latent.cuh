@@ -52,11 +52,16 @@ struct PrefillParams {
   int H;
   int causal;
   int pairs;                        // CTA pairs and items of 2 kPrefillRows rows
+  float* part;                      // partial rows of a split call, or nullptr
   int* status;
 };
 
 // Whether `rows` queries of `sequences` sequences go to CTA pairs.
 bool prefill_pairs(int64_t rows, int64_t sequences, bool packed);
+
+// Bytes that a split dense call needs for its partial rows; 0: it is not split.
+size_t prefill_split_bytes(const PrefillParams& p);
+constexpr int64_t kPrefillSplitKeys = 4096;  // fewer keys are never split
 
 // Query rows of one work item of the expanded form (of single CTAs).
 constexpr int kPrefillRows = 256;

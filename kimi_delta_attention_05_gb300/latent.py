@@ -293,6 +293,9 @@ def _token_stride(shape, strides, row, name):
     return strides[1] if T > 1 else row
 
 
+_SPLIT_KEYS = 4096  # dense calls with fewer keys need no workspace
+
+
 def latent_prefill(q, k, k_pe, v, scale, out=None, lse=None, cu_seqlens=None, cu_seqlens_k=None, *, causal=True,
                    workspace=None, stream=None):
     """Expanded attention of prompts; returns ``out``.
@@ -303,7 +306,8 @@ def latent_prefill(q, k, k_pe, v, scale, out=None, lse=None, cu_seqlens=None, cu
     [N + 1] packs sequences (B == 1); cu_seqlens_k (default: cu_seqlens) gives
     the keys' own offsets where context precedes the queries.  Query i sees the
     keys j <= i + Lk - Lq, or all with ``causal=False``.  out bf16 [B, Tq, H,
-    128]; lse an optional fp32 [B, Tq, H] tensor to be written."""
+    128]; lse an optional fp32 [B, Tq, H] tensor to be written.  ``workspace``: an
+    optional uint8 tensor of at least :func:`latent_prefill_workspace_bytes` bytes."""
     dev = _gpu(q, "q")
     _on(q, _bf16, 4, dev, "q")
     _on(k, _bf16, 4, dev, "k")
@@ -354,7 +358,7 @@ def latent_prefill(q, k, k_pe, v, scale, out=None, lse=None, cu_seqlens=None, cu
         _token_stride(k_shape, vs, H * vh, "v"), vh, scale, out.data_ptr(), 0 if lse is None else lse.data_ptr(),
         cu_q, cu_k, B, Tq, Tk, H, N, KDA_LATENT_CAUSAL if causal else 0)
     lib = _library()
-    if workspace is None and cu_seqlens is not None:
+    if workspace is None and (cu_seqlens is not None or Tk >= _SPLIT_KEYS):
         need = lib.kda_latent_prefill_workspace_bytes(a)
         workspace = _new(need, torch.uint8, dev, stream) if need else None
     rc = lib.kda_latent_prefill(a, None if workspace is None else workspace.data_ptr(),
@@ -362,3 +366,11 @@ def latent_prefill(q, k, k_pe, v, scale, out=None, lse=None, cu_seqlens=None, cu
     if rc != 0:
         _raise("kda_latent_prefill", rc)
     return out
+
+
+def latent_prefill_workspace_bytes(B, Tq, Tk, H, sequences=None, *, causal=True):
+    """Workspace bytes of :func:`latent_prefill` for these sizes on the current device; ``sequences``: how many are packed."""
+    cu = 0 if sequences is None else 16
+    return int(_library().kda_latent_prefill_workspace_bytes(_prefill_block(
+        16, 16, 16, 16, LATENT_QK_DIM * H, LATENT_QK_DIM, 128 * H, 128, LATENT_PE_DIM, 128 * H, 128, 1.0, 16, 0, cu, cu,
+        B, Tq, Tk, H, B if sequences is None else sequences, KDA_LATENT_CAUSAL if causal else 0)))

@@ -395,6 +395,33 @@ def test_prefill_packed_in_many_blocks(lq, lk, heads, causal):
     _prefill(lq, lk, heads, causal, True, seed=7)
 
 
+@pytest.mark.parametrize("lq,lk,heads", [(1, 4096, 1), (130, 5000, 2), (700, 4500, 1), (256, 9000, 3), (1030, 6001, 1),
+                                         (1500, 4300, 2), (4500, 4100, 1)])
+@pytest.mark.parametrize("causal", [True, False])
+def test_prefill_few_rows_many_keys(lq, lk, heads, causal):
+    """Few items with many keys: their key tiles are shared out and the parts joined."""
+    _prefill([lq], [lk], heads, causal, False, seed=lq)
+    _prefill([lq] * 2, [lk] * 2, heads, causal, False, seed=lk, std=8.0)
+
+
+def test_prefill_split_workspace():
+    """Without a workspace a C call is not split; one that is too small is refused; parts do not depend on what
+    the workspace holds."""
+    gen = torch.Generator().manual_seed(9)
+    q, k, pe, v = (_rand(gen, 1, *x).cuda() for x in ((200, 2, 192), (5000, 2, 128), (5000, 64), (5000, 2, 128)))
+    lse = torch.empty(1, 200, 2, device="cuda")
+    out = M.latent_prefill(q, k, pe, v, 0.07, lse=lse)
+    need = M.latent_prefill_workspace_bytes(1, 200, 5000, 2)
+    assert need > 0
+    for fill in (0, 255):
+        ws = torch.full((need,), fill, dtype=torch.uint8, device="cuda")
+        again = torch.empty_like(lse)
+        assert torch.equal(M.latent_prefill(q, k, pe, v, 0.07, lse=again, workspace=ws), out) and torch.equal(again, lse)
+    with pytest.raises(M.KdaError):
+        M.latent_prefill(q, k, pe, v, 0.07, workspace=ws[: need // 2])
+    assert M.latent_prefill_workspace_bytes(1, 200, 1000, 2) == 0 < M.latent_prefill_workspace_bytes(1, 200, 5000, 2, 3)
+
+
 def test_prefill_without_keys():
     _prefill([40], [0], 2, True, False)
 
