@@ -167,9 +167,9 @@ int kda_latent_decode(const kda_latent_decode_args *args, void *workspace, size_
  * Rows of other sequences (and past the tensors) never touch a result; within a
  * sequence, keys and values have to be finite.
  *
- * workspace: kda_latent_prefill_workspace_bytes bytes, aligned to 256.  A dense call
- * with few blocks of queries and many keys has its keys split over the SMs and the
- * parts joined, for which it needs some; with workspace NULL it is not split.
+ * workspace: kda_latent_prefill_workspace_bytes bytes, aligned to 256.  A call with
+ * few blocks of queries and many keys has its keys split over the SMs and the parts
+ * joined, for which it needs some; a dense call with workspace NULL is not split.
  */
 #define KDA_LATENT_CAUSAL 0x1u
 typedef struct kda_latent_prefill_args {

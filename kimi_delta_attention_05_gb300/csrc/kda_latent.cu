@@ -328,13 +328,18 @@ PrefillParams prefill_shape(const kda_latent_prefill_args* a) {
   p.N = a->N;
   p.H = (int)a->H;
   p.causal = (a->flags & KDA_LATENT_CAUSAL) ? 1 : 0;
-  p.pairs = prefill_pairs(a->B * a->Tq, a->N, a->cu_seqlens_q != nullptr) ? 1 : 0;
+  // (shares of a split call are even whatever the order of the items)
+  p.pairs = prefill_pairs(a->B * a->Tq, a->N, false) ? 1 : 0;
+  if (a->cu_seqlens_q && p.pairs && prefill_split_bytes(p) == 0) p.pairs = prefill_pairs(a->Tq, a->N, true) ? 1 : 0;
   return p;
 }
 
+// Packed calls: the counts and the list of blocks; then a split call's partial rows.
+size_t prefill_list_bytes(const kda_latent_prefill_args* a) {
+  return a->cu_seqlens_q ? 256 + ((size_t)prefill_blocks(a) * sizeof(PrefillItem) + 255) / 256 * 256 : 0;
+}
 size_t prefill_workspace(const kda_latent_prefill_args* a) {
-  if (!a->cu_seqlens_q) return prefill_split_bytes(prefill_shape(a));
-  return 256 + ((size_t)prefill_blocks(a) * sizeof(PrefillItem) + 255) / 256 * 256;
+  return prefill_list_bytes(a) + prefill_split_bytes(prefill_shape(a));
 }
 
 }  // namespace
@@ -357,8 +362,8 @@ __device__ __forceinline__ int work_class(int tiles) {
 
 __global__ void __launch_bounds__(1024) kda_latent_blocks_kernel(const int64_t* cu_q, const int64_t* cu_k, int64_t N,
                                                                  int64_t Tq, int64_t Tk, int causal, int rows,
-                                                                 int together, PrefillItem* items, int32_t* count,
-                                                                 int* status) {
+                                                                 int together, int split, PrefillItem* items,
+                                                                 int32_t* count, int* status) {
   __shared__ int32_t at[kWorkClasses];
   asm volatile("griddepcontrol.launch_dependents;\n" ::: "memory");
   asm volatile("griddepcontrol.wait;\n" ::: "memory");
@@ -373,14 +378,14 @@ __global__ void __launch_bounds__(1024) kda_latent_blocks_kernel(const int64_t* 
   bad = __syncthreads_or(bad);
   if (tid == 0 && bad && status) atomicExch(status, KDA_ERR_BAD_SEQLENS);
   // a warp a sequence, a lane a block: first counted, then placed
-  for (int pass = 0; pass < 2; ++pass) {
+  for (int pass = 0; pass < 2 && !split; ++pass) {
     for (int64_t n = warp; n < N && !bad; n += 32) {
       PrefillItem it;
       it.q0 = (int)cu_q[n];
       it.lq = (int)(cu_q[n + 1] - cu_q[n]);
       it.k0 = (int)cu_k[n];
       it.lk = (int)(cu_k[n + 1] - cu_k[n]);
-      it.pad[0] = it.pad[1] = it.pad[2] = 0;
+      it.tiles = it.start = it.pad = 0;
       if (together) {
         const int blocks = (int)(((int64_t)it.lq + rows - 1) / rows);
         int* place = &at[work_class(it.lk / 64)];
@@ -419,6 +424,46 @@ __global__ void __launch_bounds__(1024) kda_latent_blocks_kernel(const int64_t* 
       }
     }
     __syncthreads();
+  }
+  if (split && warp == 0) {
+    // split calls: the blocks in order (where the line is cut, and so the sums, must not
+    // depend on an atomic's), and the line of their costs
+    int n = 0;
+    for (int64_t base = 0; base < N && !bad; base += 32) {
+      const int64_t seq = base + lane;
+      PrefillItem it = {};
+      if (seq < N) {
+        it.q0 = (int)cu_q[seq];
+        it.lq = (int)(cu_q[seq + 1] - cu_q[seq]);
+        it.k0 = (int)cu_k[seq];
+        it.lk = (int)(cu_k[seq + 1] - cu_k[seq]);
+      }
+      const int blocks = (int)(((int64_t)it.lq + rows - 1) / rows), upto = (int)warp_scan(blocks, lane);
+      for (int j = 0; j < blocks; ++j) {
+        it.r0 = j * rows;
+        items[n + upto - blocks + j] = it;
+      }
+      n += __shfl_sync(0xffffffffu, upto, 31);
+    }
+    __syncwarp();
+    if (lane == 0) count[0] = n;
+    int carry = 0;
+    for (int base = 0; base < n; base += 32) {
+      const int e = base + lane;
+      int n0 = 0, n1 = 0, cost = 0;
+      if (e < n) {
+        const PrefillItem it = items[e];
+        block_tiles(it.lq, it.lk, causal, it.r0, rows / 2, n0, n1);
+        cost = max(n0, n1) + kPreItemCost;
+      }
+      const int upto = (int)warp_scan(cost, lane);
+      if (e < n) {
+        items[e].tiles = max(n0, n1);
+        items[e].start = carry + upto - cost;
+      }
+      carry += __shfl_sync(0xffffffffu, upto, 31);
+    }
+    if (lane == 0) count[2] = carry;
   }
 }
 
@@ -539,12 +584,14 @@ extern "C" int kda_latent_prefill(const kda_latent_prefill_args* a, void* worksp
   p.out = static_cast<uint16_t*>(a->out);
   p.lse = a->lse;
   p.status = status;
-  if (!a->cu_seqlens_q && need > 0) p.part = static_cast<float*>(workspace);
+  const size_t list = prefill_list_bytes(a);
+  if (workspace && need > list) p.part = reinterpret_cast<float*>(static_cast<unsigned char*>(workspace) + list);
   if (a->cu_seqlens_q) {
     int32_t* count = static_cast<int32_t*>(workspace);
     PrefillItem* items = reinterpret_cast<PrefillItem*>(static_cast<unsigned char*>(workspace) + 256);
     if (!launch_overlapped(kda_latent_blocks_kernel, dim3(1), 1024, 0, s, 1, a->cu_seqlens_q, a->cu_seqlens_k, a->N, a->Tq,
-                           a->Tk, p.causal, p.pairs ? 2 * kPrefillRows : kPrefillRows, !p.pairs, items, count, status))
+                           a->Tk, p.causal, p.pairs ? 2 * kPrefillRows : kPrefillRows, !p.pairs,
+                           p.part != nullptr, items, count, status))
       return KDA_ERR_LAUNCH;
     p.items = items;
     p.count = count;

@@ -35,7 +35,8 @@ struct PrefillItem {
   int q0, k0;                       // first query and key of the sequence
   int lq, lk;                       // its lengths
   int r0;                           // first row of the block within it
-  int pad[3];
+  int tiles, start;                 // split calls: its key tiles, and the cost of the blocks before it
+  int pad;
 };
 static_assert(sizeof(PrefillItem) == 32, "read as two 16-byte pieces");
 
@@ -47,7 +48,7 @@ struct PrefillParams {
   float* lse;                       // [tokens, H] or nullptr
   const int64_t *cu_q, *cu_k;       // [N + 1] or nullptr (dense)
   const PrefillItem* items;         // query blocks in the order of their work (packed only)
-  int32_t* count;                   // their number, and how many were taken by counter (packed only)
+  int32_t* count;                   // their number, how many were taken by counter, their cost (packed only)
   int64_t B, Tq, Tk, N;
   int H;
   int causal;
@@ -59,9 +60,24 @@ struct PrefillParams {
 // Whether `rows` queries of `sequences` sequences go to CTA pairs.
 bool prefill_pairs(int64_t rows, int64_t sequences, bool packed);
 
-// Bytes that a split dense call needs for its partial rows; 0: it is not split.
+// Bytes that a split call needs for its partial rows; 0: it is not split.
 size_t prefill_split_bytes(const PrefillParams& p);
 constexpr int64_t kPrefillSplitKeys = 4096;  // fewer keys are never split
+
+constexpr int kPreKeys = 128;     // keys of a tile
+constexpr int kPreItemCost = 2;   // what an item costs beside its key tiles, in tiles
+// Key tiles of the block of 2 `tile_rows` rows from r0 on of a sequence: of its first and its second tile.
+__host__ __device__ __forceinline__ void block_tiles(int lq, int lk, int causal, int r0, int tile_rows, int& n0, int& n1) {
+  int n[2];
+  for (int t = 0; t < 2; ++t) {
+    const int first = r0 + t * tile_rows;
+    const int last = (lq < first + tile_rows ? lq : first + tile_rows) - 1;
+    const int seen = !causal || last + lk - lq + 1 > lk ? lk : last + lk - lq + 1;
+    n[t] = first < lq && seen > 0 ? (seen + kPreKeys - 1) / kPreKeys : 0;
+  }
+  n0 = n[0];
+  n1 = n[1];
+}
 
 // Query rows of one work item of the expanded form (of single CTAs).
 constexpr int kPrefillRows = 256;

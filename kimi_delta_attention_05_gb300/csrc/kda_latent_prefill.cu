@@ -9,14 +9,20 @@ namespace {
 // more than a ninth more to do than a share and the join (taken as ten key tiles).
 // 1024 rows behind 15360 cached, 16 heads: 180 us unsplit, 99 split; 256 behind 32768,
 // 8 heads: 442 and 46; two of the first, whose 64 items nearly fill the 76 pairs: 188
-// and 195, so those stay whole.  Packed sequences have their lengths on the device and
-// are not split.
+// and 195, so those stay whole.  Packed sequences, whose lengths are on the device, are
+// split where their blocks cannot fill the GPU and they have many keys on average (1024
+// rows behind up to 15360, 16 heads: 229 us unsplit, 103 split).
 constexpr int kMostCtas = 512;
 PrefillSplit split_of(const PrefillParams& p, int sms) {
   PrefillSplit sp = {};
   const int tile_rows = p.pairs ? 2 * kPreRows : kPreRows;
   const int64_t per = (p.Tq + 2 * tile_rows - 1) / (2 * tile_rows), bh = p.B * p.H, wide = p.pairs ? sms / 2 : sms;
-  if (p.cu_q || p.Tk < kPrefillSplitKeys || per * bh == 0 || per * bh > 3 * wide || wide > kMostCtas) return sp;
+  if (p.cu_q) {
+    const int64_t items = (p.Tq / (2 * tile_rows) + p.N) * p.H;
+    if (p.Tk >= kPrefillSplitKeys * p.N && items > 0 && items <= wide) sp.shares = (int)wide;
+    return sp;
+  }
+  if (p.Tk < kPrefillSplitKeys || per * bh == 0 || per * bh > 3 * wide || wide > kMostCtas) return sp;
   int64_t total = 0, worst = 0;
   int64_t busy[kMostCtas] = {};
   for (int64_t back = 0, place = 0; back < per; ++back) {
@@ -29,7 +35,7 @@ PrefillSplit split_of(const PrefillParams& p, int sms) {
       worst = std::max(worst, busy[cta] += cost);
     }
   }
-  const int64_t size = std::max<int64_t>((total + wide - 1) / wide, 8 + kPreItemCost);
+  const int64_t size = std::max<int64_t>((total + wide - 1) / wide, kSplitLeast);
   if ((size + 10) * 10 > worst * 9) return sp;
   sp.size = size;
   sp.shares = (int)((total + size - 1) / size);
@@ -60,7 +66,7 @@ bool prefill_pairs(int64_t rows, int64_t sequences, bool packed) { return rows >
 
 size_t prefill_split_bytes(const PrefillParams& p) {
   const PrefillSplit sp = split_of(p, std::max(2, device_sms()));
-  return sp.size ? (part_floats(p, sp) + part_floats(p, sp) / kVDim) * sizeof(float) : 0;
+  return sp.shares ? (part_floats(p, sp) + part_floats(p, sp) / kVDim) * sizeof(float) : 0;
 }
 
 bool launch_latent_prefill(const PrefillParams& p, cudaStream_t s) {

@@ -55,7 +55,6 @@
 namespace kda {
 
 constexpr int kPreRows = 128;                    // query rows of a tile in one CTA
-constexpr int kPreKeys = 128;                    // keys of a tile
 constexpr int kPreQ = 0;                         // two tiles of three [128 rows][64 channels] blocks
 constexpr int kPreQTile = 3 * kPreRows * 128;
 constexpr int kPreRing = 2 * kPreQTile;          // key and value blocks
@@ -130,30 +129,22 @@ struct PreItem {
   __device__ __forceinline__ int nt() const { return max(n0, n1); }
 };
 
-// Key tiles of the block of 2 `tile_rows` rows from r0 on of a sequence: of its first and its second tile.
-__host__ __device__ __forceinline__ void block_tiles(int lq, int lk, int causal, int r0, int tile_rows, int& n0, int& n1) {
-  int n[2];
-  for (int t = 0; t < 2; ++t) {
-    const int first = r0 + t * tile_rows;
-    const int last = (lq < first + tile_rows ? lq : first + tile_rows) - 1;
-    const int seen = !causal || last + lk - lq + 1 > lk ? lk : last + lk - lq + 1;
-    n[t] = first < lq && seen > 0 ? (seen + kPreKeys - 1) / kPreKeys : 0;
-  }
-  n0 = n[0];
-  n1 = n[1];
-}
-
 // A split call: few long items leave SMs idle, so the items lie in a line of costs
-// (kPreItemCost and a key tile each), which is cut into equal shares, one CTA or pair a
+// (kPreItemCost and one a key tile), which is cut into equal shares, one CTA or pair a
 // share.  A share that holds a part of an item writes its rows (normalised) and their
 // lse in fp32 to its first or second slot, and the join kernel adds the parts up.
 struct PrefillSplit {
-  int64_t size;     // of a share; 0: not split
-  int shares;
+  int shares;       // 0: not split
+  int64_t size;     // of a share (packed: found on the device)
   float* part;      // [2 shares][rows of an item][128]
   float* part_lse;  // [2 shares][rows of an item], log2
 };
-constexpr int kPreItemCost = 2;
+constexpr int kSplitLeast = 8 + kPreItemCost;  // least share
+__device__ __forceinline__ int64_t split_size(const PrefillParams& p, const PrefillSplit& sp) {
+  if (!p.items) return sp.size;
+  const int64_t total = (int64_t)p.count[2] * p.H;
+  return max((int64_t)kSplitLeast, (total + sp.shares - 1) / sp.shares);
+}
 
 // The items of a CTA or pair, most work first: every grid-th of the list, each
 // second round backwards, so that the work of all is nearly the same.  Packed
@@ -176,6 +167,16 @@ struct PreWalk {
     it.r0 = (int)(per - 1 - back) * 2 * kTileRows;
     block_tiles(it.lq, it.lk, p.causal, it.r0, kTileRows, it.n0, it.n1);
   }
+  // An entry of the list (without its head).
+  static __device__ __forceinline__ void listed(const PrefillParams& p, uint32_t e, PreItem& it) {
+    const int4 a = *reinterpret_cast<const int4*>(p.items + e);
+    it.q0 = a.x;
+    it.k0 = a.y;
+    it.lq = a.z;
+    it.lk = a.w;
+    it.r0 = p.items[e].r0;
+    block_tiles(it.lq, it.lk, p.causal, it.r0, kTileRows, it.n0, it.n1);
+  }
   __device__ __forceinline__ void start(const PrefillParams& p, int64_t blocks) {
     round = 0;
     total = (p.items ? (int64_t)*p.count : blocks) * p.H;
@@ -194,13 +195,7 @@ struct PreWalk {
     if (p.items) {
       const uint32_t e = (uint32_t)idx / (uint32_t)p.H;
       it.h = (int)((uint32_t)idx - e * (uint32_t)p.H);
-      const int4 a = *reinterpret_cast<const int4*>(p.items + e);
-      it.q0 = a.x;
-      it.k0 = a.y;
-      it.lq = a.z;
-      it.lk = a.w;
-      it.r0 = p.items[e].r0;
-      block_tiles(it.lq, it.lk, p.causal, it.r0, kTileRows, it.n0, it.n1);
+      listed(p, e, it);
     } else {
       const uint32_t bh = (uint32_t)(p.B * p.H), back = (uint32_t)idx / bh;
       dense(p, per, back, (uint32_t)idx - back * bh, it);
@@ -209,35 +204,61 @@ struct PreWalk {
   }
 };
 
-// The items and parts of items of one share.
+// The items and parts of items of one share.  A block is one of a dense call's `per`
+// from the end, with its sequences and heads, or an entry of the list with its heads.
 template <bool kPair>
 struct PreShare {
   int64_t u0, u1, pre, cost;  // the share; start and cost of the next item
-  uint32_t bh, back, x;
+  uint32_t blocks, wide, back, x;
+  PreItem block;
   __device__ __forceinline__ void at_block(const PrefillParams& p, int64_t per) {
-    PreItem it;
-    PreWalk<kPair>::dense(p, per, back, 0, it);
-    cost = it.nt() + kPreItemCost;
+    if (p.items) PreWalk<kPair>::listed(p, back, block);
+    else PreWalk<kPair>::dense(p, per, back, 0, block);
+    cost = block.nt() + kPreItemCost;
   }
-  __device__ __forceinline__ void start(const PrefillParams& p, int64_t per, int64_t size, int64_t share) {
+  // (all lanes of a warp are here)
+  __device__ __forceinline__ void start(const PrefillParams& p, int64_t per, const PrefillSplit& sp, int64_t share) {
+    const int64_t size = split_size(p, sp);
     u0 = share * size;
     u1 = u0 + size;
     pre = 0;
-    bh = (uint32_t)(p.B * p.H);
     x = 0;
-    for (back = 0; back < per; ++back) {
-      at_block(p, per);
-      if (pre + bh * cost > u0) break;
-      pre += bh * cost;
+    blocks = p.items ? (uint32_t)*p.count : (uint32_t)per;
+    wide = p.items ? (uint32_t)p.H : (uint32_t)(p.B * p.H);
+    if (p.items) {
+      const int lane = threadIdx.x & 31;
+      for (back = 0; back < blocks; back += 32) {
+        const PrefillItem* e = p.items + min(back + lane, blocks - 1);
+        const int64_t from = (int64_t)e->start * p.H, to = from + (int64_t)(e->tiles + kPreItemCost) * p.H;
+        const unsigned here = __ballot_sync(0xffffffffu, back + lane < blocks && from <= u0 && u0 < to);
+        if (here) {
+          const int at = __ffs(here) - 1;
+          back += at;
+          pre = __shfl_sync(0xffffffffu, from, at);
+          break;
+        }
+      }
+      if (back < blocks) at_block(p, per);
+    } else {
+      for (back = 0; back < blocks; ++back) {
+        at_block(p, per);
+        if (pre + wide * cost > u0) break;
+        pre += wide * cost;
+      }
     }
-    if (back < per) {
+    if (back < blocks) {
       x = (uint32_t)((u0 - pre) / cost);
       pre += x * cost;
     }
   }
   __device__ __forceinline__ bool next(const PrefillParams& p, int64_t per, int share, PreItem& it) {
-    while (back < per && pre < u1) {
-      PreWalk<kPair>::dense(p, per, back, x, it);
+    while (back < blocks && pre < u1) {
+      if (p.items) {
+        it = block;
+        it.h = (int)x;
+      } else {
+        PreWalk<kPair>::dense(p, per, back, x, it);
+      }
       const int64_t nt = it.nt(), first = pre + kPreItemCost;  // key tile k lies at first + k
       const int t0 = (int)max((int64_t)0, min(nt, u0 - first)), t1 = (int)max((int64_t)0, min(nt, u1 - first));
       const bool mine = nt > 0 ? t0 < t1 : pre >= u0;
@@ -246,9 +267,9 @@ struct PreShare {
       it.n0 = min(it.n0, t1);
       it.n1 = min(it.n1, t1);
       pre += cost;
-      if (++x == bh) {
+      if (++x == wide) {
         x = 0;
-        if (++back < per) at_block(p, per);
+        if (++back < blocks) at_block(p, per);
       }
       if (mine) return true;
     }
@@ -675,7 +696,7 @@ __global__ void __launch_bounds__(kPreThreads, 1)
     PreWalk<kPair> walk;
     PreShare<kPair> share;
     const int mine = kPair ? blockIdx.x >> 1 : blockIdx.x;
-    if constexpr (kSplit) share.start(p, per, sp.size, mine);
+    if constexpr (kSplit) share.start(p, per, sp, mine);
     else walk.start(p, p.B * per);
     bool have = true;
     for (uint32_t n = 0; have; ++n) {

@@ -12,18 +12,26 @@ template <bool kPair>
 __global__ void __launch_bounds__(512) kda_latent_prefill_join_kernel(const PrefillParams p, int64_t per,
                                                                       const PrefillSplit sp) {
   constexpr int kRows = (kPair ? 4 : 2) * kPreRows;
-  const uint32_t bh = (uint32_t)(p.B * p.H), back = blockIdx.x / bh;
+  asm volatile("griddepcontrol.wait;\n" ::: "memory");
   PreItem it;
   int64_t first = 0;  // where the item's first key tile lies
-  for (uint32_t b = 0; b < back; ++b) {
-    PreWalk<kPair>::dense(p, per, b, 0, it);
-    first += (int64_t)bh * (it.nt() + kPreItemCost);
+  if (p.items) {
+    const uint32_t e = blockIdx.x / (uint32_t)p.H, h = blockIdx.x - e * (uint32_t)p.H;
+    if (e >= (uint32_t)*p.count) return;
+    PreWalk<kPair>::listed(p, e, it);
+    it.h = (int)h;
+    first = (int64_t)p.items[e].start * p.H + (int64_t)h * (it.nt() + kPreItemCost) + kPreItemCost;
+  } else {
+    const uint32_t bh = (uint32_t)(p.B * p.H), back = blockIdx.x / bh, x = blockIdx.x - back * bh;
+    for (uint32_t b = 0; b < back; ++b) {
+      PreWalk<kPair>::dense(p, per, b, 0, it);
+      first += (int64_t)bh * (it.nt() + kPreItemCost);
+    }
+    PreWalk<kPair>::dense(p, per, back, x, it);
+    first += (int64_t)x * (it.nt() + kPreItemCost) + kPreItemCost;
   }
-  PreWalk<kPair>::dense(p, per, back, blockIdx.x - back * bh, it);
   const int nt = it.nt();
-  first += (int64_t)(blockIdx.x - back * bh) * (nt + kPreItemCost) + kPreItemCost;
-  asm volatile("griddepcontrol.wait;\n" ::: "memory");
-  const int64_t s0 = first / sp.size, s1 = (first + nt - 1) / sp.size;
+  const int64_t size = split_size(p, sp), s0 = first / size, s1 = (first + nt - 1) / size;
   const int local = blockIdx.y * 16 + (threadIdx.x >> 5), row = it.r0 + local, lane = threadIdx.x & 31;
   if (nt == 0 || s0 == s1 || row >= it.lq) return;
   const int parts = (int)(s1 - s0) + 1;
@@ -60,9 +68,9 @@ template <bool kPair>
 bool launch_both(const PrefillParams& p, const PrefillSplit& sp, int sms, cudaStream_t s) {
   if (!launch_prefill<kPair, true>(p, sp, sms, s)) return false;
   const int rows = kPair ? 2 * kPrefillRows : kPrefillRows;
-  const int64_t per = (p.Tq + rows - 1) / rows;
-  return launch_overlapped(kda_latent_prefill_join_kernel<kPair>, dim3((unsigned)(p.B * p.H * per), (unsigned)(rows / 16)),
-                           512, 0, s, 1, p, per, sp);
+  const int64_t per = (p.Tq + rows - 1) / rows, items = (p.items ? p.Tq / rows + p.N : p.B * per) * p.H;
+  return launch_overlapped(kda_latent_prefill_join_kernel<kPair>, dim3((unsigned)items, (unsigned)(rows / 16)), 512, 0, s, 1,
+                           p, per, sp);
 }
 
 }  // namespace

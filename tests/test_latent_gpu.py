@@ -404,6 +404,34 @@ def test_prefill_few_rows_many_keys(lq, lk, heads, causal):
     _prefill([lq] * 2, [lk] * 2, heads, causal, False, seed=lk, std=8.0)
 
 
+@pytest.mark.parametrize("lq,lk,heads", [([1], [4097], 1), ([1, 130, 0, 300], [5000, 4300, 100, 9000], 2),
+                                         ([600, 257], [700, 12000], 3), ([2100], [9000], 1), ([1500, 1030], [9000, 400], 2),
+                                         ([300, 40], [20, 9000], 1)])
+@pytest.mark.parametrize("causal", [True, False])
+def test_prefill_few_rows_many_keys_packed(lq, lk, heads, causal):
+    """The same for packed sequences, whose lengths only the device knows."""
+    _prefill(lq, lk, heads, causal, True, seed=sum(lk))
+
+
+def test_prefill_split_packed_repeats_and_refuses():
+    """The parts of a packed split call are the same every time; inconsistent offsets write nothing."""
+    gen = torch.Generator().manual_seed(10)
+    n, keys = 300, 13000
+    q, k, pe, v = (_rand(gen, 1, *x).cuda() for x in ((n, 2, 192), (keys, 2, 128), (keys, 64), (keys, 2, 128)))
+    cu = torch.tensor([0, 20, 290, 300], device="cuda")
+    cu_k = torch.tensor([0, 5000, 12000, keys], device="cuda")
+    need = M.latent_prefill_workspace_bytes(1, n, keys, 2, 3)
+    assert need > M.latent_prefill_workspace_bytes(1, n, 1000, 2, 3)
+    outs = []
+    for fill in (0, 255, 255):
+        ws = torch.full((need,), fill, dtype=torch.uint8, device="cuda")
+        outs.append(M.latent_prefill(q, k, pe, v, 0.07, cu_seqlens=cu, cu_seqlens_k=cu_k, workspace=ws))
+    assert torch.equal(outs[0], outs[1]) and torch.equal(outs[0], outs[2])
+    out = torch.full_like(outs[0], 5.0)
+    M.latent_prefill(q, k, pe, v, 0.07, out=out, cu_seqlens=cu, cu_seqlens_k=torch.tensor([0, 5000, 4000, keys], device="cuda"))
+    assert get_status() == 14 and (out == 5.0).all() and get_status() == 0
+
+
 def test_prefill_split_workspace():
     """Without a workspace a C call is not split; one that is too small is refused; parts do not depend on what
     the workspace holds."""
