@@ -13,25 +13,37 @@ __global__ void __launch_bounds__(512) kda_latent_prefill_join_kernel(const Pref
                                                                       const PrefillSplit sp) {
   constexpr int kRows = (kPair ? 4 : 2) * kPreRows;
   asm volatile("griddepcontrol.wait;\n" ::: "memory");
-  PreItem it;
-  int64_t first = 0;  // where the item's first key tile lies
-  if (p.items) {
-    const uint32_t e = blockIdx.x / (uint32_t)p.H, h = blockIdx.x - e * (uint32_t)p.H;
-    if (e >= (uint32_t)*p.count) return;
-    PreWalk<kPair>::listed(p, e, it);
-    it.h = (int)h;
-    first = (int64_t)p.items[e].start * p.H + (int64_t)h * (it.nt() + kPreItemCost) + kPreItemCost;
-  } else {
-    const uint32_t bh = (uint32_t)(p.B * p.H), back = blockIdx.x / bh, x = blockIdx.x - back * bh;
-    for (uint32_t b = 0; b < back; ++b) {
-      PreWalk<kPair>::dense(p, per, b, 0, it);
-      first += (int64_t)bh * (it.nt() + kPreItemCost);
+  __shared__ PreItem shared_it;
+  __shared__ int64_t shared_at[2];
+  if (threadIdx.x == 0) {  // (divisions of 64 bits: once a CTA)
+    PreItem it;
+    int64_t first = 0;  // where the item's first key tile lies
+    it.n0 = it.n1 = 0;
+    if (p.items) {
+      const uint32_t e = blockIdx.x / (uint32_t)p.H, h = blockIdx.x - e * (uint32_t)p.H;
+      if (e < (uint32_t)*p.count) {
+        PreWalk<kPair>::listed(p, e, it);
+        it.h = (int)h;
+        first = (int64_t)p.items[e].start * p.H + (int64_t)h * (it.nt() + kPreItemCost) + kPreItemCost;
+      }
+    } else {
+      const uint32_t bh = (uint32_t)(p.B * p.H), back = blockIdx.x / bh, x = blockIdx.x - back * bh;
+      for (uint32_t b = 0; b < back; ++b) {
+        PreWalk<kPair>::dense(p, per, b, 0, it);
+        first += (int64_t)bh * (it.nt() + kPreItemCost);
+      }
+      PreWalk<kPair>::dense(p, per, back, x, it);
+      first += (int64_t)x * (it.nt() + kPreItemCost) + kPreItemCost;
     }
-    PreWalk<kPair>::dense(p, per, back, x, it);
-    first += (int64_t)x * (it.nt() + kPreItemCost) + kPreItemCost;
+    const int64_t size = split_size(p, sp);
+    shared_it = it;
+    shared_at[0] = first / size;
+    shared_at[1] = (first + it.nt() - 1) / size;
   }
+  __syncthreads();
+  const PreItem it = shared_it;
   const int nt = it.nt();
-  const int64_t size = split_size(p, sp), s0 = first / size, s1 = (first + nt - 1) / size;
+  const int64_t s0 = shared_at[0], s1 = shared_at[1];
   const int local = blockIdx.y * 16 + (threadIdx.x >> 5), row = it.r0 + local, lane = threadIdx.x & 31;
   if (nt == 0 || s0 == s1 || row >= it.lq) return;
   const int parts = (int)(s1 - s0) + 1;
