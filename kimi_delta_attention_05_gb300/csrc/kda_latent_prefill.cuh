@@ -832,16 +832,23 @@ __global__ void __launch_bounds__(kPreThreads, 1)
                            : "memory");
           }
         } else if (row < it.lq) {
-          // whole 32-byte sectors: a 16-byte store of a row alone would write halves of them
+          // whole 32-byte sectors: a 16-byte store of a row alone would write halves of them.  The
+          // wide store needs a 32-byte boundary; an `out` that starts in the middle of one gets halves
           uint16_t* dst = p.out + at * kVDim + c;
+          const bool aligned = (reinterpret_cast<uintptr_t>(p.out) & 31) == 0;  // (rows are 256 bytes)
 #pragma unroll
           for (int e = 0; e < 64; e += 16) {
             uint32_t w[8];
 #pragma unroll
             for (int x = 0; x < 8; ++x) w[x] = pack_bf16(o[e + 2 * x] * inv, o[e + 2 * x + 1] * inv);
-            asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};\n" ::"l"(dst + e), "r"(w[0]),
-                         "r"(w[1]), "r"(w[2]), "r"(w[3]), "r"(w[4]), "r"(w[5]), "r"(w[6]), "r"(w[7])
-                         : "memory");
+            if (aligned) {
+              asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};\n" ::"l"(dst + e), "r"(w[0]),
+                           "r"(w[1]), "r"(w[2]), "r"(w[3]), "r"(w[4]), "r"(w[5]), "r"(w[6]), "r"(w[7])
+                           : "memory");
+            } else {
+              reinterpret_cast<uint4*>(dst + e)[0] = make_uint4(w[0], w[1], w[2], w[3]);
+              reinterpret_cast<uint4*>(dst + e)[1] = make_uint4(w[4], w[5], w[6], w[7]);
+            }
           }
         }
       }
