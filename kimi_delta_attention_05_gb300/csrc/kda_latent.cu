@@ -354,6 +354,10 @@ size_t prefill_workspace(const kda_latent_prefill_args* a) {
 // status word and leaves no block, so nothing is written.  One block; the order
 // within a class is that of the atomics, and no result depends on it.
 constexpr int kWorkClasses = 352;
+// (a warp scans the classes 32 at a time, all lanes in every round: a shuffle waits for lanes that have left)
+static_assert(kWorkClasses % 32 == 0, "the scan over the classes needs whole warps");
+// (at most 2^30 keys: 2^24 key tiles in the two query tiles of a block, and as many 64ths of a sequence)
+static_assert(32 + (24 - 5) * 16 + 15 < kWorkClasses, "every number of key tiles needs a class");
 __device__ __forceinline__ int work_class(int tiles) {
   if (tiles < 32) return kWorkClasses - 1 - tiles;
   const int e = 31 - __clz(tiles);
