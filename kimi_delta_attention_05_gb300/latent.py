@@ -3,7 +3,8 @@ cache append, absorbed decode and expanded prefill.
 
 Checks of types, shapes and strides happen here (ValueError), everything else
 in the library (KdaError with its status code).  PyTorch supplies device memory
-and the stream; buffers made here are allocated on the stream that uses them.
+and the stream; buffers made here are allocated on the stream that uses them.  Tensors and
+stream have to be on the current device (ValueError otherwise).
 Page ids, lengths and slots are device values: what is wrong with them is read
 from :func:`get_status`.
 """
@@ -117,10 +118,21 @@ def _dense(t, name):
         raise ValueError(f"{name}: a contiguous tensor is needed")
 
 
-def _gpu(t, name):
+# The current device's index without the checks around it, where this PyTorch has the call.
+_current_device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
+
+
+def _gpu(t, name, stream):
+    """The device of a call: the library sizes, launches and keeps its status words on the
+    current device, so tensors and stream have to be of that one."""
+    dev = t.device
     if not t.is_cuda:
-        raise ValueError(f"{name}: a CUDA tensor is needed, got one on {t.device}")
-    return t.device
+        raise ValueError(f"{name}: a CUDA tensor is needed, got one on {dev}")
+    if dev.index != _current_device():
+        raise ValueError(f"{name}: on {dev}, but the current device is cuda:{_current_device()} (torch.cuda.device sets it)")
+    if stream is not None and stream.device != dev:
+        raise ValueError(f"stream: one of {dev} is needed, got one of {stream.device}")
+    return dev
 
 
 def _last(strides, t, name):
@@ -170,7 +182,7 @@ def latent_plan(cached_lens, new_lens, block_table, free_pages, page_size, num_t
     [num_tokens] (-1 behind the last token), pages_taken int32 [1].  Lengths that
     do not fit, or too few free pages, plan nothing and show in
     :func:`get_status` (18 / 19)."""
-    dev = _gpu(cached_lens, "cached_lens")
+    dev = _gpu(cached_lens, "cached_lens", stream)
     _on(cached_lens, _i32, 1, dev, "cached_lens")
     _on(new_lens, _i32, 1, dev, "new_lens")
     _on(free_pages, _i32, 1, dev, "free_pages")
@@ -203,7 +215,7 @@ def latent_append(c, k_pe, slot_map, cache, norm_weight=None, eps=1e-6, *, strea
     fine), slot_map int64 [T] (negative: skipped), cache bf16 [pages, page_size,
     576]; norm_weight fp32 [512]: the latents are RMS-normalised with ``eps``
     and scaled on the way."""
-    dev = _gpu(cache, "cache")
+    dev = _gpu(cache, "cache", stream)
     _on(c, _bf16, 2, dev, "c")
     _on(k_pe, _bf16, 2, dev, "k_pe")
     _on(slot_map, _i64, 1, dev, "slot_map")
@@ -237,7 +249,7 @@ def latent_decode(q, cache, block_table, seq_lens, scale, out=None, lse=None, *,
     seq_lens int32 [B]; out bf16 [B, R, H, 512] (allocated here if None), lse an
     optional fp32 [B, R, H] tensor to be written.  ``workspace``: an optional
     uint8 tensor of at least :func:`latent_decode_workspace_bytes` bytes."""
-    dev = _gpu(q, "q")
+    dev = _gpu(q, "q", stream)
     _on(q, _bf16, 4, dev, "q")
     B, R, H, D = q.shape
     if D != LATENT_ROW:
@@ -308,7 +320,7 @@ def latent_prefill(q, k, k_pe, v, scale, out=None, lse=None, cu_seqlens=None, cu
     keys j <= i + Lk - Lq, or all with ``causal=False``.  out bf16 [B, Tq, H,
     128]; lse an optional fp32 [B, Tq, H] tensor to be written.  ``workspace``: an
     optional uint8 tensor of at least :func:`latent_prefill_workspace_bytes` bytes."""
-    dev = _gpu(q, "q")
+    dev = _gpu(q, "q", stream)
     _on(q, _bf16, 4, dev, "q")
     _on(k, _bf16, 4, dev, "k")
     _on(k_pe, _bf16, 3, dev, "k_pe")
