@@ -164,6 +164,7 @@ int kda_latent_decode(const kda_latent_decode_args *args, void *workspace, size_
  *  cu_seqlens_q, cu_seqlens_k : int64 [N + 1] (B == 1, packed) or both NULL
  *         (N == B, sequence n = batch row n).  Checked on the device as in kda.h;
  *         a violation of either sets KDA_ERR_BAD_SEQLENS and nothing is written.
+ *         (N == 0 with Tq or Tk > 0 is refused with KDA_ERR_BAD_SEQLENS at once.)
  * Rows of other sequences (and past the tensors) never touch a result; within a
  * sequence, keys and values have to be finite.
  *

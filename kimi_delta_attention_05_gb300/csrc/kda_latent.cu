@@ -293,6 +293,7 @@ int check_prefill(const kda_latent_prefill_args* a) {
   if ((a->cu_seqlens_q == nullptr) != (a->cu_seqlens_k == nullptr)) return KDA_ERR_NULL_ARG;
   if (a->cu_seqlens_q) {
     if (a->B != 1) return KDA_ERR_VARLEN_BATCH;
+    if (a->N == 0 && (a->Tq > 0 || a->Tk > 0)) return KDA_ERR_BAD_SEQLENS;  // offsets that cannot end at T
   } else if (a->N != a->B) {
     return KDA_ERR_SHAPE;
   }

@@ -1,5 +1,7 @@
-"""Refusals of the latent-attention binding that need no GPU: stand-ins for CUDA
-tensors carry the attributes that are looked at before anything else."""
+"""Refusals of the latent-attention calls that need no GPU: stand-ins for CUDA tensors
+carry the attributes that the binding looks at before anything else; the library
+is called with addresses that it never follows."""
+import ctypes
 from types import SimpleNamespace
 
 import pytest
@@ -26,3 +28,16 @@ def test_tensors_and_streams_of_another_device_are_refused(call, monkeypatch):
     monkeypatch.setattr(M, "_current_device", lambda: 1)
     with pytest.raises(ValueError, match="cuda:0.*current device is cuda:1"):
         call(_at(0), None)
+
+
+FAKE = 0x7F0000000000
+
+
+@pytest.mark.parametrize("tq,tk,code", [(100, 120, 14), (0, 120, 14), (100, 0, 14), (0, 0, 0)])
+def test_packed_tokens_without_sequences_are_refused(tq, tk, code):
+    """Offsets of one entry cannot be 0 and T: `out` would be returned as it was allocated."""
+    a = M.kda_latent_prefill_args(FAKE, FAKE, FAKE, FAKE, 768, 192, 1024, 256, 64, 1024, 256, 0.07, FAKE, None, FAKE, FAKE,
+                                  1, tq, tk, 4, 0, 1)
+    lib = M._library()
+    assert lib.kda_latent_prefill(ctypes.byref(a), FAKE, 1 << 40, None) == code
+    assert lib.kda_latent_prefill_workspace_bytes(ctypes.byref(a)) == (0 if code else 256)
