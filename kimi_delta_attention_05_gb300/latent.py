@@ -140,6 +140,15 @@ def _last(strides, t, name):
         raise ValueError(f"{name}: the last dimension has to be contiguous")
 
 
+def _scratch(workspace, device):
+    """Address and bytes of a workspace."""
+    if workspace is None:
+        return None, 0
+    if workspace.device != device or not workspace.is_contiguous():
+        raise ValueError(f"workspace: a contiguous tensor on {device} is needed, got one on {workspace.device}")
+    return workspace.data_ptr(), workspace.numel() * workspace.element_size()
+
+
 # The handle of the current stream without the Stream object around it, where
 # this PyTorch has the call (2 us less on the host).
 _current = getattr(torch._C, "_cuda_getCurrentRawStream", None)
@@ -281,8 +290,7 @@ def latent_decode(q, cache, block_table, seq_lens, scale, out=None, lse=None, *,
     if workspace is None:
         need = lib.kda_latent_decode_workspace_bytes(a)
         workspace = _new(need, torch.uint8, dev, stream) if need else None
-    rc = lib.kda_latent_decode(a, None if workspace is None else workspace.data_ptr(),
-                               0 if workspace is None else workspace.numel(), _handle(dev, stream))
+    rc = lib.kda_latent_decode(a, *_scratch(workspace, dev), _handle(dev, stream))
     if rc != 0:
         _raise("kda_latent_decode", rc)
     return out
@@ -373,8 +381,7 @@ def latent_prefill(q, k, k_pe, v, scale, out=None, lse=None, cu_seqlens=None, cu
     if workspace is None and (cu_seqlens is not None or Tk >= _SPLIT_KEYS):
         need = lib.kda_latent_prefill_workspace_bytes(a)
         workspace = _new(need, torch.uint8, dev, stream) if need else None
-    rc = lib.kda_latent_prefill(a, None if workspace is None else workspace.data_ptr(),
-                                0 if workspace is None else workspace.numel(), _handle(dev, stream))
+    rc = lib.kda_latent_prefill(a, *_scratch(workspace, dev), _handle(dev, stream))
     if rc != 0:
         _raise("kda_latent_prefill", rc)
     return out

@@ -41,3 +41,17 @@ def test_packed_tokens_without_sequences_are_refused(tq, tk, code):
     lib = M._library()
     assert lib.kda_latent_prefill(ctypes.byref(a), FAKE, 1 << 40, None) == code
     assert lib.kda_latent_prefill_workspace_bytes(ctypes.byref(a)) == (0 if code else 256)
+
+
+def test_workspaces_that_the_gpu_cannot_write_are_refused():
+    """Not on the device, or more elements than memory (an expanded view)."""
+    cpu = torch.device("cpu")
+    assert M._scratch(None, cpu) == (None, 0)
+    ws = torch.empty(512, dtype=torch.uint8)
+    assert M._scratch(ws, cpu) == (ws.data_ptr(), 512)
+    assert M._scratch(torch.empty(8, dtype=torch.float32), cpu)[1] == 32
+    with pytest.raises(ValueError, match="workspace"):
+        M._scratch(ws, torch.device("cuda", 0))
+    for view in (ws[:1].expand(1 << 20), ws[::2]):
+        with pytest.raises(ValueError, match="workspace"):
+            M._scratch(view, cpu)

@@ -47,3 +47,19 @@ def test_prefill_writes_an_out_of_any_16_bytes(lq, lk, heads, packed, at):
     assert torch.equal(out, ref) and torch.equal(again, lse)
     assert (buf[:at] == 5.0).all() and (buf[at + n:] == 5.0).all()
     assert get_status() == 0
+
+
+# ---- refusals of the binding ----
+
+def test_workspaces_that_the_gpu_cannot_write_are_refused():
+    z = lambda *s, d=torch.bfloat16: torch.zeros(*s, dtype=d, device="cuda")  # noqa: E731
+    decode = z(2, 1, 4, 576), z(80, 8, 576), z(2, 40, d=torch.int32), z(2, d=torch.int32)
+    prefill = z(1, 5, 3, 192), z(1, 5, 3, 128), z(1, 5, 64), z(1, 5, 3, 128)
+    cu = torch.tensor([0, 5], device="cuda")
+    for ws in (torch.empty(1 << 24, dtype=torch.uint8), z(1, d=torch.uint8).expand(1 << 24), z(1 << 24, d=torch.uint8)[::2]):
+        with pytest.raises(ValueError, match="workspace"):
+            M.latent_decode(*decode, 1.0, workspace=ws)
+        with pytest.raises(ValueError, match="workspace"):
+            M.latent_prefill(*prefill, 1.0, cu_seqlens=cu, workspace=ws)
+    ws = z(1 << 22, d=torch.float32)
+    assert torch.equal(M.latent_decode(*decode, 1.0, workspace=ws), M.latent_decode(*decode, 1.0))
