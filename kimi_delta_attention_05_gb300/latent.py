@@ -61,6 +61,7 @@ class kda_latent_prefill_args(ctypes.Structure):
 def _packer(block):
     """Packs the fields of an argument block, nested ones in place, into its bytes: one call
     where filling the ctypes structure takes three times as long."""
+    # (a float beyond 32 bits goes in as infinity, _F(x).value, for the library to refuse: struct would raise its own error)
     codes = {_P: "P", _I: "q", _F: "f", ctypes.c_uint32: "I"}
 
     def fields(cls):
@@ -242,7 +243,7 @@ def latent_append(c, k_pe, slot_map, cache, norm_weight=None, eps=1e-6, *, strea
             raise ValueError("norm_weight [512] is needed")
     a = _append_block(c.data_ptr(), k_pe.data_ptr(), c_strides[0] if T > 1 else LATENT_DIM,
                       pe_strides[0] if T > 1 else LATENT_PE_DIM, slot_map.data_ptr(), *_cache_block(cache, dev),
-                      0 if norm_weight is None else norm_weight.data_ptr(), eps, T)
+                      0 if norm_weight is None else norm_weight.data_ptr(), _F(eps).value, T)
     rc = _library().kda_latent_append(a, _handle(dev, stream))
     if rc != 0:
         _raise("kda_latent_append", rc)
@@ -285,7 +286,7 @@ def latent_decode(q, cache, block_table, seq_lens, scale, out=None, lse=None, *,
         if lse.shape != (B, R, H):
             raise ValueError("lse [B, R, H] is needed")
     a = _decode_block(q.data_ptr(), *_cache_block(cache, dev), block_table.data_ptr(), strides[0] if B > 1 else width,
-                      width, seq_lens.data_ptr(), scale, out.data_ptr(), 0 if lse is None else lse.data_ptr(), B, R, H)
+                      width, seq_lens.data_ptr(), _F(scale).value, out.data_ptr(), 0 if lse is None else lse.data_ptr(), B, R, H)
     lib = _library()
     if workspace is None:
         need = lib.kda_latent_decode_workspace_bytes(a)
@@ -375,7 +376,7 @@ def latent_prefill(q, k, k_pe, v, scale, out=None, lse=None, cu_seqlens=None, cu
     a = _prefill_block(
         q.data_ptr(), k.data_ptr(), k_pe.data_ptr(), v.data_ptr(), _token_stride(shape, qs, H * qh, "q"), qh,
         _token_stride(k_shape, ks, H * kh, "k"), kh, _token_stride(k_shape, ps, LATENT_PE_DIM, "k_pe"),
-        _token_stride(k_shape, vs, H * vh, "v"), vh, scale, out.data_ptr(), 0 if lse is None else lse.data_ptr(),
+        _token_stride(k_shape, vs, H * vh, "v"), vh, _F(scale).value, out.data_ptr(), 0 if lse is None else lse.data_ptr(),
         cu_q, cu_k, B, Tq, Tk, H, N, KDA_LATENT_CAUSAL if causal else 0)
     lib = _library()
     if workspace is None and (cu_seqlens is not None or Tk >= _SPLIT_KEYS):

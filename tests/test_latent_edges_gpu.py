@@ -4,7 +4,7 @@ import numpy as np
 import pytest
 import torch
 
-from kimi_delta_attention_05_gb300 import get_status, latent as M
+from kimi_delta_attention_05_gb300 import KdaError, get_status, latent as M
 from tests.test_latent_gpu import NAN, _rand
 
 pytestmark = pytest.mark.gpu
@@ -63,3 +63,12 @@ def test_workspaces_that_the_gpu_cannot_write_are_refused():
             M.latent_prefill(*prefill, 1.0, cu_seqlens=cu, workspace=ws)
     ws = z(1 << 22, d=torch.float32)
     assert torch.equal(M.latent_decode(*decode, 1.0, workspace=ws), M.latent_decode(*decode, 1.0))
+
+
+@pytest.mark.parametrize("scale", [1e39, float("inf"), float("nan"), -1e39, 0, 1e-60])
+def test_scales_that_are_not_positive_32_bit_numbers_are_refused(scale):
+    z = lambda *s, d=torch.bfloat16: torch.zeros(*s, dtype=d, device="cuda")  # noqa: E731
+    with pytest.raises(KdaError, match="kda_latent_decode.*16"):
+        M.latent_decode(z(2, 1, 4, 576), z(8, 8, 576), z(2, 4, d=torch.int32), z(2, d=torch.int32), scale)
+    with pytest.raises(KdaError, match="kda_latent_prefill.*16"):
+        M.latent_prefill(z(1, 5, 3, 192), z(1, 5, 3, 128), z(1, 5, 64), z(1, 5, 3, 128), scale)
