@@ -286,6 +286,9 @@ DecodeParams decode_params(const kda_latent_decode_args* a) {
   return p;
 }
 
+// Query blocks of packed sequences: at most one a sequence more than the rows fill.
+int64_t prefill_blocks(const kda_latent_prefill_args* a) { return a->Tq / kPrefillRows + a->N; }
+
 int check_prefill(const kda_latent_prefill_args* a) {
   if (!a) return KDA_ERR_NULL_ARG;
   if (a->B < 0 || a->Tq < 0 || a->Tk < 0 || a->H < 0 || a->N < 0 || a->H > 65535) return KDA_ERR_SHAPE;
@@ -300,6 +303,8 @@ int check_prefill(const kda_latent_prefill_args* a) {
   const int64_t most = INT32_MAX / 2;
   if (a->N > (1 << 22) || a->Tq > most || a->Tk > most || (a->B > 0 && (a->Tq > most / a->B || a->Tk > most / a->B)))
     return KDA_ERR_SHAPE;
+  // (packed sequences may be empty: their blocks and heads are counted in 32 bits)
+  if (a->cu_seqlens_q && prefill_blocks(a) * a->H > INT32_MAX) return KDA_ERR_SHAPE;
   if (!(a->scale > 0.f) || !std::isfinite(a->scale)) return KDA_ERR_SCALE;
   const bool queries = a->B * a->Tq * a->H > 0, keys = a->B * a->Tk * a->H > 0;
   if (queries && (!a->q || !a->out)) return KDA_ERR_NULL_ARG;
@@ -314,9 +319,6 @@ int check_prefill(const kda_latent_prefill_args* a) {
     return KDA_ERR_STRIDE;
   return KDA_OK;
 }
-
-// Query blocks of packed sequences: at most one a sequence more than the rows fill.
-int64_t prefill_blocks(const kda_latent_prefill_args* a) { return a->Tq / kPrefillRows + a->N; }
 
 // The sizes and the form of a call.
 PrefillParams prefill_shape(const kda_latent_prefill_args* a) {

@@ -43,6 +43,16 @@ def test_packed_tokens_without_sequences_are_refused(tq, tk, code):
     assert lib.kda_latent_prefill_workspace_bytes(ctypes.byref(a)) == (0 if code else 256)
 
 
+def test_more_packed_blocks_than_32_bits_count_are_refused():
+    """Before anything is launched, as every argument error; empty sequences make it possible for small tensors."""
+    a = M.kda_latent_prefill_args(FAKE, FAKE, FAKE, FAKE, 192 * 1024, 192, 256 * 1024, 256, 64, 256 * 1024, 256, 0.07, FAKE,
+                                  None, FAKE, FAKE, 1, 100, 100, 1024, 1 << 22, 1)
+    lib = M._library()
+    assert lib.kda_latent_prefill(ctypes.byref(a), FAKE, 1 << 40, None) == 3
+    a.H = 500
+    assert lib.kda_latent_prefill_workspace_bytes(ctypes.byref(a)) > 0
+
+
 def test_workspaces_that_the_gpu_cannot_write_are_refused():
     """Not on the device, or more elements than memory (an expanded view)."""
     cpu = torch.device("cpu")
