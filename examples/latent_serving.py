@@ -52,9 +52,10 @@ class Layers:
         y = x @ self.kda_in.T
         q, k, v, g = (y[..., i * H * 128:(i + 1) * H * 128].reshape(B, T, H, 128).contiguous() for i in range(4))
         beta = y[..., 4 * H * 128:].contiguous()
-        call = kda_fwd_recurrent if T == 1 else kda_fwd
+        # one token updates the states in place; the chunked form reads its initial states from a buffer of their own
+        call, initial = (kda_fwd_recurrent, states) if T == 1 else (kda_fwd, states.clone())
         out = call(q, k, v, g, beta, 128 ** -0.5, A_log=self.a_log, dt_bias=self.dt_bias, lower_bound=-5.0,
-                   initial_state=states, final_state=states, cu_seqlens=cu, qk_l2norm=True)
+                   initial_state=initial, final_state=states, cu_seqlens=cu, qk_l2norm=True)
         return x + out.reshape(B, T, -1) @ self.kda_out.T
 
     def queries(self, x):
