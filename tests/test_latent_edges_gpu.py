@@ -5,7 +5,8 @@ import pytest
 import torch
 
 from kimi_delta_attention_05_gb300 import KdaError, get_status, latent as M
-from tests.test_latent_gpu import NAN, _rand
+from oracle import latent as L
+from tests.test_latent_gpu import NAN, _decode, _f64, _rand
 
 pytestmark = pytest.mark.gpu
 
@@ -72,3 +73,57 @@ def test_scales_that_are_not_positive_32_bit_numbers_are_refused(scale):
         M.latent_decode(z(2, 1, 4, 576), z(8, 8, 576), z(2, 4, d=torch.int32), z(2, d=torch.int32), scale)
     with pytest.raises(KdaError, match="kda_latent_prefill.*16"):
         M.latent_prefill(z(1, 5, 3, 192), z(1, 5, 3, 128), z(1, 5, 64), z(1, 5, 3, 128), scale)
+
+
+# ---- the forms that large calls take ----
+
+def _many_lengths(count, longest, seed):
+    """Ragged, with empty requests, single tokens, whole tiles and more than four tiles among them."""
+    lens = np.random.default_rng(seed).integers(0, longest + 1, count)
+    lens[:8] = [0, 1, 64, 128, longest, 0, 0, 65]
+    lens[-2:] = [0, longest]
+    return [int(x) for x in np.minimum(lens, longest)]
+
+
+@pytest.mark.parametrize("requests,R,H", [(400, 1, 5), (300, 1, 16), (300, 1, 32), (220, 2, 16), (200, 1, 64), (200, 3, 20),
+                                          (160, 1, 128), (120, 2, 65), (90, 3, 64)])
+def test_decode_more_requests_than_shares(requests, R, H):
+    """Every column width, one and several blocks of query rows: a CTA works on many pieces in turn, and the
+    requests that several CTAs hold are listed by share."""
+    assert requests > 152 // -(-R * H // 64)
+    _decode(_many_lengths(requests, 700, requests + H), R, H, 16, seed=requests)
+
+
+@pytest.mark.parametrize("requests,R,H", [(400, 1, 8), (333, 2, 16), (170, 1, 64), (120, 3, 64)])
+def test_decode_many_short_requests(requests, R, H):
+    """Tables of up to four tiles: requests are not split, and there are more of them than CTAs."""
+    _decode(_many_lengths(requests, 256, requests), R, H, 64, seed=H)
+
+
+@pytest.mark.parametrize("T", [4863, 4864, 4865, 14593, 29185])
+@pytest.mark.parametrize("norm", [False, True])
+def test_append_many_tokens(T, norm):
+    """At and past the limit (8 x 152 x 4 tokens) from which a warp takes two at a time, an odd token at the
+    end, and past the tokens (912 x 16) that the grid takes in one round; skipped slots and one outside."""
+    gen = torch.Generator().manual_seed(T)
+    rows = _rand(gen, T, 576, std=2.0).cuda()
+    pages = T // 16 + 3
+    cache = torch.full((pages, 16, 576), 5.0, dtype=torch.bfloat16, device="cuda")
+    slots = torch.randperm(pages * 16, generator=gen)[:T]
+    slots[torch.randperm(T, generator=gen)[:T // 50]] = -1
+    slots[T - 2] = pages * 16
+    w = (torch.rand(512, generator=gen) + 0.5).cuda() if norm else None
+    M.latent_append(rows[:, :512], rows[:, 512:], slots.cuda(), cache, w, 1e-5)
+    assert get_status() == 20  # the slot outside
+    kept = (slots >= 0) & (slots < pages * 16)
+    flat, at = cache.view(-1, 576), slots[kept].cuda()
+    got, src = flat[at], rows[kept.cuda()]
+    assert torch.equal(got[:, 512:], src[:, 512:])
+    if norm:  # fp32 arithmetic and one rounding to bf16: 2^-8, with 2^-16 for the fp32 steps
+        ref = L.normalised(_f64(src[:, :512]), _f64(w), 1e-5)
+        assert (np.abs(_f64(got[:, :512]) - ref) <= (2.0 ** -8 + 2.0 ** -16) * np.abs(ref) + 1e-38).all()
+    else:
+        assert torch.equal(got, src)
+    rest = torch.ones(pages * 16, dtype=torch.bool, device="cuda")
+    rest[at] = False
+    assert (flat[rest] == 5.0).all()
