@@ -6,7 +6,7 @@ import torch
 
 from kimi_delta_attention_05_gb300 import KdaError, get_status, latent as M
 from oracle import latent as L
-from tests.test_latent_gpu import NAN, _decode, _f64, _rand
+from tests.test_latent_gpu import NAN, _check, _decode, _f64, _paged, _rand
 
 pytestmark = pytest.mark.gpu
 
@@ -127,3 +127,88 @@ def test_append_many_tokens(T, norm):
     rest = torch.ones(pages * 16, dtype=torch.bool, device="cuda")
     rest[at] = False
     assert (flat[rest] == 5.0).all()
+
+
+# ---- graphs whose inputs change between replays ----
+
+@pytest.mark.parametrize("requests,R,H", [(5, 1, 32), (300, 1, 16), (3, 3, 64)])
+def test_decode_graph_with_other_lengths(requests, R, H):
+    """Lengths are read on the device: every replay answers the lengths of its time, whole buffers anew."""
+    gen = torch.Generator().manual_seed(requests)
+    most = _many_lengths(requests, 600, 1) if requests > 8 else [900, 2500, 37, 0, 1300][:requests]
+    cache, table = _paged(gen, most, 64, behind=0.0)
+    q = _rand(gen, requests, R, H, 576)
+    dq, dc, dt, lens = q.cuda(), cache.cuda(), table.cuda(), torch.tensor(most, dtype=torch.int32).cuda()
+    out = torch.empty(requests, R, H, 512, dtype=torch.bfloat16, device="cuda")
+    lse = torch.empty(requests, R, H, device="cuda")
+    ws = torch.empty(max(1, M.latent_decode_workspace_bytes(requests, R, H, dc, dt)), dtype=torch.uint8, device="cuda")
+    M.latent_decode(dq, dc, dt, lens, 0.07, out, lse, workspace=ws)
+    torch.cuda.synchronize()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        M.latent_decode(dq, dc, dt, lens, 0.07, out, lse, workspace=ws)
+    for now in (most, [n // 2 for n in most], [0] * requests, [min(n, 1) for n in most],
+                [n if i % 3 else 0 for i, n in enumerate(most)], most):
+        lens.copy_(torch.tensor(now, dtype=torch.int32))
+        out.fill_(NAN)
+        lse.fill_(NAN)
+        g.replay()
+        torch.cuda.synchronize()
+        _check(out, lse, L.absorbed(_f64(q), _f64(cache), table.tolist(), now, 0.07), max(now + [1]))
+    assert get_status() == 0
+
+
+@pytest.mark.parametrize("n,keys,heads,offsets", [
+    (300, 13000, 2, [([0, 20, 290, 300], [0, 5000, 12000, 13000]), ([0, 0, 1, 300], [0, 12990, 12990, 13000]),
+                     ([0, 300, 300, 300], [0, 13000, 13000, 13000])]),           # split over the keys
+    (500, 700, 3, [([0, 1, 130, 500], [0, 200, 330, 700]), ([0, 500, 500, 500], [0, 700, 700, 700]),
+                   ([0, 200, 400, 500], [0, 10, 600, 700])]),                    # not split
+])
+def test_packed_prefill_graph_with_other_offsets(n, keys, heads, offsets):
+    gen = torch.Generator().manual_seed(n)
+    q, k, pe, v = (_rand(gen, 1, *x) for x in ((n, heads, 192), (keys, heads, 128), (keys, 64), (keys, heads, 128)))
+    dev = [t.cuda() for t in (q, k, pe, v)]
+    cu, cu_k = (torch.tensor(x, device="cuda") for x in offsets[0])
+    out, lse = torch.empty(1, n, heads, 128, dtype=torch.bfloat16, device="cuda"), torch.empty(1, n, heads, device="cuda")
+    ws = torch.empty(M.latent_prefill_workspace_bytes(1, n, keys, heads, 3), dtype=torch.uint8, device="cuda")
+    M.latent_prefill(*dev, 0.07, out, lse, cu, cu_k, workspace=ws)
+    torch.cuda.synchronize()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        M.latent_prefill(*dev, 0.07, out, lse, cu, cu_k, workspace=ws)
+    for a, b in offsets:
+        cu.copy_(torch.tensor(a))
+        cu_k.copy_(torch.tensor(b))
+        out.fill_(NAN)
+        lse.fill_(NAN)
+        g.replay()
+        torch.cuda.synchronize()
+        _check(out, lse, L.expanded(_f64(q), _f64(k), _f64(pe), _f64(v), 0.07, True, a, b), keys)
+    assert get_status() == 0
+
+
+@pytest.mark.parametrize("n,keys,heads", [(200, 5000, 2), (1100, 6000, 1), (1100, 1100, 1)])
+def test_dense_prefill_graph_with_other_inputs(n, keys, heads):
+    """Split in single CTAs, split in pairs, and not split."""
+    gen = torch.Generator().manual_seed(keys)
+    shapes = (n, heads, 192), (keys, heads, 128), (keys, 64), (keys, heads, 128)
+    dev = [torch.zeros(1, *x, dtype=torch.bfloat16, device="cuda") for x in shapes]
+    out, lse = torch.empty(1, n, heads, 128, dtype=torch.bfloat16, device="cuda"), torch.empty(1, n, heads, device="cuda")
+    need = M.latent_prefill_workspace_bytes(1, n, keys, heads)
+    assert (need > 0) == (keys > 4096)
+    ws = torch.empty(need, dtype=torch.uint8, device="cuda") if need else None
+    M.latent_prefill(*dev, 0.07, out, lse, workspace=ws)
+    torch.cuda.synchronize()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        M.latent_prefill(*dev, 0.07, out, lse, workspace=ws)
+    for _ in range(2):
+        now = [_rand(gen, 1, *x) for x in shapes]
+        for d, x in zip(dev, now):
+            d.copy_(x)
+        out.fill_(NAN)
+        lse.fill_(NAN)
+        g.replay()
+        torch.cuda.synchronize()
+        _check(out, lse, L.expanded(*(_f64(x) for x in now), 0.07, True), keys)
+    assert get_status() == 0
