@@ -173,6 +173,7 @@ int kda_latent_decode(const kda_latent_decode_args *args, void *workspace, size_
  * joined, for which it needs some; a dense call with workspace NULL is not split.
  */
 #define KDA_LATENT_CAUSAL 0x1u
+#define KDA_LATENT_SPLIT_KEYS 4096 /* dense calls with fewer keys are never split and need no workspace */
 typedef struct kda_latent_prefill_args {
   const void *q, *k, *k_pe, *v;
   int64_t q_stride_t, q_stride_h, k_stride_t, k_stride_h, k_pe_stride_t, v_stride_t, v_stride_h;

@@ -5,6 +5,8 @@
 #include <stddef.h>
 #include <stdint.h>
 
+#include "../../include/kda_latent.h"
+
 namespace kda {
 
 constexpr int kLat = 512;           // latent values of a cache row
@@ -62,7 +64,7 @@ bool prefill_pairs(int64_t rows, int64_t sequences, bool packed);
 
 // Bytes that a split call needs for its partial rows; 0: it is not split.
 size_t prefill_split_bytes(const PrefillParams& p);
-constexpr int64_t kPrefillSplitKeys = 4096;  // fewer keys are never split
+constexpr int64_t kPrefillSplitKeys = KDA_LATENT_SPLIT_KEYS;  // fewer keys are never split
 
 constexpr int kPreKeys = 128;     // keys of a tile
 constexpr int kPreItemCost = 2;   // what an item costs beside its key tiles, in tiles

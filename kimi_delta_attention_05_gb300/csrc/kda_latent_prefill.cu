@@ -9,9 +9,13 @@ namespace {
 // more than a ninth more to do than a share and the join (taken as ten key tiles).
 // 1024 rows behind 15360 cached, 16 heads: 180 us unsplit, 99 split; 256 behind 32768,
 // 8 heads: 442 and 46; two of the first, whose 64 items nearly fill the 76 pairs: 188
-// and 195, so those stay whole.  Packed sequences, whose lengths are on the device, are
-// split where their blocks cannot fill the GPU and they have many keys on average (1024
-// rows behind up to 15360, 16 heads: 229 us unsplit, 103 split).
+// and 195, so those stay whole.  Fewer than kPrefillSplitKeys keys are not looked at,
+// which spares short calls the workspace and its query; at the limit a split brings 256
+// rows and 8 heads from 59.7 us to 28.5, 512 rows and 32 heads from 61.5 to 46.4.  It
+// would still gain below (the same over 3000 keys: 46.5 and 28.7, 48.0 and 39.9); from
+// 2048 keys down the rule splits none of these.  Packed sequences, whose lengths are on
+// the device, are split where their blocks cannot fill the GPU and they have many keys on
+// average (1024 rows behind up to 15360, 16 heads: 229 us unsplit, 103 split).
 constexpr int kMostCtas = 512;
 PrefillSplit split_of(const PrefillParams& p, int sms) {
   PrefillSplit sp = {};

@@ -314,7 +314,7 @@ def _token_stride(shape, strides, row, name):
     return strides[1] if T > 1 else row
 
 
-_SPLIT_KEYS = 4096  # dense calls with fewer keys need no workspace
+_SPLIT_KEYS = 4096  # KDA_LATENT_SPLIT_KEYS: dense calls with fewer keys need no workspace, so it is not asked for
 
 
 def latent_prefill(q, k, k_pe, v, scale, out=None, lse=None, cu_seqlens=None, cu_seqlens_k=None, *, causal=True,

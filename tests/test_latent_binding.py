@@ -65,3 +65,11 @@ def test_workspaces_that_the_gpu_cannot_write_are_refused():
     for view in (ws[:1].expand(1 << 20), ws[::2]):
         with pytest.raises(ValueError, match="workspace"):
             M._scratch(view, cpu)
+
+
+def test_the_binding_asks_for_a_workspace_from_the_keys_on_from_which_calls_are_split():
+    """The limit stands in the header and in the binding: were the binding's higher, calls between the two
+    would silently run whole."""
+    for rows, heads in ((1, 1), (200, 1)):
+        assert M.latent_prefill_workspace_bytes(1, rows, M._SPLIT_KEYS - 1, heads) == 0
+        assert M.latent_prefill_workspace_bytes(1, rows, M._SPLIT_KEYS, heads) > 0
