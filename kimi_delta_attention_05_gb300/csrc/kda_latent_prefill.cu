@@ -65,7 +65,10 @@ size_t part_floats(const PrefillParams& p, const PrefillSplit& sp) {
 // Pairs halve the traffic of keys and values, but their items are twice as long and
 // in a fixed order.  Packed: 12 sequences of 1167 rows on average, 32 heads, 216 us in
 // single CTAs and 236 in pairs; 8 of 2547, 16 heads, 266 and 251.  Dense, where the
-// items of single CTAs have a fixed order too: from 1024 rows on.
+// items of single CTAs have a fixed order too: from 1024 rows on (16 sequences, 32 heads,
+// in pairs and in single CTAs: 768 rows 138 us and 112, 1024 168 and 170, 1280 266 and 241,
+// 1536 304 and 329, 2048 511 and 543, 3000 1082 and 1190; one of 8 heads 14.9 and 16.3,
+// 19.1 and 19.5, 20.1 and 22.9, 24.3 and 26.1, 29.7 and 33.3, 40.8 and 46.8).
 bool prefill_pairs(int64_t rows, int64_t sequences, bool packed) { return rows >= (packed ? 2048 : 1024) * sequences; }
 
 size_t prefill_split_bytes(const PrefillParams& p) {
