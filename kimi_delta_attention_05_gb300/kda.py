@@ -149,9 +149,10 @@ def make_args(q, k, v, g, beta, scale, out, A_log=None, dt_bias=None, lower_boun
 
 def get_status(stream=None) -> int:
     """Read and clear the device status word of ``stream`` (a torch stream;
-    default: the current stream): 0, KDA_ERR_DEVICE_TIMEOUT (13) or
-    KDA_ERR_BAD_SEQLENS (14) for the calls enqueued on it; -1 if it cannot be
-    read.  Synchronises the stream."""
+    default: the current stream): 0, or the code that the calls enqueued on it
+    recorded last: KDA_ERR_DEVICE_TIMEOUT (13), KDA_ERR_BAD_SEQLENS (14), and from
+    the latent calls KDA_ERR_BAD_LENGTHS (18), KDA_ERR_NO_PAGES (19) or
+    KDA_ERR_BAD_PAGE (20); -1 if it cannot be read.  Synchronises the stream."""
     s = stream if stream is not None else torch.cuda.current_stream()
     return int(load_library().kda_get_status(ctypes.c_void_p(s.cuda_stream)))
 
