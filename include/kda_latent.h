@@ -19,6 +19,14 @@
  * query is [W_uk,h^T q_nope | q_pe] and the head's output W_uv,h o.  Those
  * products are plain matrix products and stay with the caller.
  *
+ * Arithmetic of the two attention forms: scores, maxima, sums, accumulators and
+ * the parts of a split call are fp32.  The softmax weights are rounded to bf16
+ * for the product with the values, the operands' type of the tensor cores, after
+ * their sum has been taken; with the rounding of out itself (2^-8 each) a value
+ * is off by at most about 2^-7 sum_j p_j |v_j|.  Measured against 64 bits on
+ * standard normal data: relative RMS 0.0017 to 0.0023, of which 0.0017 are the
+ * rounding of out.  lse is fp32 and does not see the weights' rounding.
+ *
  * Conventions are those of kda.h: caller-owned device memory, 16-byte aligned
  * tensor pointers, work enqueued on the given stream, argument errors returned
  * before any launch, inconsistent device values (lengths, page ids, slots)
@@ -127,7 +135,9 @@ int kda_latent_append(const kda_latent_append_args *args, void *stream);
  *                [0, max_pages * page_size] is taken as the nearer bound and
  *                sets KDA_ERR_BAD_LENGTHS; a page id outside the cache reads as
  *                zero rows and sets KDA_ERR_BAD_PAGE.
- * What the cache holds behind a request's length is never used, whatever it is.
+ * What the cache holds behind a request's length is never used, whatever it is;
+ * the rows within it have to be finite (with R > 1 also for the tokens that do not
+ * see the last of them: they take part with weight 0).
  * Results do not depend on anything but the arguments (fixed order of sums).
  */
 typedef struct kda_latent_decode_args {
@@ -166,7 +176,7 @@ int kda_latent_decode(const kda_latent_decode_args *args, void *workspace, size_
  *         a violation of either sets KDA_ERR_BAD_SEQLENS and nothing is written.
  *         (N == 0 with Tq or Tk > 0 is refused with KDA_ERR_BAD_SEQLENS at once.)
  * Rows of other sequences (and past the tensors) never touch a result; within a
- * sequence, keys and values have to be finite.
+ * sequence, keys and values have to be finite (behind the causal edge too, as there).
  *
  * workspace: kda_latent_prefill_workspace_bytes bytes, aligned to 256.  A call with
  * few blocks of queries and many keys has its keys split over the SMs and the parts

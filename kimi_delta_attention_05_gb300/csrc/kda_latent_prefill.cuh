@@ -786,7 +786,9 @@ __global__ void __launch_bounds__(kPreThreads, 1)
         f32x2 sum[2] = {f2(0.f, 0.f), f2(0.f, 0.f)};
 #pragma unroll
         for (int c = 0; c < 128; c += 32) {
-          float w[16];  // 32 weights as bf16 pairs (the operand type; the sum is taken before the rounding)
+          // 32 weights as bf16 pairs (the operand type; the sum is taken before the rounding): on the 8192-token
+          // prompt a relative RMS against 64 bits of 0.0020, of which 0.0015 are the output's rounding
+          float w[16];
 #pragma unroll
           for (int e = 0; e < 16; ++e) {
             const float2 x = f2u(fma2(f2(s[c + 2 * e], s[c + 2 * e + 1]), sl2, base2));
