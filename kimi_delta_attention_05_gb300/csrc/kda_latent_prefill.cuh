@@ -34,10 +34,12 @@
 // its place; loads from L2 halve too.  Items are then 512 rows, whose causal
 // edge wastes more, so short sequences keep single CTAs.
 //
-// Measured: one prompt of 8192 tokens, 32 heads, in pairs: 361 to 375 us by board and
-// power, 1.83 to 1.90 PFLOP/s, tensor cores active 86% of the time; two pieces of 1024
-// behind 15360 cached, 16 heads: 186 to 190 us, 93% active on the 128 SMs of 152 that have
-// an item; 24 packed sequences of up to 2048, 16 heads, in single CTAs: 161 us, 59%
+// Measured, passes back to back in a graph: one prompt of 8192 tokens, 32 heads, in pairs:
+// 361 to 377 us by board and power, 1.82 to 1.90 PFLOP/s (0.95 to 0.99 of cuBLAS's burst
+// rate), tensor cores active 86% of the time; called on new inputs each time 420 us, 1.63
+// PFLOP/s (0.85 of that rate, 0.95 of cuBLAS's sustained one).  Two pieces of 1024 behind
+// 15360 cached, 16 heads: 186 to 194 us, 93% active on the 128 SMs of 152 that have an item;
+// 24 packed sequences of up to 2048, 16 heads, in single CTAs: 161 to 190 us by process, 59%
 // active: an item of 11 tiles pays about 8000 cycles for its first loads and its output.
 //
 // Roles: warps 0-3 and 4-7 softmax and output of the two tiles, warp 8 copies,
