@@ -53,7 +53,8 @@ extern "C" {
 #define KDA_ERR_STRIDE 15      /* a stride is not a multiple of 16 bytes or rows overlap */
 #define KDA_ERR_SCALE 16       /* scale is not a positive finite number */
 #define KDA_ERR_PAGE_SIZE 17   /* page_size is not a positive multiple of 8 */
-#define KDA_ERR_BAD_LENGTHS 18 /* (device status) a length is negative, or longer than its table, slots or pages allow */
+#define KDA_ERR_BAD_LENGTHS 18 /* (device status) a length is negative, or longer than its table, slots or pages allow;
+                                  or a request's number does not fit */
 #define KDA_ERR_NO_PAGES 19    /* (device status) kda_latent_plan: too few free pages */
 #define KDA_ERR_BAD_PAGE 20    /* (device status) a page id or slot outside the cache */
 
@@ -198,6 +199,126 @@ typedef struct kda_latent_prefill_args {
 size_t kda_latent_prefill_workspace_bytes(const kda_latent_prefill_args *args);
 int kda_latent_prefill(const kda_latent_prefill_args *args, void *workspace, size_t workspace_bytes,
                        void *stream);
+
+/* ---- pages that several requests hold ----
+ *
+ * Requests that share a prefix (samples or beams of one prompt, a common system
+ * prompt) hold the same pages.  shares[page] (int32, one a page of the cache)
+ * counts a page's holders beyond the first: 0 where one row of the table holds
+ * it, so the pages that kda_latent_plan takes are right with zeros, and whole
+ * pages are never written again.  A request holds the pages
+ * block_table[b][0 .. ceil(cached_lens[b] / page_size)); B is at most 16384.
+ * Every list of pages is in an order of its own, not of time.
+ */
+
+/*
+ * Requests that go on from others: child f = children[f] gets the first
+ * fork_lens[f] tokens of request parents[f] (all of them where fork_lens is
+ * NULL).  Whole pages are shared: their ids go into the child's row, their counts
+ * up by one.  The rows of a last page that is not whole are copied into the next
+ * page of free_pages (children in order).  Entries behind a child's last page are
+ * left as they are; what a child's row held before has to be released first.
+ *
+ *  parents, children, fork_lens : int32 [F].  No child twice, and none that is a
+ *                parent in the same call; one parent may have many children
+ *  block_table : int32 [B, max_pages]; the children's rows are written
+ *  free_pages  : int32 [num_free]
+ *  shares      : int32 [num_pages], read and written
+ *  seq_lens    : int32 [B], out (another buffer than cached_lens): the children's
+ *                tokens, else cached_lens
+ *  pages_taken : int32 [1], out: entries of free_pages used (always the first ones)
+ * Numbers of requests outside [0, B), lengths that do not fit, a child twice or as
+ * parent set KDA_ERR_BAD_LENGTHS, too short a free_pages KDA_ERR_NO_PAGES, and
+ * nothing is forked (seq_lens = cached_lens, pages_taken 0).  A page id outside the
+ * cache sets KDA_ERR_BAD_PAGE; it is entered, but not counted or copied.
+ */
+typedef struct kda_latent_fork_args {
+  const int32_t *parents, *children, *fork_lens, *cached_lens;
+  int32_t *block_table;
+  int64_t table_stride;
+  const int32_t *free_pages;
+  int32_t *shares;
+  kda_latent_cache cache;
+  int32_t *seq_lens, *pages_taken;
+  int64_t F, B, max_pages, num_free;
+} kda_latent_fork_args;
+
+int kda_latent_fork(const kda_latent_fork_args *args, void *stream);
+
+/*
+ * Requests that give pages back: rows[f] keeps its first keep_lens[f] tokens (none
+ * where keep_lens is NULL) and drops the pages behind them.  The count of a dropped
+ * page goes down by one; pages whose last holder dropped them are listed.
+ *
+ *  rows, keep_lens : int32 [F]; no row twice
+ *  block_table : int32 [B, max_pages], left as it is (a request's length says
+ *                which entries hold)
+ *  shares      : int32 [num_pages], not negative, read and written
+ *  seq_lens    : int32 [B], out (another buffer than cached_lens): keep_lens for
+ *                the rows, else cached_lens
+ *  pages       : int32 [num_pages], out: the pages that are free now, ascending,
+ *                and -1 behind them
+ *  count       : int32 [1], out: how many these are
+ * A row outside [0, B) or twice, a length that does not fit or keep_lens beyond it
+ * set KDA_ERR_BAD_LENGTHS, and nothing is released (count 0).  A page id outside
+ * the cache sets KDA_ERR_BAD_PAGE and is passed over.  A page that more rows drop
+ * than its count says is listed once.
+ */
+typedef struct kda_latent_release_args {
+  const int32_t *rows, *keep_lens, *cached_lens, *block_table;
+  int64_t table_stride;
+  int32_t *shares, *seq_lens, *pages, *count;
+  int64_t F, B, max_pages, num_pages, page_size;
+} kda_latent_release_args;
+
+int kda_latent_release(const kda_latent_release_args *args, void *stream);
+
+/*
+ * Held pages together: with U pages held by the rows of the table, those with ids
+ * from U on move to the ids below U that no row holds, both in ascending order, so
+ * that pages U and behind are free.  Rows of pages are copied within the cache;
+ * tables, counts and a map of old to new ids come out.
+ *
+ *  block_table, block_table_out : int32 [B, max_pages] (may be the same buffer, with
+ *                the same stride); entries behind a request's last page are copied
+ *  shares, shares_out : int32 [num_pages] (may be the same buffer); counts by new
+ *                id, 0 from U on
+ *  page_map    : int32 [num_pages], out: new id of every held page, -1 for others
+ *  pages_used  : int32 [1], out: U
+ * A length that does not fit sets KDA_ERR_BAD_LENGTHS and nothing moves: tables and
+ * counts come out as they are, the map is the identity, pages_used num_pages.  A
+ * page id outside the cache sets KDA_ERR_BAD_PAGE and comes out as it is.
+ * workspace: kda_latent_compact_workspace_bytes bytes, aligned to 256; garbage
+ * afterwards, needs no initialisation.
+ */
+typedef struct kda_latent_compact_args {
+  const int32_t *cached_lens, *block_table;
+  int64_t table_stride;
+  int32_t *block_table_out;
+  int64_t table_out_stride;
+  const int32_t *shares;
+  int32_t *shares_out, *page_map, *pages_used;
+  kda_latent_cache cache;
+  int64_t B, max_pages;
+} kda_latent_compact_args;
+
+size_t kda_latent_compact_workspace_bytes(const kda_latent_compact_args *args);
+int kda_latent_compact(const kda_latent_compact_args *args, void *workspace, size_t workspace_bytes, void *stream);
+
+/*
+ * Page src_pages[i] of one cache into page dst_pages[i] of another (or of the same
+ * one, where no page is both read and written), with the same page_size; strides
+ * may differ.  dst_pages should be distinct.  A page id outside its cache sets
+ * KDA_ERR_BAD_PAGE and is passed over.
+ *  src_pages, dst_pages : int32 [n]
+ */
+typedef struct kda_latent_copy_args {
+  kda_latent_cache src, dst;
+  const int32_t *src_pages, *dst_pages;
+  int64_t n;
+} kda_latent_copy_args;
+
+int kda_latent_copy(const kda_latent_copy_args *args, void *stream);
 
 #ifdef __cplusplus
 }

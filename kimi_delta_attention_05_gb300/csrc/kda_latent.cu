@@ -247,6 +247,12 @@ int check_cache(const kda_latent_cache& c) {
   return KDA_OK;
 }
 
+}  // namespace
+
+int latent_check_cache(const kda_latent_cache* c) { return check_cache(*c); }
+
+namespace {
+
 int check_decode(const kda_latent_decode_args* a) {
   if (!a) return KDA_ERR_NULL_ARG;
   if (a->B < 0 || a->R < 0 || a->H < 0 || a->max_pages < 0) return KDA_ERR_SHAPE;

@@ -107,6 +107,9 @@ bool launch_overlapped(void (*kernel)(P...), dim3 grid, unsigned threads, size_t
   return cudaLaunchKernelEx(&cfg, kernel, static_cast<P>(args)...) == cudaSuccess;
 }
 
+// The checks of a cache's address, sizes and strides.
+int latent_check_cache(const kda_latent_cache* c);
+
 size_t decode_workspace_bytes(const DecodeParams& p);
 // false: a tensor map could not be made or a launch attribute set (nothing launched)
 bool launch_latent_decode(const DecodeParams& p, cudaStream_t s);

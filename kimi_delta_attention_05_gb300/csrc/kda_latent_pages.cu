@@ -1,0 +1,618 @@
+// Pages of the latent cache that several rows of a block table hold: fork,
+// release, compact and copy (include/kda_latent.h).
+//
+// Holders are counted beyond the first (shares[page]: 0 where one row holds the
+// page), so pages that kda_latent_plan takes are right as they come.  Counts are
+// changed by integer atomics, whose order does not show, and every list that
+// comes out is in ascending order of pages, by a scan: results do not depend on
+// timing.
+#include <cooperative_groups.h>
+
+#include <algorithm>
+#include <atomic>
+
+#include "../../include/kda_latent.h"
+#include "kda_common.cuh"
+#include "kda_kernels.cuh"
+#include "kda_latent.cuh"
+
+namespace kda {
+
+namespace cg = cooperative_groups;
+
+constexpr int kRowPieces = kLatRow / 8;         // 16-byte pieces of a cache row
+constexpr int kGroupRows = 8;                   // page sizes are multiples of this
+constexpr int kCopyThreads = 4 * kRowPieces;    // four rows at a time, twice a group
+constexpr int kPageThreads = 1024;
+constexpr int kPageCluster = 8;                 // CTAs of the kernels that list pages
+
+struct PageCache {
+  uint16_t* data;
+  int64_t num_pages, page_stride, token_stride;
+};
+
+__device__ __forceinline__ int warp_scan_int(int x, int lane) {
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int y = __shfl_up_sync(0xffffffffu, x, o);
+    if (lane >= o) x += y;
+  }
+  return x;
+}
+
+// Pages of a length that is not negative.
+__device__ __forceinline__ int pages_of(int tokens, int page) { return (int)(((uint32_t)tokens + (uint32_t)page - 1) / (uint32_t)page); }
+
+// Exclusive prefix of x over the block's threads; `total` gets the sum.
+template <int kThreads>
+__device__ __forceinline__ int block_scan(int x, int* sums, int& total) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int upto = warp_scan_int(x, lane);
+  if (lane == 31) sums[warp] = upto;
+  __syncthreads();
+  int before = 0;
+  total = 0;
+#pragma unroll
+  for (int w = 0; w < kThreads / 32; ++w) {
+    const int s = sums[w];
+    if (w < warp) before += s;
+    total += s;
+  }
+  __syncthreads();  // sums are read
+  return before + upto - x;
+}
+
+// ---- copies of pages ----
+//
+// A CTA takes four groups of eight rows at a time (36.9 KB), a thread eight 16-byte
+// pieces of them, all loaded before the first is stored: enough bytes in flight for
+// HBM with a few CTAs an SM, and any page size is whole groups.
+struct CopyPlace {
+  const uint16_t* src;  // nullptr: nothing to copy
+  uint16_t* dst;
+  int rows;             // of the group
+};
+
+template <class Place>
+__device__ __forceinline__ void copy_groups(int64_t groups, int64_t src_stride, int64_t dst_stride, int64_t cta,
+                                            int64_t ctas, Place place) {
+  const int row = threadIdx.x / kRowPieces, col = (threadIdx.x % kRowPieces) * 8;
+  for (int64_t g0 = cta * 4; g0 < groups; g0 += ctas * 4) {
+    CopyPlace at[4];
+    uint4 x[4][2];
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      at[k].src = nullptr;
+      if (g0 + k < groups) at[k] = place(g0 + k);
+    }
+#pragma unroll
+    for (int k = 0; k < 4; ++k)
+#pragma unroll
+      for (int h = 0; h < 2; ++h)
+        if (at[k].src && row + 4 * h < at[k].rows)
+          x[k][h] = __ldcs(reinterpret_cast<const uint4*>(at[k].src + (row + 4 * h) * src_stride + col));
+#pragma unroll
+    for (int k = 0; k < 4; ++k)
+#pragma unroll
+      for (int h = 0; h < 2; ++h)
+        if (at[k].src && row + 4 * h < at[k].rows)
+          *reinterpret_cast<uint4*>(at[k].dst + (row + 4 * h) * dst_stride + col) = x[k][h];
+  }
+}
+
+// a / b of non-negative numbers, in 32 bits where they fit
+__device__ __forceinline__ int64_t div_pages(int64_t a, int b) {
+  return (a >> 31) == 0 ? (int64_t)((uint32_t)a / (uint32_t)b) : a / b;
+}
+
+struct CopyParams {
+  PageCache src, dst;
+  const int32_t *src_pages, *dst_pages;
+  int64_t n;
+  int page;
+  int* status;
+};
+
+__device__ __forceinline__ CopyPlace page_group(const PageCache& src, const PageCache& dst, int64_t from, int64_t to,
+                                                int group, int* status) {
+  CopyPlace c = {nullptr, nullptr, kGroupRows};
+  if (from < 0 || from >= src.num_pages || to < 0 || to >= dst.num_pages) {
+    if (threadIdx.x == 0) atomicExch(status, KDA_ERR_BAD_PAGE);
+    return c;
+  }
+  c.src = src.data + from * src.page_stride + (int64_t)group * kGroupRows * src.token_stride;
+  c.dst = dst.data + to * dst.page_stride + (int64_t)group * kGroupRows * dst.token_stride;
+  return c;
+}
+
+__global__ void __launch_bounds__(kCopyThreads) kda_latent_copy_kernel(const CopyParams p) {
+  asm volatile("griddepcontrol.wait;\n" ::: "memory");
+  const int per = p.page / kGroupRows;
+  copy_groups(p.n * per, p.src.token_stride, p.dst.token_stride, blockIdx.x, gridDim.x, [&](int64_t g) {
+    const int64_t i = div_pages(g, per);
+    return page_group(p.src, p.dst, p.src_pages[i], p.dst_pages[i], (int)(g - i * per), p.status);
+  });
+}
+
+// ---- fork ----
+//
+// Child f takes the first t_f tokens of its parent: floor(t_f / P) table entries,
+// whose counts go up by one, and where t_f is not whole pages the free page
+// number sum_{e < f} [t_e mod P > 0] with the last t_f mod P rows.  Every CTA checks
+// all forks and counts the pages of those before its own for itself (as the plan
+// kernel does: a second launch would cost more), then does its share of one fork.
+struct ForkParams {
+  const int32_t *parents, *children, *take, *cached;
+  int32_t* table;
+  int64_t table_stride, max_pages;
+  const int32_t* free_pages;
+  int64_t num_free;
+  int32_t* shares;
+  PageCache cache;
+  int32_t *seq_lens, *taken;
+  int F, B, page, parts;  // parts: CTAs a fork
+  int* status;
+};
+
+__global__ void __launch_bounds__(kCopyThreads) kda_latent_fork_kernel(const ForkParams p) {
+  extern __shared__ uint32_t is_child[];  // a bit a row of the table
+  __shared__ int counts[2];               // free pages taken: by the forks before this one, by all
+  const int tid = threadIdx.x, mine = blockIdx.x / p.parts, part = blockIdx.x % p.parts;
+  asm volatile("griddepcontrol.wait;\n" ::: "memory");
+  for (int i = tid; i < (p.B + 31) / 32; i += kCopyThreads) is_child[i] = 0;
+  if (tid < 2) counts[tid] = 0;
+  __syncthreads();
+  int bad = 0, before = 0, all = 0;
+  for (int f = tid; f < p.F; f += kCopyThreads) {
+    const int from = p.parents[f], to = p.children[f];
+    if (from < 0 || from >= p.B || to < 0 || to >= p.B) {
+      bad = 1;
+      continue;
+    }
+    if (atomicOr(&is_child[to >> 5], 1u << (to & 31)) >> (to & 31) & 1) bad = 1;  // twice
+    const int held = p.cached[from], t = p.take ? p.take[f] : held;
+    if (held < 0 || t < 0 || t > held || held > p.max_pages * p.page) {
+      bad = 1;
+      continue;
+    }
+    const int need = t % p.page > 0;
+    all += need;
+    if (f < mine) before += need;
+  }
+  if (before) atomicAdd(&counts[0], before);
+  if (all) atomicAdd(&counts[1], all);
+  __syncthreads();
+  for (int f = tid; f < p.F; f += kCopyThreads) {  // a parent that is a child too
+    const int from = p.parents[f];
+    if (from >= 0 && from < p.B && (is_child[from >> 5] >> (from & 31) & 1)) bad = 1;
+  }
+  bad = __syncthreads_or(bad);
+  const bool refused = bad || counts[1] > p.num_free;
+  if (blockIdx.x == 0) {
+    if (tid == 0) {
+      if (refused) atomicExch(p.status, bad ? KDA_ERR_BAD_LENGTHS : KDA_ERR_NO_PAGES);
+      p.taken[0] = refused ? 0 : counts[1];
+    }
+    for (int b = tid; b < p.B; b += kCopyThreads)
+      if (refused || !(is_child[b >> 5] >> (b & 31) & 1)) p.seq_lens[b] = p.cached[b];
+    if (!refused)
+      for (int f = tid; f < p.F; f += kCopyThreads) p.seq_lens[p.children[f]] = p.take ? p.take[f] : p.cached[p.parents[f]];
+  }
+  if (refused || mine >= p.F) return;
+  const int from = p.parents[mine], to = p.children[mine];
+  const int t = p.take ? p.take[mine] : p.cached[from];
+  const int full = t / p.page, rest = t - full * p.page;
+  const int32_t* src = p.table + from * p.table_stride;
+  int32_t* dst = p.table + to * p.table_stride;
+  for (int j = part * kCopyThreads + tid; j < full; j += p.parts * kCopyThreads) {
+    const int id = src[j];
+    dst[j] = id;
+    if (id < 0 || id >= p.cache.num_pages) atomicExch(p.status, KDA_ERR_BAD_PAGE);
+    else atomicAdd(p.shares + id, 1);
+  }
+  if (rest == 0) return;
+  const int fresh = p.free_pages[counts[0]], old = src[full];
+  if (part == 0 && tid == 0) dst[full] = fresh;
+  copy_groups((rest + kGroupRows - 1) / kGroupRows, p.cache.token_stride, p.cache.token_stride, part, p.parts,
+              [&](int64_t g) {
+                CopyPlace c = page_group(p.cache, p.cache, old, fresh, (int)g, p.status);
+                c.rows = min(kGroupRows, rest - (int)g * kGroupRows);
+                return c;
+              });
+}
+
+// ---- release ----
+//
+// One cluster of eight CTAs: all counts go down (L2 atomics), the cluster's barrier,
+// then each CTA lists the pages of its eighth that fell below 0, its place in the
+// list from the others' numbers over distributed shared memory.  One launch and no
+// workspace.
+struct ReleaseParams {
+  const int32_t *rows, *keep, *cached, *table;
+  int64_t table_stride, max_pages;
+  int32_t* shares;
+  int64_t num_pages;
+  int32_t *seq_lens, *pages, *count;
+  int F, B, page;
+  int* status;
+};
+
+constexpr int kReleasePart = 128;  // table entries that a warp takes at a time
+
+__global__ void __launch_bounds__(kPageThreads) kda_latent_release_kernel(const ReleaseParams p) {
+  extern __shared__ uint32_t is_released[];  // a bit a row of the table
+  __shared__ int sums[kPageThreads / 32];
+  __shared__ int freed;
+  cg::cluster_group cluster = cg::this_cluster();
+  const int tid = threadIdx.x, lane = tid & 31, rank = (int)cluster.block_rank();
+  asm volatile("griddepcontrol.wait;\n" ::: "memory");
+  for (int i = tid; i < (p.B + 31) / 32; i += kPageThreads) is_released[i] = 0;
+  __syncthreads();
+  int bad = 0;
+  for (int f = tid; f < p.F; f += kPageThreads) {
+    const int b = p.rows[f];
+    if (b < 0 || b >= p.B) {
+      bad = 1;
+      continue;
+    }
+    if (atomicOr(&is_released[b >> 5], 1u << (b & 31)) >> (b & 31) & 1) bad = 1;  // twice
+    const int held = p.cached[b], keep = p.keep ? p.keep[f] : 0;
+    if (held < 0 || keep < 0 || keep > held || held > p.max_pages * p.page) bad = 1;
+  }
+  bad = __syncthreads_or(bad);
+  if (rank == 0) {
+    if (bad && tid == 0) atomicExch(p.status, KDA_ERR_BAD_LENGTHS);
+    for (int b = tid; b < p.B; b += kPageThreads)
+      if (bad || !(is_released[b >> 5] >> (b & 31) & 1)) p.seq_lens[b] = p.cached[b];
+    if (!bad)
+      for (int f = tid; f < p.F; f += kPageThreads) p.seq_lens[p.rows[f]] = p.keep ? p.keep[f] : 0;
+  }
+  if (!bad) {
+    const int64_t parts = (p.max_pages + kReleasePart - 1) / kReleasePart;
+    const int warps = kPageCluster * kPageThreads / 32;
+    for (int64_t i = rank * (kPageThreads / 32) + (tid >> 5); i < parts * p.F; i += warps) {
+      const int f = (int)(i / parts), j0 = (int)(i - f * parts) * kReleasePart;
+      const int b = p.rows[f], keep = p.keep ? p.keep[f] : 0;
+      const int held = pages_of(p.cached[b], p.page), stays = pages_of(keep, p.page);
+#pragma unroll
+      for (int k = 0; k < kReleasePart / 32; ++k) {
+        const int j = j0 + 32 * k + lane;
+        if (j < stays || j >= held) continue;
+        const int id = p.table[b * p.table_stride + j];
+        if (id < 0 || id >= p.num_pages) atomicExch(p.status, KDA_ERR_BAD_PAGE);
+        else atomicSub(p.shares + id, 1);
+      }
+    }
+  }
+  cluster.sync();
+  // this CTA's eighth of the pages, four a thread and round
+  const int64_t chunk = (p.num_pages + kPageCluster - 1) / kPageCluster;
+  const int64_t lo = min(p.num_pages, rank * chunk), hi = min(p.num_pages, lo + chunk);
+  int n = 0;
+  if (!bad)
+    for (int64_t i = lo + tid * 4; i < hi; i += 4 * kPageThreads)
+#pragma unroll
+      for (int k = 0; k < 4; ++k) n += i + k < hi && __ldcg(p.shares + i + k) < 0;
+  int total;
+  block_scan<kPageThreads>(n, sums, total);
+  if (tid == 0) freed = total;
+  cluster.sync();
+  int64_t at = 0, all = 0;
+  for (int r = 0; r < kPageCluster; ++r) {
+    const int x = *cluster.map_shared_rank(&freed, r);
+    if (r < rank) at += x;
+    all += x;
+  }
+  if (total > 0)
+    for (int64_t base = lo; base < hi; base += 4 * kPageThreads) {
+      const int64_t i = base + tid * 4;
+      int is[4], m = 0;
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        is[k] = i + k < hi && __ldcg(p.shares + i + k) < 0;
+        m += is[k];
+      }
+      int64_t to = at + block_scan<kPageThreads>(m, sums, total);
+      at += total;
+#pragma unroll
+      for (int k = 0; k < 4; ++k)
+        if (is[k]) {
+          p.pages[to++] = (int32_t)(i + k);
+          p.shares[i + k] = 0;
+        }
+    }
+  for (int64_t i = max(lo, all) + tid; i < hi; i += kPageThreads) p.pages[i] = -1;
+  if (rank == 0 && tid == 0) p.count[0] = (int32_t)all;
+  cluster.sync();  // the others may still read `freed`
+}
+
+// ---- compact ----
+//
+// U pages are held.  Those at U and behind move to the places below U that nobody
+// holds; there are as many of the one as of the other, and both go in ascending
+// order.  A cluster marks the held pages, counts and lists them (its barriers
+// between the steps), and a second kernel moves the rows and renames the tables'
+// entries: no page is both read and written.
+struct CompactParams {
+  const int32_t *cached, *table;
+  int32_t* table_out;
+  int64_t table_stride, table_out_stride, max_pages;
+  const int32_t* shares;
+  int32_t *shares_out, *page_map, *used;
+  PageCache cache;
+  uint8_t* held;               // [num_pages] whether a row of the table holds the page
+  int32_t *moves, *to, *from;  // their number (-1: refused), the places and the pages that move there
+  int B, page;
+  int* status;
+};
+
+__global__ void __launch_bounds__(kPageThreads) kda_latent_compact_kernel(const CompactParams p) {
+  __shared__ int sums[kPageThreads / 32];
+  __shared__ int count;
+  cg::cluster_group cluster = cg::this_cluster();
+  const int tid = threadIdx.x, lane = tid & 31, rank = (int)cluster.block_rank();
+  const int64_t pages = p.cache.num_pages;
+  const int64_t chunk = max((int64_t)4, ((pages + kPageCluster - 1) / kPageCluster + 3) / 4 * 4);
+  const int64_t lo = min(pages, rank * chunk), hi = min(pages, lo + chunk);
+  asm volatile("griddepcontrol.launch_dependents;\n" ::: "memory");
+  asm volatile("griddepcontrol.wait;\n" ::: "memory");
+  int bad = 0;
+  for (int b = tid; b < p.B; b += kPageThreads) {
+    const int len = p.cached[b];
+    bad |= len < 0 || len > p.max_pages * p.page;
+  }
+  bad = __syncthreads_or(bad);
+  if (bad) {  // (every CTA of the cluster finds the same)
+    for (int64_t i = lo + tid; i < hi; i += kPageThreads) {
+      p.page_map[i] = (int32_t)i;
+      p.shares_out[i] = p.shares[i];
+    }
+    if (rank == 0 && tid == 0) {
+      atomicExch(p.status, KDA_ERR_BAD_LENGTHS);
+      p.used[0] = (int32_t)pages;
+      p.moves[0] = -1;
+    }
+    return;
+  }
+  for (int64_t i = lo + tid * 4; i < hi; i += 4 * kPageThreads) *reinterpret_cast<uint32_t*>(p.held + i) = 0;
+  cluster.sync();
+  {
+    const int64_t parts = (p.max_pages + 127) / 128;
+    const int warps = kPageCluster * kPageThreads / 32;
+    for (int64_t i = rank * (kPageThreads / 32) + (tid >> 5); i < parts * p.B; i += warps) {
+      const int b = (int)(i / parts), j0 = (int)(i - b * parts) * 128;
+      const int held = pages_of(p.cached[b], p.page);
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        const int j = j0 + 32 * k + lane;
+        if (j >= held) continue;
+        const int id = p.table[b * p.table_stride + j];
+        if (id < 0 || id >= pages) atomicExch(p.status, KDA_ERR_BAD_PAGE);
+        else p.held[id] = 1;
+      }
+    }
+  }
+  cluster.sync();
+  auto four = [&](int64_t i) { return __ldcg(reinterpret_cast<const uint32_t*>(p.held + i)); };  // (the last one is padded)
+  int n = 0, total;
+  for (int64_t i = lo + tid * 4; i < hi; i += 4 * kPageThreads) n += __popc(four(i));
+  block_scan<kPageThreads>(n, sums, total);
+  if (tid == 0) count = total;
+  cluster.sync();
+  // U, and how many held pages lie before this CTA's and before place U
+  int64_t used = 0, before = 0, below = 0;
+  int counts[kPageCluster];
+#pragma unroll
+  for (int r = 0; r < kPageCluster; ++r) {
+    counts[r] = *cluster.map_shared_rank(&count, r);
+    if (r < rank) before += counts[r];
+    used += counts[r];
+  }
+  const int64_t owner = used / chunk;
+#pragma unroll
+  for (int r = 0; r < kPageCluster; ++r)
+    if (r < owner) below += counts[r];
+  n = 0;
+  for (int64_t i = owner * chunk + tid * 4; i < used; i += 4 * kPageThreads) {
+    const uint32_t x = four(i);
+#pragma unroll
+    for (int k = 0; k < 4; ++k) n += i + k < used && (x >> (8 * k) & 1);
+  }
+  block_scan<kPageThreads>(n, sums, total);
+  below += total;
+  // places and movers, in order; a mover's number waits in the map for the places of the other CTAs
+  int64_t at = before;
+  for (int64_t base = lo; base < hi; base += 4 * kPageThreads) {
+    const int64_t i = base + tid * 4;
+    const uint32_t x = i < hi ? four(i) : 0;
+    int64_t held = at + block_scan<kPageThreads>(__popc(x), sums, total);
+    at += total;
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      const int64_t page = i + k;
+      if (page >= hi) continue;
+      const bool is = x >> (8 * k) & 1;
+      if (!is && page < used) p.to[page - held] = (int32_t)page;
+      if (is && page >= used) p.from[held - below] = (int32_t)page;
+      p.page_map[page] = !is ? -1 : (int32_t)(page < used ? page : held - below);
+      held += is;
+    }
+  }
+  if (rank == 0 && tid == 0) {
+    p.used[0] = (int32_t)used;
+    p.moves[0] = (int32_t)(used - below);
+  }
+  cluster.sync();
+  // (shares_out may be shares: a mover's count is taken before it is cleared)
+  for (int64_t i = lo + tid; i < hi; i += kPageThreads)
+    if (i < used && __ldcg(p.page_map + i) >= 0) p.shares_out[i] = p.shares[i];
+  for (int64_t k = rank * kPageThreads + tid; k < used - below; k += kPageCluster * kPageThreads) {
+    const int to = __ldcg(p.to + k), from = __ldcg(p.from + k);
+    p.shares_out[to] = p.shares[from];
+    p.page_map[from] = to;
+  }
+  cluster.sync();
+  for (int64_t i = max(lo, used) + tid; i < hi; i += kPageThreads) p.shares_out[i] = 0;
+}
+
+__global__ void __launch_bounds__(kCopyThreads) kda_latent_move_kernel(const CompactParams p) {
+  asm volatile("griddepcontrol.wait;\n" ::: "memory");
+  const int64_t moves = p.moves[0];
+  const int per = p.page / kGroupRows;
+  const int64_t entries = p.B * p.max_pages;
+  // the tables first: they are small, and their entries are renamed while the first rows are on their way
+  for (int64_t e = (int64_t)blockIdx.x * kCopyThreads + threadIdx.x; e < entries; e += (int64_t)gridDim.x * kCopyThreads) {
+    const int b = (int)div_pages(e, (int)p.max_pages), j = (int)(e - b * p.max_pages);
+    int id = p.table[b * p.table_stride + j];
+    if (moves >= 0 && j < pages_of(p.cached[b], p.page) && id >= 0 && id < p.cache.num_pages)
+      id = p.page_map[id];
+    p.table_out[b * p.table_out_stride + j] = id;
+  }
+  copy_groups(max((int64_t)0, moves) * per, p.cache.token_stride, p.cache.token_stride, blockIdx.x, gridDim.x,
+              [&](int64_t g) {
+                const int64_t i = div_pages(g, per);
+                return page_group(p.cache, p.cache, p.from[i], p.to[i], (int)(g - i * per), p.status);
+              });
+}
+
+namespace {
+
+bool al4(const void* p) { return ((uintptr_t)p & 3) == 0; }
+
+PageCache page_cache(const kda_latent_cache& c) {
+  return {static_cast<uint16_t*>(c.data), c.num_pages, c.page_stride, c.token_stride};
+}
+
+// Table sizes that all calls check alike.
+int check_table(int64_t rows, int64_t max_pages, int64_t stride, const void* table) {
+  if (rows < 0 || rows > kMaxPlanRequests || max_pages < 0 || max_pages > INT32_MAX || stride < max_pages)
+    return KDA_ERR_SHAPE;
+  if (rows > 0 && max_pages > 0 && !table) return KDA_ERR_NULL_ARG;
+  return al4(table) ? KDA_OK : KDA_ERR_ALIGNMENT;
+}
+
+unsigned copy_ctas(int64_t groups) { return (unsigned)std::min<int64_t>(std::max<int64_t>(1, (groups + 3) / 4), 152 * 6); }
+
+constexpr size_t kCompactHead = 256;
+size_t compact_held_bytes(int64_t pages) { return ((size_t)pages + 255) / 256 * 256; }
+size_t compact_list_bytes(int64_t pages) { return ((size_t)pages / 2 * 4 + 255) / 256 * 256 + 256; }
+
+int check_compact(const kda_latent_compact_args* a) {
+  if (!a) return KDA_ERR_NULL_ARG;
+  int rc = check_table(a->B, a->max_pages, a->table_stride, a->block_table);
+  if (rc != KDA_OK) return rc;
+  rc = check_table(a->B, a->max_pages, a->table_out_stride, a->block_table_out);
+  if (rc != KDA_OK) return rc;
+  rc = latent_check_cache(&a->cache);
+  if (rc != KDA_OK) return rc;
+  if (!a->pages_used || (a->B > 0 && !a->cached_lens) ||
+      (a->cache.num_pages > 0 && (!a->shares || !a->shares_out || !a->page_map)))
+    return KDA_ERR_NULL_ARG;
+  if (!al4(a->cached_lens) || !al4(a->shares) || !al4(a->shares_out) || !al4(a->page_map) || !al4(a->pages_used))
+    return KDA_ERR_ALIGNMENT;
+  return KDA_OK;
+}
+
+}  // namespace
+
+}  // namespace kda
+
+using namespace kda;
+
+extern "C" int kda_latent_copy(const kda_latent_copy_args* a, void* stream) {
+  if (!a) return KDA_ERR_NULL_ARG;
+  if (a->n < 0 || a->n > INT32_MAX) return KDA_ERR_SHAPE;
+  int rc = latent_check_cache(&a->src);
+  if (rc == KDA_OK) rc = latent_check_cache(&a->dst);
+  if (rc != KDA_OK) return rc;
+  if (a->src.page_size != a->dst.page_size) return KDA_ERR_PAGE_SIZE;
+  if (a->n > 0 && (!a->src_pages || !a->dst_pages)) return KDA_ERR_NULL_ARG;
+  if (!al4(a->src_pages) || !al4(a->dst_pages)) return KDA_ERR_ALIGNMENT;
+  if (a->n == 0) return KDA_OK;
+  cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+  int* status = status_slot(s);
+  if (!status) return KDA_ERR_LAUNCH;
+  const CopyParams p{page_cache(a->src), page_cache(a->dst), a->src_pages, a->dst_pages, a->n, (int)a->src.page_size, status};
+  const unsigned ctas = copy_ctas(a->n * (a->src.page_size / kGroupRows));
+  return launch_overlapped(kda_latent_copy_kernel, dim3(ctas), kCopyThreads, 0, s, 1, p) ? KDA_OK : KDA_ERR_LAUNCH;
+}
+
+extern "C" int kda_latent_fork(const kda_latent_fork_args* a, void* stream) {
+  if (!a) return KDA_ERR_NULL_ARG;
+  int rc = check_table(a->B, a->max_pages, a->table_stride, a->block_table);
+  if (rc != KDA_OK) return rc;
+  if (a->F < 0 || a->F > kMaxPlanRequests || a->num_free < 0 || a->num_free > INT32_MAX) return KDA_ERR_SHAPE;
+  rc = latent_check_cache(&a->cache);
+  if (rc != KDA_OK) return rc;
+  if (!a->pages_taken || (a->B > 0 && (!a->cached_lens || !a->seq_lens)) || (a->F > 0 && (!a->parents || !a->children)) ||
+      (a->num_free > 0 && !a->free_pages) || (a->cache.num_pages > 0 && !a->shares))
+    return KDA_ERR_NULL_ARG;
+  if (!al4(a->parents) || !al4(a->children) || !al4(a->fork_lens) || !al4(a->cached_lens) || !al4(a->free_pages) ||
+      !al4(a->shares) || !al4(a->seq_lens) || !al4(a->pages_taken))
+    return KDA_ERR_ALIGNMENT;
+  cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+  int* status = status_slot(s);
+  if (!status) return KDA_ERR_LAUNCH;
+  ForkParams p{a->parents, a->children, a->fork_lens, a->cached_lens, a->block_table, a->table_stride, a->max_pages,
+               a->free_pages, a->num_free, a->shares, page_cache(a->cache), a->seq_lens, a->pages_taken, (int)a->F,
+               (int)a->B, (int)a->cache.page_size, 1, status};
+  // CTAs a fork: one for 32 rows of its last page, as long as all are on the GPU at once
+  const int64_t forks = std::max<int64_t>(1, a->F);
+  p.parts = (int)std::max<int64_t>(1, std::min<int64_t>(152 * 4 / forks, (a->cache.page_size + 31) / 32));
+  return launch_overlapped(kda_latent_fork_kernel, dim3((unsigned)(forks * p.parts)), kCopyThreads,
+                           (size_t)(a->B + 31) / 32 * 4, s, 1, p)
+             ? KDA_OK
+             : KDA_ERR_LAUNCH;
+}
+
+extern "C" int kda_latent_release(const kda_latent_release_args* a, void* stream) {
+  if (!a) return KDA_ERR_NULL_ARG;
+  const int rc = check_table(a->B, a->max_pages, a->table_stride, a->block_table);
+  if (rc != KDA_OK) return rc;
+  if (a->F < 0 || a->F > kMaxPlanRequests || a->num_pages < 0 || a->num_pages > INT32_MAX) return KDA_ERR_SHAPE;
+  if (a->page_size <= 0 || a->page_size % 8 || a->page_size > (1 << 24)) return KDA_ERR_PAGE_SIZE;
+  if (!a->count || (a->B > 0 && (!a->cached_lens || !a->seq_lens)) || (a->F > 0 && !a->rows) ||
+      (a->num_pages > 0 && (!a->shares || !a->pages)))
+    return KDA_ERR_NULL_ARG;
+  if (!al4(a->rows) || !al4(a->keep_lens) || !al4(a->cached_lens) || !al4(a->shares) || !al4(a->seq_lens) ||
+      !al4(a->pages) || !al4(a->count))
+    return KDA_ERR_ALIGNMENT;
+  cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+  int* status = status_slot(s);
+  if (!status) return KDA_ERR_LAUNCH;
+  const ReleaseParams p{a->rows, a->keep_lens, a->cached_lens, a->block_table, a->table_stride, a->max_pages, a->shares,
+                        a->num_pages, a->seq_lens, a->pages, a->count, (int)a->F, (int)a->B, (int)a->page_size, status};
+  return launch_overlapped(kda_latent_release_kernel, dim3(kPageCluster), kPageThreads, (size_t)(a->B + 31) / 32 * 4, s,
+                           kPageCluster, p)
+             ? KDA_OK
+             : KDA_ERR_LAUNCH;
+}
+
+extern "C" size_t kda_latent_compact_workspace_bytes(const kda_latent_compact_args* a) {
+  if (check_compact(a) != KDA_OK) return 0;
+  return kCompactHead + compact_held_bytes(a->cache.num_pages) + 2 * compact_list_bytes(a->cache.num_pages);
+}
+
+extern "C" int kda_latent_compact(const kda_latent_compact_args* a, void* workspace, size_t workspace_bytes, void* stream) {
+  const int rc = check_compact(a);
+  if (rc != KDA_OK) return rc;
+  if (!workspace || ((uintptr_t)workspace & 255) || workspace_bytes < kda_latent_compact_workspace_bytes(a))
+    return KDA_ERR_WORKSPACE;
+  cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+  int* status = status_slot(s);
+  if (!status) return KDA_ERR_LAUNCH;
+  unsigned char* ws = static_cast<unsigned char*>(workspace);
+  CompactParams p{a->cached_lens, a->block_table, a->block_table_out, a->table_stride, a->table_out_stride, a->max_pages,
+                  a->shares, a->shares_out, a->page_map, a->pages_used, page_cache(a->cache), ws + kCompactHead,
+                  reinterpret_cast<int32_t*>(ws), nullptr, nullptr, (int)a->B, (int)a->cache.page_size, status};
+  unsigned char* lists = ws + kCompactHead + compact_held_bytes(a->cache.num_pages);
+  p.to = reinterpret_cast<int32_t*>(lists);
+  p.from = reinterpret_cast<int32_t*>(lists + compact_list_bytes(a->cache.num_pages));
+  if (!launch_overlapped(kda_latent_compact_kernel, dim3(kPageCluster), kPageThreads, 0, s, kPageCluster, p))
+    return KDA_ERR_LAUNCH;
+  // as many CTAs as half of the pages could need, the most that can move
+  const int64_t groups = a->cache.num_pages / 2 * (a->cache.page_size / kGroupRows);
+  const int64_t entries = (a->B * a->max_pages + kCopyThreads - 1) / kCopyThreads;
+  const unsigned ctas = std::max(copy_ctas(groups), (unsigned)std::min<int64_t>(entries, 152));
+  return launch_overlapped(kda_latent_move_kernel, dim3(ctas), kCopyThreads, 0, s, 1, p) ? KDA_OK : KDA_ERR_LAUNCH;
+}

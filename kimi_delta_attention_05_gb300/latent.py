@@ -92,6 +92,12 @@ def _library():
             size = getattr(lib, f"kda_latent_{name}_workspace_bytes")
             size.restype = ctypes.c_size_t
             size.argtypes = [_P]
+        for name in ("fork", "release", "copy", "compact"):
+            fn = getattr(lib, f"kda_latent_{name}")
+            fn.restype = ctypes.c_int
+            fn.argtypes = [_P, _P, ctypes.c_size_t, _P] if name == "compact" else [_P, _P]
+        lib.kda_latent_compact_workspace_bytes.restype = ctypes.c_size_t
+        lib.kda_latent_compact_workspace_bytes.argtypes = [_P]
         _fns = lib
     return _fns
 

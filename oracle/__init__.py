@@ -22,8 +22,9 @@ hand through the chunk algebra (``chunk_backward.py``), pinned to the autograd
 oracle and exposing per-chunk gradient intermediates.
 
 :mod:`oracle.latent` states the latent-attention calls (plan, cache append,
-absorbed and expanded attention) in fp64 numpy; ``tests/test_latent_oracle.py``
-pins it.
+absorbed and expanded attention) in fp64 numpy, and those on shared pages (fork,
+release, compact) on lists; ``tests/test_latent_oracle.py`` and
+``tests/test_latent_pages_oracle.py`` pin it.
 
 Parity status: every function is pinned (see ``tests/test_oracle_pins.py``,
 ``tests/test_oracle_mutations.py`` and ``tests/test_backward_oracle.py``).

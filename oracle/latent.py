@@ -77,3 +77,48 @@ def expanded(q, k, k_pe, v, scale, causal, cu_q=None, cu_k=None):
                 o, z, sp, re = _attend(q[b, i:i + 1, h], keys[:seen], v[b, k0:k0 + seen, h], scale)
                 out[b, i, h], lse[b, i, h], spread[b, i, h], reach[b, i, h] = o[0], z[0], sp[0], re[0]
     return out, lse, spread, reach
+
+
+# ---- pages that several requests hold: lists in, lists out, nothing changed in place ----
+
+def fork(parents, children, take, cached, table, free, shares, page):
+    """Also returns the copies as (page, from page, rows)."""
+    rows, counts, lens, copies = [list(r) for r in table], list(shares), list(cached), []
+    for f, (parent, child) in enumerate(zip(parents, children)):
+        tokens = cached[parent] if take is None else take[f]
+        for at in range(tokens // page):
+            rows[child][at] = table[parent][at]
+            counts[table[parent][at]] += 1
+        if tokens % page:
+            rows[child][tokens // page] = free[len(copies)]
+            copies.append((free[len(copies)], table[parent][tokens // page], tokens % page))
+        lens[child] = tokens
+    return dict(table=rows, shares=counts, seq_lens=lens, pages_taken=[len(copies)], copies=copies)
+
+
+def release(which, keep, cached, table, shares, page):
+    counts, lens = list(shares), list(cached)
+    for f, b in enumerate(which):
+        kept = 0 if keep is None else keep[f]
+        for at in range(-(-kept // page), -(-cached[b] // page)):
+            counts[table[b][at]] -= 1
+        lens[b] = kept
+    free = [p for p, c in enumerate(counts) if c < 0]
+    return dict(shares=[max(0, c) for c in counts], seq_lens=lens, pages=free + [-1] * (len(counts) - len(free)),
+                count=[len(free)])
+
+
+def compact(cached, table, shares, page):
+    """Also returns the moves as (to page, from page)."""
+    held = sorted({table[b][at] for b, n in enumerate(cached) for at in range(-(-n // page))})
+    used = len(held)
+    places = [p for p in range(used) if p not in set(held)]
+    moves = list(zip(places, [p for p in held if p >= used]))
+    new = {p: p for p in held}
+    new.update({was: to for to, was in moves})
+    counts = [0] * len(shares)
+    for was, to in new.items():
+        counts[to] = shares[was]
+    rows = [[new[p] if at < -(-cached[b] // page) else p for at, p in enumerate(r)] for b, r in enumerate(table)]
+    return dict(table=rows, shares=counts, page_map=[new.get(p, -1) for p in range(len(shares))], pages_used=[used],
+                moves=moves)
