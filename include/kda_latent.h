@@ -19,6 +19,10 @@
  * query is [W_uk,h^T q_nope | q_pe] and the head's output W_uv,h o.  Those
  * products are plain matrix products and stay with the caller.
  *
+ * Beside them: kda_latent_decode_shared, the absorbed form for requests that share
+ * long prefixes, and calls for the pages that several requests hold
+ * (kda_latent_fork, _release, _compact, _copy).
+ *
  * Arithmetic of the two attention forms: scores, maxima, sums, accumulators and
  * the parts of a split call are fp32.  The softmax weights are rounded to bf16
  * for the product with the values, the operands' type of the tensor cores, after
@@ -160,6 +164,39 @@ int kda_latent_decode(const kda_latent_decode_args *args, void *workspace, size_
                       void *stream);
 
 /*
+ * Absorbed attention of a batch whose requests share long prefixes: the result of
+ * kda_latent_decode on the same arguments, with each shared prefix read once for
+ * all requests of its group instead of once a request.
+ *
+ *  decode      : the arguments of kda_latent_decode; requests of a group are
+ *                neighbours, and each request's row of the table names its whole
+ *                context, prefix first (as kda_latent_fork leaves it)
+ *  cu_groups   : int64 [G + 1]: group g has the requests [cu_groups[g], cu_groups[g + 1])
+ *  prefix_lens : int32 [G]: the first prefix_lens[g] tokens hold the same values for
+ *                all requests of the group.  Where only whole pages are the same
+ *                pages, the rows behind them may be copies
+ * Which request's row names the pages that are read for a shared prefix is not
+ * said.  A request that does not see the whole prefix (a shorter or an empty one)
+ * is taken on its own, as are the requests of groups of one.  A prefix_lens below 0
+ * or beyond the table is taken as the nearer bound and sets KDA_ERR_BAD_LENGTHS;
+ * offsets that do not go from 0 to B without decreasing set KDA_ERR_BAD_SEQLENS, and
+ * every request is taken on its own.  B * R * H is below 2^31 - 128.
+ * Prefix and remaining tokens are joined by their fp32 parts, so outputs have the
+ * error of kda_latent_decode's; they are not bit for bit the same.
+ */
+typedef struct kda_latent_decode_shared_args {
+  kda_latent_decode_args decode;
+  const int64_t *cu_groups;
+  const int32_t *prefix_lens;
+  int64_t G;
+} kda_latent_decode_shared_args;
+
+/* As kda_latent_decode_workspace_bytes. */
+size_t kda_latent_decode_shared_workspace_bytes(const kda_latent_decode_shared_args *args);
+int kda_latent_decode_shared(const kda_latent_decode_shared_args *args, void *workspace, size_t workspace_bytes,
+                             void *stream);
+
+/*
  * Expanded attention of prompts.  Sequence n has queries i < Lq and keys
  * j < Lk (Lk may exceed Lq: context that is already there); query i sees every
  * key, or with KDA_LATENT_CAUSAL those with j <= i + Lk - Lq.  A query that
@@ -249,6 +286,9 @@ int kda_latent_fork(const kda_latent_fork_args *args, void *stream);
  * Requests that give pages back: rows[f] keeps its first keep_lens[f] tokens (none
  * where keep_lens is NULL) and drops the pages behind them.  The count of a dropped
  * page goes down by one; pages whose last holder dropped them are listed.
+ * A row that keeps part of a page which others hold must not grow from there: its
+ * next tokens would be written into their page.  kda_latent_fork with fork_lens goes
+ * on from any place, as it copies that part; the row itself is then released.
  *
  *  rows, keep_lens : int32 [F]; no row twice
  *  block_table : int32 [B, max_pages], left as it is (a request's length says

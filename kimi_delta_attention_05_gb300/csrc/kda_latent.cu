@@ -269,6 +269,17 @@ int check_decode(const kda_latent_decode_args* a) {
   return KDA_OK;
 }
 
+int check_shared(const kda_latent_decode_shared_args* a) {
+  if (!a) return KDA_ERR_NULL_ARG;
+  const int rc = check_decode(&a->decode);
+  if (rc != KDA_OK) return rc;
+  if (a->G < 0 || a->G > (1 << 20) || a->decode.B * a->decode.R * a->decode.H > INT32_MAX - 128) return KDA_ERR_SHAPE;
+  if (a->G == 0 && a->decode.B > 0) return KDA_ERR_BAD_SEQLENS;  // offsets that cannot end at B
+  if (!a->cu_groups || (a->G > 0 && !a->prefix_lens)) return KDA_ERR_NULL_ARG;
+  if (!al(a->cu_groups, 8) || !al(a->prefix_lens, 4)) return KDA_ERR_ALIGNMENT;
+  return KDA_OK;
+}
+
 DecodeParams decode_params(const kda_latent_decode_args* a) {
   DecodeParams p;
   p.q = static_cast<const uint16_t*>(a->q);
@@ -563,6 +574,18 @@ extern "C" int kda_latent_decode(const kda_latent_decode_args* a, void* workspac
   p.status = status_slot(s);
   if (!p.status || !launch_latent_decode(p, s)) return KDA_ERR_LAUNCH;
   return cudaGetLastError() == cudaSuccess ? KDA_OK : KDA_ERR_LAUNCH;
+}
+
+extern "C" size_t kda_latent_decode_shared_workspace_bytes(const kda_latent_decode_shared_args* a) {
+  if (check_shared(a) != KDA_OK || a->decode.B * a->decode.R * a->decode.H == 0) return 0;
+  return decode_workspace_bytes(decode_params(&a->decode));
+}
+
+extern "C" int kda_latent_decode_shared(const kda_latent_decode_shared_args* a, void* workspace, size_t workspace_bytes,
+                                        void* stream) {
+  const int rc = check_shared(a);
+  if (rc != KDA_OK) return rc;
+  return kda_latent_decode(&a->decode, workspace, workspace_bytes, stream);
 }
 
 extern "C" size_t kda_latent_prefill_workspace_bytes(const kda_latent_prefill_args* a) {

@@ -50,6 +50,10 @@ class kda_latent_decode_args(ctypes.Structure):
                 ("B", _I), ("R", _I), ("H", _I)]
 
 
+class kda_latent_decode_shared_args(ctypes.Structure):
+    _fields_ = [("decode", kda_latent_decode_args), ("cu_groups", _P), ("prefix_lens", _P), ("G", _I)]
+
+
 class kda_latent_prefill_args(ctypes.Structure):
     _fields_ = [("q", _P), ("k", _P), ("k_pe", _P), ("v", _P),
                 ("q_stride_t", _I), ("q_stride_h", _I), ("k_stride_t", _I), ("k_stride_h", _I),
@@ -74,6 +78,7 @@ def _packer(block):
 
 _plan_block, _append_block = _packer(kda_latent_plan_args), _packer(kda_latent_append_args)
 _decode_block, _prefill_block = _packer(kda_latent_decode_args), _packer(kda_latent_prefill_args)
+_shared_block = _packer(kda_latent_decode_shared_args)
 
 _fns = None
 
@@ -82,7 +87,7 @@ def _library():
     global _fns
     if _fns is None:
         lib = load_library()
-        for name in ("plan", "append", "decode", "prefill"):
+        for name in ("plan", "append", "decode", "prefill", "decode_shared"):
             fn = getattr(lib, f"kda_latent_{name}")
             fn.restype = ctypes.c_int
             if name in ("plan", "append"):  # the block (its bytes or a reference), the stream
@@ -256,15 +261,8 @@ def latent_append(c, k_pe, slot_map, cache, norm_weight=None, eps=1e-6, *, strea
     return cache
 
 
-def latent_decode(q, cache, block_table, seq_lens, scale, out=None, lse=None, *, workspace=None, stream=None):
-    """Absorbed attention of every request's newest tokens over the paged cache;
-    returns ``out``.
-
-    q bf16 [B, R, H, 576] (R new tokens a request, whose rows the cache already
-    holds), cache bf16 [pages, page_size, 576], block_table int32 [B, max_pages],
-    seq_lens int32 [B]; out bf16 [B, R, H, 512] (allocated here if None), lse an
-    optional fp32 [B, R, H] tensor to be written.  ``workspace``: an optional
-    uint8 tensor of at least :func:`latent_decode_workspace_bytes` bytes."""
+def _decode_fields(q, cache, block_table, seq_lens, scale, out, lse, stream):
+    """Device, out and the fields of the argument block of an absorbed call."""
     dev = _gpu(q, "q", stream)
     _on(q, _bf16, 4, dev, "q")
     B, R, H, D = q.shape
@@ -291,8 +289,21 @@ def latent_decode(q, cache, block_table, seq_lens, scale, out=None, lse=None, *,
         _dense(lse, "lse")
         if lse.shape != (B, R, H):
             raise ValueError("lse [B, R, H] is needed")
-    a = _decode_block(q.data_ptr(), *_cache_block(cache, dev), block_table.data_ptr(), strides[0] if B > 1 else width,
-                      width, seq_lens.data_ptr(), _F(scale).value, out.data_ptr(), 0 if lse is None else lse.data_ptr(), B, R, H)
+    return dev, out, (q.data_ptr(), *_cache_block(cache, dev), block_table.data_ptr(), strides[0] if B > 1 else width, width,
+                      seq_lens.data_ptr(), _F(scale).value, out.data_ptr(), 0 if lse is None else lse.data_ptr(), B, R, H)
+
+
+def latent_decode(q, cache, block_table, seq_lens, scale, out=None, lse=None, *, workspace=None, stream=None):
+    """Absorbed attention of every request's newest tokens over the paged cache;
+    returns ``out``.
+
+    q bf16 [B, R, H, 576] (R new tokens a request, whose rows the cache already
+    holds), cache bf16 [pages, page_size, 576], block_table int32 [B, max_pages],
+    seq_lens int32 [B]; out bf16 [B, R, H, 512] (allocated here if None), lse an
+    optional fp32 [B, R, H] tensor to be written.  ``workspace``: an optional
+    uint8 tensor of at least :func:`latent_decode_workspace_bytes` bytes."""
+    dev, out, fields = _decode_fields(q, cache, block_table, seq_lens, scale, out, lse, stream)
+    a = _decode_block(*fields)
     lib = _library()
     if workspace is None:
         need = lib.kda_latent_decode_workspace_bytes(a)
@@ -308,6 +319,44 @@ def latent_decode_workspace_bytes(B, R, H, cache, block_table):
     width = block_table.shape[1]
     return int(_library().kda_latent_decode_workspace_bytes(
         _decode_block(16, *_cache_block(cache, cache.device), 16, width, width, 16, 1.0, 16, 0, B, R, H)))
+
+
+def latent_decode_shared(q, cache, block_table, seq_lens, cu_groups, prefix_lens, scale, out=None, lse=None, *,
+                         workspace=None, stream=None):
+    """:func:`latent_decode` for a batch whose requests share long prefixes, each read
+    once for all requests of its group; returns ``out``.
+
+    Arguments as there, and cu_groups int64 [G + 1] (group g: the requests
+    ``cu_groups[g] .. cu_groups[g + 1] - 1``), prefix_lens int32 [G]: the tokens at the
+    start of a group's requests whose cached rows are the same.  Every row of
+    block_table names the request's whole context, as :func:`latent_fork` leaves it.
+    Offsets or prefixes that do not fit show in :func:`get_status` (14 / 18).
+    ``workspace``: an optional uint8 tensor of at least
+    :func:`latent_decode_shared_workspace_bytes` bytes."""
+    dev, out, fields = _decode_fields(q, cache, block_table, seq_lens, scale, out, lse, stream)
+    _on(cu_groups, _i64, 1, dev, "cu_groups")
+    _on(prefix_lens, _i32, 1, dev, "prefix_lens")
+    _dense(cu_groups, "cu_groups")
+    _dense(prefix_lens, "prefix_lens")
+    G = prefix_lens.shape[0]
+    if cu_groups.shape[0] != G + 1:
+        raise ValueError("cu_groups [G + 1] and prefix_lens [G] are needed")
+    a = _shared_block(*fields, cu_groups.data_ptr(), prefix_lens.data_ptr(), G)
+    lib = _library()
+    if workspace is None:
+        need = lib.kda_latent_decode_shared_workspace_bytes(a)
+        workspace = _new(need, torch.uint8, dev, stream) if need else None
+    rc = lib.kda_latent_decode_shared(a, *_scratch(workspace, dev), _handle(dev, stream))
+    if rc != 0:
+        _raise("kda_latent_decode_shared", rc)
+    return out
+
+
+def latent_decode_shared_workspace_bytes(B, R, H, groups, cache, block_table):
+    """Workspace bytes of :func:`latent_decode_shared` for these sizes on the current device."""
+    width = block_table.shape[1]
+    return int(_library().kda_latent_decode_shared_workspace_bytes(
+        _shared_block(16, *_cache_block(cache, cache.device), 16, width, width, 16, 1.0, 16, 0, B, R, H, 16, 16, groups)))
 
 
 def _token_stride(shape, strides, row, name):

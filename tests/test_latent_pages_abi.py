@@ -112,3 +112,43 @@ def test_tensors_of_another_place_are_refused(name, monkeypatch):
         CALLS[name](at(1))
     with pytest.raises(ValueError, match="stream.*cuda:0.*cuda:1"):
         CALLS[name](at(0), SimpleNamespace(device=torch.device("cuda", 1)))
+
+
+def _shared_args(over):
+    d = M.kda_latent_decode_args(FAKE, _cache(), FAKE, 4, 4, FAKE, 0.07, FAKE, None, 2, 1, 32)
+    a = M.kda_latent_decode_shared_args(d, FAKE, FAKE, 1)
+    for k, v in over.items():
+        setattr(a.decode if hasattr(d, k) else a, k, v)
+    return a
+
+
+@pytest.mark.parametrize("over,code", [
+    (dict(q=None), 1), (dict(out=None), 1), (dict(seq_lens=None), 1), (dict(block_table=None), 1), (dict(cu_groups=None), 1),
+    (dict(prefix_lens=None), 1), (dict(B=-1), 3), (dict(G=-1), 3), (dict(G=(1 << 20) + 1), 3), (dict(G=0), 14),
+    (dict(B=1 << 20, H=4096), 3), (dict(table_stride=3), 3), (dict(scale=0.0), 16), (dict(cu_groups=FAKE + 4), 9),
+    (dict(prefix_lens=FAKE + 2), 9), (dict(q=FAKE + 8), 9), (dict(cache=_cache(page_size=100)), 17),
+    (dict(cache=_cache(token_stride=570)), 15),
+])
+def test_decode_shared_refusals(over, code):
+    a = _shared_args(over)
+    assert _call("decode_shared", a, (FAKE, 1 << 50)) == code
+    assert M._library().kda_latent_decode_shared_workspace_bytes(ctypes.byref(a)) == 0
+
+
+def test_decode_shared_workspace_is_checked():
+    a = _shared_args(dict(max_pages=400, table_stride=400))
+    need = M._library().kda_latent_decode_shared_workspace_bytes(ctypes.byref(a))
+    assert need > 0
+    for ws in ((None, need), (FAKE, need - 1), (FAKE + 16, need)):
+        assert _call("decode_shared", a, ws) == 10
+
+
+def test_decode_shared_of_nothing_is_nothing():
+    d = M.kda_latent_decode_args(None, _cache(), None, 0, 0, None, 0.07, None, None, 0, 1, 32)
+    assert _call("decode_shared", M.kda_latent_decode_shared_args(d, FAKE, None, 0), (None, 0)) == 0
+
+
+def test_decode_shared_refuses_tensors_of_another_place():
+    with pytest.raises(ValueError, match="CUDA"):
+        t = torch.zeros(1, dtype=torch.int32)
+        M.latent_decode_shared(torch.zeros(1, 1, 1, 576), t, t, t, t, t, 1.0)
