@@ -177,7 +177,8 @@ int kda_latent_decode(const kda_latent_decode_args *args, void *workspace, size_
  *                pages, the rows behind them may be copies
  * Which request's row names the pages that are read for a shared prefix is not
  * said.  A request that does not see the whole prefix (a shorter or an empty one)
- * is taken on its own, as are the requests of groups of one.  A prefix_lens below 0
+ * is taken on its own, as are the requests of groups of one.  The prefix_lens of a group
+ * without requests is not looked at; another below 0
  * or beyond the table is taken as the nearer bound and sets KDA_ERR_BAD_LENGTHS;
  * offsets that do not go from 0 to B without decreasing set KDA_ERR_BAD_SEQLENS, and
  * every request is taken on its own.  B * R * H is below 2^31 - 128.

@@ -578,14 +578,21 @@ extern "C" int kda_latent_decode(const kda_latent_decode_args* a, void* workspac
 
 extern "C" size_t kda_latent_decode_shared_workspace_bytes(const kda_latent_decode_shared_args* a) {
   if (check_shared(a) != KDA_OK || a->decode.B * a->decode.R * a->decode.H == 0) return 0;
-  return decode_workspace_bytes(decode_params(&a->decode));
+  return shared_workspace_bytes(decode_params(&a->decode), a->G);
 }
 
 extern "C" int kda_latent_decode_shared(const kda_latent_decode_shared_args* a, void* workspace, size_t workspace_bytes,
                                         void* stream) {
   const int rc = check_shared(a);
   if (rc != KDA_OK) return rc;
-  return kda_latent_decode(&a->decode, workspace, workspace_bytes, stream);
+  if (a->decode.B * a->decode.R * a->decode.H == 0) return KDA_OK;
+  DecodeParams p = decode_params(&a->decode);
+  if (!workspace || !al(workspace, 256) || workspace_bytes < shared_workspace_bytes(p, a->G)) return KDA_ERR_WORKSPACE;
+  cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+  p.ws = static_cast<unsigned char*>(workspace);
+  p.status = status_slot(s);
+  if (!p.status || !launch_latent_shared(p, a->cu_groups, a->prefix_lens, a->G, s)) return KDA_ERR_LAUNCH;
+  return cudaGetLastError() == cudaSuccess ? KDA_OK : KDA_ERR_LAUNCH;
 }
 
 extern "C" size_t kda_latent_prefill_workspace_bytes(const kda_latent_prefill_args* a) {

@@ -110,6 +110,60 @@ bool launch_overlapped(void (*kernel)(P...), dim3 grid, unsigned threads, size_t
 // The checks of a cache's address, sizes and strides.
 int latent_check_cache(const kda_latent_cache* c);
 
+// ---- decoding behind shared prefixes ----
+constexpr int kPfxTile = 128;      // cached rows of a tile of the shared pass
+constexpr int kPfxRows = 128;      // query rows of an item, a CTA pair's
+// A share's cost: 4 a tile, and an item's set-up and output.
+constexpr int kPfxTileCost = 4, kPfxItemCost = 6;
+
+struct SharedHead {
+  int64_t total, size;             // cost of all items, and of a share
+  int32_t active, pad;             // groups that share tiles
+};
+// A group of which at least two requests see at least one tile of the prefix.
+struct SharedGroup {
+  int tiles, source;               // shared tiles; the request whose row of the table names them
+  int row0, rows;                  // first query row (request * R * H + ...), and how many
+};
+static_assert(sizeof(SharedGroup) == 16, "read at once");
+
+struct SharedParams {
+  DecodeParams d;
+  const int64_t* cu;               // [G + 1]
+  const int32_t* prefix;           // [G]
+  int G;
+  int pairs;                       // CTA pairs of the shared pass, a share each
+  // workspace
+  SharedHead* head;
+  int2* first;                     // [pairs] group (of the active ones) and block of rows at a share's start
+  int32_t* start;                  // [B] first token that a request takes on its own
+  int32_t* of;                     // [B] its active group, or -1
+  SharedGroup* groups;             // [active]
+  int64_t* line;                   // [active] cost of the items before the group's
+  // fp32 rows and their lse (log2): a row's first part at its own place, those that begin
+  // within a share behind them
+  float *pre_part, *pre_lse;       // [B R H + pairs * kPfxRows]
+  float *own_part, *own_lse;       // [B R H + CTAs * N]
+  int4* split;                     // [B][blocks of N rows] first and last share of the own pass
+  int own_n, own_row_blocks;       // N and the blocks of N rows
+};
+
+// An item's place on the line of costs: the share that holds its tile t.
+__host__ __device__ __forceinline__ int64_t prefix_share(int64_t item, int t, int64_t size) {
+  return (item + kPfxItemCost + (int64_t)t * kPfxTileCost) / size;
+}
+
+size_t shared_workspace_bytes(const DecodeParams& p, int64_t G);
+bool launch_latent_shared(const DecodeParams& p, const int64_t* cu, const int32_t* prefix, int64_t G, cudaStream_t s);
+// Its parts: the shared pass; a request's own tokens (sizes first, then the launch).
+bool launch_latent_prefix(const SharedParams& p, cudaStream_t s);
+struct OwnLayout {
+  int n, row_blocks, ctas;
+};
+OwnLayout own_layout(const DecodeParams& p);
+bool launch_latent_own(const SharedParams& p, cudaStream_t s);
+int device_sm_count();
+
 size_t decode_workspace_bytes(const DecodeParams& p);
 // false: a tensor map could not be made or a launch attribute set (nothing launched)
 bool launch_latent_decode(const DecodeParams& p, cudaStream_t s);

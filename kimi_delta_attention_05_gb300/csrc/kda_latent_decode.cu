@@ -79,6 +79,8 @@ struct DecodePlan {
   int whole;           // requests are not split: the share that holds a request's start has all of it
   float* part;         // [row_blocks * shares * 2][N][512] normalised partial rows
   float* part_lse;     // [row_blocks * shares * 2][N] their lse, log2
+  const int32_t* start;  // (own tokens behind shared prefixes) [B] first token of the pass
+  int64_t first_rows;  // (the same) B R H: a row's first part is at its own place of part, the others behind them
   int by_request;      // the join works by request (fewer than shares), else by share
   int4* split;         // [requests or shares][row_blocks]: (request or -1, first share, last share)
 };
@@ -117,16 +119,24 @@ __device__ __forceinline__ int64_t div_fast(int64_t a, int64_t b) {
   return ((a | b) >> 32) == 0 ? (int64_t)((uint32_t)a / (uint32_t)b) : a / b;
 }
 
+// The first token that the pass takes: 0, or behind shared prefixes where the request's own begin.
+template <bool kOwn>
+__device__ __forceinline__ int dec_start(const DecodePlan& pl, int b) {
+  return kOwn ? pl.start[b] : 0;
+}
+
 // The pieces of one share [u0, u1) of the line of costs, in order.  Request b
 // takes [pre, pre + cost) of it; its tile k starts at pre + kDecReqCost + k
 // kDecTileCost and belongs to the share that holds that point; a request
 // without tiles, or one that is not split, belongs to the share that holds pre.
+template <bool kOwn>
 struct DecPieces {
+  const int32_t* start;  // (kOwn) first token of each request
   int unsplit;
   int64_t u0, u1, pre;  // the share; start of request b
   int b;
-  // the current piece: request, its length, tiles [t0, t1) of its `tiles`
-  int req, len, t0, t1, tiles;
+  // the current piece: request, its first token and length, tiles [t0, t1) of its `tiles` from there
+  int req, from, len, t0, t1, tiles;
   __device__ __forceinline__ int tiles_before(int64_t u) const {
     const int64_t d = u - pre - kDecReqCost;
     return d <= 0 ? 0 : (int)min((int64_t)tiles, (d + kDecTileCost - 1) >> 2);
@@ -135,7 +145,8 @@ struct DecPieces {
     while (b < p.B && pre < u1) {
       req = b;
       len = dec_len(p, b);
-      tiles = dec_tiles(len);
+      from = kOwn ? start[b] : 0;
+      tiles = dec_tiles(len - from);
       t0 = tiles_before(u0);
       t1 = tiles_before(u1);
       if (unsplit && pre >= u0) t1 = tiles;  // (and t0 is 0)
@@ -151,12 +162,13 @@ struct DecPieces {
 };
 
 // A walk over the tiles of a share.
+template <bool kOwn>
 struct DecCursor {
-  DecPieces it;
+  DecPieces<kOwn> it;
   int tile;
   int piece;  // index of the piece among those with tiles
   bool ok;
-  __device__ __forceinline__ void start(const DecPieces& s, const DecodeParams& p) {
+  __device__ __forceinline__ void start(const DecPieces<kOwn>& s, const DecodeParams& p) {
     it = s;
     piece = -1;
     ok = true;
@@ -176,7 +188,9 @@ struct DecCursor {
   __device__ __forceinline__ bool last() const { return tile + 1 == it.t1; }
 };
 
-template <int N>
+// kOwn: only the tokens from pl.start[request] on, and every piece leaves a part:
+// the join of the shared call adds those of the prefixes.
+template <int N, bool kOwn>
 __global__ void __launch_bounds__(kDecThreads, 1)
     kda_latent_decode_kernel(const DecodeParams p, const DecodePlan pl, const __grid_constant__ DecodeMaps maps) {
   using C = DecCfg<N>;
@@ -219,7 +233,7 @@ __global__ void __launch_bounds__(kDecThreads, 1)
   for (int b = b0; b < b1; ++b) {
     const int raw = p.lens[b], len = dec_len(p, b);
     odd |= raw != len;
-    mine += dec_cost(dec_tiles(len));
+    mine += dec_cost(dec_tiles(len - dec_start<kOwn>(pl, b)));
   }
   if (odd && blockIdx.x == 0) atomicExch(p.status, KDA_ERR_BAD_LENGTHS);
   int64_t incl = mine;
@@ -244,7 +258,7 @@ __global__ void __launch_bounds__(kDecThreads, 1)
   if (u0 < u1 && u0 >= before && u0 < before + mine) {
     int64_t pre = before;
     for (int b = b0; b < b1; ++b) {
-      const int64_t t = dec_cost(dec_tiles(dec_len(p, b)));
+      const int64_t t = dec_cost(dec_tiles(dec_len(p, b) - dec_start<kOwn>(pl, b)));
       if (u0 < pre + t) {
         s_scan[10] = b;
         s_scan[11] = pre;
@@ -254,7 +268,8 @@ __global__ void __launch_bounds__(kDecThreads, 1)
     }
   }
   __syncthreads();
-  DecPieces pieces;
+  DecPieces<kOwn> pieces;
+  pieces.start = pl.start;
   pieces.unsplit = pl.whole;
   pieces.u0 = u0;
   pieces.u1 = u1;
@@ -275,18 +290,18 @@ __global__ void __launch_bounds__(kDecThreads, 1)
   if (warp == kDecCopyWarp) {
     // ---- copies: the tiles of the share into the stages, the query rows of each piece ----
     const int box = pl.box_rows;
-    DecCursor c;
+    DecCursor<kOwn> c;
     c.start(pieces, p);
     int it = 0, qi = 0;  // tiles and query blocks issued
     bool gone = false;
     while (c.ok && !gone) {
       const int s = it & 1;
-      const int valid = min(kDecTile, c.it.len - c.tile * kDecTile);
+      const int valid = min(kDecTile, c.it.len - c.it.from - c.tile * kDecTile);
       const int segs = (valid + box - 1) / box;
       // page of this lane's run of box rows (lanes below segs), fetched before the wait
       int page = 0, off = 0;
       if (lane < segs) {
-        const uint32_t j = (uint32_t)(c.tile * kDecTile + lane * box), in_table = j / (uint32_t)p.page_size;
+        const uint32_t j = (uint32_t)(c.it.from + c.tile * kDecTile + lane * box), in_table = j / (uint32_t)p.page_size;
         page = p.table[c.it.req * p.table_stride + in_table];
         off = (int)(j - in_table * (uint32_t)p.page_size);
         if (page < 0 || page >= p.num_pages) {
@@ -330,7 +345,7 @@ __global__ void __launch_bounds__(kDecThreads, 1)
     const uint64_t d_x = smem_desc(sb, 16, kDecGroup), d_c = smem_desc(sb, kDecAtom, kDecGroup);
     const uint64_t d_q = smem_desc(sb + C::kQ, 16, 1024), d_p = smem_desc(sb + C::kP, 16, 1024);
     const uint32_t t_s = tmem + 4 * N;
-    DecCursor cs, co;
+    DecCursor<kOwn> cs, co;
     cs.start(pieces, p);
     co = cs;
     int is = 0, io = 0;  // tiles of the scores and of the values
@@ -372,7 +387,7 @@ __global__ void __launch_bounds__(kDecThreads, 1)
       // O^T += C^T P^T of tile `io`
       const int s = io & 1;
       wait(bar(C::kPReady), (uint32_t)(io & 1));
-      const int valid = min(kDecTile, co.it.len - co.tile * kDecTile);
+      const int valid = min(kDecTile, co.it.len - co.it.from - co.tile * kDecTile);
       if (valid < kDecTile) {
         // what lies behind the length takes part in the product with weight 0: it has to be finite
         for (int t = valid; t < kDecTile; ++t)
@@ -419,7 +434,7 @@ __global__ void __launch_bounds__(kDecThreads, 1)
     int it = 0;
     while (pieces.next(p)) {
       const int nt = pieces.count();
-      const bool whole = pieces.whole();
+      const bool whole = !kOwn && pieces.whole();
       float m[kM], l[kM];
 #pragma unroll
       for (int i = 0; i < kM; ++i) {
@@ -435,8 +450,8 @@ __global__ void __launch_bounds__(kDecThreads, 1)
         tc_ld16x256(tmem + lane_base + 4 * N + N * s, v);
 #pragma unroll
         for (int i = 0; i < kV; ++i) v[i] *= p.scale_log2;
-        const int j = tile * kDecTile + tok;
-        if ((tile + 1) * kDecTile > pieces.len - (p.R - 1)) {
+        const int j = pieces.from + tile * kDecTile + tok;
+        if (pieces.from + (tile + 1) * kDecTile > pieces.len - (p.R - 1)) {
           // the last tiles: row (token i, head) sees j < len - (R - 1 - i)
 #pragma unroll
           for (int i = 0; i < kM; ++i) {
@@ -535,7 +550,10 @@ __global__ void __launch_bounds__(kDecThreads, 1)
         if (lane < 4) wmax[w4 * N + 8 * (i >> 1) + c0 + (i & 1)] = l[i];
       }
       named_bar(bar_id, 128);
-      const int slot = 2 * blockIdx.x + (pieces.t0 > 0 ? 0 : 1);
+      // first row of the part: two blocks of N rows a CTA, or (kOwn) the rows' own place or this CTA's behind them
+      const int64_t part_row = !kOwn ? (int64_t)(2 * blockIdx.x + (pieces.t0 > 0 ? 0 : 1)) * N
+                               : pieces.t0 > 0 ? pl.first_rows + (int64_t)blockIdx.x * N
+                                               : (int64_t)pieces.req * rows + row0;
       if (w4 == 0 && lane < 4) {
 #pragma unroll
         for (int i = 0; i < kM; ++i) {
@@ -544,7 +562,7 @@ __global__ void __launch_bounds__(kDecThreads, 1)
           fac[c] = sum > 0.f ? 1.0f / sum : (sum == 0.f ? 0.f : sum);
           const float lse2 = sum == 0.f ? -INFINITY : m[i] + __log2f(sum);
           if (!whole) {
-            pl.part_lse[(int64_t)slot * N + h0 + c] = lse2;
+            if (!kOwn || row0 + h0 + c < rows) pl.part_lse[part_row + h0 + c] = lse2;
           } else if (p.lse && row0 + h0 + c < rows) {
             p.lse[(int64_t)pieces.req * rows + row0 + h0 + c] = lse2 * 0.6931471805599453f;
           }
@@ -578,7 +596,7 @@ __global__ void __launch_bounds__(kDecThreads, 1)
         }
         const int left = rows - row0 - h0;  // query rows there are from this half's first
         if (!whole) {
-          float* dst = pl.part + ((int64_t)slot * N + h0) * kLat + dim + lane;
+          float* dst = pl.part + (part_row + h0) * kLat + dim + lane;
 #pragma unroll
           for (int r = 0; r < kH; ++r)
             if (r < left) dst[r * kLat] = o[r];
@@ -598,17 +616,18 @@ __global__ void __launch_bounds__(kDecThreads, 1)
     }
     tc_fence_before();
   }
-  if (tid == 0 && !pl.whole) {
+  if (tid == 0 && (kOwn || !pl.whole)) {
     // what the join kernel has to do, by request or by the share a request starts in
     if (!pl.by_request) pl.split[blockIdx.x] = make_int4(-1, 0, 0, 0);
-    DecPieces each = pieces;
+    DecPieces<kOwn> each = pieces;
     each.b = u0 < u1 ? (int)s_scan[10] : p.B;
     each.pre = s_scan[11];
     while (each.next(p)) {
       if (each.t0 > 0) continue;
       // (the request's last tile starts kDecTileCost before the next request)
-      const int4 info = each.whole() ? make_int4(-1, 0, 0, 0)
-                                     : make_int4(each.req, share, (int)div_fast(each.pre - kDecTileCost, size), 0);
+      const int4 info = kOwn && each.whole() ? make_int4(each.req, share, share, 0)
+                        : each.whole()       ? make_int4(-1, 0, 0, 0)
+                                             : make_int4(each.req, share, (int)div_fast(each.pre - kDecTileCost, size), 0);
       if (pl.by_request) pl.split[each.req * pl.row_blocks + rblk] = info;
       else if (!each.whole()) pl.split[blockIdx.x] = info;
     }
@@ -704,8 +723,6 @@ __global__ void __launch_bounds__(512) kda_latent_join_kernel(const DecodeParams
   }
 }
 
-namespace {
-
 int device_sm_count() {
   int dev = 0, sms = 0;
   if (cudaGetDevice(&dev) != cudaSuccess ||
@@ -715,6 +732,8 @@ int device_sm_count() {
   }
   return sms;
 }
+
+namespace {
 
 // Columns of the products: the query rows of a request rounded up to 16, 32 or
 // 64; blocks of 64 beyond that.
@@ -754,7 +773,7 @@ DecLayout dec_layout(const DecodeParams& p) {
   return d;
 }
 
-template <int N>
+template <int N, bool kOwn>
 bool launch_dec(const DecodeParams& p, const DecLayout& d, const DecodeMaps& maps, cudaStream_t s) {
   const unsigned ctas = (unsigned)(d.plan.row_blocks * d.plan.shares);
   static std::once_flag once[64];
@@ -762,19 +781,42 @@ bool launch_dec(const DecodeParams& p, const DecLayout& d, const DecodeMaps& map
   int dev = 0;
   if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return false;
   std::call_once(once[dev], [&] {
-    rc[dev] = cudaFuncSetAttribute(kda_latent_decode_kernel<N>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+    rc[dev] = cudaFuncSetAttribute(kda_latent_decode_kernel<N, kOwn>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                    DecCfg<N>::kSmem);
   });
   if (rc[dev] != cudaSuccess) return false;
-  if (!launch_overlapped(kda_latent_decode_kernel<N>, dim3(ctas), kDecThreads, DecCfg<N>::kSmem, s, 1, p, d.plan, maps))
+  if (!launch_overlapped(kda_latent_decode_kernel<N, kOwn>, dim3(ctas), kDecThreads, DecCfg<N>::kSmem, s, 1, p, d.plan,
+                         maps))
     return false;
-  if (d.plan.whole) return true;  // nothing to join
+  if (kOwn || d.plan.whole) return true;  // nothing to join
   // a row a CTA where a request is in more than four parts on average, else a row a warp
   const bool wide = (int64_t)p.B * 4 < d.plan.shares;
   const int most = std::min(N, p.R * p.H);
   const dim3 grid((unsigned)d.joins, (unsigned)(wide ? most : (most + 15) / 16));
   return launch_overlapped(wide ? kda_latent_join_kernel<true> : kda_latent_join_kernel<false>, grid, 512, 0, s, 1, p,
                            d.plan, N);
+}
+
+// The tensor maps of a call; false: one could not be made.
+bool dec_maps(DecodeParams& p, const DecLayout& d, DecodeMaps& maps) {
+  memset(&maps, 0, sizeof(maps));
+  const int rows = p.R * p.H;
+  {  // query rows [B][rows][576] as [64 values][rows][9 blocks][B]: one copy brings N rows of a request
+    const cuuint64_t dims[4] = {64, (cuuint64_t)rows, (cuuint64_t)kDecChunks, (cuuint64_t)p.B};
+    const cuuint64_t strides[3] = {kLatRow * 2, 128, (cuuint64_t)rows * kLatRow * 2};
+    const cuuint32_t box[4] = {64, (cuuint32_t)d.n, (cuuint32_t)kDecChunks, 1};
+    if (!encode_map_bf16(&maps.q, p.q, 4, dims, strides, box)) return false;
+  }
+  if (p.num_pages == 0) {
+    p.max_pages = 0;  // no cache: every length is taken as 0, and nothing is copied
+    return true;
+  }
+  // the cache as [64 values][8 tokens][9 blocks][8-token groups of a page][pages]
+  const cuuint64_t dims[5] = {64, 8, (cuuint64_t)kDecChunks, (cuuint64_t)p.page_size / 8, (cuuint64_t)p.num_pages};
+  const cuuint64_t strides[4] = {(cuuint64_t)p.token_stride * 2, 128, (cuuint64_t)p.token_stride * 16,
+                                 (cuuint64_t)p.page_stride * 2};
+  const cuuint32_t box[5] = {64, 8, (cuuint32_t)kDecChunks, (cuuint32_t)d.plan.box_rows / 8, 1};
+  return encode_map_bf16(&maps.cache, p.cache, 5, dims, strides, box);
 }
 
 }  // namespace
@@ -788,27 +830,34 @@ bool launch_latent_decode(const DecodeParams& args, cudaStream_t s) {
   d.plan.part_lse = reinterpret_cast<float*>(p.ws + d.lse_at);
   d.plan.split = reinterpret_cast<int4*>(p.ws + d.split_at);
   DecodeMaps maps;
-  memset(&maps, 0, sizeof(maps));
-  const int rows = p.R * p.H;
-  {  // query rows [B][rows][576] as [64 values][rows][9 blocks][B]: one copy brings N rows of a request
-    const cuuint64_t dims[4] = {64, (cuuint64_t)rows, (cuuint64_t)kDecChunks, (cuuint64_t)p.B};
-    const cuuint64_t strides[3] = {kLatRow * 2, 128, (cuuint64_t)rows * kLatRow * 2};
-    const cuuint32_t box[4] = {64, (cuuint32_t)d.n, (cuuint32_t)kDecChunks, 1};
-    if (!encode_map_bf16(&maps.q, p.q, 4, dims, strides, box)) return false;
-  }
-  if (p.num_pages == 0) {
-    p.max_pages = 0;  // no cache: every length is taken as 0, and nothing is copied
-  } else {  // the cache as [64 values][8 tokens][9 blocks][8-token groups of a page][pages]
-    const cuuint64_t dims[5] = {64, 8, (cuuint64_t)kDecChunks, (cuuint64_t)p.page_size / 8, (cuuint64_t)p.num_pages};
-    const cuuint64_t strides[4] = {(cuuint64_t)p.token_stride * 2, 128, (cuuint64_t)p.token_stride * 16,
-                                   (cuuint64_t)p.page_stride * 2};
-    const cuuint32_t box[5] = {64, 8, (cuuint32_t)kDecChunks, (cuuint32_t)d.plan.box_rows / 8, 1};
-    if (!encode_map_bf16(&maps.cache, p.cache, 5, dims, strides, box)) return false;
-  }
+  if (!dec_maps(p, d, maps)) return false;
   switch (d.n) {
-    case 16: return launch_dec<16>(p, d, maps, s);
-    case 32: return launch_dec<32>(p, d, maps, s);
-    default: return launch_dec<64>(p, d, maps, s);
+    case 16: return launch_dec<16, false>(p, d, maps, s);
+    case 32: return launch_dec<32, false>(p, d, maps, s);
+    default: return launch_dec<64, false>(p, d, maps, s);
+  }
+}
+
+OwnLayout own_layout(const DecodeParams& p) {
+  const DecLayout d = dec_layout(p);
+  return {d.n, d.plan.row_blocks, d.plan.row_blocks * d.plan.shares};
+}
+
+bool launch_latent_own(const SharedParams& sp, cudaStream_t s) {
+  DecodeParams p = sp.d;
+  DecLayout d = dec_layout(p);
+  d.plan.part = sp.own_part;
+  d.plan.part_lse = sp.own_lse;
+  d.plan.split = sp.split;
+  d.plan.start = sp.start;
+  d.plan.first_rows = (int64_t)p.B * p.R * p.H;
+  d.plan.by_request = 1;
+  DecodeMaps maps;
+  if (!dec_maps(p, d, maps)) return false;
+  switch (d.n) {
+    case 16: return launch_dec<16, true>(p, d, maps, s);
+    case 32: return launch_dec<32, true>(p, d, maps, s);
+    default: return launch_dec<64, true>(p, d, maps, s);
   }
 }
 
