@@ -402,16 +402,34 @@ __global__ void __launch_bounds__(kPfxThreads, 1)
       wait(bar(kFO), (uint32_t)((n - 1) & 1));
       __syncwarp();
       tc_fence_after();
-      float* dst = sp.pre_part + at * kLat + 256 * side + 128 * right;
+      // A warp turns 32 rows x 16 dimensions in 2 KB of P's place (its own: the last products have read it) and
+      // stores 64 bytes of 8 rows at a time; a thread's own row at a time, each store touched 32 lines and the
+      // 128 KB took 12000 cycles.
+      const uint32_t turn = sb + kPfxP + warp * 2048;
+      const int64_t first = at - r + 32 * (w4 & 1);  // this warp's first row; all of one part are side by side
+      const int rows_there = it.g.rows - (it.row + 64 * rank + 32 * (w4 & 1));
+      float* dst = sp.pre_part + first * kLat + 256 * side + 128 * right;
 #pragma unroll 1
       for (int c = 0; c < 128; c += 16) {
         float o[16];
         tc_ld16(tmem + lane_base + 128 * right + c, o);
-        if (there) {
 #pragma unroll
-          for (int i = 0; i < 16; i += 4)
-            *reinterpret_cast<float4*>(dst + c + i) = make_float4(o[i] * inv, o[i + 1] * inv, o[i + 2] * inv, o[i + 3] * inv);
+        for (int i = 0; i < 4; ++i)
+          asm volatile("st.shared.v4.f32 [%0], {%1, %2, %3, %4};\n" ::"r"(turn + lane * 64 + ((i ^ (lane >> 1 & 3)) << 4)),
+                       "f"(o[4 * i] * inv), "f"(o[4 * i + 1] * inv), "f"(o[4 * i + 2] * inv), "f"(o[4 * i + 3] * inv)
+                       : "memory");
+        __syncwarp();
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          const int row_of = 8 * k + (lane >> 2), piece = lane & 3;
+          float4 x;
+          asm volatile("ld.shared.v4.f32 {%0, %1, %2, %3}, [%4];\n"
+                       : "=f"(x.x), "=f"(x.y), "=f"(x.z), "=f"(x.w)
+                       : "r"(turn + row_of * 64 + ((piece ^ (row_of >> 1 & 3)) << 4))
+                       : "memory");
+          if (row_of < rows_there) *reinterpret_cast<float4*>(dst + row_of * kLat + c + 4 * piece) = x;
         }
+        __syncwarp();
       }
       tc_fence_before();
       named_bar(1, 256);  // wmax is read
