@@ -23,7 +23,7 @@ namespace cg = cooperative_groups;
 constexpr int kRowPieces = kLatRow / 8;         // 16-byte pieces of a cache row
 constexpr int kGroupRows = 8;                   // page sizes are multiples of this
 constexpr int kCopyThreads = 4 * kRowPieces;    // four rows at a time, twice a group
-constexpr int kPageThreads = 1024;
+constexpr int kPageThreads = 512;
 constexpr int kPageCluster = 8;                 // CTAs of the kernels that list pages
 
 struct PageCache {
@@ -43,23 +43,30 @@ __device__ __forceinline__ int warp_scan_int(int x, int lane) {
 // Pages of a length that is not negative.
 __device__ __forceinline__ int pages_of(int tokens, int page) { return (int)(((uint32_t)tokens + (uint32_t)page - 1) / (uint32_t)page); }
 
-// Exclusive prefix of x over the block's threads; `total` gets the sum.
+// Exclusive prefix over the block's warps of a value that each warp's lanes share; `total` gets the sum.  (One warp
+// adds up the warps' values: every thread for itself took 3600 cycles of 1024 threads.)
 template <int kThreads>
-__device__ __forceinline__ int block_scan(int x, int* sums, int& total) {
+__device__ __forceinline__ int warps_before(int x, int* sums, int& total) {
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const int upto = warp_scan_int(x, lane);
-  if (lane == 31) sums[warp] = upto;
+  if (lane == 0) sums[warp] = x;
   __syncthreads();
-  int before = 0;
-  total = 0;
-#pragma unroll
-  for (int w = 0; w < kThreads / 32; ++w) {
-    const int s = sums[w];
-    if (w < warp) before += s;
-    total += s;
+  if (warp == 0) {
+    const int own = lane < kThreads / 32 ? sums[lane] : 0, upto = warp_scan_int(own, lane);
+    __syncwarp();
+    if (lane < kThreads / 32) sums[lane] = upto - own;
+    if (lane == 31) sums[kThreads / 32] = upto;
   }
+  __syncthreads();
+  const int before = sums[warp];
+  total = sums[kThreads / 32];
   __syncthreads();  // sums are read
-  return before + upto - x;
+  return before;
+}
+
+__device__ __forceinline__ int warp_sum(int x) {
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) x += __shfl_xor_sync(0xffffffffu, x, o);
+  return x;
 }
 
 // ---- copies of pages ----
@@ -223,10 +230,12 @@ __global__ void __launch_bounds__(kCopyThreads) kda_latent_fork_kernel(const For
 
 // ---- release ----
 //
-// One cluster of eight CTAs: all counts go down (L2 atomics), the cluster's barrier,
-// then each CTA lists the pages of its eighth that fell below 0, its place in the
-// list from the others' numbers over distributed shared memory.  One launch and no
-// workspace.
+// The counts of the dropped pages go down (L2 atomics), then the pages that fell
+// below 0 are listed in order.  One cluster of eight CTAs does both: its barrier
+// stands between them, a CTA lists an eighth, and its place in the list comes from
+// the others' numbers over distributed shared memory: one launch, no workspace.  Eight
+// SMs take 2.5 cycles an atomic each, so calls with many entries have a kernel on all
+// SMs do the counts first.
 struct ReleaseParams {
   const int32_t *rows, *keep, *cached, *table;
   int64_t table_stride, max_pages;
@@ -237,19 +246,23 @@ struct ReleaseParams {
   int* status;
 };
 
-constexpr int kReleasePart = 128;  // table entries that a warp takes at a time
+constexpr int kReleaseCached = 2048;  // rows whose entries to drop are kept in shared memory
 
-__global__ void __launch_bounds__(kPageThreads) kda_latent_release_kernel(const ReleaseParams p) {
-  extern __shared__ uint32_t is_released[];  // a bit a row of the table
-  __shared__ int sums[kPageThreads / 32];
-  __shared__ int freed;
-  cg::cluster_group cluster = cg::this_cluster();
-  const int tid = threadIdx.x, lane = tid & 31, rank = (int)cluster.block_rank();
-  asm volatile("griddepcontrol.wait;\n" ::: "memory");
-  for (int i = tid; i < (p.B + 31) / 32; i += kPageThreads) is_released[i] = 0;
+// What a row drops: entries [first, end) of row b of the table.
+struct Dropped {
+  int b, first, end;
+};
+
+size_t release_smem(int64_t B, int64_t F) {
+  return (size_t)(B + 31) / 32 * 4 + (size_t)std::min<int64_t>(F, kReleaseCached) * sizeof(Dropped);
+}
+
+// Checks the rows, for every CTA by itself: a bit a released row of the table, and what each drops.
+__device__ __forceinline__ bool release_rows(const ReleaseParams& p, uint32_t* is_released, Dropped* rows) {
+  for (int i = threadIdx.x; i < (p.B + 31) / 32; i += kPageThreads) is_released[i] = 0;
   __syncthreads();
   int bad = 0;
-  for (int f = tid; f < p.F; f += kPageThreads) {
+  for (int f = threadIdx.x; f < p.F; f += kPageThreads) {
     const int b = p.rows[f];
     if (b < 0 || b >= p.B) {
       bad = 1;
@@ -258,72 +271,117 @@ __global__ void __launch_bounds__(kPageThreads) kda_latent_release_kernel(const 
     if (atomicOr(&is_released[b >> 5], 1u << (b & 31)) >> (b & 31) & 1) bad = 1;  // twice
     const int held = p.cached[b], keep = p.keep ? p.keep[f] : 0;
     if (held < 0 || keep < 0 || keep > held || held > p.max_pages * p.page) bad = 1;
+    else if (f < kReleaseCached) rows[f] = {b, pages_of(keep, p.page), pages_of(held, p.page)};
   }
-  bad = __syncthreads_or(bad);
-  if (rank == 0) {
-    if (bad && tid == 0) atomicExch(p.status, KDA_ERR_BAD_LENGTHS);
+  return !__syncthreads_or(bad);
+}
+
+// The counts of all dropped pages down: warps take equal parts of rows, eight loads of 32 entries at a time.
+__device__ __forceinline__ void release_counts(const ReleaseParams& p, const Dropped* rows, int cta, int ctas) {
+  const int lane = threadIdx.x & 31, warps = ctas * (kPageThreads / 32);
+  const int part = (int)min((p.F * p.max_pages / warps / 256 + 1) * 256, (int64_t)1 << 30);
+  const int parts = ((int)p.max_pages + part - 1) / part;  // (parts * F is at most about the warps and F)
+  for (int i = cta * (kPageThreads / 32) + (threadIdx.x >> 5); i < parts * p.F; i += warps) {
+    const int f = i / parts;
+    Dropped d;
+    if (f < kReleaseCached) {
+      d = rows[f];
+    } else {
+      d.b = p.rows[f];
+      d.first = pages_of(p.keep ? p.keep[f] : 0, p.page);
+      d.end = pages_of(p.cached[d.b], p.page);
+    }
+    const int32_t* ids = p.table + d.b * p.table_stride;
+    const uint32_t j0 = (uint32_t)(i - f * parts) * part, end = min((uint32_t)d.end, j0 + part);
+    for (uint32_t j = max(j0, (uint32_t)d.first) + lane; j < end; j += 256) {
+      int id[8];
+#pragma unroll
+      for (int k = 0; k < 8; ++k) id[k] = j + 32 * k < end ? ids[j + 32 * k] : INT32_MIN;
+#pragma unroll
+      for (int k = 0; k < 8; ++k) {
+        if (id[k] >= 0 && id[k] < p.num_pages) atomicSub(p.shares + id[k], 1);
+        else if (j + 32 * k < end) atomicExch(p.status, KDA_ERR_BAD_PAGE);
+      }
+    }
+  }
+}
+
+__global__ void __launch_bounds__(kPageThreads) kda_latent_release_counts_kernel(const ReleaseParams p) {
+  extern __shared__ uint32_t release_smem_[];
+  Dropped* rows = reinterpret_cast<Dropped*>(release_smem_ + (p.B + 31) / 32);
+  asm volatile("griddepcontrol.launch_dependents;\n" ::: "memory");
+  asm volatile("griddepcontrol.wait;\n" ::: "memory");
+  if (release_rows(p, release_smem_, rows)) release_counts(p, rows, blockIdx.x, gridDim.x);
+}
+
+// counts: whether this kernel does the counts too
+__global__ void __launch_bounds__(kPageThreads) kda_latent_release_kernel(const ReleaseParams p, const int counts) {
+  extern __shared__ uint32_t release_smem_[];
+  __shared__ int sums[kPageThreads / 32 + 1];
+  __shared__ int freed[2][kPageCluster];  // pages that each CTA lists in a round, and in the one before or behind it
+  cg::cluster_group cluster = cg::this_cluster();
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, rank = (int)cluster.block_rank();
+  Dropped* rows = reinterpret_cast<Dropped*>(release_smem_ + (p.B + 31) / 32);
+  asm volatile("griddepcontrol.wait;\n" ::: "memory");
+  const bool good = release_rows(p, release_smem_, rows);
+  if (good && counts) release_counts(p, rows, rank, kPageCluster);
+  if (rank == kPageCluster - 1) {  // (the last CTA: it has the least to do)
+    if (!good && tid == 0) atomicExch(p.status, KDA_ERR_BAD_LENGTHS);
     for (int b = tid; b < p.B; b += kPageThreads)
-      if (bad || !(is_released[b >> 5] >> (b & 31) & 1)) p.seq_lens[b] = p.cached[b];
-    if (!bad)
+      if (!good || !(release_smem_[b >> 5] >> (b & 31) & 1)) p.seq_lens[b] = p.cached[b];
+    if (good)
       for (int f = tid; f < p.F; f += kPageThreads) p.seq_lens[p.rows[f]] = p.keep ? p.keep[f] : 0;
   }
-  if (!bad) {
-    const int64_t parts = (p.max_pages + kReleasePart - 1) / kReleasePart;
-    const int warps = kPageCluster * kPageThreads / 32;
-    for (int64_t i = rank * (kPageThreads / 32) + (tid >> 5); i < parts * p.F; i += warps) {
-      const int f = (int)(i / parts), j0 = (int)(i - f * parts) * kReleasePart;
-      const int b = p.rows[f], keep = p.keep ? p.keep[f] : 0;
-      const int held = pages_of(p.cached[b], p.page), stays = pages_of(keep, p.page);
+  cluster.sync();  // (waits for the atomics)
+  // Rounds of runs of up to 32 x 32 pages, a run a warp: lane w keeps the bits of its pages 32 w .. 32 w + 31, so that
+  // a page is read once and stores are of neighbouring lanes.
+  constexpr uint32_t kWarps = kPageThreads / 32;
+  const uint32_t pages = (uint32_t)p.num_pages;
+  const int words = (int)min(32u, (pages + kPageCluster * kWarps * 32 - 1) / (kPageCluster * kWarps * 32));
+  const uint32_t length = 32 * words;
+  uint32_t all = 0;
+  int round = 0;
+  for (uint32_t base = 0; base < pages; base += kPageCluster * kWarps * length, ++round) {
+    const uint32_t run = base + (rank * kWarps + warp) * length;
+    uint32_t bits = 0;
+    if (good && run < pages) {
+#pragma unroll 1
+      for (int w0 = 0; w0 < words; w0 += 16) {
+        int x[16];  // (loaded without a branch, so that all are on their way at once)
 #pragma unroll
-      for (int k = 0; k < kReleasePart / 32; ++k) {
-        const int j = j0 + 32 * k + lane;
-        if (j < stays || j >= held) continue;
-        const int id = p.table[b * p.table_stride + j];
-        if (id < 0 || id >= p.num_pages) atomicExch(p.status, KDA_ERR_BAD_PAGE);
-        else atomicSub(p.shares + id, 1);
-      }
-    }
-  }
-  cluster.sync();
-  // this CTA's eighth of the pages, four a thread and round
-  const int64_t chunk = (p.num_pages + kPageCluster - 1) / kPageCluster;
-  const int64_t lo = min(p.num_pages, rank * chunk), hi = min(p.num_pages, lo + chunk);
-  int n = 0;
-  if (!bad)
-    for (int64_t i = lo + tid * 4; i < hi; i += 4 * kPageThreads)
+        for (int w = 0; w < 16; ++w) x[w] = __ldcg(p.shares + min(run + 32 * (w0 + w) + lane, pages - 1));
 #pragma unroll
-      for (int k = 0; k < 4; ++k) n += i + k < hi && __ldcg(p.shares + i + k) < 0;
-  int total;
-  block_scan<kPageThreads>(n, sums, total);
-  if (tid == 0) freed = total;
-  cluster.sync();
-  int64_t at = 0, all = 0;
-  for (int r = 0; r < kPageCluster; ++r) {
-    const int x = *cluster.map_shared_rank(&freed, r);
-    if (r < rank) at += x;
-    all += x;
-  }
-  if (total > 0)
-    for (int64_t base = lo; base < hi; base += 4 * kPageThreads) {
-      const int64_t i = base + tid * 4;
-      int is[4], m = 0;
-#pragma unroll
-      for (int k = 0; k < 4; ++k) {
-        is[k] = i + k < hi && __ldcg(p.shares + i + k) < 0;
-        m += is[k];
-      }
-      int64_t to = at + block_scan<kPageThreads>(m, sums, total);
-      at += total;
-#pragma unroll
-      for (int k = 0; k < 4; ++k)
-        if (is[k]) {
-          p.pages[to++] = (int32_t)(i + k);
-          p.shares[i + k] = 0;
+        for (int w = 0; w < 16; ++w) {
+          const uint32_t mask = __ballot_sync(0xffffffffu, x[w] < 0 && w0 + w < words && run + 32 * (w0 + w) + lane < pages);
+          if (lane == w0 + w) bits = mask;
         }
+      }
     }
-  for (int64_t i = max(lo, all) + tid; i < hi; i += kPageThreads) p.pages[i] = -1;
+    int total;
+    const int before = warps_before<kPageThreads>(warp_sum(__popc(bits)), sums, total);
+    if (tid < kPageCluster) *cluster.map_shared_rank(&freed[round & 1][rank], tid) = total;
+    cluster.sync();
+    uint32_t at = all + before;
+#pragma unroll
+    for (int r = 0; r < kPageCluster; ++r) {
+      const int c = freed[round & 1][r];
+      if (r < rank) at += c;
+      all += c;
+    }
+    uint32_t left = __ballot_sync(0xffffffffu, bits != 0);
+    while (left) {
+      const int w = __ffs(left) - 1;
+      left &= left - 1;
+      const uint32_t mask = __shfl_sync(0xffffffffu, bits, w), page = run + 32 * w + lane;
+      if (mask >> lane & 1) {
+        p.pages[at + __popc(mask & ((1u << lane) - 1))] = (int32_t)page;
+        p.shares[page] = 0;
+      }
+      at += __popc(mask);
+    }
+  }
+  for (uint32_t i = all + rank * kPageThreads + tid; i < pages; i += kPageCluster * kPageThreads) p.pages[i] = -1;
   if (rank == 0 && tid == 0) p.count[0] = (int32_t)all;
-  cluster.sync();  // the others may still read `freed`
 }
 
 // ---- compact ----
@@ -347,7 +405,7 @@ struct CompactParams {
 };
 
 __global__ void __launch_bounds__(kPageThreads) kda_latent_compact_kernel(const CompactParams p) {
-  __shared__ int sums[kPageThreads / 32];
+  __shared__ int sums[kPageThreads / 32 + 1];
   __shared__ int count;
   cg::cluster_group cluster = cg::this_cluster();
   const int tid = threadIdx.x, lane = tid & 31, rank = (int)cluster.block_rank();
@@ -396,7 +454,7 @@ __global__ void __launch_bounds__(kPageThreads) kda_latent_compact_kernel(const 
   auto four = [&](int64_t i) { return __ldcg(reinterpret_cast<const uint32_t*>(p.held + i)); };  // (the last one is padded)
   int n = 0, total;
   for (int64_t i = lo + tid * 4; i < hi; i += 4 * kPageThreads) n += __popc(four(i));
-  block_scan<kPageThreads>(n, sums, total);
+  warps_before<kPageThreads>(warp_sum(n), sums, total);
   if (tid == 0) count = total;
   cluster.sync();
   // U, and how many held pages lie before this CTA's and before place U
@@ -418,14 +476,15 @@ __global__ void __launch_bounds__(kPageThreads) kda_latent_compact_kernel(const 
 #pragma unroll
     for (int k = 0; k < 4; ++k) n += i + k < used && (x >> (8 * k) & 1);
   }
-  block_scan<kPageThreads>(n, sums, total);
+  warps_before<kPageThreads>(warp_sum(n), sums, total);
   below += total;
   // places and movers, in order; a mover's number waits in the map for the places of the other CTAs
   int64_t at = before;
   for (int64_t base = lo; base < hi; base += 4 * kPageThreads) {
     const int64_t i = base + tid * 4;
     const uint32_t x = i < hi ? four(i) : 0;
-    int64_t held = at + block_scan<kPageThreads>(__popc(x), sums, total);
+    const int mine = __popc(x), upto = warp_scan_int(mine, lane);
+    int64_t held = at + warps_before<kPageThreads>(__shfl_sync(0xffffffffu, upto, 31), sums, total) + upto - mine;
     at += total;
 #pragma unroll
     for (int k = 0; k < 4; ++k) {
@@ -476,6 +535,9 @@ __global__ void __launch_bounds__(kCopyThreads) kda_latent_move_kernel(const Com
 }
 
 namespace {
+
+// Entries from which on the counts go to a kernel of their own.
+constexpr int64_t kReleaseApart = 32768;
 
 bool al4(const void* p) { return ((uintptr_t)p & 3) == 0; }
 
@@ -582,8 +644,14 @@ extern "C" int kda_latent_release(const kda_latent_release_args* a, void* stream
   if (!status) return KDA_ERR_LAUNCH;
   const ReleaseParams p{a->rows, a->keep_lens, a->cached_lens, a->block_table, a->table_stride, a->max_pages, a->shares,
                         a->num_pages, a->seq_lens, a->pages, a->count, (int)a->F, (int)a->B, (int)a->page_size, status};
-  return launch_overlapped(kda_latent_release_kernel, dim3(kPageCluster), kPageThreads, (size_t)(a->B + 31) / 32 * 4, s,
-                           kPageCluster, p)
+  const size_t smem = release_smem(a->B, a->F);
+  const bool apart = a->F * a->max_pages > kReleaseApart;
+  if (apart) {
+    const int64_t ctas = std::min<int64_t>((a->F * a->max_pages + 1023) / 1024, 152);
+    if (!launch_overlapped(kda_latent_release_counts_kernel, dim3((unsigned)ctas), kPageThreads, smem, s, 1, p))
+      return KDA_ERR_LAUNCH;
+  }
+  return launch_overlapped(kda_latent_release_kernel, dim3(kPageCluster), kPageThreads, smem, s, kPageCluster, p, !apart)
              ? KDA_OK
              : KDA_ERR_LAUNCH;
 }
