@@ -181,7 +181,7 @@ int kda_latent_decode(const kda_latent_decode_args *args, void *workspace, size_
  * without requests is not looked at; another below 0
  * or beyond the table is taken as the nearer bound and sets KDA_ERR_BAD_LENGTHS;
  * offsets that do not go from 0 to B without decreasing set KDA_ERR_BAD_SEQLENS, and
- * every request is taken on its own.  B * R * H is below 2^31 - 128.
+ * every request is taken on its own.  B * R * H is below 2^31 - 128, G at most 16384.
  * Prefix and remaining tokens are joined by their fp32 parts, so outputs have the
  * error of kda_latent_decode's; they are not bit for bit the same.
  */

@@ -273,7 +273,7 @@ int check_shared(const kda_latent_decode_shared_args* a) {
   if (!a) return KDA_ERR_NULL_ARG;
   const int rc = check_decode(&a->decode);
   if (rc != KDA_OK) return rc;
-  if (a->G < 0 || a->G > (1 << 20) || a->decode.B * a->decode.R * a->decode.H > INT32_MAX - 128) return KDA_ERR_SHAPE;
+  if (a->G < 0 || a->G > kMaxPlanRequests || a->decode.B * a->decode.R * a->decode.H > INT32_MAX - 128) return KDA_ERR_SHAPE;
   if (a->G == 0 && a->decode.B > 0) return KDA_ERR_BAD_SEQLENS;  // offsets that cannot end at B
   if (!a->cu_groups || (a->G > 0 && !a->prefix_lens)) return KDA_ERR_NULL_ARG;
   if (!al(a->cu_groups, 8) || !al(a->prefix_lens, 4)) return KDA_ERR_ALIGNMENT;
@@ -591,7 +591,7 @@ extern "C" int kda_latent_decode_shared(const kda_latent_decode_shared_args* a, 
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
   p.ws = static_cast<unsigned char*>(workspace);
   p.status = status_slot(s);
-  if (!p.status || !launch_latent_shared(p, a->cu_groups, a->prefix_lens, a->G, s)) return KDA_ERR_LAUNCH;
+  if (!p.status || !launch_latent_shared(p, {a->cu_groups, a->prefix_lens, (int)a->G}, s)) return KDA_ERR_LAUNCH;
   return cudaGetLastError() == cudaSuccess ? KDA_OK : KDA_ERR_LAUNCH;
 }
 

@@ -118,43 +118,58 @@ constexpr int kPfxTileCost = 4, kPfxItemCost = 6;
 
 struct SharedHead {
   int64_t total, size;             // cost of all items, and of a share
-  int32_t active, pad;             // groups that share tiles
 };
-// A group of which at least two requests see at least one tile of the prefix.
-struct SharedGroup {
-  int tiles, source;               // shared tiles; the request whose row of the table names them
-  int row0, rows;                  // first query row (request * R * H + ...), and how many
-};
-static_assert(sizeof(SharedGroup) == 16, "read at once");
 
-struct SharedParams {
-  DecodeParams d;
+// Groups of requests: group g has the requests [cu[g], cu[g + 1]).
+struct SharedGroups {
   const int64_t* cu;               // [G + 1]
   const int32_t* prefix;           // [G]
   int G;
-  int pairs;                       // CTA pairs of the shared pass, a share each
+};
+
+struct SharedParams {
+  DecodeParams d;
+  SharedGroups groups;
+  int pairs;                       // CTA pairs of the shared pass, a share each; 0: there is none
   // workspace
   SharedHead* head;
-  int2* first;                     // [pairs] group (of the active ones) and block of rows at a share's start
-  int32_t* start;                  // [B] first token that a request takes on its own
-  int32_t* of;                     // [B] its active group, or -1
-  SharedGroup* groups;             // [active]
-  int64_t* line;                   // [active] cost of the items before the group's
+  int64_t* line;                   // [G] cost of the items before the group's
   // fp32 rows and their lse (log2): a row's first part at its own place, those that begin
   // within a share behind them
   float *pre_part, *pre_lse;       // [B R H + pairs * kPfxRows]
   float *own_part, *own_lse;       // [B R H + CTAs * N]
-  int4* split;                     // [B][blocks of N rows] first and last share of the own pass
+  int4* split;                     // [B][blocks of N rows] what is left to join: request or -1, first and last share
+                                   // of the own pass, group or -1
   int own_n, own_row_blocks;       // N and the blocks of N rows
 };
 
-// An item's place on the line of costs: the share that holds its tile t.
-__host__ __device__ __forceinline__ int64_t prefix_share(int64_t item, int t, int64_t size) {
+// Tokens of a group's prefix that are shared: whole tiles, of groups of two and more.
+__device__ __forceinline__ int shared_tokens(int64_t first, int64_t end, int64_t prefix, int64_t cap) {
+  const int64_t len = prefix < 0 ? 0 : (prefix > cap ? cap : prefix);
+  return end - first < 2 ? 0 : (int)(len / kPfxTile * kPfxTile);
+}
+// Whether all new tokens of a request see the shared ones.
+__device__ __forceinline__ bool sees_shared(int len, int64_t cap, int R, int tokens) {
+  const int64_t n = len < 0 ? 0 : (len > cap ? cap : len);
+  return n - (R - 1) >= tokens;
+}
+// Cost of an item, and the share that holds tile t of the one that begins at `item` of the line.
+__device__ __forceinline__ int64_t prefix_item_cost(int tokens) {
+  return kPfxItemCost + (int64_t)(tokens / kPfxTile) * kPfxTileCost;
+}
+__device__ __forceinline__ int64_t prefix_share(int64_t item, int t, int64_t size) {
   return (item + kPfxItemCost + (int64_t)t * kPfxTileCost) / size;
+}
+// The parts of a row of a group in the shared pass: how many, and the place of the second.
+__device__ __forceinline__ int prefix_parts(int64_t line, int64_t size, int tokens, int row, int64_t all, int64_t& second) {
+  const int64_t item = line + row / kPfxRows * prefix_item_cost(tokens);
+  const int64_t first = prefix_share(item, 0, size);
+  second = all + (first + 1) * kPfxRows + row % kPfxRows;
+  return (int)(prefix_share(item, tokens / kPfxTile - 1, size) - first) + 1;
 }
 
 size_t shared_workspace_bytes(const DecodeParams& p, int64_t G);
-bool launch_latent_shared(const DecodeParams& p, const int64_t* cu, const int32_t* prefix, int64_t G, cudaStream_t s);
+bool launch_latent_shared(const DecodeParams& p, const SharedGroups& groups, cudaStream_t s);
 // Its parts: the shared pass; a request's own tokens (sizes first, then the launch).
 bool launch_latent_prefix(const SharedParams& p, cudaStream_t s);
 struct OwnLayout {

@@ -79,8 +79,10 @@ struct DecodePlan {
   int whole;           // requests are not split: the share that holds a request's start has all of it
   float* part;         // [row_blocks * shares * 2][N][512] normalised partial rows
   float* part_lse;     // [row_blocks * shares * 2][N] their lse, log2
-  const int32_t* start;  // (own tokens behind shared prefixes) [B] first token of the pass
-  int64_t first_rows;  // (the same) B R H: a row's first part is at its own place of part, the others behind them
+  // own tokens behind shared prefixes: the groups; whether the shared pass runs beside this kernel.  A row's first part is
+  // at its own place of part, the others behind all rows
+  SharedGroups groups;
+  int early;
   int by_request;      // the join works by request (fewer than shares), else by share
   int4* split;         // [requests or shares][row_blocks]: (request or -1, first share, last share)
 };
@@ -98,7 +100,7 @@ struct DecCfg {
   static constexpr int kFull = 0, kEmpty = 2, kQFull = 4, kQEmpty = 6, kSFull = 8, kPReady = 10, kPvDone = 11,
                        kBars = 12;
   static constexpr int kScan = kBar + 8 * kBars;            // int64 [10] sums of the warps, [2] first request and its start
-  static constexpr int kTmem = kScan + 96;
+  static constexpr int kTmem = kScan + 96;                  // and (kOwn) the group of the first request
   static constexpr int kAbort = kTmem + 8;
   static constexpr int kSmem = kAbort + 8;
   static constexpr uint32_t kCols = N == 16 ? 128 : N == 32 ? 256 : 512;  // 6 N rounded up
@@ -107,8 +109,10 @@ struct DecCfg {
 };
 
 // A request's length, clamped to what its table can hold.
+// (kOwn: read past L1, see OwnStarts)
+template <bool kOwn>
 __device__ __forceinline__ int dec_len(const DecodeParams& p, int b) {
-  const int64_t len = p.lens[b], cap = p.max_pages * p.page_size;
+  const int64_t len = kOwn ? __ldcg(p.lens + b) : p.lens[b], cap = p.max_pages * p.page_size;
   return (int)(len < 0 ? 0 : (len > cap ? cap : len));
 }
 __device__ __forceinline__ int dec_tiles(int len) { return len > 0 ? (len - 1) / kDecTile + 1 : 0; }
@@ -119,11 +123,25 @@ __device__ __forceinline__ int64_t div_fast(int64_t a, int64_t b) {
   return ((a | b) >> 32) == 0 ? (int64_t)((uint32_t)a / (uint32_t)b) : a / b;
 }
 
-// The first token that the pass takes: 0, or behind shared prefixes where the request's own begin.
-template <bool kOwn>
-__device__ __forceinline__ int dec_start(const DecodePlan& pl, int b) {
-  return kOwn ? pl.start[b] : 0;
-}
+// Of the own pass: where a request's tokens begin, its group's shared ones being before it.  Requests are visited in
+// order.  (Values that the kernel before this one's predecessor may have written are read past L1: this kernel starts
+// while its predecessor runs.)
+struct OwnStarts {
+  const int64_t* cu;
+  const int32_t* prefix;
+  int G, g, end, tokens;  // the current group, the request behind it, its shared tokens
+  __device__ __forceinline__ void enter(int group, int64_t cap) {
+    g = group;
+    end = g < 0 || g >= G ? INT32_MAX : (int)__ldcg(cu + g + 1);
+    tokens = g < 0 || g >= G ? 0 : shared_tokens(__ldcg(cu + g), end, __ldcg(prefix + g), cap);
+  }
+  // first token of request b (b grows from call to call)
+  __device__ __forceinline__ int from(const DecodeParams& p, int b, int len) {
+    const int64_t cap = p.max_pages * p.page_size;
+    while (b >= end) enter(g + 1, cap);
+    return tokens > 0 && sees_shared(len, cap, p.R, tokens) ? tokens : 0;
+  }
+};
 
 // The pieces of one share [u0, u1) of the line of costs, in order.  Request b
 // takes [pre, pre + cost) of it; its tile k starts at pre + kDecReqCost + k
@@ -131,7 +149,7 @@ __device__ __forceinline__ int dec_start(const DecodePlan& pl, int b) {
 // without tiles, or one that is not split, belongs to the share that holds pre.
 template <bool kOwn>
 struct DecPieces {
-  const int32_t* start;  // (kOwn) first token of each request
+  OwnStarts own;  // (kOwn)
   int unsplit;
   int64_t u0, u1, pre;  // the share; start of request b
   int b;
@@ -144,8 +162,8 @@ struct DecPieces {
   __device__ __forceinline__ bool next(const DecodeParams& p) {
     while (b < p.B && pre < u1) {
       req = b;
-      len = dec_len(p, b);
-      from = kOwn ? start[b] : 0;
+      len = dec_len<kOwn>(p, b);
+      from = kOwn ? own.from(p, b, len) : 0;
       tiles = dec_tiles(len - from);
       t0 = tiles_before(u0);
       t1 = tiles_before(u1);
@@ -188,8 +206,8 @@ struct DecCursor {
   __device__ __forceinline__ bool last() const { return tile + 1 == it.t1; }
 };
 
-// kOwn: only the tokens from pl.start[request] on, and every piece leaves a part:
-// the join of the shared call adds those of the prefixes.
+// kOwn: only the tokens behind the shared ones.  Requests that share none and are in one share write their result; the
+// others leave parts, and the join of the shared call adds those of the prefixes.
 template <int N, bool kOwn>
 __global__ void __launch_bounds__(kDecThreads, 1)
     kda_latent_decode_kernel(const DecodeParams p, const DecodePlan pl, const __grid_constant__ DecodeMaps maps) {
@@ -222,18 +240,50 @@ __global__ void __launch_bounds__(kDecThreads, 1)
     prefetch_map(&maps.q);
     prefetch_map(&maps.cache);
   }
-  // (set up while the kernel before this one ends; nothing it wrote is read until here)
-  asm volatile("griddepcontrol.wait;\n" ::: "memory");
+  // (set up while the kernel before this one ends; nothing it wrote is read until here.  The own pass may run beside
+  // the shared pass, which has waited for the kernels before it and writes nothing that is read here)
+  if (!kOwn || !pl.early) asm volatile("griddepcontrol.wait;\n" ::: "memory");
+  OwnStarts own = {};
+  if constexpr (kOwn) {  // the groups' offsets, checked and in shared memory while each thread looks for its own
+    int* cu = reinterpret_cast<int*>(smem);
+    const int G = pl.groups.G;
+    const int64_t cap = p.max_pages * p.page_size;
+    int bad = 0, far = 0;
+    for (int g = tid; g <= G; g += kDecThreads) {
+      const int64_t c = __ldcg(pl.groups.cu + g), next = g < G ? __ldcg(pl.groups.cu + g + 1) : c;
+      bad |= (g == 0 && c != 0) || (g == G && c != p.B) || c < 0 || c > p.B || next < c;
+      if (g < G && next > c) {
+        const int len = __ldcg(pl.groups.prefix + g);
+        far |= len < 0 || len > cap;
+      }
+      cu[g] = (int)c;
+    }
+    bad = __syncthreads_or(bad);
+    if (far && blockIdx.x == 0) atomicExch(p.status, KDA_ERR_BAD_LENGTHS);
+    if (bad && blockIdx.x == 0 && tid == 0) atomicExch(p.status, KDA_ERR_BAD_SEQLENS);
+    own.cu = pl.groups.cu;
+    own.prefix = pl.groups.prefix;
+    own.G = bad ? 0 : G;
+    const int b = min(p.B - 1, tid * ((p.B + kDecThreads - 1) / kDecThreads));
+    int lo = 0, hi = own.G - 1;  // last group that begins at request b or before
+    while (lo < hi) {
+      const int mid = (lo + hi + 1) >> 1;
+      if (cu[mid] <= b) lo = mid; else hi = mid - 1;
+    }
+    own.enter(bad ? -1 : lo, cap);
+    fence_proxy_async_smem();  // (the place goes to the tensor copies)
+  }
   // each thread sums a run of requests; a scan over threads gives the total
   // (hence the shares' size) and the run that holds this share's first tile
   const int run = (p.B + kDecThreads - 1) / kDecThreads;
   const int b0 = min(p.B, tid * run), b1 = min(p.B, b0 + run);
   int64_t mine = 0;
   bool odd = false;
+  OwnStarts walk = own;
   for (int b = b0; b < b1; ++b) {
-    const int raw = p.lens[b], len = dec_len(p, b);
+    const int raw = __ldcg(p.lens + b), len = dec_len<kOwn>(p, b);
     odd |= raw != len;
-    mine += dec_cost(dec_tiles(len - dec_start<kOwn>(pl, b)));
+    mine += dec_cost(dec_tiles(len - (kOwn ? walk.from(p, b, len) : 0)));
   }
   if (odd && blockIdx.x == 0) atomicExch(p.status, KDA_ERR_BAD_LENGTHS);
   int64_t incl = mine;
@@ -258,10 +308,12 @@ __global__ void __launch_bounds__(kDecThreads, 1)
   if (u0 < u1 && u0 >= before && u0 < before + mine) {
     int64_t pre = before;
     for (int b = b0; b < b1; ++b) {
-      const int64_t t = dec_cost(dec_tiles(dec_len(p, b) - dec_start<kOwn>(pl, b)));
+      const int len = dec_len<kOwn>(p, b);
+      const int64_t t = dec_cost(dec_tiles(len - (kOwn ? own.from(p, b, len) : 0)));
       if (u0 < pre + t) {
         s_scan[10] = b;
         s_scan[11] = pre;
+        if (kOwn) *reinterpret_cast<int*>(smem + C::kTmem + 4) = own.g;
         break;
       }
       pre += t;
@@ -269,7 +321,8 @@ __global__ void __launch_bounds__(kDecThreads, 1)
   }
   __syncthreads();
   DecPieces<kOwn> pieces;
-  pieces.start = pl.start;
+  pieces.own = own;
+  if (kOwn && u0 < u1) pieces.own.enter(*reinterpret_cast<int*>(smem + C::kTmem + 4), p.max_pages * p.page_size);
   pieces.unsplit = pl.whole;
   pieces.u0 = u0;
   pieces.u1 = u1;
@@ -302,7 +355,8 @@ __global__ void __launch_bounds__(kDecThreads, 1)
       int page = 0, off = 0;
       if (lane < segs) {
         const uint32_t j = (uint32_t)(c.it.from + c.tile * kDecTile + lane * box), in_table = j / (uint32_t)p.page_size;
-        page = p.table[c.it.req * p.table_stride + in_table];
+        const int32_t* at = p.table + c.it.req * p.table_stride + in_table;
+        page = kOwn ? __ldcg(at) : *at;
         off = (int)(j - in_table * (uint32_t)p.page_size);
         if (page < 0 || page >= p.num_pages) {
           atomicExch(p.status, KDA_ERR_BAD_PAGE);
@@ -434,7 +488,12 @@ __global__ void __launch_bounds__(kDecThreads, 1)
     int it = 0;
     while (pieces.next(p)) {
       const int nt = pieces.count();
-      const bool whole = !kOwn && pieces.whole();
+      const bool whole = pieces.whole() && (!kOwn || pieces.from == 0);
+      if (kOwn && tid == 0 && pieces.t0 == 0)  // what is left to the join
+        pl.split[pieces.req * pl.row_blocks + rblk] =
+            whole ? make_int4(-1, 0, 0, 0)
+                  : make_int4(pieces.req, share, pieces.tiles > 0 ? (int)div_fast(pieces.pre - kDecTileCost, size) : share,
+                              pieces.from > 0 ? pieces.own.g : -1);
       float m[kM], l[kM];
 #pragma unroll
       for (int i = 0; i < kM; ++i) {
@@ -552,7 +611,7 @@ __global__ void __launch_bounds__(kDecThreads, 1)
       named_bar(bar_id, 128);
       // first row of the part: two blocks of N rows a CTA, or (kOwn) the rows' own place or this CTA's behind them
       const int64_t part_row = !kOwn ? (int64_t)(2 * blockIdx.x + (pieces.t0 > 0 ? 0 : 1)) * N
-                               : pieces.t0 > 0 ? pl.first_rows + (int64_t)blockIdx.x * N
+                               : pieces.t0 > 0 ? (int64_t)p.B * rows + (int64_t)blockIdx.x * N
                                                : (int64_t)pieces.req * rows + row0;
       if (w4 == 0 && lane < 4) {
 #pragma unroll
@@ -616,7 +675,7 @@ __global__ void __launch_bounds__(kDecThreads, 1)
     }
     tc_fence_before();
   }
-  if (tid == 0 && (kOwn || !pl.whole)) {
+  if (!kOwn && tid == 0 && !pl.whole) {
     // what the join kernel has to do, by request or by the share a request starts in
     if (!pl.by_request) pl.split[blockIdx.x] = make_int4(-1, 0, 0, 0);
     DecPieces<kOwn> each = pieces;
@@ -625,9 +684,8 @@ __global__ void __launch_bounds__(kDecThreads, 1)
     while (each.next(p)) {
       if (each.t0 > 0) continue;
       // (the request's last tile starts kDecTileCost before the next request)
-      const int4 info = kOwn && each.whole() ? make_int4(each.req, share, share, 0)
-                        : each.whole()       ? make_int4(-1, 0, 0, 0)
-                                             : make_int4(each.req, share, (int)div_fast(each.pre - kDecTileCost, size), 0);
+      const int4 info = each.whole() ? make_int4(-1, 0, 0, 0)
+                                     : make_int4(each.req, share, (int)div_fast(each.pre - kDecTileCost, size), 0);
       if (pl.by_request) pl.split[each.req * pl.row_blocks + rblk] = info;
       else if (!each.whole()) pl.split[blockIdx.x] = info;
     }
@@ -637,6 +695,8 @@ __global__ void __launch_bounds__(kDecThreads, 1)
   tc_fence_after();
   if (warp == kDecMmaWarp)
     asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;\n" ::"r"(tmem), "r"(C::kCols));
+  // the join waits for this kernel alone, and reads what the shared pass wrote
+  if (kOwn) asm volatile("griddepcontrol.wait;\n" ::: "memory");
 }
 
 // Joins the parts of a request that several shares hold: out = sum_k w_k o_k,
@@ -776,17 +836,16 @@ DecLayout dec_layout(const DecodeParams& p) {
 template <int N, bool kOwn>
 bool launch_dec(const DecodeParams& p, const DecLayout& d, const DecodeMaps& maps, cudaStream_t s) {
   const unsigned ctas = (unsigned)(d.plan.row_blocks * d.plan.shares);
+  constexpr int smem = DecCfg<N>::kSmem;
   static std::once_flag once[64];
   static cudaError_t rc[64];
   int dev = 0;
   if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return false;
   std::call_once(once[dev], [&] {
-    rc[dev] = cudaFuncSetAttribute(kda_latent_decode_kernel<N, kOwn>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                   DecCfg<N>::kSmem);
+    rc[dev] = cudaFuncSetAttribute(kda_latent_decode_kernel<N, kOwn>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
   });
   if (rc[dev] != cudaSuccess) return false;
-  if (!launch_overlapped(kda_latent_decode_kernel<N, kOwn>, dim3(ctas), kDecThreads, DecCfg<N>::kSmem, s, 1, p, d.plan,
-                         maps))
+  if (!launch_overlapped(kda_latent_decode_kernel<N, kOwn>, dim3(ctas), kDecThreads, smem, s, 1, p, d.plan, maps))
     return false;
   if (kOwn || d.plan.whole) return true;  // nothing to join
   // a row a CTA where a request is in more than four parts on average, else a row a warp
@@ -849,9 +908,9 @@ bool launch_latent_own(const SharedParams& sp, cudaStream_t s) {
   d.plan.part = sp.own_part;
   d.plan.part_lse = sp.own_lse;
   d.plan.split = sp.split;
-  d.plan.start = sp.start;
-  d.plan.first_rows = (int64_t)p.B * p.R * p.H;
   d.plan.by_request = 1;
+  d.plan.groups = sp.groups;
+  d.plan.early = sp.pairs > 0;
   DecodeMaps maps;
   if (!dec_maps(p, d, maps)) return false;
   switch (d.n) {

@@ -65,42 +65,48 @@ struct PrefixMaps {
 
 // The pieces with tiles of one share [u0, u1) of the line of costs, in order.
 struct PrefixPieces {
-  const SharedGroup* groups;
-  int active, k, block;  // next item
-  int64_t u0, u1, pre;   // the share; start of the next item
-  // the current piece: its group, first row within it, tiles [t0, t1), whether it is its item's first on the line
-  SharedGroup g;
-  int row, t0, t1, leads;
-  __device__ __forceinline__ int before(int64_t u, int64_t item) const {
-    const int64_t d = u - item - kPfxItemCost;
-    return d <= 0 ? 0 : (int)min((int64_t)g.tiles, (d + kPfxTileCost - 1) / kPfxTileCost);
-  }
+  SharedGroups groups;
+  int64_t cap, u0, u1, pre;  // tokens that a table can hold; the share; start of the next item
+  int g, block, row_heads;   // next item; R H
+  // the current piece: its group, the group's first query row and their number, the piece's first row within it,
+  // tiles [t0, t1), whether it is its item's first on the line
+  int of, row0, rows, row, t0, t1, leads;
   // Called by whole warps; the values are broadcast, so that the compiler knows them as uniform.
   __device__ __forceinline__ bool next() {
     bool more = false;
-    while (!more && k < active && pre < u1) {
-      const int4 x = *reinterpret_cast<const int4*>(groups + k);
-      g = {x.x, x.y, x.z, x.w};
+    while (!more && g < groups.G && pre < u1) {
+      const int64_t first = groups.cu[g], end = groups.cu[g + 1];
+      const int tokens = shared_tokens(first, end, groups.prefix[g], cap);
+      of = g;
+      row0 = (int)first * row_heads;
+      rows = tokens > 0 ? (int)(end - first) * row_heads : 0;
       row = block * kPfxRows;
-      const int a = before(u0, pre), b = before(u1, pre);
+      ++block;
+      if (row + kPfxRows >= rows) {
+        block = 0;
+        ++g;
+      }
+      if (rows == 0) continue;
+      const int tiles = tokens / kPfxTile;
+      auto before = [&](int64_t u) {
+        const int64_t d = u - pre - kPfxItemCost;
+        return d <= 0 ? 0 : (int)min((int64_t)tiles, (d + kPfxTileCost - 1) / kPfxTileCost);
+      };
+      const int a = before(u0), b = before(u1);
       leads = a == 0;
       // An item lies on the line from its last tile to its first: a share that ends one item and begins another
       // takes the one's first tiles, then the other's last, and so do the others at the same time (read from
       // DRAM for 48 requests of three tokens behind two prefixes of 49152: 254 MB, the other way round 1010).
-      t0 = g.tiles - b;
-      t1 = g.tiles - a;
-      pre += kPfxItemCost + (int64_t)g.tiles * kPfxTileCost;
-      if (row + kPfxRows >= g.rows) {
-        block = 0;
-        ++k;
-      } else {
-        ++block;
-      }
+      t0 = tiles - b;
+      t1 = tiles - a;
+      pre += prefix_item_cost(tokens);
       more = t0 < t1;
     }
     auto same = [](int v) { return __shfl_sync(0xffffffffu, v, 0); };
     if (!same(more)) return false;
-    g = {same(g.tiles), same(g.source), same(g.row0), same(g.rows)};
+    of = same(of);
+    row0 = same(row0);
+    rows = same(rows);
     row = same(row);
     t0 = same(t0);
     t1 = same(t1);
@@ -142,7 +148,7 @@ __global__ void __launch_bounds__(kPfxThreads, 1)
     asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;\n" ::"r"(sb + kPfxTmem), "r"(512u));
     asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;\n");
   }
-  // (set up while the kernel before this one ends: it makes the list of groups)
+  // (set up while the kernel before this one ends)
   asm volatile("griddepcontrol.wait;\n" ::: "memory");
   tc_fence_before();
   __syncthreads();
@@ -151,22 +157,67 @@ __global__ void __launch_bounds__(kPfxThreads, 1)
   const uint32_t tmem = *reinterpret_cast<volatile uint32_t*>(smem + kPfxTmem);
   asm volatile("griddepcontrol.launch_dependents;\n" ::: "memory");
 
+  // ---- this pair's share of the line of items: each thread sums a run of groups ----
   PrefixPieces it;
+  it.groups = sp.groups;
+  it.cap = p.max_pages * p.page_size;
+  it.row_heads = p.R * p.H;
   {
-    const SharedHead h = *sp.head;
-    it.groups = sp.groups;
-    it.active = h.active;
-    it.u0 = min(h.total, share * h.size);
-    it.u1 = min(h.total, it.u0 + h.size);
-    it.k = h.active;
-    it.block = 0;
-    it.pre = 0;
-    if (it.u0 < it.u1) {
-      const int2 at = sp.first[share];
-      it.k = at.x;
-      it.block = at.y;
-      it.pre = sp.line[at.x] + at.y * (kPfxItemCost + (int64_t)sp.groups[at.x].tiles * kPfxTileCost);
+    int64_t* scan = reinterpret_cast<int64_t*>(smem + kPfxMax);  // sums of the warps; then the share's first item
+    const int G = sp.groups.G, run = (G + kPfxThreads - 1) / kPfxThreads;
+    const int g0 = min(G, tid * run), g1 = min(G, g0 + run);
+    int bad = 0;
+    int64_t mine = 0;
+    auto cost_of = [&](int g) {
+      const int64_t first = sp.groups.cu[g], end = sp.groups.cu[g + 1];
+      bad |= first < 0 || end < first || end > p.B || (g == 0 && first != 0) || (g == G - 1 && end != p.B);
+      const int tokens = shared_tokens(first, end, sp.groups.prefix[g], it.cap);
+      if (tokens == 0 || bad) return (int64_t)0;
+      return ((end - first) * it.row_heads + kPfxRows - 1) / kPfxRows * prefix_item_cost(tokens);
+    };
+    for (int g = g0; g < g1; ++g) mine += cost_of(g);
+    int64_t before = mine;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int64_t y = __shfl_up_sync(0xffffffffu, before, o);
+      if (lane >= o) before += y;
     }
+    if (lane == 31) scan[warp] = before;
+    before -= mine;
+    const bool refused = __syncthreads_or(bad);  // (the requests' own pass reports it)
+    int64_t total = 0;
+#pragma unroll
+    for (int w = 0; w < kPfxThreads / 32; ++w) {
+      if (w < warp) before += scan[w];
+      total += scan[w];
+    }
+    if (refused) total = 0;
+    const int64_t size = max((int64_t)kPfxTileCost, (total + sp.pairs - 1) / sp.pairs);  // at least a tile
+    it.u0 = min(total, share * size);
+    it.u1 = min(total, it.u0 + size);
+    const bool writes = blockIdx.x == 0;
+    if (writes && tid == 0) *sp.head = {total, size};
+    if (writes || (it.u0 >= before && it.u0 < before + mine)) {
+      int64_t pre = before;
+      for (int g = g0; g < g1; ++g) {
+        const int64_t cost = cost_of(g);
+        if (writes) sp.line[g] = pre;
+        if (it.u0 >= pre && it.u0 < pre + cost) {
+          const int64_t item = prefix_item_cost(shared_tokens(sp.groups.cu[g], sp.groups.cu[g + 1], sp.groups.prefix[g], it.cap));
+          const int64_t block = (it.u0 - pre) / item;
+          scan[12] = g;
+          scan[13] = block;
+          scan[14] = pre + block * item;
+        }
+        pre += cost;
+      }
+    }
+    __syncthreads();
+    const bool any = it.u0 < it.u1;
+    it.g = any ? (int)scan[12] : G;
+    it.block = any ? (int)scan[13] : 0;
+    it.pre = any ? scan[14] : 0;
+    __syncthreads();  // the place goes to the softmax
   }
   auto wait = [&](uint32_t b, uint32_t parity) {
     if (mbar_try_wait(b, parity) || *s_abort) return;
@@ -186,12 +237,24 @@ __global__ void __launch_bounds__(kPfxThreads, 1)
     while (clock64() - t0 < (1LL << 22)) {
     }
   };
+  // The request of a piece's group whose row of the table is read: the first that sees the shared tokens; -1: none
+  // does, and what is read does not count.
+  auto source_of = [&]() {
+    const int64_t first = sp.groups.cu[it.of], end = sp.groups.cu[it.of + 1];
+    const int tokens = shared_tokens(first, end, sp.groups.prefix[it.of], it.cap);
+    for (int64_t b = first; b < end; b += 32) {
+      const uint32_t in =
+          __ballot_sync(0xffffffffu, b + lane < end && sees_shared(p.lens[min(b + lane, end - 1)], it.cap, p.R, tokens));
+      if (in) return (int)b + __ffs(in) - 1;
+    }
+    return -1;
+  };
   // Page and 8-token group of the run of `box` tokens that starts at a token of the prefix.
   auto place = [&](int source, int64_t token, int& group) {
     const uint32_t in_table = (uint32_t)token / (uint32_t)p.page_size;
-    int page = p.table[source * p.table_stride + in_table];
+    int page = source < 0 ? (int)p.num_pages : p.table[source * p.table_stride + in_table];
     group = (int)((uint32_t)token - in_table * (uint32_t)p.page_size) >> 3;
-    if (page < 0 || page >= p.num_pages) {
+    if (source >= 0 && (page < 0 || page >= p.num_pages)) {
       atomicExch(p.status, KDA_ERR_BAD_PAGE);
       page = (int)p.num_pages;  // past the map: reads as zeros
     }
@@ -204,16 +267,17 @@ __global__ void __launch_bounds__(kPfxThreads, 1)
     int n = 0, q = 0;
     bool gone = false;
     while (!gone && it.next()) {
+      const int source = source_of();
       for (int t = it.t0; t < it.t1 && !gone; ++t, ++n) {
         int page = 0, group = 0;
-        if (lane < runs) page = place(it.g.source, (int64_t)t * kPfxTile + rank * 64 + lane * box, group);
+        if (lane < runs) page = place(source, (int64_t)t * kPfxTile + rank * 64 + lane * box, group);
         if (t == it.t0) {
           if (q > 0) wait(bar(kEQ), (uint32_t)((q - 1) & 1));
           if ((gone = stop())) break;
           if (lane == 0) {
             const uint32_t full = lead(kFQ);
             mbar_expect_tx_cluster(full, kPfxQBytes);
-            tma_pair_3d(sb + kPfxQ, &maps.q, 0, it.g.row0 + it.row + rank * 64, 0, full);
+            tma_pair_3d(sb + kPfxQ, &maps.q, 0, it.row0 + it.row + rank * 64, 0, full);
           }
           ++q;
         }
@@ -235,9 +299,10 @@ __global__ void __launch_bounds__(kPfxThreads, 1)
     int n = 0;
     bool gone = false;
     while (!gone && it.next()) {
+      const int source = source_of();
       for (int t = it.t0; t < it.t1 && !gone; ++t, ++n) {
         int page = 0, group = 0;
-        if (lane < 2 * runs) page = place(it.g.source, (int64_t)t * kPfxTile + lane * box, group);
+        if (lane < 2 * runs) page = place(source, (int64_t)t * kPfxTile + lane * box, group);
         for (int h = 0; h < 2; ++h) {
           if (n > 0) wait(bar(kEValues + h), (uint32_t)((n - 1) & 1));
           if ((gone = stop())) break;
@@ -394,9 +459,9 @@ __global__ void __launch_bounds__(kPfxThreads, 1)
       const float sum = (wmax[r] + wmax[64 + r]) + (wmax[128 + r] + wmax[192 + r]);
       const float inv = sum > 0.f ? 1.0f / sum : (sum == 0.f ? 0.f : sum);
       const int row = it.row + 64 * rank + r;  // of the group
-      const bool there = row < it.g.rows;
+      const bool there = row < it.rows;
       // a row's first part at its own place, a later one at this share's
-      const int64_t at = it.leads ? (int64_t)it.g.row0 + row
+      const int64_t at = it.leads ? (int64_t)it.row0 + row
                                   : (int64_t)p.B * p.R * p.H + (int64_t)share * kPfxRows + 64 * rank + r;
       if (quarter == 0 && there) sp.pre_lse[at] = sum == 0.f ? -INFINITY : m + __log2f(sum);
       wait(bar(kFO), (uint32_t)((n - 1) & 1));
@@ -407,7 +472,7 @@ __global__ void __launch_bounds__(kPfxThreads, 1)
       // 128 KB took 12000 cycles.
       const uint32_t turn = sb + kPfxP + warp * 2048;
       const int64_t first = at - r + 32 * (w4 & 1);  // this warp's first row; all of one part are side by side
-      const int rows_there = it.g.rows - (it.row + 64 * rank + 32 * (w4 & 1));
+      const int rows_there = it.rows - (it.row + 64 * rank + 32 * (w4 & 1));
       float* dst = sp.pre_part + first * kLat + 256 * side + 128 * right;
 #pragma unroll 1
       for (int c = 0; c < 128; c += 16) {
