@@ -280,6 +280,14 @@ int check_shared(const kda_latent_decode_shared_args* a) {
   return KDA_OK;
 }
 
+// Whether a call's tables hold so little that it is taken as kda_latent_decode.  Device times alone and shared, us: 8
+// requests behind 1024 tokens, 16 heads 12.5 and 18.8; 32 behind 4096, 32 heads 33.0 and 31.3; 128 behind 1024,
+// 16 heads 29.6 and 29.8, behind 2048 46.8 and 32.5; 128 behind 1024, 128 heads 72.4 and 78.6, behind 2048 114 and 96.
+bool shares_little(const kda_latent_decode_args& a) {
+  const int64_t rows = a.B * a.R * a.H, blocks = (a.R * a.H + 63) / 64;  // (at most 2^20 * 2^31 * 2^10)
+  return a.B * (a.max_pages * a.cache.page_size) * blocks <= KDA_LATENT_SHARED_TOKENS + 16 * rows;
+}
+
 DecodeParams decode_params(const kda_latent_decode_args* a) {
   DecodeParams p;
   p.q = static_cast<const uint16_t*>(a->q);
@@ -578,14 +586,15 @@ extern "C" int kda_latent_decode(const kda_latent_decode_args* a, void* workspac
 
 extern "C" size_t kda_latent_decode_shared_workspace_bytes(const kda_latent_decode_shared_args* a) {
   if (check_shared(a) != KDA_OK || a->decode.B * a->decode.R * a->decode.H == 0) return 0;
-  return shared_workspace_bytes(decode_params(&a->decode), a->G);
+  const DecodeParams p = decode_params(&a->decode);
+  return shares_little(a->decode) ? decode_workspace_bytes(p) : shared_workspace_bytes(p, a->G);
 }
 
 extern "C" int kda_latent_decode_shared(const kda_latent_decode_shared_args* a, void* workspace, size_t workspace_bytes,
                                         void* stream) {
   const int rc = check_shared(a);
   if (rc != KDA_OK) return rc;
-  if (a->decode.B * a->decode.R * a->decode.H == 0) return KDA_OK;
+  if (shares_little(a->decode)) return kda_latent_decode(&a->decode, workspace, workspace_bytes, stream);
   DecodeParams p = decode_params(&a->decode);
   if (!workspace || !al(workspace, 256) || workspace_bytes < shared_workspace_bytes(p, a->G)) return KDA_ERR_WORKSPACE;
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);

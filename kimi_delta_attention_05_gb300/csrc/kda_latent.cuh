@@ -153,12 +153,16 @@ __device__ __forceinline__ bool sees_shared(int len, int64_t cap, int R, int tok
   const int64_t n = len < 0 ? 0 : (len > cap ? cap : len);
   return n - (R - 1) >= tokens;
 }
+// a / b of numbers that are not negative, in 32 bits where they fit (a 64-bit division takes some 100 instructions)
+__device__ __forceinline__ int64_t div_costs(int64_t a, int64_t b) {
+  return ((a | b) >> 32) == 0 ? (int64_t)((uint32_t)a / (uint32_t)b) : a / b;
+}
 // Cost of an item, and the share that holds tile t of the one that begins at `item` of the line.
 __device__ __forceinline__ int64_t prefix_item_cost(int tokens) {
   return kPfxItemCost + (int64_t)(tokens / kPfxTile) * kPfxTileCost;
 }
 __device__ __forceinline__ int64_t prefix_share(int64_t item, int t, int64_t size) {
-  return (item + kPfxItemCost + (int64_t)t * kPfxTileCost) / size;
+  return div_costs(item + kPfxItemCost + (int64_t)t * kPfxTileCost, size);
 }
 // The parts of a row of a group in the shared pass: how many, and the place of the second.
 __device__ __forceinline__ int prefix_parts(int64_t line, int64_t size, int tokens, int row, int64_t all, int64_t& second) {

@@ -57,6 +57,7 @@ constexpr int kPfxSmem = kPfxAbort + 8;
 static_assert(kPfxK % 1024 == 0 && kPfxV % 1024 == 0 && kPfxP % 1024 == 0 && kPfxKeyPart % 1024 == 0,
               "operand images need 1024-byte alignment");
 static_assert(kPfxSmem <= 232448, "exceeds the opt-in shared memory of one CTA");
+constexpr int kPfxLeast = 2 * kPfxTileCost;  // least cost of a share: two tiles
 constexpr float kPfxSlack = 8.0f;  // log2 growth of a maximum that is let pass
 
 struct PrefixMaps {
@@ -192,7 +193,7 @@ __global__ void __launch_bounds__(kPfxThreads, 1)
       total += scan[w];
     }
     if (refused) total = 0;
-    const int64_t size = max((int64_t)kPfxTileCost, (total + sp.pairs - 1) / sp.pairs);  // at least a tile
+    const int64_t size = max((int64_t)kPfxLeast, div_costs(total + sp.pairs - 1, sp.pairs));
     it.u0 = min(total, share * size);
     it.u1 = min(total, it.u0 + size);
     const bool writes = blockIdx.x == 0;
@@ -204,7 +205,7 @@ __global__ void __launch_bounds__(kPfxThreads, 1)
         if (writes) sp.line[g] = pre;
         if (it.u0 >= pre && it.u0 < pre + cost) {
           const int64_t item = prefix_item_cost(shared_tokens(sp.groups.cu[g], sp.groups.cu[g + 1], sp.groups.prefix[g], it.cap));
-          const int64_t block = (it.u0 - pre) / item;
+          const int64_t block = div_costs(it.u0 - pre, item);
           scan[12] = g;
           scan[13] = block;
           scan[14] = pre + block * item;

@@ -58,7 +58,7 @@ __global__ void __launch_bounds__(256) kda_latent_shared_join_kernel(const Share
     float acc[16], sum = 0.f;
 #pragma unroll
     for (int i = 0; i < 16; ++i) acc[i] = 0.f;
-#pragma unroll 2
+#pragma unroll 4
     for (int k = 0; k < parts; ++k) {
       const int64_t at_k = place(k);
       const float w = ex2((k < pre ? p.pre_lse : p.own_lse)[at_k] - base);

@@ -330,7 +330,8 @@ def latent_decode_shared(q, cache, block_table, seq_lens, cu_groups, prefix_lens
     ``cu_groups[g] .. cu_groups[g + 1] - 1``), prefix_lens int32 [G]: the tokens at the
     start of a group's requests whose cached rows are the same.  Every row of
     block_table names the request's whole context, as :func:`latent_fork` leaves it.
-    Offsets or prefixes that do not fit show in :func:`get_status` (14 / 18).
+    Offsets or prefixes that do not fit show in :func:`get_status` (14 / 18); calls
+    whose tables hold little are taken as :func:`latent_decode`, without a look at them.
     ``workspace``: an optional uint8 tensor of at least
     :func:`latent_decode_shared_workspace_bytes` bytes."""
     dev, out, fields = _decode_fields(q, cache, block_table, seq_lens, scale, out, lse, stream)

@@ -34,7 +34,12 @@ def _rand(gen, *shape, std=1.0):
     return (torch.randn(shape, generator=gen) * std).to(torch.bfloat16)
 
 
-def _batch(members, prefix, tails, page, R, H, seed=0, std=1.0, spare=2, rows=None):
+def _wide(B, page, R, H):
+    """Pages of a table that the call does not take as latent_decode (KDA_LATENT_SHARED_TOKENS)."""
+    return (131072 + 16 * B * R * H) // max(1, B * page * (-(-R * H // 64))) + 1
+
+
+def _batch(members, prefix, tails, page, R, H, seed=0, std=1.0, spare=2, rows=None, wide=True):
     """q, cache, table, lens, cu, prefix as fork leaves them: whole pages of a prefix in one place, the rest of
     it copied; rows behind the lengths NaN, pages of nobody NaN, entries behind the last page not to be followed."""
     gen = torch.Generator().manual_seed(seed)
@@ -45,6 +50,8 @@ def _batch(members, prefix, tails, page, R, H, seed=0, std=1.0, spare=2, rows=No
     ids = torch.randperm(need + spare, generator=gen).tolist()
     cache = torch.full((need + spare, page, 576), NAN, dtype=torch.bfloat16)
     width = max([-(-n // page) for n in lens] + [1]) + 1
+    if wide:
+        width = max(width, _wide(len(lens), page, R, H))
     table = torch.full((len(lens), width), 1 << 30, dtype=torch.int32)
     at, start = 0, []
     first = [rows(p) if rows else _rand(gen, p, 576) for p in prefix]
@@ -115,6 +122,27 @@ def _run(batch, status=0, scale=SCALE, **kw):
 @pytest.mark.parametrize("prefix", [0, 1, 64, 127, 128, 129, 255, 256, 383, 640, 1000])
 def test_prefix_lengths(prefix, page):
     _run(_batch([5], [prefix], [1, 64, 7, 200, 65], page, 1, 16, seed=prefix + page))
+
+
+def test_tables_that_hold_little():
+    """Taken as latent_decode, whose results they are; groups that do not fit do not show."""
+    for H in (16, 128):
+        batch = _batch([3, 2], [300, 129], [5, 64, 1, 2, 70], 16, 1, H, seed=H, wide=False)
+        q, cache, table, lens, cu, prefix = batch
+        out, lse = _run(batch)
+        alone = torch.empty_like(lse)
+        assert torch.equal(out, M.latent_decode(q, cache, table, lens, SCALE, lse=alone)) and torch.equal(lse, alone)
+        batch[4] = torch.tensor([0, 9, 2], device="cuda")
+        assert torch.equal(_run(batch)[0], out)
+
+
+@pytest.mark.parametrize("more", [-1, 0, 1])
+def test_tables_about_as_wide_as_the_limit(more):
+    batch = _batch([4, 4], [1000, 600], [20] * 8, 16, 1, 40, seed=30 + more)
+    q, cache, table, lens, cu, prefix = batch
+    width = (131072 + 16 * 8 * 40) // (8 * 16) + more
+    batch[2] = torch.cat([table, torch.full((8, 9), 1 << 30, **I32)], 1)[:, :width]
+    _run(batch)
 
 
 @pytest.mark.parametrize("members", [[1], [2], [1, 1, 1], [1, 5, 0, 3], [0, 0, 4], [9, 0], [2, 17, 1, 30]])
@@ -214,10 +242,17 @@ def test_pages_outside_the_cache_read_as_zeros():
 
 
 def test_lengths_past_the_table():
-    batch = _batch([2, 2], [256, 128], [0] * 4, 64, 1, 16, seed=12)
-    batch[2] = batch[2][:, :4].contiguous()  # room for 256 tokens
-    batch[3][0], batch[3][3] = 500, -4
-    _run(batch, status=18)
+    """Taken as the table's; with R = 3 its last tokens are then not seen by the first of the new ones."""
+    gen = torch.Generator().manual_seed(12)
+    page, width, R = 64, 600, 3
+    cache = _rand(gen, 40, page, 576).cuda()
+    table = torch.randint(0, 40, (4, width), generator=gen, dtype=torch.int32).cuda()
+    table[1], table[2] = table[0], table[0]
+    q = _rand(gen, 4, R, 16, 576).cuda()
+    cap = page * width
+    lens = torch.tensor([10 ** 6, cap, cap + 1, -4], **I32)
+    for prefix in (cap, cap - 2, cap - 128, 256):
+        _run([q, cache, table, lens, torch.tensor([0, 3, 4], device="cuda"), torch.tensor([prefix, 64], **I32)], status=18)
 
 
 def test_no_requests_and_refusals():
@@ -237,9 +272,10 @@ def test_no_requests_and_refusals():
         M.latent_decode_shared(q, cache, table, lens, cu, prefix[0], SCALE)
     with pytest.raises(KdaError):
         M.latent_decode_shared(q, cache, table, lens, cu, prefix, -1.0)
-    with pytest.raises(KdaError):
-        M.latent_decode_shared(q, cache, table, lens, cu, prefix, SCALE,
-                               workspace=torch.empty(0, dtype=torch.uint8, device="cuda"))
+    need = M.latent_decode_shared_workspace_bytes(*q.shape[:3], 1, cache, table)
+    for ws in (torch.empty(0, dtype=torch.uint8, device="cuda"), torch.empty(need - 1, dtype=torch.uint8, device="cuda")):
+        with pytest.raises(KdaError):
+            M.latent_decode_shared(q, cache, table, lens, cu, prefix, SCALE, workspace=ws)
     assert get_status() == 0
 
 
@@ -247,9 +283,9 @@ def test_strided_cache_and_table():
     batch = _batch([3, 2], [500, 300], [30] * 5, 16, 1, 32, seed=14)
     big = torch.full((batch[1].shape[0], 3, 16, 640), NAN, dtype=torch.bfloat16, device="cuda")
     big[:, 1, :, :576] = batch[1]
-    wide = torch.full((5, batch[2].shape[1] + 5), 1 << 30, **I32)
-    wide[:, :batch[2].shape[1]] = batch[2]
-    batch[1], batch[2] = big[:, 1, :, :576], wide[:, :batch[2].shape[1]]
+    rows = torch.full((5, batch[2].shape[1] + 5), 1 << 30, **I32)
+    rows[:, :batch[2].shape[1]] = batch[2]
+    batch[1], batch[2] = big[:, 1, :, :576], rows[:, :batch[2].shape[1]]
     _run(batch)
 
 
@@ -344,7 +380,7 @@ def test_samples_of_prompts_from_prompt_to_release():
     lens0 = [333, 64, 100]
     B, pages = prompts * (each + 1), 200
     cache = torch.full((pages, page, 576), NAN, dtype=torch.bfloat16, device="cuda")
-    table = torch.full((B, 40), 1 << 30, **I32)
+    table = torch.full((B, _wide(B, page, 1, heads)), 1 << 30, **I32)
     shares, free = torch.zeros(pages, **I32), torch.randperm(pages, generator=gen).int().cuda()
     first = [p * (each + 1) for p in range(prompts)]  # a prompt's row, then its samples
     lens = torch.zeros(B, **I32)
