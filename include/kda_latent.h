@@ -334,9 +334,9 @@ int kda_latent_release(const kda_latent_release_args *args, void *stream);
  * A length that does not fit sets KDA_ERR_BAD_LENGTHS and nothing moves: tables and
  * counts come out as they are, the map is the identity, pages_used num_pages.  A
  * page id outside the cache sets KDA_ERR_BAD_PAGE and comes out as it is.
- * workspace: kda_latent_compact_workspace_bytes bytes, aligned to 256; garbage
- * afterwards, needs no initialisation.
+ * num_pages is at most KDA_LATENT_COMPACT_PAGES.
  */
+#define KDA_LATENT_COMPACT_PAGES 12582912
 typedef struct kda_latent_compact_args {
   const int32_t *cached_lens, *block_table;
   int64_t table_stride;
@@ -348,8 +348,7 @@ typedef struct kda_latent_compact_args {
   int64_t B, max_pages;
 } kda_latent_compact_args;
 
-size_t kda_latent_compact_workspace_bytes(const kda_latent_compact_args *args);
-int kda_latent_compact(const kda_latent_compact_args *args, void *workspace, size_t workspace_bytes, void *stream);
+int kda_latent_compact(const kda_latent_compact_args *args, void *stream);
 
 /*
  * Page src_pages[i] of one cache into page dst_pages[i] of another (or of the same

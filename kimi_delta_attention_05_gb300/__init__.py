@@ -10,8 +10,7 @@ from .kda import (kda_bwd, kda_fwd, kda_fwd_host, kda_fwd_recurrent, get_status,
 from .latent import (latent_append, latent_decode, latent_decode_shared,  # noqa: F401
                      latent_decode_shared_workspace_bytes, latent_decode_workspace_bytes, latent_plan, latent_prefill,
                      latent_prefill_workspace_bytes)
-from .latent_pages import (latent_compact, latent_compact_workspace_bytes, latent_copy, latent_fork,  # noqa: F401
-                           latent_release)
+from .latent_pages import latent_compact, latent_copy, latent_fork, latent_release  # noqa: F401
 from . import workloads  # noqa: F401
 
 __version__ = "0.1.0"

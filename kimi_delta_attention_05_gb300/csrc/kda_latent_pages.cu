@@ -388,9 +388,10 @@ __global__ void __launch_bounds__(kPageThreads) kda_latent_release_kernel(const 
 //
 // U pages are held.  Those at U and behind move to the places below U that nobody
 // holds; there are as many of the one as of the other, and both go in ascending
-// order.  A cluster marks the held pages, counts and lists them (its barriers
-// between the steps), and a second kernel moves the rows and renames the tables'
-// entries: no page is both read and written.
+// order.  A cluster of eight CTAs keeps a bit a page in distributed shared memory,
+// an eighth each: marks, counts and places need its barriers and no other memory.
+// A second kernel moves the rows and renames the tables' entries: no page is both
+// read and written.
 struct CompactParams {
   const int32_t *cached, *table;
   int32_t* table_out;
@@ -398,21 +399,20 @@ struct CompactParams {
   const int32_t* shares;
   int32_t *shares_out, *page_map, *used;
   PageCache cache;
-  uint8_t* held;               // [num_pages] whether a row of the table holds the page
-  int32_t *moves, *to, *from;  // their number (-1: refused), the places and the pages that move there
+  int words;  // of 32 pages, of a CTA
   int B, page;
   int* status;
 };
 
 __global__ void __launch_bounds__(kPageThreads) kda_latent_compact_kernel(const CompactParams p) {
+  extern __shared__ uint32_t held_words[];  // [words] a bit a page of this CTA's eighth
   __shared__ int sums[kPageThreads / 32 + 1];
-  __shared__ int count;
+  __shared__ int counts[kPageCluster];
   cg::cluster_group cluster = cg::this_cluster();
-  const int tid = threadIdx.x, lane = tid & 31, rank = (int)cluster.block_rank();
-  const int64_t pages = p.cache.num_pages;
-  const int64_t chunk = max((int64_t)4, ((pages + kPageCluster - 1) / kPageCluster + 3) / 4 * 4);
-  const int64_t lo = min(pages, rank * chunk), hi = min(pages, lo + chunk);
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, rank = (int)cluster.block_rank();
+  const uint32_t pages = (uint32_t)p.cache.num_pages, eighth = 32 * (uint32_t)p.words;
   asm volatile("griddepcontrol.launch_dependents;\n" ::: "memory");
+  for (int w = tid; w < p.words; w += kPageThreads) held_words[w] = 0;
   asm volatile("griddepcontrol.wait;\n" ::: "memory");
   int bad = 0;
   for (int b = tid; b < p.B; b += kPageThreads) {
@@ -421,116 +421,120 @@ __global__ void __launch_bounds__(kPageThreads) kda_latent_compact_kernel(const 
   }
   bad = __syncthreads_or(bad);
   if (bad) {  // (every CTA of the cluster finds the same)
-    for (int64_t i = lo + tid; i < hi; i += kPageThreads) {
+    for (uint32_t i = rank * kPageThreads + tid; i < pages; i += kPageCluster * kPageThreads) {
       p.page_map[i] = (int32_t)i;
       p.shares_out[i] = p.shares[i];
     }
     if (rank == 0 && tid == 0) {
       atomicExch(p.status, KDA_ERR_BAD_LENGTHS);
       p.used[0] = (int32_t)pages;
-      p.moves[0] = -1;
     }
     return;
   }
-  for (int64_t i = lo + tid * 4; i < hi; i += 4 * kPageThreads) *reinterpret_cast<uint32_t*>(p.held + i) = 0;
   cluster.sync();
-  {
-    const int64_t parts = (p.max_pages + 127) / 128;
+  {  // warps take equal parts of rows
     const int warps = kPageCluster * kPageThreads / 32;
-    for (int64_t i = rank * (kPageThreads / 32) + (tid >> 5); i < parts * p.B; i += warps) {
-      const int b = (int)(i / parts), j0 = (int)(i - b * parts) * 128;
-      const int held = pages_of(p.cached[b], p.page);
+    const int part = (int)min((p.B * p.max_pages / warps / 128 + 1) * 128, (int64_t)1 << 30);
+    const int parts = ((int)p.max_pages + part - 1) / part;  // (parts * B is at most about the warps and B)
+    for (int i = rank * (kPageThreads / 32) + warp; i < parts * p.B; i += warps) {
+      const int b = i / parts;
+      const int32_t* ids = p.table + b * p.table_stride;
+      const uint32_t j0 = (uint32_t)(i - b * parts) * part;
+      const uint32_t end = min((uint32_t)pages_of(p.cached[b], p.page), j0 + part);
+      for (uint32_t j = j0 + lane; j < end; j += 128) {
+        int id[4];
 #pragma unroll
-      for (int k = 0; k < 4; ++k) {
-        const int j = j0 + 32 * k + lane;
-        if (j >= held) continue;
-        const int id = p.table[b * p.table_stride + j];
-        if (id < 0 || id >= pages) atomicExch(p.status, KDA_ERR_BAD_PAGE);
-        else p.held[id] = 1;
+        for (int k = 0; k < 4; ++k) id[k] = j + 32 * k < end ? ids[j + 32 * k] : INT32_MIN;
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          if (id[k] >= 0 && (uint32_t)id[k] < pages) {
+            const uint32_t owner = (uint32_t)id[k] / eighth, in = (uint32_t)id[k] - owner * eighth;
+            atomicOr(cluster.map_shared_rank(held_words + (in >> 5), (int)owner), 1u << (in & 31));
+          } else if (j + 32 * k < end) {
+            atomicExch(p.status, KDA_ERR_BAD_PAGE);
+          }
+        }
       }
     }
   }
   cluster.sync();
-  auto four = [&](int64_t i) { return __ldcg(reinterpret_cast<const uint32_t*>(p.held + i)); };  // (the last one is padded)
+  // a warp a run of words; held pages before it, first of this CTA's
+  const int run = (p.words + kPageThreads / 32 - 1) / (kPageThreads / 32);
+  const int w0 = min(p.words, warp * run), w1 = min(p.words, w0 + run);
   int n = 0, total;
-  for (int64_t i = lo + tid * 4; i < hi; i += 4 * kPageThreads) n += __popc(four(i));
-  warps_before<kPageThreads>(warp_sum(n), sums, total);
-  if (tid == 0) count = total;
+  for (int w = w0 + lane; w < w1; w += 32) n += __popc(held_words[w]);
+  uint32_t before = warps_before<kPageThreads>(warp_sum(n), sums, total);
+  if (tid < kPageCluster) *cluster.map_shared_rank(counts + rank, tid) = total;
   cluster.sync();
-  // U, and how many held pages lie before this CTA's and before place U
-  int64_t used = 0, before = 0, below = 0;
-  int counts[kPageCluster];
+  uint32_t used = 0, below = 0;  // U, and the held pages below place U
 #pragma unroll
   for (int r = 0; r < kPageCluster; ++r) {
-    counts[r] = *cluster.map_shared_rank(&count, r);
     if (r < rank) before += counts[r];
     used += counts[r];
   }
-  const int64_t owner = used / chunk;
-#pragma unroll
-  for (int r = 0; r < kPageCluster; ++r)
-    if (r < owner) below += counts[r];
+  const uint32_t owner = used / eighth;  // the CTA of place U (none where all pages are held and fill their eighths)
+  for (uint32_t r = 0; r < owner; ++r) below += counts[r];
   n = 0;
-  for (int64_t i = owner * chunk + tid * 4; i < used; i += 4 * kPageThreads) {
-    const uint32_t x = four(i);
-#pragma unroll
-    for (int k = 0; k < 4; ++k) n += i + k < used && (x >> (8 * k) & 1);
+  if (owner < kPageCluster) {
+    const uint32_t* words = cluster.map_shared_rank(held_words, (int)owner);
+    const uint32_t in = used - owner * eighth;
+    for (uint32_t w = tid; 32 * w < in; w += kPageThreads)
+      n += __popc(words[w] & (in - 32 * w >= 32 ? 0xffffffffu : (1u << (in - 32 * w)) - 1));
   }
   warps_before<kPageThreads>(warp_sum(n), sums, total);
   below += total;
-  // places and movers, in order; a mover's number waits in the map for the places of the other CTAs
-  int64_t at = before;
-  for (int64_t base = lo; base < hi; base += 4 * kPageThreads) {
-    const int64_t i = base + tid * 4;
-    const uint32_t x = i < hi ? four(i) : 0;
-    const int mine = __popc(x), upto = warp_scan_int(mine, lane);
-    int64_t held = at + warps_before<kPageThreads>(__shfl_sync(0xffffffffu, upto, 31), sums, total) + upto - mine;
-    at += total;
-#pragma unroll
-    for (int k = 0; k < 4; ++k) {
-      const int64_t page = i + k;
-      if (page >= hi) continue;
-      const bool is = x >> (8 * k) & 1;
-      if (!is && page < used) p.to[page - held] = (int32_t)page;
-      if (is && page >= used) p.from[held - below] = (int32_t)page;
-      p.page_map[page] = !is ? -1 : (int32_t)(page < used ? page : held - below);
-      held += is;
+  // the places, listed in the map's first entries, which get their values at the end
+  auto each = [&](auto body) {
+    uint32_t at = before;  // held pages before the word
+    for (int w = w0; w < w1; ++w) {
+      const uint32_t mask = held_words[w], page = rank * eighth + 32 * w + lane;
+      if (page < pages) body(page, mask >> lane & 1, at + __popc(mask & ((1u << lane) - 1)));
+      at += __popc(mask);
     }
-  }
-  if (rank == 0 && tid == 0) {
-    p.used[0] = (int32_t)used;
-    p.moves[0] = (int32_t)(used - below);
-  }
+  };
+  each([&](uint32_t page, bool held, uint32_t k) {
+    if (!held && page < used) p.page_map[page - k] = (int32_t)page;
+  });
+  if (rank == 0 && tid == 0) p.used[0] = (int32_t)used;
   cluster.sync();
-  // (shares_out may be shares: a mover's count is taken before it is cleared)
-  for (int64_t i = lo + tid; i < hi; i += kPageThreads)
-    if (i < used && __ldcg(p.page_map + i) >= 0) p.shares_out[i] = p.shares[i];
-  for (int64_t k = rank * kPageThreads + tid; k < used - below; k += kPageCluster * kPageThreads) {
-    const int to = __ldcg(p.to + k), from = __ldcg(p.from + k);
-    p.shares_out[to] = p.shares[from];
-    p.page_map[from] = to;
-  }
+  // (shares_out may be shares: a mover's count is taken and cleared by one thread)
+  each([&](uint32_t page, bool held, uint32_t k) {
+    if (page < used) {
+      if (held) p.shares_out[page] = p.shares[page];
+      return;
+    }
+    int to = -1;
+    if (held) {
+      to = __ldcg(p.page_map + (k - below));
+      p.shares_out[to] = p.shares[page];
+    }
+    p.page_map[page] = to;
+    p.shares_out[page] = 0;
+  });
   cluster.sync();
-  for (int64_t i = max(lo, used) + tid; i < hi; i += kPageThreads) p.shares_out[i] = 0;
+  each([&](uint32_t page, bool held, uint32_t) {
+    if (page < used) p.page_map[page] = held ? (int32_t)page : -1;
+  });
 }
 
 __global__ void __launch_bounds__(kCopyThreads) kda_latent_move_kernel(const CompactParams p) {
   asm volatile("griddepcontrol.wait;\n" ::: "memory");
-  const int64_t moves = p.moves[0];
+  const int64_t used = p.used[0];
   const int per = p.page / kGroupRows;
   const int64_t entries = p.B * p.max_pages;
   // the tables first: they are small, and their entries are renamed while the first rows are on their way
   for (int64_t e = (int64_t)blockIdx.x * kCopyThreads + threadIdx.x; e < entries; e += (int64_t)gridDim.x * kCopyThreads) {
     const int b = (int)div_pages(e, (int)p.max_pages), j = (int)(e - b * p.max_pages);
     int id = p.table[b * p.table_stride + j];
-    if (moves >= 0 && j < pages_of(p.cached[b], p.page) && id >= 0 && id < p.cache.num_pages)
-      id = p.page_map[id];
+    if (p.cached[b] > 0 && j < pages_of(p.cached[b], p.page) && id >= 0 && id < p.cache.num_pages) id = p.page_map[id];
     p.table_out[b * p.table_out_stride + j] = id;
   }
-  copy_groups(max((int64_t)0, moves) * per, p.cache.token_stride, p.cache.token_stride, blockIdx.x, gridDim.x,
+  // (refused: the map is the identity, and no page lies behind U)
+  copy_groups((p.cache.num_pages - used) * per, p.cache.token_stride, p.cache.token_stride, blockIdx.x, gridDim.x,
               [&](int64_t g) {
-                const int64_t i = div_pages(g, per);
-                return page_group(p.cache, p.cache, p.from[i], p.to[i], (int)(g - i * per), p.status);
+                const int64_t i = div_pages(g, per), to = p.page_map[used + i];
+                CopyPlace c = {nullptr, nullptr, kGroupRows};
+                return to < 0 ? c : page_group(p.cache, p.cache, used + i, to, (int)(g - i * per), p.status);
               });
 }
 
@@ -555,10 +559,6 @@ int check_table(int64_t rows, int64_t max_pages, int64_t stride, const void* tab
 
 unsigned copy_ctas(int64_t groups) { return (unsigned)std::min<int64_t>(std::max<int64_t>(1, (groups + 3) / 4), 152 * 6); }
 
-constexpr size_t kCompactHead = 256;
-size_t compact_held_bytes(int64_t pages) { return ((size_t)pages + 255) / 256 * 256; }
-size_t compact_list_bytes(int64_t pages) { return ((size_t)pages / 2 * 4 + 255) / 256 * 256 + 256; }
-
 int check_compact(const kda_latent_compact_args* a) {
   if (!a) return KDA_ERR_NULL_ARG;
   int rc = check_table(a->B, a->max_pages, a->table_stride, a->block_table);
@@ -567,6 +567,7 @@ int check_compact(const kda_latent_compact_args* a) {
   if (rc != KDA_OK) return rc;
   rc = latent_check_cache(&a->cache);
   if (rc != KDA_OK) return rc;
+  if (a->cache.num_pages > KDA_LATENT_COMPACT_PAGES) return KDA_ERR_SHAPE;
   if (!a->pages_used || (a->B > 0 && !a->cached_lens) ||
       (a->cache.num_pages > 0 && (!a->shares || !a->shares_out || !a->page_map)))
     return KDA_ERR_NULL_ARG;
@@ -656,30 +657,33 @@ extern "C" int kda_latent_release(const kda_latent_release_args* a, void* stream
              : KDA_ERR_LAUNCH;
 }
 
-extern "C" size_t kda_latent_compact_workspace_bytes(const kda_latent_compact_args* a) {
-  if (check_compact(a) != KDA_OK) return 0;
-  return kCompactHead + compact_held_bytes(a->cache.num_pages) + 2 * compact_list_bytes(a->cache.num_pages);
-}
-
-extern "C" int kda_latent_compact(const kda_latent_compact_args* a, void* workspace, size_t workspace_bytes, void* stream) {
+extern "C" int kda_latent_compact(const kda_latent_compact_args* a, void* stream) {
   const int rc = check_compact(a);
   if (rc != KDA_OK) return rc;
-  if (!workspace || ((uintptr_t)workspace & 255) || workspace_bytes < kda_latent_compact_workspace_bytes(a))
-    return KDA_ERR_WORKSPACE;
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
   int* status = status_slot(s);
   if (!status) return KDA_ERR_LAUNCH;
-  unsigned char* ws = static_cast<unsigned char*>(workspace);
+  const int64_t pages = a->cache.num_pages;
   CompactParams p{a->cached_lens, a->block_table, a->block_table_out, a->table_stride, a->table_out_stride, a->max_pages,
-                  a->shares, a->shares_out, a->page_map, a->pages_used, page_cache(a->cache), ws + kCompactHead,
-                  reinterpret_cast<int32_t*>(ws), nullptr, nullptr, (int)a->B, (int)a->cache.page_size, status};
-  unsigned char* lists = ws + kCompactHead + compact_held_bytes(a->cache.num_pages);
-  p.to = reinterpret_cast<int32_t*>(lists);
-  p.from = reinterpret_cast<int32_t*>(lists + compact_list_bytes(a->cache.num_pages));
-  if (!launch_overlapped(kda_latent_compact_kernel, dim3(kPageCluster), kPageThreads, 0, s, kPageCluster, p))
+                  a->shares, a->shares_out, a->page_map, a->pages_used, page_cache(a->cache),
+                  (int)std::max<int64_t>(1, (pages + 32 * kPageCluster - 1) / (32 * kPageCluster)), (int)a->B,
+                  (int)a->cache.page_size, status};
+  const size_t smem = (size_t)p.words * 4;
+  if (smem > 40 * 1024) {
+    static std::atomic<int> set[64];
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return KDA_ERR_LAUNCH;
+    if (!set[dev].load()) {
+      if (cudaFuncSetAttribute(kda_latent_compact_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                               KDA_LATENT_COMPACT_PAGES / (8 * kPageCluster)) != cudaSuccess)
+        return KDA_ERR_LAUNCH;
+      set[dev].store(1);
+    }
+  }
+  if (!launch_overlapped(kda_latent_compact_kernel, dim3(kPageCluster), kPageThreads, smem, s, kPageCluster, p))
     return KDA_ERR_LAUNCH;
   // as many CTAs as half of the pages could need, the most that can move
-  const int64_t groups = a->cache.num_pages / 2 * (a->cache.page_size / kGroupRows);
+  const int64_t groups = pages / 2 * (a->cache.page_size / kGroupRows);
   const int64_t entries = (a->B * a->max_pages + kCopyThreads - 1) / kCopyThreads;
   const unsigned ctas = std::max(copy_ctas(groups), (unsigned)std::min<int64_t>(entries, 152));
   return launch_overlapped(kda_latent_move_kernel, dim3(ctas), kCopyThreads, 0, s, 1, p) ? KDA_OK : KDA_ERR_LAUNCH;

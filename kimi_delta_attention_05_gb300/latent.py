@@ -100,9 +100,7 @@ def _library():
         for name in ("fork", "release", "copy", "compact"):
             fn = getattr(lib, f"kda_latent_{name}")
             fn.restype = ctypes.c_int
-            fn.argtypes = [_P, _P, ctypes.c_size_t, _P] if name == "compact" else [_P, _P]
-        lib.kda_latent_compact_workspace_bytes.restype = ctypes.c_size_t
-        lib.kda_latent_compact_workspace_bytes.argtypes = [_P]
+            fn.argtypes = [_P, _P]
         _fns = lib
     return _fns
 

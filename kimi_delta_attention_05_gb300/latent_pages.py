@@ -11,10 +11,8 @@ from __future__ import annotations
 
 import ctypes
 
-import torch
-
 from .latent import (_I, _P, _cache_block, _dense, _gpu, _handle, _i32, _last, _library, _new, _on, _packer, _raise,
-                     _scratch, kda_latent_cache)
+                     kda_latent_cache)
 
 
 class kda_latent_fork_args(ctypes.Structure):
@@ -45,8 +43,9 @@ _compact_block, _copy_block = _packer(kda_latent_compact_args), _packer(kda_late
 
 def _ints(t, device, name):
     """Address and length of a contiguous int32 vector."""
-    _on(t, _i32, 1, device, name)
-    _dense(t, name)
+    if t.dtype is not _i32 or t.ndim != 1 or t.device != device or not t.is_contiguous():
+        _on(t, _i32, 1, device, name)
+        _dense(t, name)
     return t.data_ptr(), t.shape[0]
 
 
@@ -133,16 +132,15 @@ def latent_release(rows, cached_lens, block_table, shares, page_size, keep_lens=
     return {"seq_lens": out, "pages": pages, "count": count}
 
 
-def latent_compact(cached_lens, block_table, shares, cache, *, out_table=None, out_shares=None, workspace=None, stream=None):
+def latent_compact(cached_lens, block_table, shares, cache, *, out_table=None, out_shares=None, stream=None):
     """Held pages together: of the U pages that the table's rows hold, those with ids
     from U on move to the places below that nobody holds, in ascending order.
 
     Rows move within ``cache``.  Returns a dict of device tensors: block_table and
     shares by the new ids (new tensors, or ``out_table`` and ``out_shares``, which may
     be the inputs), page_map int32 [num_pages] (new id of every held page, -1 for
-    others) and pages_used int32 [1], U: pages U and behind are free.  ``workspace``:
-    an optional uint8 tensor of at least :func:`latent_compact_workspace_bytes`
-    bytes.  Lengths that do not fit move nothing and show in :func:`get_status` (18)."""
+    others) and pages_used int32 [1], U: pages U and behind are free.  Lengths that do
+    not fit move nothing and show in :func:`get_status` (18)."""
     dev, lens, table, stride, B, width = _requests(cached_lens, block_table, stream)
     block = _cache_block(cache, dev)
     pages = block[1]
@@ -165,20 +163,10 @@ def latent_compact(cached_lens, block_table, shares, cache, *, out_table=None, o
     used = _new(1, _i32, dev, stream)
     a = _compact_block(lens, table, stride, to, to_stride, counts, to_counts, page_map.data_ptr(), used.data_ptr(), *block, B,
                        width)
-    lib = _library()
-    if workspace is None:
-        workspace = _new(max(256, lib.kda_latent_compact_workspace_bytes(a)), torch.uint8, dev, stream)
-    rc = lib.kda_latent_compact(a, *_scratch(workspace, dev), _handle(dev, stream))
+    rc = _library().kda_latent_compact(a, _handle(dev, stream))
     if rc != 0:
         _raise("kda_latent_compact", rc)
     return {"block_table": out_table, "shares": out_shares, "page_map": page_map, "pages_used": used}
-
-
-def latent_compact_workspace_bytes(block_table, cache):
-    """Workspace bytes of :func:`latent_compact` for these sizes."""
-    B, width = block_table.shape
-    return int(_library().kda_latent_compact_workspace_bytes(
-        _compact_block(4, 4, width, 4, width, 4, 4, 4, 4, *_cache_block(cache, cache.device), B, width)))
 
 
 def latent_copy(src, src_pages, dst, dst_pages, *, stream=None):

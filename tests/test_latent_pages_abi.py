@@ -65,19 +65,10 @@ def _compact_args(**over):
     (dict(cached_lens=None), 1), (dict(block_table=None), 1), (dict(block_table_out=None), 1), (dict(shares=None), 1),
     (dict(shares_out=None), 1), (dict(page_map=None), 1), (dict(pages_used=None), 1), (dict(B=-1), 3), (dict(B=16385), 3),
     (dict(table_stride=5), 3), (dict(table_out_stride=5), 3), (dict(page_map=FAKE + 2), 9),
+    (dict(cache=_cache(num_pages=12582913)), 3),
 ] + BAD_CACHES)
 def test_compact_refusals(over, code):
-    a = _compact_args(**over)
-    assert _call("compact", a, (FAKE, 1 << 40)) == code
-    assert M._library().kda_latent_compact_workspace_bytes(ctypes.byref(a)) == 0
-
-
-def test_compact_workspace_is_checked():
-    a = _compact_args()
-    need = M._library().kda_latent_compact_workspace_bytes(ctypes.byref(a))
-    assert need > 0
-    for ws in ((None, need), (FAKE, need - 1), (FAKE + 16, need)):
-        assert _call("compact", a, ws) == 10
+    assert _call("compact", _compact_args(**over)) == code
 
 
 @pytest.mark.parametrize("over,code", [
