@@ -401,15 +401,16 @@ extern "C" const char* kda_error_string(int code) {
     case KDA_ERR_DEVICE_TIMEOUT:
       return "a kernel gave up waiting for its operand copies (device status)";
     case KDA_ERR_BAD_SEQLENS:
-      return "cu_seqlens is not 0 = cu[0] <= ... <= cu[N] = T; the call skipped the sequences "
-             "(device status)";
+      return "cu_seqlens is not 0 = cu[0] <= ... <= cu[N] = T, the call skipped the sequences; or cu_groups "
+             "not 0 = cu[0] <= ... <= cu[G] = B, the call took every request on its own (device status)";
     case KDA_ERR_NOALLOC_LIMIT:
       return "problem needs more scratch than kda_fwd_noalloc's built-in buffer holds";
     case KDA_ERR_STRIDE: return "a stride is not a multiple of 16 bytes or makes rows overlap";
     case KDA_ERR_SCALE: return "scale must be positive and finite";
     case KDA_ERR_PAGE_SIZE: return "page_size must be a positive multiple of 8";
     case KDA_ERR_BAD_LENGTHS:
-      return "a request's length is negative or longer than its table, slots or pages allow (device status)";
+      return "a request's length is negative or longer than its table, slots or pages allow, or its number does not fit "
+             "(device status)";
     case KDA_ERR_NO_PAGES: return "too few free pages for the requests' new tokens (device status)";
     case KDA_ERR_BAD_PAGE: return "a page id or slot lies outside the cache (device status)";
     default: return "unknown status code";
