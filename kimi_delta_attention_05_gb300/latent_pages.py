@@ -11,6 +11,8 @@ from __future__ import annotations
 
 import ctypes
 
+import torch
+
 from .latent import (_I, _P, _cache_block, _dense, _gpu, _handle, _i32, _last, _library, _new, _on, _packer, _raise,
                      kda_latent_cache)
 
@@ -37,6 +39,7 @@ class kda_latent_copy_args(ctypes.Structure):
     _fields_ = [("src", kda_latent_cache), ("dst", kda_latent_cache), ("src_pages", _P), ("dst_pages", _P), ("n", _I)]
 
 
+_empty_like = torch.empty_like
 _fork_block, _release_block = _packer(kda_latent_fork_args), _packer(kda_latent_release_args)
 _compact_block, _copy_block = _packer(kda_latent_compact_args), _packer(kda_latent_copy_args)
 
@@ -47,6 +50,13 @@ def _ints(t, device, name):
         _on(t, _i32, 1, device, name)
         _dense(t, name)
     return t.data_ptr(), t.shape[0]
+
+
+def _like(t, stream):
+    """Memory as large as t, dense, allocated on the stream that uses it."""
+    if stream is None and t.is_contiguous():
+        return _empty_like(t)  # (a fifth faster than a call with sizes, type and device)
+    return _new(t.shape, t.dtype, t.device, stream)
 
 
 def _requests(cached_lens, block_table, stream):
@@ -60,10 +70,13 @@ def _requests(cached_lens, block_table, stream):
 
 
 def _table(t, device, name):
-    _on(t, _i32, 2, device, name)
+    """Address, stride, rows and width of a table."""
+    if t.dtype is not _i32 or t.ndim != 2 or t.device != device:
+        _on(t, _i32, 2, device, name)
     B, width = t.shape
     strides = t.stride()
-    _last(strides, t, name)
+    if strides[1] != 1:
+        _last(strides, t, name)
     return t.data_ptr(), strides[0] if B > 1 else width, B, width
 
 
@@ -93,7 +106,7 @@ def latent_fork(parents, children, cached_lens, block_table, free_pages, shares,
     counts, n = _ints(shares, dev, "shares")
     if n != block[1]:
         raise ValueError("shares: one entry a page of the cache")
-    out = _new(B, _i32, dev, stream)
+    out = _like(cached_lens, stream)
     taken = _new(1, _i32, dev, stream)
     a = _fork_block(of, to, take, lens, table, stride, free, counts, *block, out.data_ptr(), taken.data_ptr(), F, B, width,
                     num_free)
@@ -121,8 +134,8 @@ def latent_release(rows, cached_lens, block_table, shares, page_size, keep_lens=
         if n != F:
             raise ValueError("keep_lens: one entry a row")
     counts, num_pages = _ints(shares, dev, "shares")
-    out = _new(B, _i32, dev, stream)
-    pages = _new(num_pages, _i32, dev, stream)
+    out = _like(cached_lens, stream)
+    pages = _like(shares, stream)
     count = _new(1, _i32, dev, stream)
     a = _release_block(at, keep, lens, table, stride, counts, out.data_ptr(), pages.data_ptr(), count.data_ptr(), F, B, width,
                        num_pages, int(page_size))
@@ -148,18 +161,18 @@ def latent_compact(cached_lens, block_table, shares, cache, *, out_table=None, o
     if n != pages:
         raise ValueError("shares: one entry a page of the cache")
     if out_table is None:
-        out_table = _new((B, width), _i32, dev, stream)
+        out_table = _like(block_table, stream)
     to, to_stride, rows, columns = _table(out_table, dev, "out_table")
     if (rows, columns) != (B, width):
         raise ValueError("out_table: as large as block_table")
     if to == table and to_stride != stride:
         raise ValueError("out_table: another view of block_table's memory")
     if out_shares is None:
-        out_shares = _new(pages, _i32, dev, stream)
+        out_shares = _like(shares, stream)
     to_counts, n = _ints(out_shares, dev, "out_shares")
     if n != pages:
         raise ValueError("out_shares: one entry a page of the cache")
-    page_map = _new(pages, _i32, dev, stream)
+    page_map = _like(shares, stream)
     used = _new(1, _i32, dev, stream)
     a = _compact_block(lens, table, stride, to, to_stride, counts, to_counts, page_map.data_ptr(), used.data_ptr(), *block, B,
                        width)
