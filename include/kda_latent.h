@@ -181,7 +181,8 @@ int kda_latent_decode(const kda_latent_decode_args *args, void *workspace, size_
  * without requests is not looked at; another below 0
  * or beyond the table is taken as the nearer bound and sets KDA_ERR_BAD_LENGTHS;
  * offsets that do not go from 0 to B without decreasing set KDA_ERR_BAD_SEQLENS, and
- * every request is taken on its own.  B * R * H is below 2^31 - 128, G at most 16384.
+ * every request is taken on its own.  B * R * H is below 2^31 - 128, a table
+ * holds at most 2^30 tokens, and G is at most KDA_LATENT_SHARED_GROUPS.
  * Prefix and remaining tokens are joined by their fp32 parts, so outputs have the
  * error of kda_latent_decode's; they are not bit for bit the same.
  * Where the tables hold little (B * max_pages * page_size tokens, times the blocks of
@@ -190,6 +191,7 @@ int kda_latent_decode(const kda_latent_decode_args *args, void *workspace, size_
  * prefix_lens are then not looked at.
  */
 #define KDA_LATENT_SHARED_TOKENS 131072
+#define KDA_LATENT_SHARED_GROUPS 16384
 typedef struct kda_latent_decode_shared_args {
   kda_latent_decode_args decode;
   const int64_t *cu_groups;

@@ -17,8 +17,7 @@ OUT_DIR = os.path.join(PKG, "_lib")
 LIB = os.path.join(OUT_DIR, "libkda.so")
 SOURCES = ["kda_api.cu", "kda_chunk.cu", "kda_state.cu", "kda_recurrent.cu", "kda_noalloc.cu",
            "kda_host.cu", "kda_status.cu", "kda_bwd.cu", "kda_latent.cu", "kda_latent_decode.cu",
-           "kda_latent_prefill.cu", "kda_latent_prefill_split.cu", "kda_latent_pages.cu", "kda_latent_prefix.cu",
-           "kda_latent_shared.cu"]
+           "kda_latent_prefill.cu", "kda_latent_prefill_split.cu", "kda_latent_pages.cu", "kda_latent_shared.cu"]
 HEADERS = ["kda_common.cuh", "kda_kernels.cuh", "kda_tc.cuh", "kda_latent.cuh",
            "kda_latent_prefill.cuh", "kda_latent_tc.cuh"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]

@@ -273,7 +273,8 @@ int check_shared(const kda_latent_decode_shared_args* a) {
   if (!a) return KDA_ERR_NULL_ARG;
   const int rc = check_decode(&a->decode);
   if (rc != KDA_OK) return rc;
-  if (a->G < 0 || a->G > kMaxPlanRequests || a->decode.B * a->decode.R * a->decode.H > INT32_MAX - 128) return KDA_ERR_SHAPE;
+  if (a->G < 0 || a->G > KDA_LATENT_SHARED_GROUPS || a->decode.B * a->decode.R * a->decode.H > INT32_MAX - 128) return KDA_ERR_SHAPE;
+  if (a->decode.max_pages * a->decode.cache.page_size > (1 << 30)) return KDA_ERR_SHAPE;  // tiles of an item stay in 32 bits
   if (a->G == 0 && a->decode.B > 0) return KDA_ERR_BAD_SEQLENS;  // offsets that cannot end at B
   if (!a->cu_groups || (a->G > 0 && !a->prefix_lens)) return KDA_ERR_NULL_ARG;
   if (!al(a->cu_groups, 8) || !al(a->prefix_lens, 4)) return KDA_ERR_ALIGNMENT;

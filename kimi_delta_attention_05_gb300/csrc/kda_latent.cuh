@@ -110,78 +110,14 @@ bool launch_overlapped(void (*kernel)(P...), dim3 grid, unsigned threads, size_t
 // The checks of a cache's address, sizes and strides.
 int latent_check_cache(const kda_latent_cache* c);
 
-// ---- decoding behind shared prefixes ----
-constexpr int kPfxTile = 128;      // cached rows of a tile of the shared pass
-constexpr int kPfxRows = 128;      // query rows of an item, a CTA pair's
-// A share's cost: 4 a tile, and an item's set-up and output.
-constexpr int kPfxTileCost = 4, kPfxItemCost = 6;
-
-struct SharedHead {
-  int64_t total, size;             // cost of all items, and of a share
-};
-
-// Groups of requests: group g has the requests [cu[g], cu[g + 1]).
+// Groups of requests that share prefixes: group g has the requests [cu[g], cu[g + 1]).
 struct SharedGroups {
-  const int64_t* cu;               // [G + 1]
-  const int32_t* prefix;           // [G]
+  const int64_t* cu;                // [G + 1]
+  const int32_t* prefix;            // [G]
   int G;
 };
-
-struct SharedParams {
-  DecodeParams d;
-  SharedGroups groups;
-  int pairs;                       // CTA pairs of the shared pass, a share each; 0: there is none
-  // workspace
-  SharedHead* head;
-  int64_t* line;                   // [G] cost of the items before the group's
-  // fp32 rows and their lse (log2): a row's first part at its own place, those that begin
-  // within a share behind them
-  float *pre_part, *pre_lse;       // [B R H + pairs * kPfxRows]
-  float *own_part, *own_lse;       // [B R H + CTAs * N]
-  int4* split;                     // [B][blocks of N rows] what is left to join: request or -1, first and last share
-                                   // of the own pass, group or -1
-  int own_n, own_row_blocks;       // N and the blocks of N rows
-};
-
-// Tokens of a group's prefix that are shared: whole tiles, of groups of two and more.
-__device__ __forceinline__ int shared_tokens(int64_t first, int64_t end, int64_t prefix, int64_t cap) {
-  const int64_t len = prefix < 0 ? 0 : (prefix > cap ? cap : prefix);
-  return end - first < 2 ? 0 : (int)(len / kPfxTile * kPfxTile);
-}
-// Whether all new tokens of a request see the shared ones.
-__device__ __forceinline__ bool sees_shared(int len, int64_t cap, int R, int tokens) {
-  const int64_t n = len < 0 ? 0 : (len > cap ? cap : len);
-  return n - (R - 1) >= tokens;
-}
-// a / b of numbers that are not negative, in 32 bits where they fit (a 64-bit division takes some 100 instructions)
-__device__ __forceinline__ int64_t div_costs(int64_t a, int64_t b) {
-  return ((a | b) >> 32) == 0 ? (int64_t)((uint32_t)a / (uint32_t)b) : a / b;
-}
-// Cost of an item, and the share that holds tile t of the one that begins at `item` of the line.
-__device__ __forceinline__ int64_t prefix_item_cost(int tokens) {
-  return kPfxItemCost + (int64_t)(tokens / kPfxTile) * kPfxTileCost;
-}
-__device__ __forceinline__ int64_t prefix_share(int64_t item, int t, int64_t size) {
-  return div_costs(item + kPfxItemCost + (int64_t)t * kPfxTileCost, size);
-}
-// The parts of a row of a group in the shared pass: how many, and the place of the second.
-__device__ __forceinline__ int prefix_parts(int64_t line, int64_t size, int tokens, int row, int64_t all, int64_t& second) {
-  const int64_t item = line + row / kPfxRows * prefix_item_cost(tokens);
-  const int64_t first = prefix_share(item, 0, size);
-  second = all + (first + 1) * kPfxRows + row % kPfxRows;
-  return (int)(prefix_share(item, tokens / kPfxTile - 1, size) - first) + 1;
-}
-
 size_t shared_workspace_bytes(const DecodeParams& p, int64_t G);
 bool launch_latent_shared(const DecodeParams& p, const SharedGroups& groups, cudaStream_t s);
-// Its parts: the shared pass; a request's own tokens (sizes first, then the launch).
-bool launch_latent_prefix(const SharedParams& p, cudaStream_t s);
-struct OwnLayout {
-  int n, row_blocks, ctas;
-};
-OwnLayout own_layout(const DecodeParams& p);
-bool launch_latent_own(const SharedParams& p, cudaStream_t s);
-int device_sm_count();
 
 size_t decode_workspace_bytes(const DecodeParams& p);
 // false: a tensor map could not be made or a launch attribute set (nothing launched)

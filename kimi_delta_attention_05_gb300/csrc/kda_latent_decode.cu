@@ -79,10 +79,6 @@ struct DecodePlan {
   int whole;           // requests are not split: the share that holds a request's start has all of it
   float* part;         // [row_blocks * shares * 2][N][512] normalised partial rows
   float* part_lse;     // [row_blocks * shares * 2][N] their lse, log2
-  // own tokens behind shared prefixes: the groups; whether the shared pass runs beside this kernel.  A row's first part is
-  // at its own place of part, the others behind all rows
-  SharedGroups groups;
-  int early;
   int by_request;      // the join works by request (fewer than shares), else by share
   int4* split;         // [requests or shares][row_blocks]: (request or -1, first share, last share)
 };
@@ -100,7 +96,7 @@ struct DecCfg {
   static constexpr int kFull = 0, kEmpty = 2, kQFull = 4, kQEmpty = 6, kSFull = 8, kPReady = 10, kPvDone = 11,
                        kBars = 12;
   static constexpr int kScan = kBar + 8 * kBars;            // int64 [10] sums of the warps, [2] first request and its start
-  static constexpr int kTmem = kScan + 96;                  // and (kOwn) the group of the first request
+  static constexpr int kTmem = kScan + 96;
   static constexpr int kAbort = kTmem + 8;
   static constexpr int kSmem = kAbort + 8;
   static constexpr uint32_t kCols = N == 16 ? 128 : N == 32 ? 256 : 512;  // 6 N rounded up
@@ -109,10 +105,8 @@ struct DecCfg {
 };
 
 // A request's length, clamped to what its table can hold.
-// (kOwn: read past L1, see OwnStarts)
-template <bool kOwn>
 __device__ __forceinline__ int dec_len(const DecodeParams& p, int b) {
-  const int64_t len = kOwn ? __ldcg(p.lens + b) : p.lens[b], cap = p.max_pages * p.page_size;
+  const int64_t len = p.lens[b], cap = p.max_pages * p.page_size;
   return (int)(len < 0 ? 0 : (len > cap ? cap : len));
 }
 __device__ __forceinline__ int dec_tiles(int len) { return len > 0 ? (len - 1) / kDecTile + 1 : 0; }
@@ -123,38 +117,16 @@ __device__ __forceinline__ int64_t div_fast(int64_t a, int64_t b) {
   return ((a | b) >> 32) == 0 ? (int64_t)((uint32_t)a / (uint32_t)b) : a / b;
 }
 
-// Of the own pass: where a request's tokens begin, its group's shared ones being before it.  Requests are visited in
-// order.  (Values that the kernel before this one's predecessor may have written are read past L1: this kernel starts
-// while its predecessor runs.)
-struct OwnStarts {
-  const int64_t* cu;
-  const int32_t* prefix;
-  int G, g, end, tokens;  // the current group, the request behind it, its shared tokens
-  __device__ __forceinline__ void enter(int group, int64_t cap) {
-    g = group;
-    end = g < 0 || g >= G ? INT32_MAX : (int)__ldcg(cu + g + 1);
-    tokens = g < 0 || g >= G ? 0 : shared_tokens(__ldcg(cu + g), end, __ldcg(prefix + g), cap);
-  }
-  // first token of request b (b grows from call to call)
-  __device__ __forceinline__ int from(const DecodeParams& p, int b, int len) {
-    const int64_t cap = p.max_pages * p.page_size;
-    while (b >= end) enter(g + 1, cap);
-    return tokens > 0 && sees_shared(len, cap, p.R, tokens) ? tokens : 0;
-  }
-};
-
 // The pieces of one share [u0, u1) of the line of costs, in order.  Request b
 // takes [pre, pre + cost) of it; its tile k starts at pre + kDecReqCost + k
 // kDecTileCost and belongs to the share that holds that point; a request
 // without tiles, or one that is not split, belongs to the share that holds pre.
-template <bool kOwn>
 struct DecPieces {
-  OwnStarts own;  // (kOwn)
   int unsplit;
   int64_t u0, u1, pre;  // the share; start of request b
   int b;
-  // the current piece: request, its first token and length, tiles [t0, t1) of its `tiles` from there
-  int req, from, len, t0, t1, tiles;
+  // the current piece: request, its length, tiles [t0, t1) of its `tiles`
+  int req, len, t0, t1, tiles;
   __device__ __forceinline__ int tiles_before(int64_t u) const {
     const int64_t d = u - pre - kDecReqCost;
     return d <= 0 ? 0 : (int)min((int64_t)tiles, (d + kDecTileCost - 1) >> 2);
@@ -162,9 +134,8 @@ struct DecPieces {
   __device__ __forceinline__ bool next(const DecodeParams& p) {
     while (b < p.B && pre < u1) {
       req = b;
-      len = dec_len<kOwn>(p, b);
-      from = kOwn ? own.from(p, b, len) : 0;
-      tiles = dec_tiles(len - from);
+      len = dec_len(p, b);
+      tiles = dec_tiles(len);
       t0 = tiles_before(u0);
       t1 = tiles_before(u1);
       if (unsplit && pre >= u0) t1 = tiles;  // (and t0 is 0)
@@ -180,13 +151,12 @@ struct DecPieces {
 };
 
 // A walk over the tiles of a share.
-template <bool kOwn>
 struct DecCursor {
-  DecPieces<kOwn> it;
+  DecPieces it;
   int tile;
   int piece;  // index of the piece among those with tiles
   bool ok;
-  __device__ __forceinline__ void start(const DecPieces<kOwn>& s, const DecodeParams& p) {
+  __device__ __forceinline__ void start(const DecPieces& s, const DecodeParams& p) {
     it = s;
     piece = -1;
     ok = true;
@@ -206,9 +176,7 @@ struct DecCursor {
   __device__ __forceinline__ bool last() const { return tile + 1 == it.t1; }
 };
 
-// kOwn: only the tokens behind the shared ones.  Requests that share none and are in one share write their result; the
-// others leave parts, and the join of the shared call adds those of the prefixes.
-template <int N, bool kOwn>
+template <int N>
 __global__ void __launch_bounds__(kDecThreads, 1)
     kda_latent_decode_kernel(const DecodeParams p, const DecodePlan pl, const __grid_constant__ DecodeMaps maps) {
   using C = DecCfg<N>;
@@ -240,50 +208,18 @@ __global__ void __launch_bounds__(kDecThreads, 1)
     prefetch_map(&maps.q);
     prefetch_map(&maps.cache);
   }
-  // (set up while the kernel before this one ends; nothing it wrote is read until here.  The own pass may run beside
-  // the shared pass, which has waited for the kernels before it and writes nothing that is read here)
-  if (!kOwn || !pl.early) asm volatile("griddepcontrol.wait;\n" ::: "memory");
-  OwnStarts own = {};
-  if constexpr (kOwn) {  // the groups' offsets, checked and in shared memory while each thread looks for its own
-    int* cu = reinterpret_cast<int*>(smem);
-    const int G = pl.groups.G;
-    const int64_t cap = p.max_pages * p.page_size;
-    int bad = 0, far = 0;
-    for (int g = tid; g <= G; g += kDecThreads) {
-      const int64_t c = __ldcg(pl.groups.cu + g), next = g < G ? __ldcg(pl.groups.cu + g + 1) : c;
-      bad |= (g == 0 && c != 0) || (g == G && c != p.B) || c < 0 || c > p.B || next < c;
-      if (g < G && next > c) {
-        const int len = __ldcg(pl.groups.prefix + g);
-        far |= len < 0 || len > cap;
-      }
-      cu[g] = (int)c;
-    }
-    bad = __syncthreads_or(bad);
-    if (far && blockIdx.x == 0) atomicExch(p.status, KDA_ERR_BAD_LENGTHS);
-    if (bad && blockIdx.x == 0 && tid == 0) atomicExch(p.status, KDA_ERR_BAD_SEQLENS);
-    own.cu = pl.groups.cu;
-    own.prefix = pl.groups.prefix;
-    own.G = bad ? 0 : G;
-    const int b = min(p.B - 1, tid * ((p.B + kDecThreads - 1) / kDecThreads));
-    int lo = 0, hi = own.G - 1;  // last group that begins at request b or before
-    while (lo < hi) {
-      const int mid = (lo + hi + 1) >> 1;
-      if (cu[mid] <= b) lo = mid; else hi = mid - 1;
-    }
-    own.enter(bad ? -1 : lo, cap);
-    fence_proxy_async_smem();  // (the place goes to the tensor copies)
-  }
+  // (set up while the kernel before this one ends; nothing it wrote is read until here)
+  asm volatile("griddepcontrol.wait;\n" ::: "memory");
   // each thread sums a run of requests; a scan over threads gives the total
   // (hence the shares' size) and the run that holds this share's first tile
   const int run = (p.B + kDecThreads - 1) / kDecThreads;
   const int b0 = min(p.B, tid * run), b1 = min(p.B, b0 + run);
   int64_t mine = 0;
   bool odd = false;
-  OwnStarts walk = own;
   for (int b = b0; b < b1; ++b) {
-    const int raw = __ldcg(p.lens + b), len = dec_len<kOwn>(p, b);
+    const int raw = p.lens[b], len = dec_len(p, b);
     odd |= raw != len;
-    mine += dec_cost(dec_tiles(len - (kOwn ? walk.from(p, b, len) : 0)));
+    mine += dec_cost(dec_tiles(len));
   }
   if (odd && blockIdx.x == 0) atomicExch(p.status, KDA_ERR_BAD_LENGTHS);
   int64_t incl = mine;
@@ -308,21 +244,17 @@ __global__ void __launch_bounds__(kDecThreads, 1)
   if (u0 < u1 && u0 >= before && u0 < before + mine) {
     int64_t pre = before;
     for (int b = b0; b < b1; ++b) {
-      const int len = dec_len<kOwn>(p, b);
-      const int64_t t = dec_cost(dec_tiles(len - (kOwn ? own.from(p, b, len) : 0)));
+      const int64_t t = dec_cost(dec_tiles(dec_len(p, b)));
       if (u0 < pre + t) {
         s_scan[10] = b;
         s_scan[11] = pre;
-        if (kOwn) *reinterpret_cast<int*>(smem + C::kTmem + 4) = own.g;
         break;
       }
       pre += t;
     }
   }
   __syncthreads();
-  DecPieces<kOwn> pieces;
-  pieces.own = own;
-  if (kOwn && u0 < u1) pieces.own.enter(*reinterpret_cast<int*>(smem + C::kTmem + 4), p.max_pages * p.page_size);
+  DecPieces pieces;
   pieces.unsplit = pl.whole;
   pieces.u0 = u0;
   pieces.u1 = u1;
@@ -343,20 +275,19 @@ __global__ void __launch_bounds__(kDecThreads, 1)
   if (warp == kDecCopyWarp) {
     // ---- copies: the tiles of the share into the stages, the query rows of each piece ----
     const int box = pl.box_rows;
-    DecCursor<kOwn> c;
+    DecCursor c;
     c.start(pieces, p);
     int it = 0, qi = 0;  // tiles and query blocks issued
     bool gone = false;
     while (c.ok && !gone) {
       const int s = it & 1;
-      const int valid = min(kDecTile, c.it.len - c.it.from - c.tile * kDecTile);
+      const int valid = min(kDecTile, c.it.len - c.tile * kDecTile);
       const int segs = (valid + box - 1) / box;
       // page of this lane's run of box rows (lanes below segs), fetched before the wait
       int page = 0, off = 0;
       if (lane < segs) {
-        const uint32_t j = (uint32_t)(c.it.from + c.tile * kDecTile + lane * box), in_table = j / (uint32_t)p.page_size;
-        const int32_t* at = p.table + c.it.req * p.table_stride + in_table;
-        page = kOwn ? __ldcg(at) : *at;
+        const uint32_t j = (uint32_t)(c.tile * kDecTile + lane * box), in_table = j / (uint32_t)p.page_size;
+        page = p.table[c.it.req * p.table_stride + in_table];
         off = (int)(j - in_table * (uint32_t)p.page_size);
         if (page < 0 || page >= p.num_pages) {
           atomicExch(p.status, KDA_ERR_BAD_PAGE);
@@ -399,7 +330,7 @@ __global__ void __launch_bounds__(kDecThreads, 1)
     const uint64_t d_x = smem_desc(sb, 16, kDecGroup), d_c = smem_desc(sb, kDecAtom, kDecGroup);
     const uint64_t d_q = smem_desc(sb + C::kQ, 16, 1024), d_p = smem_desc(sb + C::kP, 16, 1024);
     const uint32_t t_s = tmem + 4 * N;
-    DecCursor<kOwn> cs, co;
+    DecCursor cs, co;
     cs.start(pieces, p);
     co = cs;
     int is = 0, io = 0;  // tiles of the scores and of the values
@@ -441,7 +372,7 @@ __global__ void __launch_bounds__(kDecThreads, 1)
       // O^T += C^T P^T of tile `io`
       const int s = io & 1;
       wait(bar(C::kPReady), (uint32_t)(io & 1));
-      const int valid = min(kDecTile, co.it.len - co.it.from - co.tile * kDecTile);
+      const int valid = min(kDecTile, co.it.len - co.tile * kDecTile);
       if (valid < kDecTile) {
         // what lies behind the length takes part in the product with weight 0: it has to be finite
         for (int t = valid; t < kDecTile; ++t)
@@ -488,12 +419,7 @@ __global__ void __launch_bounds__(kDecThreads, 1)
     int it = 0;
     while (pieces.next(p)) {
       const int nt = pieces.count();
-      const bool whole = pieces.whole() && (!kOwn || pieces.from == 0);
-      if (kOwn && tid == 0 && pieces.t0 == 0)  // what is left to the join
-        pl.split[pieces.req * pl.row_blocks + rblk] =
-            whole ? make_int4(-1, 0, 0, 0)
-                  : make_int4(pieces.req, share, pieces.tiles > 0 ? (int)div_fast(pieces.pre - kDecTileCost, size) : share,
-                              pieces.from > 0 ? pieces.own.g : -1);
+      const bool whole = pieces.whole();
       float m[kM], l[kM];
 #pragma unroll
       for (int i = 0; i < kM; ++i) {
@@ -509,8 +435,8 @@ __global__ void __launch_bounds__(kDecThreads, 1)
         tc_ld16x256(tmem + lane_base + 4 * N + N * s, v);
 #pragma unroll
         for (int i = 0; i < kV; ++i) v[i] *= p.scale_log2;
-        const int j = pieces.from + tile * kDecTile + tok;
-        if (pieces.from + (tile + 1) * kDecTile > pieces.len - (p.R - 1)) {
+        const int j = tile * kDecTile + tok;
+        if ((tile + 1) * kDecTile > pieces.len - (p.R - 1)) {
           // the last tiles: row (token i, head) sees j < len - (R - 1 - i)
 #pragma unroll
           for (int i = 0; i < kM; ++i) {
@@ -609,10 +535,7 @@ __global__ void __launch_bounds__(kDecThreads, 1)
         if (lane < 4) wmax[w4 * N + 8 * (i >> 1) + c0 + (i & 1)] = l[i];
       }
       named_bar(bar_id, 128);
-      // first row of the part: two blocks of N rows a CTA, or (kOwn) the rows' own place or this CTA's behind them
-      const int64_t part_row = !kOwn ? (int64_t)(2 * blockIdx.x + (pieces.t0 > 0 ? 0 : 1)) * N
-                               : pieces.t0 > 0 ? (int64_t)p.B * rows + (int64_t)blockIdx.x * N
-                                               : (int64_t)pieces.req * rows + row0;
+      const int slot = 2 * blockIdx.x + (pieces.t0 > 0 ? 0 : 1);
       if (w4 == 0 && lane < 4) {
 #pragma unroll
         for (int i = 0; i < kM; ++i) {
@@ -621,7 +544,7 @@ __global__ void __launch_bounds__(kDecThreads, 1)
           fac[c] = sum > 0.f ? 1.0f / sum : (sum == 0.f ? 0.f : sum);
           const float lse2 = sum == 0.f ? -INFINITY : m[i] + __log2f(sum);
           if (!whole) {
-            if (!kOwn || row0 + h0 + c < rows) pl.part_lse[part_row + h0 + c] = lse2;
+            pl.part_lse[(int64_t)slot * N + h0 + c] = lse2;
           } else if (p.lse && row0 + h0 + c < rows) {
             p.lse[(int64_t)pieces.req * rows + row0 + h0 + c] = lse2 * 0.6931471805599453f;
           }
@@ -655,7 +578,7 @@ __global__ void __launch_bounds__(kDecThreads, 1)
         }
         const int left = rows - row0 - h0;  // query rows there are from this half's first
         if (!whole) {
-          float* dst = pl.part + (part_row + h0) * kLat + dim + lane;
+          float* dst = pl.part + ((int64_t)slot * N + h0) * kLat + dim + lane;
 #pragma unroll
           for (int r = 0; r < kH; ++r)
             if (r < left) dst[r * kLat] = o[r];
@@ -675,10 +598,10 @@ __global__ void __launch_bounds__(kDecThreads, 1)
     }
     tc_fence_before();
   }
-  if (!kOwn && tid == 0 && !pl.whole) {
+  if (tid == 0 && !pl.whole) {
     // what the join kernel has to do, by request or by the share a request starts in
     if (!pl.by_request) pl.split[blockIdx.x] = make_int4(-1, 0, 0, 0);
-    DecPieces<kOwn> each = pieces;
+    DecPieces each = pieces;
     each.b = u0 < u1 ? (int)s_scan[10] : p.B;
     each.pre = s_scan[11];
     while (each.next(p)) {
@@ -695,8 +618,6 @@ __global__ void __launch_bounds__(kDecThreads, 1)
   tc_fence_after();
   if (warp == kDecMmaWarp)
     asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;\n" ::"r"(tmem), "r"(C::kCols));
-  // the join waits for this kernel alone, and reads what the shared pass wrote
-  if (kOwn) asm volatile("griddepcontrol.wait;\n" ::: "memory");
 }
 
 // Joins the parts of a request that several shares hold: out = sum_k w_k o_k,
@@ -783,6 +704,8 @@ __global__ void __launch_bounds__(512) kda_latent_join_kernel(const DecodeParams
   }
 }
 
+namespace {
+
 int device_sm_count() {
   int dev = 0, sms = 0;
   if (cudaGetDevice(&dev) != cudaSuccess ||
@@ -792,8 +715,6 @@ int device_sm_count() {
   }
   return sms;
 }
-
-namespace {
 
 // Columns of the products: the query rows of a request rounded up to 16, 32 or
 // 64; blocks of 64 beyond that.
@@ -833,49 +754,27 @@ DecLayout dec_layout(const DecodeParams& p) {
   return d;
 }
 
-template <int N, bool kOwn>
+template <int N>
 bool launch_dec(const DecodeParams& p, const DecLayout& d, const DecodeMaps& maps, cudaStream_t s) {
   const unsigned ctas = (unsigned)(d.plan.row_blocks * d.plan.shares);
-  constexpr int smem = DecCfg<N>::kSmem;
   static std::once_flag once[64];
   static cudaError_t rc[64];
   int dev = 0;
   if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return false;
   std::call_once(once[dev], [&] {
-    rc[dev] = cudaFuncSetAttribute(kda_latent_decode_kernel<N, kOwn>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    rc[dev] = cudaFuncSetAttribute(kda_latent_decode_kernel<N>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                   DecCfg<N>::kSmem);
   });
   if (rc[dev] != cudaSuccess) return false;
-  if (!launch_overlapped(kda_latent_decode_kernel<N, kOwn>, dim3(ctas), kDecThreads, smem, s, 1, p, d.plan, maps))
+  if (!launch_overlapped(kda_latent_decode_kernel<N>, dim3(ctas), kDecThreads, DecCfg<N>::kSmem, s, 1, p, d.plan, maps))
     return false;
-  if (kOwn || d.plan.whole) return true;  // nothing to join
+  if (d.plan.whole) return true;  // nothing to join
   // a row a CTA where a request is in more than four parts on average, else a row a warp
   const bool wide = (int64_t)p.B * 4 < d.plan.shares;
   const int most = std::min(N, p.R * p.H);
   const dim3 grid((unsigned)d.joins, (unsigned)(wide ? most : (most + 15) / 16));
   return launch_overlapped(wide ? kda_latent_join_kernel<true> : kda_latent_join_kernel<false>, grid, 512, 0, s, 1, p,
                            d.plan, N);
-}
-
-// The tensor maps of a call; false: one could not be made.
-bool dec_maps(DecodeParams& p, const DecLayout& d, DecodeMaps& maps) {
-  memset(&maps, 0, sizeof(maps));
-  const int rows = p.R * p.H;
-  {  // query rows [B][rows][576] as [64 values][rows][9 blocks][B]: one copy brings N rows of a request
-    const cuuint64_t dims[4] = {64, (cuuint64_t)rows, (cuuint64_t)kDecChunks, (cuuint64_t)p.B};
-    const cuuint64_t strides[3] = {kLatRow * 2, 128, (cuuint64_t)rows * kLatRow * 2};
-    const cuuint32_t box[4] = {64, (cuuint32_t)d.n, (cuuint32_t)kDecChunks, 1};
-    if (!encode_map_bf16(&maps.q, p.q, 4, dims, strides, box)) return false;
-  }
-  if (p.num_pages == 0) {
-    p.max_pages = 0;  // no cache: every length is taken as 0, and nothing is copied
-    return true;
-  }
-  // the cache as [64 values][8 tokens][9 blocks][8-token groups of a page][pages]
-  const cuuint64_t dims[5] = {64, 8, (cuuint64_t)kDecChunks, (cuuint64_t)p.page_size / 8, (cuuint64_t)p.num_pages};
-  const cuuint64_t strides[4] = {(cuuint64_t)p.token_stride * 2, 128, (cuuint64_t)p.token_stride * 16,
-                                 (cuuint64_t)p.page_stride * 2};
-  const cuuint32_t box[5] = {64, 8, (cuuint32_t)kDecChunks, (cuuint32_t)d.plan.box_rows / 8, 1};
-  return encode_map_bf16(&maps.cache, p.cache, 5, dims, strides, box);
 }
 
 }  // namespace
@@ -889,34 +788,27 @@ bool launch_latent_decode(const DecodeParams& args, cudaStream_t s) {
   d.plan.part_lse = reinterpret_cast<float*>(p.ws + d.lse_at);
   d.plan.split = reinterpret_cast<int4*>(p.ws + d.split_at);
   DecodeMaps maps;
-  if (!dec_maps(p, d, maps)) return false;
-  switch (d.n) {
-    case 16: return launch_dec<16, false>(p, d, maps, s);
-    case 32: return launch_dec<32, false>(p, d, maps, s);
-    default: return launch_dec<64, false>(p, d, maps, s);
+  memset(&maps, 0, sizeof(maps));
+  const int rows = p.R * p.H;
+  {  // query rows [B][rows][576] as [64 values][rows][9 blocks][B]: one copy brings N rows of a request
+    const cuuint64_t dims[4] = {64, (cuuint64_t)rows, (cuuint64_t)kDecChunks, (cuuint64_t)p.B};
+    const cuuint64_t strides[3] = {kLatRow * 2, 128, (cuuint64_t)rows * kLatRow * 2};
+    const cuuint32_t box[4] = {64, (cuuint32_t)d.n, (cuuint32_t)kDecChunks, 1};
+    if (!encode_map_bf16(&maps.q, p.q, 4, dims, strides, box)) return false;
   }
-}
-
-OwnLayout own_layout(const DecodeParams& p) {
-  const DecLayout d = dec_layout(p);
-  return {d.n, d.plan.row_blocks, d.plan.row_blocks * d.plan.shares};
-}
-
-bool launch_latent_own(const SharedParams& sp, cudaStream_t s) {
-  DecodeParams p = sp.d;
-  DecLayout d = dec_layout(p);
-  d.plan.part = sp.own_part;
-  d.plan.part_lse = sp.own_lse;
-  d.plan.split = sp.split;
-  d.plan.by_request = 1;
-  d.plan.groups = sp.groups;
-  d.plan.early = sp.pairs > 0;
-  DecodeMaps maps;
-  if (!dec_maps(p, d, maps)) return false;
+  if (p.num_pages == 0) {
+    p.max_pages = 0;  // no cache: every length is taken as 0, and nothing is copied
+  } else {  // the cache as [64 values][8 tokens][9 blocks][8-token groups of a page][pages]
+    const cuuint64_t dims[5] = {64, 8, (cuuint64_t)kDecChunks, (cuuint64_t)p.page_size / 8, (cuuint64_t)p.num_pages};
+    const cuuint64_t strides[4] = {(cuuint64_t)p.token_stride * 2, 128, (cuuint64_t)p.token_stride * 16,
+                                   (cuuint64_t)p.page_stride * 2};
+    const cuuint32_t box[5] = {64, 8, (cuuint32_t)kDecChunks, (cuuint32_t)d.plan.box_rows / 8, 1};
+    if (!encode_map_bf16(&maps.cache, p.cache, 5, dims, strides, box)) return false;
+  }
   switch (d.n) {
-    case 16: return launch_dec<16, true>(p, d, maps, s);
-    case 32: return launch_dec<32, true>(p, d, maps, s);
-    default: return launch_dec<64, true>(p, d, maps, s);
+    case 16: return launch_dec<16>(p, d, maps, s);
+    case 32: return launch_dec<32>(p, d, maps, s);
+    default: return launch_dec<64>(p, d, maps, s);
   }
 }
 

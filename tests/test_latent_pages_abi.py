@@ -116,7 +116,7 @@ def _shared_args(over):
 @pytest.mark.parametrize("over,code", [
     (dict(q=None), 1), (dict(out=None), 1), (dict(seq_lens=None), 1), (dict(block_table=None), 1), (dict(cu_groups=None), 1),
     (dict(prefix_lens=None), 1), (dict(B=-1), 3), (dict(G=-1), 3), (dict(G=16385), 3), (dict(G=0), 14),
-    (dict(B=1 << 20, H=4096), 3), (dict(table_stride=3), 3), (dict(scale=0.0), 16), (dict(cu_groups=FAKE + 4), 9),
+    (dict(B=1 << 20, H=4096), 3), (dict(max_pages=(1 << 24) + 1, table_stride=1 << 25), 3), (dict(table_stride=3), 3), (dict(scale=0.0), 16), (dict(cu_groups=FAKE + 4), 9),
     (dict(prefix_lens=FAKE + 2), 9), (dict(q=FAKE + 8), 9), (dict(cache=_cache(page_size=100)), 17),
     (dict(cache=_cache(token_stride=570)), 15),
 ])
