@@ -47,8 +47,10 @@ constexpr int kShTile = 128;       // cached rows of a tile
 constexpr int kShRows = 128;       // query rows of an item, a CTA pair's
 constexpr int kShThreads = 352, kShWarps = kShThreads / 32;
 constexpr int kShKeyWarp = 8, kShMmaWarp = 9, kShValueWarp = 10;
-// A share's cost: 4 a tile, and what an item's set-up and output take; at least two tiles.
-constexpr int kShTileCost = 4, kShItemCost = 6, kShLeast = 2 * kShTileCost;
+// The line's costs: 4 a tile, and what an item's set-up and output take (8, 14 and 20 measured: 89.4, 88.2 and 87.6 us on
+// 24 prefixes of up to 8192); least cost of a share.  (A request's own tiles, which come from HBM, take longer than the
+// prefix's, but at 6 they made the shares less even: 95.8.)
+constexpr int kShTileCost = 4, kShItemCost = 16, kShLeast = 2 * kShTileCost;
 constexpr float kShSlack = 8.0f;   // log2 growth of a maximum that is let pass
 
 constexpr int kShKeyPart = 64 * 3 * 128;      // 64 tokens of three 64-column blocks
@@ -65,7 +67,9 @@ constexpr int kFKeys = 0, kFValues = 3, kEKeys = 5, kEValues = 8, kFQ = 10, kEQ 
               kFTail = 16, kShBars = 17;
 constexpr int kShTmem = kShBar + 8 * kShBars;
 constexpr int kShAbort = kShTmem + 8;
-constexpr int kShSmem = kShAbort + 8;
+constexpr int kShItems = (kShAbort + 8 + 15) / 16 * 16;  // the share's first items
+constexpr int kShKept = 32;
+constexpr int kShSmem = kShItems + 32 * kShKept;
 static_assert(kShK % 1024 == 0 && kShV % 1024 == 0 && kShP % 1024 == 0 && kShKeyPart % 1024 == 0,
               "operand images need 1024-byte alignment");
 static_assert(kShSmem <= 232448, "exceeds the opt-in shared memory of one CTA");
@@ -140,8 +144,8 @@ __device__ __forceinline__ SharedView shared_view(const SharedParams& p, bool al
 
 // The pieces of one share [u0, u1) of the line of costs, in order.
 struct SharedPieces {
-  const SharedItem* items;
-  int next_item, count;
+  const SharedItem *items, *kept;  // all; those from first_item on in shared memory
+  int next_item, first_item, count;
   int64_t u0, u1;
   // the current piece: its item's, the tiles [t0, t1) of all, whether it is the item's first on the line
   int group, block, common, tiles, t0, t1, leads;
@@ -149,8 +153,9 @@ struct SharedPieces {
   __device__ __forceinline__ bool next() {
     bool more = false;
     while (!more && next_item < count) {
-      const int4 a = reinterpret_cast<const int4*>(items + next_item)[0];
-      const int64_t start = items[next_item].start;
+      const SharedItem* from = next_item - first_item < kShKept ? kept + (next_item - first_item) : items + next_item;
+      const int4 a = *reinterpret_cast<const int4*>(from);
+      const int64_t start = from->start;
       if (start >= u1) break;
       ++next_item;
       group = a.x;
@@ -377,22 +382,33 @@ __global__ void __launch_bounds__(kShThreads, 1)
     it.u0 = min(total, share * size);
     it.u1 = min(total, it.u0 + size);
     it.items = sp.items;
+    it.kept = reinterpret_cast<const SharedItem*>(smem + kShItems);
     it.count = items;
     if (writes && tid == 0) *sp.head = {size, items, view.alone ? 1 : 0};
-    if (writes || (start < it.u1 && start + cost > it.u0)) {
+    const bool has = start < it.u1 && start + cost > it.u0;  // some of the share
+    int64_t begin = start;
+    if (has && start <= it.u0)
+      for (int i = i0, g = group; i < i1 && begin <= it.u0; ++i) {
+        if (per > 1) look(i, g, x);
+        begin += item_cost(x.tiles);
+        if (begin > it.u0) scan[12] = i;
+      }
+    fence_proxy_async_smem();  // (the place of first_item, last read below, goes to the tensor copies)
+    __syncthreads();
+    it.next_item = it.first_item = it.u0 < it.u1 ? (int)scan[12] : items;
+    if (writes || has) {
       for (int i = i0, g = group; i < i1; ++i) {
         if (per > 1) look(i, g, x);
         x.start = start;
         const int64_t end = start + item_cost(x.tiles);
         if (writes || (start < it.u1 && end > it.u0)) sp.items[i] = x;
-        if (start <= it.u0 && end > it.u0) scan[12] = i;
+        if (start < it.u1 && end > it.u0 && i - it.first_item < kShKept)
+          reinterpret_cast<SharedItem*>(smem + kShItems)[i - it.first_item] = x;
         start = end;
       }
     }
-    fence_proxy_async_smem();  // (the place of first_item goes to the tensor copies)
-    __syncthreads();
-    it.next_item = it.u0 < it.u1 ? (int)scan[12] : items;
-    __syncthreads();  // that of scan to the softmax
+    fence_proxy_async_smem();
+    __syncthreads();  // (and the place of scan goes to the softmax)
   }
 
   auto wait = [&](uint32_t b, uint32_t parity) {
@@ -451,11 +467,14 @@ __global__ void __launch_bounds__(kShThreads, 1)
       ++q;
       const int source = source_of();
       tile.start(view, it);
-      for (int t = it.t0; t < it.t1 && !gone; ++t, ++n) {
-        if (t > it.t0) tile.advance(view, it, t);
-        const int runs = (min(64, max(0, tile.valid - rank * 64)) + box - 1) / box;  // what is not copied is masked
-        int page = 0, group = 0;
+      int runs, page, group;  // of this CTA's 64 tokens; what is not copied is masked
+      auto look = [&]() {
+        runs = (min(64, max(0, tile.valid - rank * 64)) + box - 1) / box;
+        page = group = 0;
         if (lane < runs) page = place(tile.request < 0 ? source : tile.request, tile.token + rank * 64 + lane * box, group);
+      };
+      look();
+      for (int t = it.t0; t < it.t1 && !gone; ++t, ++n) {
         for (int c = 0; c < 3; ++c) {
           if (n > 0) wait(bar(kEKeys + c), (uint32_t)((n - 1) & 1));
           if ((gone = stop())) break;
@@ -464,6 +483,10 @@ __global__ void __launch_bounds__(kShThreads, 1)
           __syncwarp();
           if (lane < runs)
             tma_pair_5d(sb + kShK + c * kShKeyPart + lane * box * (3 * 128), &maps.keys, 0, 0, 3 * c, group, page, full);
+        }
+        if (t + 1 < it.t1) {  // the next tile's places while this one's copies run
+          tile.advance(view, it, t + 1);
+          look();
         }
       }
     }
@@ -705,6 +728,27 @@ __global__ void __launch_bounds__(kShThreads, 1)
       const int64_t warp_row = at - r + 32 * (w4 & 1);  // this warp's first row; all of one part are side by side
       const int64_t rows_there = rows - ((int64_t)it.block * kShRows + 64 * rank + 32 * (w4 & 1));
       const int dims = 256 * side + 128 * right;
+      auto turned = [&](const uint32_t (&x)[16], auto store) {  // 64 bytes of a row a lane
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+          asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};\n" ::"r"(turn + lane * 64 + ((i ^ (lane >> 1 & 3)) << 4)),
+                       "r"(x[4 * i]), "r"(x[4 * i + 1]), "r"(x[4 * i + 2]), "r"(x[4 * i + 3])
+                       : "memory");
+        __syncwarp();
+        uint4 y[4];
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          const int row_of = 8 * k + (lane >> 2);
+          asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];\n"
+                       : "=r"(y[k].x), "=r"(y[k].y), "=r"(y[k].z), "=r"(y[k].w)
+                       : "r"(turn + row_of * 64 + (((lane & 3) ^ (row_of >> 1 & 3)) << 4))
+                       : "memory");
+        }
+#pragma unroll
+        for (int k = 0; k < 4; ++k)
+          if (8 * k + (lane >> 2) < rows_there) store(8 * k + (lane >> 2), y[k]);
+        __syncwarp();
+      };
 #pragma unroll 1
       for (int c = 0; c < 128; c += 32) {
         float o[32];
@@ -716,39 +760,20 @@ __global__ void __launch_bounds__(kShThreads, 1)
 #pragma unroll
           for (int i = 0; i < 32; ++i) o[i] = 0.f;
         }
-        // fp32 parts 16 dimensions at a time, results 32
-        for (int h = 0; h < (whole ? 1 : 2); ++h) {
+        uint32_t x[16];
+        if (whole) {
 #pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            uint4 x;
-            if (whole) {
-              x = make_uint4(pack_bf16(o[8 * i], o[8 * i + 1]), pack_bf16(o[8 * i + 2], o[8 * i + 3]),
-                             pack_bf16(o[8 * i + 4], o[8 * i + 5]), pack_bf16(o[8 * i + 6], o[8 * i + 7]));
-            } else {
-              const float a = h ? o[16 + 4 * i] : o[4 * i], b = h ? o[17 + 4 * i] : o[4 * i + 1];
-              const float e = h ? o[18 + 4 * i] : o[4 * i + 2], g = h ? o[19 + 4 * i] : o[4 * i + 3];
-              x = make_uint4(__float_as_uint(a), __float_as_uint(b), __float_as_uint(e), __float_as_uint(g));
-            }
-            asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};\n" ::"r"(turn + lane * 64 + ((i ^ (lane >> 1 & 3)) << 4)),
-                         "r"(x.x), "r"(x.y), "r"(x.z), "r"(x.w)
-                         : "memory");
-          }
-          __syncwarp();
+          for (int i = 0; i < 16; ++i) x[i] = pack_bf16(o[2 * i], o[2 * i + 1]);
+          uint16_t* dst = p.out + warp_row * kLat + dims + c + 8 * (lane & 3);
+          turned(x, [&](int row_of, const uint4& y) { *reinterpret_cast<uint4*>(dst + row_of * kLat) = y; });
+        } else {
+          float* dst = sp.part + warp_row * kLat + dims + c + 4 * (lane & 3);
 #pragma unroll
-          for (int k = 0; k < 4; ++k) {
-            const int row_of = 8 * k + (lane >> 2), piece = lane & 3;
-            uint4 x;
-            asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];\n"
-                         : "=r"(x.x), "=r"(x.y), "=r"(x.z), "=r"(x.w)
-                         : "r"(turn + row_of * 64 + ((piece ^ (row_of >> 1 & 3)) << 4))
-                         : "memory");
-            if (row_of < rows_there) {
-              const int64_t to = (warp_row + row_of) * kLat + dims + c;
-              if (whole) *reinterpret_cast<uint4*>(p.out + to + 8 * piece) = x;
-              else *reinterpret_cast<uint4*>(sp.part + to + 16 * h + 4 * piece) = x;
-            }
+          for (int h = 0; h < 2; ++h) {
+#pragma unroll
+            for (int i = 0; i < 16; ++i) x[i] = __float_as_uint(o[16 * h + i]);
+            turned(x, [&](int row_of, const uint4& y) { *reinterpret_cast<uint4*>(dst + 16 * h + row_of * kLat) = y; });
           }
-          __syncwarp();
         }
       }
       tc_fence_before();
@@ -774,7 +799,8 @@ __global__ void __launch_bounds__(256) kda_latent_shared_join_kernel(const Share
   const SharedItem item = p.items[blockIdx.x];
   // its tiles' places on the line, hence the shares that hold them
   const int64_t first = div_costs(item.start + kShItemCost, head.size);
-  const int parts = item.tiles == 0 ? 1 : (int)(div_costs(item.start + item_cost(item.tiles - 1), head.size) - first) + 1;
+  const int64_t last = item.start + item_cost(max(0, item.tiles - 1));
+  const int parts = (int)(div_costs(last, head.size) - first) + 1;
   if (parts == 1) return;
   const int64_t rows_of = (int64_t)d.R * d.H, all = (int64_t)d.B * rows_of;
   const int64_t c = head.alone ? 0 : p.groups.cu[item.group], end = head.alone ? d.B : p.groups.cu[item.group + 1];
