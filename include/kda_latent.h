@@ -185,12 +185,11 @@ int kda_latent_decode(const kda_latent_decode_args *args, void *workspace, size_
  * holds at most 2^30 tokens, and G is at most KDA_LATENT_SHARED_GROUPS.
  * Prefix and remaining tokens are joined by their fp32 parts, so outputs have the
  * error of kda_latent_decode's; they are not bit for bit the same.
- * Where the tables hold little (B * max_pages * page_size tokens, times the blocks of
- * 64 rows that R * H make, are at most KDA_LATENT_SHARED_TOKENS + 16 B R H) the call
- * is kda_latent_decode, which is faster there; the values of cu_groups and
- * prefix_lens are then not looked at.
+ * Where the tables hold little (B * max_pages * page_size tokens, times the square of
+ * ceil(R H / 64), are at most KDA_LATENT_SHARED_TOKENS) the call is kda_latent_decode,
+ * which is faster there; the values of cu_groups and prefix_lens are then not looked at.
  */
-#define KDA_LATENT_SHARED_TOKENS 131072
+#define KDA_LATENT_SHARED_TOKENS 98304
 #define KDA_LATENT_SHARED_GROUPS 16384
 typedef struct kda_latent_decode_shared_args {
   kda_latent_decode_args decode;

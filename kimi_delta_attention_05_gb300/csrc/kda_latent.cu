@@ -281,12 +281,13 @@ int check_shared(const kda_latent_decode_shared_args* a) {
   return KDA_OK;
 }
 
-// Whether a call's tables hold so little that it is taken as kda_latent_decode.  Device times alone and shared, us: 8
-// requests behind 1024 tokens, 16 heads 12.5 and 18.8; 32 behind 4096, 32 heads 33.0 and 31.3; 128 behind 1024,
-// 16 heads 29.6 and 29.8, behind 2048 46.8 and 32.5; 128 behind 1024, 128 heads 72.4 and 78.6, behind 2048 114 and 96.
+// Whether a call's tables hold so little that it is taken as kda_latent_decode, whose blocks of 64 rows read each
+// token once a block.  Device times alone and shared, us: 8 requests of 1088 tokens, 16 heads 12.2 and 19.4; 32 of 2112,
+// 16 heads 19.8 and 23.2; 128 of 576, 32 heads 24.0 and 26.5; 128 of 1088, 32 heads 33.9 and 29.1; with two blocks 8 of 1088,
+// 128 heads 20.8 and 20.2; 32 of 1088 30.9 and 26.8.
 bool shares_little(const kda_latent_decode_args& a) {
-  const int64_t rows = a.B * a.R * a.H, blocks = (a.R * a.H + 63) / 64;  // (at most 2^20 * 2^31 * 2^10)
-  return a.B * (a.max_pages * a.cache.page_size) * blocks <= KDA_LATENT_SHARED_TOKENS + 16 * rows;
+  const int64_t tokens = a.B * (a.max_pages * a.cache.page_size), blocks = (a.R * a.H + 63) / 64;
+  return tokens <= KDA_LATENT_SHARED_TOKENS && tokens * blocks * blocks <= KDA_LATENT_SHARED_TOKENS;
 }
 
 DecodeParams decode_params(const kda_latent_decode_args* a) {

@@ -111,35 +111,34 @@ __device__ __forceinline__ int64_t div_costs(int64_t a, int64_t b) {
 }
 __device__ __forceinline__ int64_t item_cost(int tiles) { return kShItemCost + (int64_t)tiles * kShTileCost; }
 
-// What one call's groups and lengths mean.
+// What one call's groups and lengths mean, in 32 bits (offsets that do not fit are found before they are used): the code
+// of the set-up runs once, and every instruction of it is fetched for that.
 struct SharedView {
   const int64_t* cu;
   const int32_t *prefix, *lens;
   int B, R, H, rows_of;        // rows_of: R H, the rows of a request
-  int64_t cap;                 // tokens that a table can hold
+  int cap;                     // tokens that a table can hold
   bool alone;                  // offsets that do not fit: all requests are one group without a prefix
-  __device__ __forceinline__ int64_t first(int g) const { return alone ? 0 : cu[g]; }
-  __device__ __forceinline__ int64_t end(int g) const { return alone ? B : cu[g + 1]; }
+  __device__ __forceinline__ int first(int g) const { return alone ? 0 : (int)cu[g]; }
+  __device__ __forceinline__ int end(int g) const { return alone ? B : (int)cu[g + 1]; }
   // tokens of the prefix that are shared: whole tiles, of groups of two and more
-  __device__ __forceinline__ int tokens(int g) const {
-    if (alone || cu[g + 1] - cu[g] < 2) return 0;
-    const int64_t len = prefix[g];
-    return (int)((len < 0 ? 0 : (len > cap ? cap : len)) / kShTile * kShTile);
+  __device__ __forceinline__ int tokens(int g, int requests) const {
+    return alone || requests < 2 ? 0 : min(max(prefix[g], 0), cap) / kShTile * kShTile;
   }
-  __device__ __forceinline__ int len(int b) const {
-    const int64_t n = lens[b];
-    return (int)(n < 0 ? 0 : (n > cap ? cap : n));
-  }
+  __device__ __forceinline__ int len(int b) const { return min(max(lens[b], 0), cap); }
   // first token that a request takes on its own: behind the shared ones if all its new tokens see them
   __device__ __forceinline__ int own_from(int n, int shared) const { return shared > 0 && n - (R - 1) >= shared ? shared : 0; }
   __device__ __forceinline__ int own_tiles(int b, int shared) const {
     const int n = len(b);
     return (n - own_from(n, shared) + kShTile - 1) / kShTile;
   }
+  // the request, counted within its group, that has a row
+  __device__ __forceinline__ int request(int row) const { return (int)((uint32_t)row / (uint32_t)rows_of); }
 };
 
 __device__ __forceinline__ SharedView shared_view(const SharedParams& p, bool alone) {
-  return {p.groups.cu, p.groups.prefix, p.d.lens, p.d.B, p.d.R, p.d.H, p.d.R * p.d.H, p.d.max_pages * p.d.page_size, alone};
+  return {p.groups.cu, p.groups.prefix, p.d.lens, p.d.B, p.d.R, p.d.H, p.d.R * p.d.H, (int)(p.d.max_pages * p.d.page_size),
+          alone};
 }
 
 // The pieces of one share [u0, u1) of the line of costs, in order.
@@ -193,7 +192,8 @@ struct SharedPieces {
 struct SharedTile {
   int request;      // whose own tokens, or -1: the prefix's
   int token, valid; // first token, and how many
-  int last, left;   // last request of the item; tiles of this request behind the current one
+  int first, last;  // the item's requests
+  int left;         // tiles of this request behind the current one
   int shared;       // tokens of the prefix that are shared
   __device__ __forceinline__ void own(const SharedView& v, int b, int skip) {
     for (;; ++b) {
@@ -210,21 +210,27 @@ struct SharedTile {
     valid = min(kShTile, n - token);
   }
   __device__ __forceinline__ void start(const SharedView& v, const SharedPieces& it) {
-    const int64_t c = v.first(it.group);
-    shared = v.tokens(it.group);
-    const int64_t rows = (v.end(it.group) - c) * v.rows_of, row = (int64_t)it.block * kShRows;
-    last = (int)(c + (min(rows, row + kShRows) - 1) / v.rows_of);
+    const int c = v.first(it.group), n = v.end(it.group) - c, row = it.block * kShRows;
+    shared = v.tokens(it.group, n);
+    first = c + v.request(row);
+    last = c + v.request(min(n * v.rows_of, row + kShRows) - 1);
     request = -1;
     token = it.t0 * kShTile;
     valid = kShTile;
-    if (it.t0 >= it.common && it.t0 < it.t1) own(v, (int)(c + row / v.rows_of), it.t0 - it.common);
+    if (it.t0 >= it.common && it.t0 < it.t1) own(v, first, it.t0 - it.common);
+  }
+  // The request whose row of the table names the prefix: the first that takes it as shared, where there is one.
+  __device__ __forceinline__ int source(const SharedView& v) const {
+    int b = first;
+    while (b < last && v.own_from(v.len(b), shared) == 0) ++b;
+    return b;
   }
   // to tile t of the piece, which has one
   __device__ __forceinline__ void advance(const SharedView& v, const SharedPieces& it, int t) {
     if (t < it.common) {
       token += kShTile;
     } else if (request < 0) {
-      own(v, (int)(v.first(it.group) + (int64_t)it.block * kShRows / v.rows_of), 0);
+      own(v, first, 0);
     } else if (left > 0) {
       --left;
       token += kShTile;
@@ -270,95 +276,88 @@ __global__ void __launch_bounds__(kShThreads, 1)
     asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;\n" ::"r"(sb + kShTmem), "r"(512u));
     asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;\n");
   }
+  tc_fence_before();
+  __syncwarp();
+  cluster_arrive();  // (waited for behind the plan)
   // (set up while the kernel before this one ends)
   asm volatile("griddepcontrol.wait;\n" ::: "memory");
 
   // ---- this pair's share of the line: every CTA finds the items and their costs for itself ----
-  uint32_t tmem;
   SharedPieces it;
   SharedView view = shared_view(sp, false);
   {
     int* first_item = reinterpret_cast<int*>(smem);                // [G] items before each group
     int64_t* scan = reinterpret_cast<int64_t*>(smem + kShMax);     // sums of the warps; then the share's first item
     const bool writes = blockIdx.x == 0;
-    auto prefix_sum = [&](int64_t x, int64_t& total) {             // over the threads before this one
-      int64_t upto = x;
+    auto prefix_sum = [&](auto x, auto& total) {                   // over the threads before this one
+      auto upto = x;
 #pragma unroll
       for (int o = 1; o < 32; o <<= 1) {
-        const int64_t y = __shfl_up_sync(0xffffffffu, upto, o);
+        const auto y = __shfl_up_sync(0xffffffffu, upto, o);
         if (lane >= o) upto += y;
       }
       if (lane == 31) scan[warp] = upto;
       __syncthreads();
-      int64_t before = 0;
+      upto -= x;
       total = 0;
-#pragma unroll
+#pragma unroll 1
       for (int w = 0; w < kShWarps; ++w) {
-        const int64_t s = scan[w];
-        if (w < warp) before += s;
+        const auto s = (decltype(x))scan[w];
+        if (w < warp) upto += s;
         total += s;
       }
       __syncthreads();  // sums are read
-      return before + upto - x;
+      return upto;
     };
     // groups: a run a thread
     int G = sp.groups.G;
     const int run = (G + kShThreads - 1) / kShThreads, g0 = min(G, tid * run), g1 = min(G, g0 + run);
-    int bad = 0, far = 0;
-    int64_t mine = 0;
-    auto blocks_of = [&](int64_t first, int64_t end) { return ((end - first) * view.rows_of + kShRows - 1) / kShRows; };
+    int bad = 0, far = 0, mine = 0;
+    auto blocks_of = [&](int requests) { return (int)(((uint32_t)(requests * view.rows_of) + kShRows - 1) / kShRows); };
     for (int g = g0; g < g1; ++g) {
-      const int64_t first = view.cu[g], end = view.cu[g + 1], len = view.prefix[g];
+      const int64_t first = view.cu[g], end = view.cu[g + 1];
+      const int len = view.prefix[g];
       bad |= first < 0 || end < first || end > p.B || (g == 0 && first != 0) || (g == G - 1 && end != p.B);
-      if (!bad) mine += blocks_of(first, end);
+      if (!bad) mine += blocks_of((int)(end - first));
       far |= end > first && (len < 0 || len > view.cap);
     }
-    // (the loads above while the set-up of the other warps and of the other CTA ends)
-    tc_fence_before();
-    __syncthreads();
-    cluster_sync();  // the other CTA's barriers are ready too
-    tc_fence_after();
-    tmem = *reinterpret_cast<volatile uint32_t*>(smem + kShTmem);
-    asm volatile("griddepcontrol.launch_dependents;\n" ::: "memory");
     bad = __syncthreads_or(bad);
     if (writes && far) atomicExch(p.status, KDA_ERR_BAD_LENGTHS);
     if (bad) {  // (a group without a prefix: every request on its own)
       if (writes && tid == 0) atomicExch(p.status, KDA_ERR_BAD_SEQLENS);
       view.alone = true;
       G = 1;
-      mine = tid == 0 ? blocks_of(0, p.B) : 0;
+      mine = tid == 0 ? blocks_of(p.B) : 0;
     }
-    int64_t count;
-    int64_t at = prefix_sum(mine, count);
+    int items, at = prefix_sum(mine, items);
     if (bad) {
       if (tid == 0) first_item[0] = 0;
     } else {
       for (int g = g0; g < g1; ++g) {
-        first_item[g] = (int)at;
-        at += blocks_of(view.cu[g], view.cu[g + 1]);
+        first_item[g] = at;
+        at += blocks_of(view.end(g) - view.first(g));
       }
     }
     __syncthreads();
     // items: a run a thread
-    const int items = (int)count, per = (items + kShThreads - 1) / kShThreads;
+    const int per = (items + kShThreads - 1) / kShThreads;
     const int i0 = min(items, tid * per), i1 = min(items, i0 + per);
     int odd = 0, group = 0;
     auto look = [&](int i, int& g, SharedItem& x) {  // item i, g being the group of the one before
       while (g + 1 < G && first_item[g + 1] <= i) ++g;
       x.group = g;
       x.block = i - first_item[g];
-      const int64_t first = view.first(g), end = view.end(g), row = (int64_t)x.block * kShRows;
-      const int shared = view.tokens(g);
-      const int b0 = (int)(first + row / view.rows_of);
-      const int b1 = (int)(first + (min((end - first) * view.rows_of, row + kShRows) - 1) / view.rows_of);
+      const int first = view.first(g), n = view.end(g) - first, row = x.block * kShRows;
+      const int shared = view.tokens(g, n);
+      const int b0 = first + view.request(row), b1 = first + view.request(min(n * view.rows_of, row + kShRows) - 1);
       x.common = 0;
       x.tiles = 0;
 #pragma unroll 4
       for (int b = b0; b <= b1; ++b) {
-        const int raw = view.lens[b], n = view.len(b), from = view.own_from(n, shared);
-        odd |= raw != n;
+        const int raw = view.lens[b], len = min(max(raw, 0), view.cap), from = view.own_from(len, shared);
+        odd |= raw != len;
         if (from > 0) x.common = shared / kShTile;
-        x.tiles += (n - from + kShTile - 1) / kShTile;
+        x.tiles += (len - from + kShTile - 1) / kShTile;
       }
       x.tiles += x.common;
     };
@@ -393,7 +392,6 @@ __global__ void __launch_bounds__(kShThreads, 1)
         begin += item_cost(x.tiles);
         if (begin > it.u0) scan[12] = i;
       }
-    fence_proxy_async_smem();  // (the place of first_item, last read below, goes to the tensor copies)
     __syncthreads();
     it.next_item = it.first_item = it.u0 < it.u1 ? (int)scan[12] : items;
     if (writes || has) {
@@ -407,9 +405,13 @@ __global__ void __launch_bounds__(kShThreads, 1)
         start = end;
       }
     }
-    fence_proxy_async_smem();
-    __syncthreads();  // (and the place of scan goes to the softmax)
+    fence_proxy_async_smem();  // (the place of first_item goes to the tensor copies)
+    __syncthreads();           // (and that of scan to the softmax)
   }
+  cluster_wait();  // the other CTA's barriers are ready too
+  tc_fence_after();
+  const uint32_t tmem = *reinterpret_cast<volatile uint32_t*>(smem + kShTmem);
+  asm volatile("griddepcontrol.launch_dependents;\n" ::: "memory");
 
   auto wait = [&](uint32_t b, uint32_t parity) {
     if (mbar_try_wait(b, parity) || *s_abort) return;
@@ -428,15 +430,6 @@ __global__ void __launch_bounds__(kShThreads, 1)
     const long long t0 = clock64();
     while (clock64() - t0 < (1LL << 22)) {
     }
-  };
-  // The request of a piece's item whose row of the table names the prefix: the first that takes it as shared.
-  auto source_of = [&]() {
-    const int64_t c = view.first(it.group), row = (int64_t)it.block * kShRows;
-    const int shared = view.tokens(it.group);
-    int b = (int)(c + row / view.rows_of);
-    if (it.common > 0)
-      while (view.own_from(view.len(b), shared) == 0) ++b;  // (there is one)
-    return b;
   };
   // Page and 8-token group of the run of `box` tokens that starts at a token of a request.
   auto place = [&](int request, int token, int& group) {
@@ -462,11 +455,11 @@ __global__ void __launch_bounds__(kShThreads, 1)
       if (lane == 0) {
         const uint32_t full = lead(kFQ);
         mbar_expect_tx_cluster(full, kShQBytes);
-        tma_pair_3d(sb + kShQ, &maps.q, 0, (int)view.first(it.group) * view.rows_of + it.block * kShRows + rank * 64, 0, full);
+        tma_pair_3d(sb + kShQ, &maps.q, 0, view.first(it.group) * view.rows_of + it.block * kShRows + rank * 64, 0, full);
       }
       ++q;
-      const int source = source_of();
       tile.start(view, it);
+      const int source = it.t0 < it.common ? tile.source(view) : 0;
       int runs, page, group;  // of this CTA's 64 tokens; what is not copied is masked
       auto look = [&]() {
         runs = (min(64, max(0, tile.valid - rank * 64)) + box - 1) / box;
@@ -499,8 +492,8 @@ __global__ void __launch_bounds__(kShThreads, 1)
     SharedTile tile;
     while (!gone && it.next()) {
       if (it.t0 == it.t1) continue;
-      const int source = source_of();
       tile.start(view, it);
+      const int source = it.t0 < it.common ? tile.source(view) : 0;
       for (int t = it.t0; t < it.t1 && !gone; ++t, ++n) {
         if (t > it.t0) tile.advance(view, it, t);
         int page = 0, group = 0;
@@ -619,18 +612,18 @@ __global__ void __launch_bounds__(kShThreads, 1)
     SharedTile tile;
     while (it.next()) {
       // this thread's row: its request, the tokens that it sees, whether it sees the shared ones
-      const int64_t first = view.first(it.group), rows = (view.end(it.group) - first) * view.rows_of;
-      const int64_t row = (int64_t)it.block * kShRows + 64 * rank + r;  // of the group
+      tile.start(view, it);
+      const int first = view.first(it.group), rows = (view.end(it.group) - first) * view.rows_of;
+      const int row = it.block * kShRows + 64 * rank + r;  // of the group
       int request = -2, seen = 0;
       bool sees = false;
       if (row < rows) {
-        const int b = (int)(row / view.rows_of), len = view.len((int)first + b);
-        request = (int)first + b;
-        seen = len - (view.R - 1 - (int)(row - (int64_t)b * view.rows_of) / view.H);
-        sees = view.own_from(len, view.tokens(it.group)) > 0;
+        const int b = view.request(row), len = view.len(first + b);
+        request = first + b;
+        seen = len - (view.R - 1 - (int)((uint32_t)(row - b * view.rows_of) / (uint32_t)view.H));
+        sees = view.own_from(len, tile.shared) > 0;
       }
       float m = -INFINITY, l = 0.f;
-      tile.start(view, it);
       for (int t = it.t0; t < it.t1; ++t, ++n) {
         if (t > it.t0) tile.advance(view, it, t);
         // how many of the thread's 32 tokens its row sees
@@ -711,8 +704,8 @@ __global__ void __launch_bounds__(kShThreads, 1)
       const bool whole = it.whole(), there = row < rows;
       const float lse2 = sum == 0.f ? -INFINITY : m + __log2f(sum);
       // the row in q, and of a part: a row's first at its own place, a later one at this share's
-      const int64_t global = first * view.rows_of + row;
-      const int64_t at = whole || it.leads ? global : (int64_t)p.B * view.rows_of + (int64_t)share * kShRows + 64 * rank + r;
+      const int64_t at = whole || it.leads ? (int64_t)first * view.rows_of + row
+                                           : (int64_t)p.B * view.rows_of + (int64_t)share * kShRows + 64 * rank + r;
       if (quarter == 0 && there) {
         if (!whole) sp.part_lse[at] = lse2;
         else if (p.lse) p.lse[at] = lse2 * 0.6931471805599453f;
@@ -726,7 +719,7 @@ __global__ void __launch_bounds__(kShThreads, 1)
       // rows at a time; a thread's own row at a time, each store touched 32 lines and the 128 KB took 12000 cycles.
       const uint32_t turn = sb + kShP + warp * 2048;
       const int64_t warp_row = at - r + 32 * (w4 & 1);  // this warp's first row; all of one part are side by side
-      const int64_t rows_there = rows - ((int64_t)it.block * kShRows + 64 * rank + 32 * (w4 & 1));
+      const int rows_there = rows - (row - lane);
       const int dims = 256 * side + 128 * right;
       auto turned = [&](const uint32_t (&x)[16], auto store) {  // 64 bytes of a row a lane
 #pragma unroll

@@ -36,7 +36,7 @@ def _rand(gen, *shape, std=1.0):
 
 def _wide(B, page, R, H):
     """Pages of a table that the call does not take as latent_decode (KDA_LATENT_SHARED_TOKENS)."""
-    return (131072 + 16 * B * R * H) // max(1, B * page * (-(-R * H // 64))) + 1
+    return 98304 // max(1, B * page * (-(-R * H // 64)) ** 2) + 1
 
 
 def _batch(members, prefix, tails, page, R, H, seed=0, std=1.0, spare=2, rows=None, wide=True):
@@ -140,7 +140,7 @@ def test_tables_that_hold_little():
 def test_tables_about_as_wide_as_the_limit(more):
     batch = _batch([4, 4], [1000, 600], [20] * 8, 16, 1, 40, seed=30 + more)
     q, cache, table, lens, cu, prefix = batch
-    width = (131072 + 16 * 8 * 40) // (8 * 16) + more
+    width = 98304 // (8 * 16) + more
     batch[2] = torch.cat([table, torch.full((8, 9), 1 << 30, **I32)], 1)[:, :width]
     _run(batch)
 
