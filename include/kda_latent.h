@@ -177,14 +177,17 @@ int kda_latent_decode(const kda_latent_decode_args *args, void *workspace, size_
  *                pages, the rows behind them may be copies
  * Which request's row names the pages that are read for a shared prefix is not
  * said.  A request that does not see the whole prefix (a shorter or an empty one)
- * is taken on its own, as are the requests of groups of one.  The prefix_lens of a group
- * without requests is not looked at; another below 0
- * or beyond the table is taken as the nearer bound and sets KDA_ERR_BAD_LENGTHS;
- * offsets that do not go from 0 to B without decreasing set KDA_ERR_BAD_SEQLENS, and
- * every request is taken on its own.  B * R * H is below 2^31 - 128, a table
+ * is taken on its own, as are the requests of groups of one.  The prefix_lens of a
+ * group without requests is not looked at; another below 0 or beyond the table is
+ * taken as the nearer bound and sets KDA_ERR_BAD_LENGTHS; offsets that do not go from 0
+ * to B without decreasing set KDA_ERR_BAD_SEQLENS, and every request is taken on its
+ * own.  B * R * H is below 2^31 - 128, a table
  * holds at most 2^30 tokens, and G is at most KDA_LATENT_SHARED_GROUPS.
- * Prefix and remaining tokens are joined by their fp32 parts, so outputs have the
- * error of kda_latent_decode's; they are not bit for bit the same.
+ * The cached rows of all requests of a group have to be finite, within their lengths:
+ * a request's tokens take part with weight 0 in the products of its group's others.
+ * What the cache holds behind a request's length is never used, whatever it is.
+ * Parts are joined in fp32, so outputs have the error of kda_latent_decode's; they are
+ * not bit for bit the same, but do not depend on anything but the arguments.
  * Where the tables hold little (B * max_pages * page_size tokens, times the square of
  * ceil(R H / 64), are at most KDA_LATENT_SHARED_TOKENS) the call is kda_latent_decode,
  * which is faster there; the values of cu_groups and prefix_lens are then not looked at.

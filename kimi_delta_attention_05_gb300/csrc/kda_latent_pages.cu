@@ -73,7 +73,9 @@ __device__ __forceinline__ int warp_sum(int x) {
 //
 // A CTA takes four groups of eight rows at a time (36.9 KB), a thread eight 16-byte
 // pieces of them, all loaded before the first is stored: enough bytes in flight for
-// HBM with a few CTAs an SM, and any page size is whole groups.
+// HBM with a few CTAs an SM, and any page size is whole groups.  8000 pages of 16
+// tokens, 295 MB read and written: 49.7 us, 5.9 TB/s; 33 pages of 64 in 2.8 us, the
+// latency of a launch.
 struct CopyPlace {
   const uint16_t* src;  // nullptr: nothing to copy
   uint16_t* dst;
@@ -148,6 +150,8 @@ __global__ void __launch_bounds__(kCopyThreads) kda_latent_copy_kernel(const Cop
 // number sum_{e < f} [t_e mod P > 0] with the last t_f mod P rows.  Every CTA checks
 // all forks and counts the pages of those before its own for itself (as the plan
 // kernel does: a second launch would cost more), then does its share of one fork.
+// Bound by launch and three rounds of latency: 8 children of 1000 tokens in 3.4 us, 256
+// of up to 8192 tokens, 17.7 MB of rows and entries, in 6.6.
 struct ForkParams {
   const int32_t *parents, *children, *take, *cached;
   int32_t* table;
@@ -235,7 +239,8 @@ __global__ void __launch_bounds__(kCopyThreads) kda_latent_fork_kernel(const For
 // stands between them, a CTA lists an eighth, and its place in the list comes from
 // the others' numbers over distributed shared memory: one launch, no workspace.  Eight
 // SMs take 2.5 cycles an atomic each, so calls with many entries have a kernel on all
-// SMs do the counts first.
+// SMs do the counts first.  16 rows of up to 64 pages 5.4 us; 256 rows of up to 1024,
+// 100000 pages, 28 us in one kernel and 17.4 in two; a million pages listed in 31 us.
 struct ReleaseParams {
   const int32_t *rows, *keep, *cached, *table;
   int64_t table_stride, max_pages;
@@ -280,7 +285,7 @@ __device__ __forceinline__ bool release_rows(const ReleaseParams& p, uint32_t* i
 __device__ __forceinline__ void release_counts(const ReleaseParams& p, const Dropped* rows, int cta, int ctas) {
   const int lane = threadIdx.x & 31, warps = ctas * (kPageThreads / 32);
   const int part = (int)min((p.F * p.max_pages / warps / 256 + 1) * 256, (int64_t)1 << 30);
-  const int parts = ((int)p.max_pages + part - 1) / part;  // (parts * F is at most about the warps and F)
+  const int parts = (int)(((uint32_t)p.max_pages + part - 1) / part);  // (parts * F is at most about the warps and F)
   for (int i = cta * (kPageThreads / 32) + (threadIdx.x >> 5); i < parts * p.F; i += warps) {
     const int f = i / parts;
     Dropped d;
@@ -391,7 +396,8 @@ __global__ void __launch_bounds__(kPageThreads) kda_latent_release_kernel(const 
 // order.  A cluster of eight CTAs keeps a bit a page in distributed shared memory,
 // an eighth each: marks, counts and places need its barriers and no other memory.
 // A second kernel moves the rows and renames the tables' entries: no page is both
-// read and written.
+// read and written.  8 requests of up to 512 tokens 8.7 us; 72 MB to move, 31.8 us, 8 of
+// them the list's.
 struct CompactParams {
   const int32_t *cached, *table;
   int32_t* table_out;
@@ -435,7 +441,7 @@ __global__ void __launch_bounds__(kPageThreads) kda_latent_compact_kernel(const 
   {  // warps take equal parts of rows
     const int warps = kPageCluster * kPageThreads / 32;
     const int part = (int)min((p.B * p.max_pages / warps / 128 + 1) * 128, (int64_t)1 << 30);
-    const int parts = ((int)p.max_pages + part - 1) / part;  // (parts * B is at most about the warps and B)
+    const int parts = (int)(((uint32_t)p.max_pages + part - 1) / part);  // (parts * B is at most about the warps and B)
     for (int i = rank * (kPageThreads / 32) + warp; i < parts * p.B; i += warps) {
       const int b = i / parts;
       const int32_t* ids = p.table + b * p.table_stride;
@@ -540,7 +546,8 @@ __global__ void __launch_bounds__(kCopyThreads) kda_latent_move_kernel(const Com
 
 namespace {
 
-// Entries from which on the counts go to a kernel of their own.
+// Entries from which on the counts go to a kernel of their own (16 rows of 1024 entries 7.9 us in one kernel, 256 of 64
+// 6.8; 256 of 256 22 in one and 12 in two).
 constexpr int64_t kReleaseApart = 32768;
 
 bool al4(const void* p) { return ((uintptr_t)p & 3) == 0; }

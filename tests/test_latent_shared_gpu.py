@@ -197,6 +197,28 @@ def test_many_groups():
     _run(_batch(members, [(g * 37) % 400 for g in range(300)], [1 + b % 40 for b in range(n)], 16, 1, 16, seed=7))
 
 
+def test_more_items_than_a_share_keeps_at_hand():
+    """Groups of one, each an item of its own: some tens of items a share, some without a token."""
+    n = 6000
+    lens = [(b * 7) % 5 for b in range(n)]
+    _run(_batch([1] * n, [0] * n, lens, 8, 1, 2, seed=31))
+
+
+def test_the_most_groups_of_a_call():
+    """16384 of them, most without requests."""
+    members = [0] * 16384
+    for g in range(0, 16384, 500):
+        members[g] = 1 + g % 3
+    members[-1] = 2
+    n = sum(members)
+    _run(_batch(members, [(g % 400) if m else 0 for g, m in enumerate(members)], [1 + b % 30 for b in range(n)], 16, 1, 16, seed=32))
+
+
+@pytest.mark.parametrize("H,R", [(1, 1), (3, 2), (200, 1), (65, 3)])
+def test_many_requests_an_item_and_many_items_a_request(H, R):
+    _run(_batch([150, 40], [260, 129], [R + 29 * b % 300 for b in range(190)], 32, R, H, seed=H))
+
+
 def test_large_scores():
     _run(_batch([6], [1500], [400, 1, 30, 64, 65, 2], 64, 1, 16, seed=8, std=30.0))
 
@@ -314,6 +336,22 @@ def test_deterministic_whatever_the_workspace_holds():
             if first is None:
                 first = got
             assert torch.equal(got[0], first[0]) and torch.equal(got[1], first[1])
+
+
+def test_calls_of_other_sizes_in_turn():
+    """Shares of no, one and many items, each call after one that left other items in shared memory and workspace."""
+    batches = [_batch([5, 2, 3], [300, 700, 129], [4 + 11 * b % 90 for b in range(10)], 16, 4, 64, seed=40),
+               _batch([1] * 3000, [0] * 3000, [(b * 7) % 5 for b in range(3000)], 8, 1, 2, seed=41),
+               _batch([3], [9000], [5, 6, 700], 64, 1, 16, seed=42), _batch([2, 9], [128, 0], [1] * 11, 8, 1, 128, seed=43)]
+    need = max(M.latent_decode_shared_workspace_bytes(*x[0].shape[:3], x[5].shape[0], x[1], x[2]) for x in batches)
+    ws = torch.zeros(need, dtype=torch.uint8, device="cuda")
+    want = [_run(x, workspace=ws) for x in batches]
+    for k in range(200):
+        i = (k * k + k // 3) % len(batches)
+        lse = torch.empty_like(want[i][1])
+        out = M.latent_decode_shared(*batches[i], SCALE, lse=lse, workspace=ws)
+        assert torch.equal(out, want[i][0]) and torch.equal(lse, want[i][1])
+    assert get_status() == 0
 
 
 def test_on_another_stream_and_in_a_graph():
