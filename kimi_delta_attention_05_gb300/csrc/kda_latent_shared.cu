@@ -58,6 +58,7 @@ constexpr int kShKeyWarp = 8, kShMmaWarp = 9, kShValueWarp = 10;
 // 24 prefixes of up to 8192); least cost of a share.  (A request's own tiles, which come from HBM, take longer than the
 // prefix's, but at 6 they made the shares less even: 95.8.)
 constexpr int kShTileCost = 4, kShItemCost = 16, kShLeast = 2 * kShTileCost;
+constexpr int kShWhole = 60;      // cost that a share may take longer where it is one whole item
 constexpr float kShSlack = 8.0f;   // log2 growth of a maximum that is let pass
 
 constexpr int kShKeyPart = 64 * 3 * 128;      // 64 tokens of three 64-column blocks
@@ -377,15 +378,26 @@ __global__ void __launch_bounds__(kShThreads, 1)
     }
     SharedItem x = {};
     int64_t cost = 0;
+    int most = 0;  // tiles of an item
     for (int i = i0, g = group; i < i1; ++i) {
       look(i, g, x);
       cost += item_cost(x.tiles);
+      most = max(most, x.tiles);
     }
+    most = __reduce_max_sync(0xffffffffu, most);
+    int* mosts = reinterpret_cast<int*>(scan + 16);
+    if (lane == 0) mosts[warp] = most;
     if (writes && odd) atomicExch(p.status, KDA_ERR_BAD_LENGTHS);
     int64_t total, start = prefix_sum(cost, total);
-    const int64_t size = max((int64_t)kShLeast, div_costs(total + sp.pairs - 1, sp.pairs));
-    it.u0 = min(total, share * size);
-    it.u1 = min(total, it.u0 + size);
+    for (int w = 0; w < kShWarps; ++w) most = max(most, mosts[w]);
+    int64_t size = max((int64_t)kShLeast, div_costs(total + sp.pairs - 1, sp.pairs));
+    // No more items than pairs, and none that takes much longer than an equal share would with the output of a second
+    // piece and the join: every item is a share, and writes its rows (64 items of 36 to 48 tiles 77 us, cut 84; with 24 prefixes
+    // of up to 8192 tokens, where items differ, 188 and 83).
+    const bool whole = items <= sp.pairs && item_cost(most) <= size + kShWhole;
+    if (whole) size = total + 1;  // (the join finds no cut)
+    it.u0 = whole ? 0 : min(total, share * size);
+    it.u1 = min(total, it.u0 + size);  // (whole items: those of the line that the pair takes are set below)
     it.items = sp.items;
     it.kept = reinterpret_cast<const SharedItem*>(smem + kShItems);
     if (writes && tid == 0) *sp.head = {size, items, view.alone ? 1 : 0};
@@ -403,13 +415,17 @@ __global__ void __launch_bounds__(kShThreads, 1)
     __syncthreads();
     it.next_item = it.first_item = it.u0 < it.u1 ? (int)scan[12] : 0;
     it.end_item = it.u0 < it.u1 ? (int)scan[13] + 1 : 0;
+    if (whole) {
+      it.next_item = it.first_item = share;
+      it.end_item = min(items, share + 1);
+    }
     if (writes || has) {
       for (int i = i0, g = group; i < i1; ++i) {
         if (per > 1) look(i, g, x);
         x.start = start;
         const int64_t end = start + item_cost(x.tiles);
         if (writes || (start < it.u1 && end > it.u0)) sp.items[i] = x;
-        if (start < it.u1 && end > it.u0 && i - it.first_item < kShKept)
+        if (start < it.u1 && end > it.u0 && i >= it.first_item && i - it.first_item < kShKept)
           reinterpret_cast<SharedItem*>(smem + kShItems)[i - it.first_item] = x;
         start = end;
       }
