@@ -58,7 +58,7 @@ constexpr int kShKeyWarp = 8, kShMmaWarp = 9, kShValueWarp = 10;
 // 24 prefixes of up to 8192); least cost of a share.  (A request's own tiles, which come from HBM, take longer than the
 // prefix's, but at 6 they made the shares less even: 95.8.)
 constexpr int kShTileCost = 4, kShItemCost = 16, kShLeast = 2 * kShTileCost;
-constexpr int kShWhole = 60;      // cost that a share may take longer where it is one whole item
+constexpr int kShWhole = 16;       // cost that cuts add, beside that which grows with the items
 constexpr float kShSlack = 8.0f;   // log2 growth of a maximum that is let pass
 
 constexpr int kShKeyPart = 64 * 3 * 128;      // 64 tokens of three 64-column blocks
@@ -391,10 +391,10 @@ __global__ void __launch_bounds__(kShThreads, 1)
     int64_t total, start = prefix_sum(cost, total);
     for (int w = 0; w < kShWarps; ++w) most = max(most, mosts[w]);
     int64_t size = max((int64_t)kShLeast, div_costs(total + sp.pairs - 1, sp.pairs));
-    // No more items than pairs, and none that takes much longer than an equal share would with the output of a second
-    // piece and the join: every item is a share, and writes its rows (64 items of 36 to 48 tiles 77 us, cut 84; with 24 prefixes
-    // of up to 8192 tokens, where items differ, 188 and 83).
-    const bool whole = items <= sp.pairs && item_cost(most) <= size + kShWhole;
+    // No more items than pairs, and none that takes much longer than an equal share would with what cuts add, fp32 parts to
+    // write, read and join, which grows with the items: every item is a share, and writes its rows.  Whole and cut, us: 64
+    // items of 36 to 48 tiles 77 and 84, 32 of 12 27.8 and 29.1, of 20 37.0 and 35.3, 8 of 3 14.7 and 18.2, one of 10 27.5 and 17.6.
+    const bool whole = items <= sp.pairs && item_cost(most) <= size + kShWhole + items * 3 / 4;
     if (whole) size = total + 1;  // (the join finds no cut)
     it.u0 = whole ? 0 : min(total, share * size);
     it.u1 = min(total, it.u0 + size);  // (whole items: those of the line that the pair takes are set below)
