@@ -283,8 +283,8 @@ int check_shared(const kda_latent_decode_shared_args* a) {
 
 // Whether a call's tables hold so little that it is taken as kda_latent_decode, whose blocks of 64 rows read each
 // token once a block.  Device times alone and shared, us: 8 requests of 1088 tokens, 16 heads 12.2 and 19.4; 32 of 2112,
-// 16 heads 19.8 and 23.2; 128 of 576, 32 heads 24.0 and 26.5; 128 of 1088, 32 heads 33.9 and 29.1; with two blocks 8 of 1088,
-// 128 heads 20.8 and 20.2; 32 of 1088 30.9 and 26.8.
+// 16 heads 19.8 and 23.2; 128 of 576, 32 heads 24.0 and 26.5; 128 of 1088, 32 heads 34.0 and 27.8; with two blocks 8 of 1088,
+// 128 heads 20.7 and 19.9; 32 of 1088 31.0 and 21.8.
 bool shares_little(const kda_latent_decode_args& a) {
   const int64_t tokens = a.B * (a.max_pages * a.cache.page_size), blocks = (a.R * a.H + 63) / 64;
   return tokens <= KDA_LATENT_SHARED_TOKENS && tokens * blocks * blocks <= KDA_LATENT_SHARED_TOKENS;

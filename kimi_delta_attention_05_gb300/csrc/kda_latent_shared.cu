@@ -28,15 +28,16 @@
 // cycles, the products' own time.
 //
 // Work: the tiles of all items in one line, cut into equal shares, one CTA pair a
-// share.  A piece that is its whole item writes its rows; the others leave normalised
-// rows and their lse in fp32, which the join adds in the order of the tiles.
+// share, or an item a share where none is much longer than that.  A piece that is its
+// whole item writes its rows; the others leave normalised rows and their lse in fp32,
+// which the join adds in the order of the tiles.
 //
 // Measured: 48 requests of three tokens behind two prefixes of 49152, 32 heads, 277 us or
 // 1.79 PFLOP/s, tensor pipe 86 % active; 256 requests of up to 512 own tokens behind 4096,
-// 32 heads, 84 us, of which 9 pass before a share's first scores (its plan, first copies
-// and first product), 4 to 6 in each piece's output and 10 in the join; 24 prefixes of up
-// to 8192, 16 heads, 84 us: a tile takes 3400 cycles, as 12 TB/s of keys and values come
-// from L2 and a third of that from HBM.
+// 32 heads, 74 to 77 us, of which 7 pass before a share's first scores (its plan 3.5, first
+// copies and first product); 24 prefixes of up to 8192, 16 heads, 83 us: a tile takes 3400
+// cycles, as 12 TB/s of keys and values come from L2 and a third of that from HBM, and a
+// piece's 128 KB of fp32 output a CTA 4 to 6 us, the join 10.
 //
 // Roles: warps 0-7 softmax and output, warp 8 queries and keys, warp 9 products
 // (first CTA), warp 10 values.  Every wait is bounded.
@@ -144,9 +145,9 @@ struct SharedView {
   __device__ __forceinline__ int request(int row) const { return (int)((uint32_t)row / (uint32_t)rows_of); }
 };
 
-__device__ __forceinline__ SharedView shared_view(const SharedParams& p, bool alone) {
+__device__ __forceinline__ SharedView shared_view(const SharedParams& p) {
   return {p.groups.cu, p.groups.prefix, p.d.lens, p.d.B, p.d.R, p.d.H, p.d.R * p.d.H, (int)(p.d.max_pages * p.d.page_size),
-          alone};
+          false};
 }
 
 // The pieces of one share [u0, u1) of the line of costs, in order.
@@ -176,7 +177,7 @@ struct SharedPieces {
       leads = x == 0;
       // An item lies on the line from its last tile to its first: a share that ends one item and begins another
       // takes the one's first tiles, then the other's last, and so do the others at the same time (read from
-      // DRAM for 48 requests of three tokens behind two prefixes of 49152: 254 MB, the other way round 1010).
+      // DRAM for 48 requests of three tokens behind two prefixes of 49152: 290 MB, the other way round 1010).
       t0 = tiles - y;
       t1 = tiles - x;
       more = t0 < t1 || (tiles == 0 && start >= u0);  // (an item without tiles: rows that see nothing)
@@ -291,7 +292,7 @@ __global__ void __launch_bounds__(kShThreads, 1)
 
   // ---- this pair's share of the line: every CTA finds the items and their costs for itself ----
   SharedPieces it;
-  SharedView view = shared_view(sp, false);
+  SharedView view = shared_view(sp);
   {
     int* first_item = reinterpret_cast<int*>(smem);                // [G] items before each group
     int64_t* scan = reinterpret_cast<int64_t*>(smem + kShMax);     // sums of the warps; then the share's first item
@@ -393,7 +394,7 @@ __global__ void __launch_bounds__(kShThreads, 1)
     int64_t size = max((int64_t)kShLeast, div_costs(total + sp.pairs - 1, sp.pairs));
     // No more items than pairs, and none that takes much longer than an equal share would with what cuts add, fp32 parts to
     // write, read and join, which grows with the items: every item is a share, and writes its rows.  Whole and cut, us: 64
-    // items of 36 to 48 tiles 77 and 84, 32 of 12 27.8 and 29.1, of 20 37.0 and 35.3, 8 of 3 14.7 and 18.2, one of 10 27.5 and 17.6.
+    // items of 36 to 48 tiles 74 and 84, 32 of 12 27.8 and 29.1, of 20 37.0 and 35.3, 8 of 3 14.7 and 18.2, one of 10 27.5 and 17.6.
     const bool whole = items <= sp.pairs && item_cost(most) <= size + kShWhole + items * 3 / 4;
     if (whole) size = total + 1;  // (the join finds no cut)
     it.u0 = whole ? 0 : min(total, share * size);
