@@ -94,14 +94,13 @@ struct SharedItem {
   int group, block;   // of the group's rows
   int common, tiles;  // tiles of the prefix, and all
   int64_t start;      // on the line
-  int64_t pad;
+  int row, rows;      // the group's first row, and its rows
 };
 static_assert(sizeof(SharedItem) == 32, "read as two 16-byte pieces");
 
 struct SharedHead {
   int64_t size;       // cost of a share
   int items;
-  int alone;          // the offsets do not fit: all requests are one group without a prefix
 };
 
 struct SharedParams {
@@ -361,6 +360,8 @@ __global__ void __launch_bounds__(kShThreads, 1)
       x.group = g;
       x.block = i - first_item[g];
       const int first = view.first(g), n = view.end(g) - first, row = x.block * kShRows;
+      x.row = first * view.rows_of;
+      x.rows = n * view.rows_of;
       const int shared = view.tokens(g, n);
       const int b0 = first + view.request(row), b1 = first + view.request(min(n * view.rows_of, row + kShRows) - 1);
       x.common = 0;
@@ -406,7 +407,7 @@ __global__ void __launch_bounds__(kShThreads, 1)
     it.u1 = min(total, it.u0 + size);  // (whole items: those of the line that the pair takes are set below)
     it.items = sp.items;
     it.kept = reinterpret_cast<const SharedItem*>(smem + kShItems);
-    if (writes && tid == 0) *sp.head = {size, items, view.alone ? 1 : 0};
+    if (writes && tid == 0) *sp.head = {size, items};
     const bool has = start < it.u1 && start + cost > it.u0;  // some of the share
     if (has) {  // its first and its last item
       int64_t begin = start;
@@ -820,7 +821,7 @@ __global__ void __launch_bounds__(kShJoinThreads) kda_latent_shared_join_kernel(
   const DecodeParams& d = p.d;
   const int lane = threadIdx.x & 31;
   const SharedHead head = *p.head;
-  const int64_t rows_of = (int64_t)d.R * d.H, all = (int64_t)d.B * rows_of;
+  const int64_t all = (int64_t)d.B * d.R * d.H;
   for (int unit = blockIdx.x; unit < head.items * kShJoinUnits; unit += gridDim.x) {
     const SharedItem item = p.items[unit / kShJoinUnits];
     // its tiles' places on the line, hence the shares that hold them
@@ -828,12 +829,16 @@ __global__ void __launch_bounds__(kShJoinThreads) kda_latent_shared_join_kernel(
     const int64_t last = item.start + item_cost(max(0, item.tiles - 1));
     const int parts = (int)(div_costs(last, head.size) - first) + 1;
     if (parts == 1) continue;
-    const int64_t c = head.alone ? 0 : p.groups.cu[item.group], end = head.alone ? d.B : p.groups.cu[item.group + 1];
-    const int r = unit % kShJoinUnits * kShJoinRows + (threadIdx.x >> 5);
-    const int64_t row = (int64_t)item.block * kShRows + r;
-    if (row >= (end - c) * rows_of) continue;
-    const int64_t at = c * rows_of + row;
+    const int r = unit % kShJoinUnits * kShJoinRows + (threadIdx.x >> 5), row = item.block * kShRows + r;
+    if (row >= item.rows) continue;
+    const int64_t at = item.row + row;
     auto place = [&](int k) { return k == 0 ? at : all + (first + k) * kShRows + r; };
+    auto piece = [&](int k) { return reinterpret_cast<const float4*>(p.part + place(k) * kLat) + lane; };
+    float4 x[2][4];  // the first two parts, on their way while the weights are found
+#pragma unroll
+    for (int k = 0; k < 2; ++k)
+#pragma unroll
+      for (int i = 0; i < 4; ++i) x[k][i] = piece(k)[32 * i];
     float top = -INFINITY;
     for (int k = lane; k < parts; k += 32) top = fmaxf(top, p.part_lse[place(k)]);
 #pragma unroll
@@ -842,22 +847,26 @@ __global__ void __launch_bounds__(kShJoinThreads) kda_latent_shared_join_kernel(
     float acc[16], sum = 0.f;
 #pragma unroll
     for (int i = 0; i < 16; ++i) acc[i] = 0.f;
-#pragma unroll 4
-    for (int k = 0; k < parts; ++k) {
-      const int64_t from = place(k);
-      const float w = ex2(p.part_lse[from] - base);
-      const float4* src = reinterpret_cast<const float4*>(p.part + from * kLat) + lane;
+    auto add = [&](int k, const float4 (&y)[4]) {
+      const float w = ex2(p.part_lse[place(k)] - base);
       sum += w;
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
-        const float4 x = src[32 * i];
         if (w != 0.f) {
-          acc[4 * i] += w * x.x;
-          acc[4 * i + 1] += w * x.y;
-          acc[4 * i + 2] += w * x.z;
-          acc[4 * i + 3] += w * x.w;
+          acc[4 * i] += w * y[i].x;
+          acc[4 * i + 1] += w * y[i].y;
+          acc[4 * i + 2] += w * y[i].z;
+          acc[4 * i + 3] += w * y[i].w;
         }
       }
+    };
+    add(0, x[0]);
+    add(1, x[1]);
+#pragma unroll 2
+    for (int k = 2; k < parts; ++k) {
+#pragma unroll
+      for (int i = 0; i < 4; ++i) x[0][i] = piece(k)[32 * i];
+      add(k, x[0]);
     }
     const float inv = sum > 0.f ? 1.0f / sum : (sum == 0.f ? 0.f : sum);
     uint2* dst = reinterpret_cast<uint2*>(d.out + at * kLat) + lane;
