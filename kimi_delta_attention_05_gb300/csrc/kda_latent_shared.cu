@@ -200,13 +200,14 @@ struct SharedPieces {
   __device__ __forceinline__ bool whole() const { return t1 - t0 == tiles; }
 };
 
-// A walk over a piece's tiles: whose tokens each has, and which.
+// A walk over a piece's tiles, the prefix's and own ones: whose tokens each has, and which.
 struct SharedTile {
   int request;      // whose own tokens, or -1: the prefix's
   int token, valid; // first token, and how many
   int first, last;  // the item's requests
   int left;         // tiles of this request behind the current one
   int shared;       // tokens of the prefix that are shared
+  int turn;         // the tile at which the prefix begins: the piece's first, or behind its own ones where it takes those first
   __device__ __forceinline__ void own(const SharedView& v, int b, int skip) {
     for (;; ++b) {
       const int n = b <= last ? v.own_tiles(b, shared) : INT32_MAX;  // (no tile is asked for behind the last request's)
@@ -221,15 +222,22 @@ struct SharedTile {
     token = v.own_from(n, shared) + skip * kShTile;
     valid = min(kShTile, n - token);
   }
+  __device__ __forceinline__ void prefix(const SharedPieces& it) {
+    request = -1;
+    token = it.t0 * kShTile;
+    valid = kShTile;
+  }
   __device__ __forceinline__ void start(const SharedView& v, const SharedPieces& it) {
     const int c = v.first(it.group), n = v.end(it.group) - c, row = it.block * kShRows;
     shared = v.tokens(it.group, n);
     first = c + v.request(row);
     last = c + v.request(min(n * v.rows_of, row + kShRows) - 1);
-    request = -1;
-    token = it.t0 * kShTile;
-    valid = kShTile;
-    if (it.t0 >= it.common && it.t0 < it.t1) own(v, first, it.t0 - it.common);
+    // Own tiles come from HBM, the prefix's from L2 where the group has several items: every second one takes its own
+    // first, so that not all wait for HBM at the same time (256 requests of up to 512 own tokens behind 4096: 75.7 -> 73.5 us).
+    turn = it.t0;
+    if (it.t0 < it.common && it.t1 > it.common && (it.block & 1) && n * v.rows_of > 4 * kShRows) turn += it.t1 - it.common;
+    prefix(it);
+    if ((it.t0 >= it.common && it.t0 < it.t1) || turn > it.t0) own(v, first, max(0, it.t0 - it.common));
   }
   // The request whose row of the table names the prefix: the first that takes it as shared, where there is one.
   __device__ __forceinline__ int source(const SharedView& v) const {
@@ -239,7 +247,9 @@ struct SharedTile {
   }
   // to tile t of the piece, which has one
   __device__ __forceinline__ void advance(const SharedView& v, const SharedPieces& it, int t) {
-    if (t < it.common) {
+    if (t == turn) {
+      prefix(it);
+    } else if (request < 0 && token + kShTile < it.common * kShTile) {
       token += kShTile;
     } else if (request < 0) {
       own(v, first, 0);
