@@ -219,6 +219,18 @@ def test_many_requests_an_item_and_many_items_a_request(H, R):
     _run(_batch([150, 40], [260, 129], [R + 29 * b % 300 for b in range(190)], 32, R, H, seed=H))
 
 
+@pytest.mark.parametrize("long", [0, 700, 6000])
+@pytest.mark.parametrize("prefix", [127, 128, 1300, 5000])
+def test_groups_of_many_items(prefix, long):
+    """Every second item of such a group takes its own tokens first: items that are a share each, and cut ones; a
+    request that is far longer than the others, one that does not see the whole prefix, one without a token."""
+    tails = [1 + 53 * b % 400 for b in range(25)]
+    tails[6] += long
+    batch = _batch([25], [prefix], tails, 16, 1, 32, seed=prefix + long)
+    batch[3][13], batch[3][14] = 100, 0
+    _run(batch)
+
+
 def test_large_scores():
     _run(_batch([6], [1500], [400, 1, 30, 64, 65, 2], 64, 1, 16, seed=8, std=30.0))
 
