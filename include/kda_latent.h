@@ -188,11 +188,13 @@ int kda_latent_decode(const kda_latent_decode_args *args, void *workspace, size_
  * What the cache holds behind a request's length is never used, whatever it is.
  * Parts are joined in fp32, so outputs have the error of kda_latent_decode's; they are
  * not bit for bit the same, but do not depend on anything but the arguments.
- * Where the tables hold little (B * max_pages * page_size tokens, times the square of
- * ceil(R H / 64), are at most KDA_LATENT_SHARED_TOKENS) the call is kda_latent_decode,
- * which is faster there; the values of cu_groups and prefix_lens are then not looked at.
+ * Where the tables hold little (B * max_pages * page_size tokens times R H, or 16 if that
+ * is more, are at most KDA_LATENT_SHARED_LEAST) and the rows are few (R H at most 32, or
+ * B R H at most KDA_LATENT_SHARED_ROWS) the call is kda_latent_decode, which is faster
+ * there; the values of cu_groups and prefix_lens are then not looked at.
  */
-#define KDA_LATENT_SHARED_TOKENS 98304
+#define KDA_LATENT_SHARED_LEAST 2097152
+#define KDA_LATENT_SHARED_ROWS 512
 #define KDA_LATENT_SHARED_GROUPS 16384
 typedef struct kda_latent_decode_shared_args {
   kda_latent_decode_args decode;

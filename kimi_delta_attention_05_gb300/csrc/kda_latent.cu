@@ -282,12 +282,15 @@ int check_shared(const kda_latent_decode_shared_args* a) {
 }
 
 // Whether a call's tables hold so little that it is taken as kda_latent_decode, whose blocks of 64 rows read each
-// token once a block.  Device times alone and shared, us: 8 requests of 1088 tokens, 16 heads 12.2 and 19.4; 32 of 2112,
-// 16 heads 19.8 and 23.2; 128 of 576, 32 heads 24.0 and 26.5; 128 of 1088, 32 heads 34.0 and 27.8; with two blocks 8 of 1088,
-// 128 heads 20.7 and 19.9; 32 of 1088 31.0 and 21.8.
+// token once a block, or whose rows fill so few items that the SMs wait for one another's parts.  Device times alone and
+// shared, us: 16 heads, 8 requests of 1088 tokens 12.3 and 19.3, 32 of 2112 19.7 and 22.4, 128 of 1088 29.7 and 26.1;
+// 32 heads, 32 of 1088 19.6 and 20.0, 128 of 320 18.9 and 20.6, 128 of 1088 33.8 and 27.6; 64 heads, 8 of 1088 18.1 and
+// 18.3, 16 of 1088 20.8 and 19.1, 64 of 320 22.5 and 16.9; 128 heads, 2 of 1088 16.8 and 17.4, 8 of 1088 20.7 and 18.6,
+// 32 of 320 22.6 and 14.8.  (Of 444 such calls the rule's choice is 0.6 % slower on average than the better one.)
 bool shares_little(const kda_latent_decode_args& a) {
-  const int64_t tokens = a.B * (a.max_pages * a.cache.page_size), blocks = (a.R * a.H + 63) / 64;
-  return tokens <= KDA_LATENT_SHARED_TOKENS && tokens * blocks * blocks <= KDA_LATENT_SHARED_TOKENS;
+  const int64_t tokens = a.B * (a.max_pages * a.cache.page_size), rows = a.R * a.H;
+  return tokens <= KDA_LATENT_SHARED_LEAST && tokens * std::max<int64_t>(rows, 16) <= KDA_LATENT_SHARED_LEAST &&
+         (rows <= 32 || a.B * rows <= KDA_LATENT_SHARED_ROWS);
 }
 
 DecodeParams decode_params(const kda_latent_decode_args* a) {

@@ -34,10 +34,10 @@
 //
 // Measured: 48 requests of three tokens behind two prefixes of 49152, 32 heads, 277 us or
 // 1.79 PFLOP/s, tensor pipe 86 % active; 256 requests of up to 512 own tokens behind 4096,
-// 32 heads, 74 to 77 us, of which 7 pass before a share's first scores (its plan 3.5, first
-// copies and first product); 24 prefixes of up to 8192, 16 heads, 83 us: a tile takes 3400
-// cycles, as 12 TB/s of keys and values come from L2 and a third of that from HBM, and a
-// piece's 128 KB of fp32 output a CTA 4 to 6 us, the join 10.
+// 32 heads, 73.5 us, of which 7 pass before a share's first scores (its plan 3.5, first
+// copies and first product); 24 prefixes of up to 8192, 16 heads, 80 us: a tile takes 3400
+// cycles, as most come from HBM, at 5 TB/s while there are any, and a piece's 128 KB of
+// fp32 output a CTA 4 to 6 us, the join 5.
 //
 // Roles: warps 0-7 softmax and output, warp 8 queries and keys, warp 9 products
 // (first CTA), warp 10 values.  Every wait is bounded.
@@ -181,7 +181,7 @@ struct SharedPieces {
       leads = x == 0;
       // An item lies on the line from its last tile to its first: a share that ends one item and begins another
       // takes the one's first tiles, then the other's last, and so do the others at the same time (read from
-      // DRAM for 48 requests of three tokens behind two prefixes of 49152: 290 MB, the other way round 1010).
+      // DRAM for 48 requests of three tokens behind two prefixes of 49152: 275 MB, the other way round 1010).
       t0 = tiles - y;
       t1 = tiles - x;
       more = t0 < t1 || (tiles == 0 && start >= u0);  // (an item without tiles: rows that see nothing)
@@ -410,7 +410,8 @@ __global__ void __launch_bounds__(kShThreads, 1)
     int64_t size = max((int64_t)kShLeast, div_costs(total + sp.pairs - 1, sp.pairs));
     // No more items than pairs, and none that takes much longer than an equal share would with what cuts add, fp32 parts to
     // write, read and join, which grows with the items: every item is a share, and writes its rows.  Whole and cut, us: 64
-    // items of 36 to 48 tiles 74 and 84, 32 of 12 27.8 and 29.1, of 20 37.0 and 35.3, 8 of 3 14.7 and 18.2, one of 10 27.5 and 17.6.
+    // items of 36 to 48 tiles 76 and 79, of 12 to 24 45 and 52, 72 of 12 to 16 37 and 49; 50 of 36 to 48 72 and 67, 32 of 12
+    // 32.7 and 31.4, of 20 to 32 51 and 40, 16 of 12 to 16 34 and 25.
     const bool whole = items <= sp.pairs && item_cost(most) <= size + kShWhole + items * 3 / 4;
     if (whole) size = total + 1;  // (the join finds no cut)
     it.u0 = whole ? 0 : min(total, share * size);

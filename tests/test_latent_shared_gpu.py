@@ -35,8 +35,8 @@ def _rand(gen, *shape, std=1.0):
 
 
 def _wide(B, page, R, H):
-    """Pages of a table that the call does not take as latent_decode (KDA_LATENT_SHARED_TOKENS)."""
-    return 98304 // max(1, B * page * (-(-R * H // 64)) ** 2) + 1
+    """Pages of a table that the call does not take as latent_decode (KDA_LATENT_SHARED_LEAST)."""
+    return (1 << 21) // max(1, B * page * max(16, R * H)) + 1
 
 
 def _batch(members, prefix, tails, page, R, H, seed=0, std=1.0, spare=2, rows=None, wide=True):
@@ -126,8 +126,8 @@ def test_prefix_lengths(prefix, page):
 
 def test_tables_that_hold_little():
     """Taken as latent_decode, whose results they are; groups that do not fit do not show."""
-    for H in (16, 128):
-        batch = _batch([3, 2], [300, 129], [5, 64, 1, 2, 70], 16, 1, H, seed=H, wide=False)
+    for H, members, tails in ((16, [3, 2], [5, 64, 1, 2, 70]), (32, [20, 2], [1 + b for b in range(22)]), (128, [2, 2], [5, 64, 1, 2])):
+        batch = _batch(members, [300, 129], tails, 16, 1, H, seed=H, wide=False)
         q, cache, table, lens, cu, prefix = batch
         out, lse = _run(batch)
         alone = torch.empty_like(lse)
@@ -140,9 +140,15 @@ def test_tables_that_hold_little():
 def test_tables_about_as_wide_as_the_limit(more):
     batch = _batch([4, 4], [1000, 600], [20] * 8, 16, 1, 40, seed=30 + more)
     q, cache, table, lens, cu, prefix = batch
-    width = 98304 // (8 * 16) + more
+    width = (1 << 21) // (8 * 16 * 40) + more
     batch[2] = torch.cat([table, torch.full((8, 9), 1 << 30, **I32)], 1)[:, :width]
     _run(batch)
+
+
+@pytest.mark.parametrize("n", [12, 13])
+def test_rows_about_as_many_as_the_limit(n):
+    """480 and 520 rows of 40 heads, in tables that hold little."""
+    _run(_batch([n], [300], [3 + b for b in range(n)], 16, 1, 40, seed=n, wide=False))
 
 
 @pytest.mark.parametrize("members", [[1], [2], [1, 1, 1], [1, 5, 0, 3], [0, 0, 4], [9, 0], [2, 17, 1, 30]])
