@@ -183,8 +183,9 @@ int kda_latent_decode(const kda_latent_decode_args *args, void *workspace, size_
  * to B without decreasing set KDA_ERR_BAD_SEQLENS, and every request is taken on its
  * own.  B * R * H is below 2^31 - 128, a table
  * holds at most 2^30 tokens, and G is at most KDA_LATENT_SHARED_GROUPS.
- * The cached rows of all requests of a group have to be finite, within their lengths:
- * a request's tokens take part with weight 0 in the products of its group's others.
+ * Cached rows that are not finite touch no result of a request that does not see them
+ * (such a call is slow: a request's tokens take part with weight 0 in the products of its
+ * group's others, and what that spoils is computed anew).
  * What the cache holds behind a request's length is never used, whatever it is.
  * Parts are joined in fp32, so outputs have the error of kda_latent_decode's; they are
  * not bit for bit the same, but do not depend on anything but the arguments.

@@ -32,6 +32,9 @@
 // whole item writes its rows; the others leave normalised rows and their lse in fp32,
 // which the join adds in the order of the tiles.
 //
+// Rows that are not finite: with weight 0 they make NaN of the O of rows that do not see
+// them, whose weights are finite; those rows are marked, and the join computes them anew.
+//
 // Measured: 48 requests of three tokens behind two prefixes of 49152, 32 heads, 277 us or
 // 1.79 PFLOP/s, tensor pipe 86 % active; 256 requests of up to 512 own tokens behind 4096,
 // 32 heads, 73.5 us, of which 7 pass before a share's first scores (its plan 3.5, first
@@ -102,7 +105,7 @@ static_assert(sizeof(SharedItem) == 32, "read as two 16-byte pieces");
 
 struct SharedHead {
   int64_t size;       // cost of a share
-  int items;
+  int items, cut;     // all, and those that shares may have cut: all or none
 };
 
 struct SharedParams {
@@ -112,6 +115,7 @@ struct SharedParams {
   // workspace
   SharedHead* head;
   SharedItem* items;           // written by the first CTA (all) and by each whose share they are in (the same)
+  int* spoilt;                 // [2 * pairs], of each CTA: whether it has found a row that another request's rows spoilt
   float *part, *part_lse;      // fp32 rows and their lse (log2): a row's first part at its own place, those that begin
                                // within a share behind them; [B R H + pairs * kShRows]
 };
@@ -286,11 +290,13 @@ __global__ void __launch_bounds__(kShThreads, 1)
   auto bar = [&](int i) { return bars + 8 * i; };
   auto lead = [&](int i) { return map_rank(bar(i), 0); };
   volatile int* s_abort = reinterpret_cast<volatile int*>(smem + kShAbort);
+  volatile int* s_spoilt = s_abort + 1;
 
   if (warp == kShKeyWarp && lane == 0) {
     for (int i = 0; i < kShBars; ++i)
       mbar_init(bar(i), i == kFP ? 16 : i == kFQ || (i >= kFKeys && i < kEKeys) ? 2 : 1);
     *s_abort = (sb & 1023) ? 1 : 0;
+    *s_spoilt = 0;
     if (sb & 1023) atomicExch(p.status, KDA_ERR_DEVICE_TIMEOUT);
     asm volatile("fence.mbarrier_init.release.cluster;\n" ::: "memory");
     prefetch_map(&maps.q);
@@ -422,7 +428,7 @@ __global__ void __launch_bounds__(kShThreads, 1)
     it.u1 = min(total, it.u0 + size);  // (whole items: those of the line that the pair takes are set below)
     it.items = sp.items;
     it.kept = reinterpret_cast<const SharedItem*>(smem + kShItems);
-    if (writes && tid == 0) *sp.head = {size, items};
+    if (writes && tid == 0) *sp.head = {size, items, whole ? 0 : items};
     const bool has = start < it.u1 && start + cost > it.u0;  // some of the share
     if (has) {  // its first and its last item
       int64_t begin = start;
@@ -753,8 +759,8 @@ __global__ void __launch_bounds__(kShThreads, 1)
       const int64_t at = whole || it.leads ? (int64_t)it.row + row
                                            : (int64_t)p.B * view.rows_of + (int64_t)share * kShRows + 64 * rank + r;
       if (quarter == 0 && there) {
-        if (!whole) sp.part_lse[at] = lse2;
-        else if (p.lse) p.lse[at] = lse2 * 0.6931471805599453f;
+        sp.part_lse[at] = lse2;
+        if (whole && p.lse) p.lse[at] = lse2 * 0.6931471805599453f;
       }
       if (it.t0 < it.t1) {
         wait(bar(kFO), (uint32_t)((n - 1) & 1));
@@ -788,11 +794,14 @@ __global__ void __launch_bounds__(kShThreads, 1)
           if (8 * k + (lane >> 2) < rows_there) store(8 * k + (lane >> 2), y[k]);
         __syncwarp();
       };
+      float spoilt = 0.f;  // NaN with an o that is not finite
 #pragma unroll 1
       for (int c = 0; c < 128; c += 32) {
         float o[32];
         if (it.t0 < it.t1) {
           tc_ld32(tmem + lane_base + 128 * right + c, o);
+#pragma unroll
+          for (int i = 0; i < 32; ++i) spoilt = fmaf(o[i], 0.f, spoilt);
 #pragma unroll
           for (int i = 0; i < 32; ++i) o[i] = inv == 0.f ? 0.f : o[i] * inv;
         } else {
@@ -817,26 +826,107 @@ __global__ void __launch_bounds__(kShThreads, 1)
       }
       tc_fence_before();
       named_bar(1, 256);  // wmax is read
+      // A row whose weights are finite and whose o is not: rows of another request, with weight 0, were not finite (or its
+      // own gave infinities that it did not see).  The join computes it anew.
+      if (there && sum > 0.f && spoilt != 0.f) {
+        sp.part_lse[at] = __int_as_float(0x7fffffff);
+        *s_spoilt = 1;
+      }
     }
   }
   tc_fence_before();
   __syncthreads();
+  if (tid == 0) sp.spoilt[blockIdx.x] = *s_spoilt;
   cluster_sync();  // nothing of this pair reaches a CTA that has left
   tc_fence_after();
   if (warp == kShMmaWarp)
     asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;\n" ::"r"(tmem), "r"(512u));
 }
 
+// A row by its own request's tokens alone, by a warp, 16 dimensions a lane: for rows that what their request does not see
+// spoilt, so that no request's rows touch another's result.  (32 requests of 5100 tokens with one such row: 3.8 ms instead
+// of 0.05.)
+__device__ __forceinline__ void shared_row_alone(const SharedParams& p, int64_t row) {
+  const DecodeParams& d = p.d;
+  const int lane = threadIdx.x & 31, rows_of = d.R * d.H;
+  const int b = (int)(row / rows_of), i = (int)(row - (int64_t)b * rows_of) / d.H;
+  const int page = (int)d.page_size, cap = (int)(d.max_pages * d.page_size);
+  const int seen = min(max(d.lens[b], 0), cap) - (d.R - 1 - i);
+  auto load = [&](const uint16_t* from, uint32_t (&x)[9]) {  // latents 16 lane .., and two of the 64 others
+    const uint4 a = reinterpret_cast<const uint4*>(from)[2 * lane], c = reinterpret_cast<const uint4*>(from)[2 * lane + 1];
+    x[0] = a.x, x[1] = a.y, x[2] = a.z, x[3] = a.w, x[4] = c.x, x[5] = c.y, x[6] = c.z, x[7] = c.w;
+    x[8] = reinterpret_cast<const uint32_t*>(from + kLat)[lane];
+  };
+  uint32_t q[9];
+  load(d.q + row * kLatRow, q);
+  float acc[16] = {}, m = -INFINITY, l = 0.f;
+#pragma unroll 1
+  for (int j = 0; j < seen; j += 2) {
+    uint32_t x[2][9];
+    float v[2], top = m;
+#pragma unroll
+    for (int u = 0; u < 2; ++u) {
+      const int t = min(j + u, seen - 1), at = t / page, id = d.table[b * d.table_stride + at];
+      if (id >= 0 && id < d.num_pages) {
+        load(d.cache + id * d.page_stride + (int64_t)(t - at * page) * d.token_stride, x[u]);
+      } else {  // (flagged already; reads as zeros)
+#pragma unroll
+        for (int k = 0; k < 9; ++k) x[u][k] = 0;
+      }
+    }
+#pragma unroll
+    for (int u = 0; u < 2; ++u) {
+      v[u] = 0.f;
+#pragma unroll
+      for (int k = 0; k < 9; ++k) {
+        const float2 a = unpack_bf16(q[k]), c = unpack_bf16(x[u][k]);
+        v[u] = fmaf(a.x, c.x, fmaf(a.y, c.y, v[u]));
+      }
+#pragma unroll
+      for (int o = 16; o > 0; o >>= 1) v[u] += __shfl_xor_sync(0xffffffffu, v[u], o);
+      v[u] = j + u < seen ? v[u] * d.scale_log2 : -INFINITY;
+      top = fmaxf(top, v[u]);
+    }
+    const float base = top == -INFINITY ? 0.f : top, f = ex2(m - base);
+    m = top;
+    l *= f;
+#pragma unroll
+    for (int k = 0; k < 16; ++k) acc[k] *= f;
+#pragma unroll
+    for (int u = 0; u < 2; ++u) {
+      if (j + u >= seen) continue;
+      const float w = ex2(v[u] - base);
+      l += w;
+#pragma unroll
+      for (int k = 0; k < 8; ++k) {
+        const float2 c = unpack_bf16(x[u][k]);
+        acc[2 * k] = fmaf(w, c.x, acc[2 * k]);
+        acc[2 * k + 1] = fmaf(w, c.y, acc[2 * k + 1]);
+      }
+    }
+  }
+  const float inv = l > 0.f ? 1.0f / l : (l == 0.f ? 0.f : l);
+  uint32_t y[8];
+#pragma unroll
+  for (int k = 0; k < 8; ++k) y[k] = l == 0.f ? 0 : pack_bf16(acc[2 * k] * inv, acc[2 * k + 1] * inv);
+  uint4* dst = reinterpret_cast<uint4*>(d.out + row * kLat) + 2 * lane;
+  dst[0] = make_uint4(y[0], y[1], y[2], y[3]);
+  dst[1] = make_uint4(y[4], y[5], y[6], y[7]);
+  if (lane == 0 && d.lse) d.lse[row] = l == 0.f ? -INFINITY : (m + __log2f(l)) * 0.6931471805599453f;
+}
+
 // The rows of items that several shares hold: out = sum_k w_k o_k, w_k = 2^(lse_k - lse), in the order of the shares.  A
 // warp a row, 16 dimensions a lane; parts are in L2.
-__global__ void __launch_bounds__(kShJoinThreads) kda_latent_shared_join_kernel(const SharedParams p) {
+__global__ void __launch_bounds__(kShJoinThreads, 3) kda_latent_shared_join_kernel(const SharedParams p) {
   asm volatile("griddepcontrol.launch_dependents;\n" ::: "memory");
   asm volatile("griddepcontrol.wait;\n" ::: "memory");
   const DecodeParams& d = p.d;
   const int lane = threadIdx.x & 31;
   const SharedHead head = *p.head;
+  int spoilt = 0;
+  for (int i = lane; i < 2 * p.pairs; i += 32) spoilt |= p.spoilt[i];
   const int64_t all = (int64_t)d.B * d.R * d.H;
-  for (int unit = blockIdx.x; unit < head.items * kShJoinUnits; unit += gridDim.x) {
+  for (int unit = blockIdx.x; unit < head.cut * kShJoinUnits; unit += gridDim.x) {
     const SharedItem item = p.items[unit / kShJoinUnits];
     // its tiles' places on the line, hence the shares that hold them
     const int64_t first = div_costs(item.start + kShItemCost, head.size);
@@ -890,6 +980,22 @@ __global__ void __launch_bounds__(kShJoinThreads) kda_latent_shared_join_kernel(
                                pack_bf16(acc[4 * i + 2] * inv, acc[4 * i + 3] * inv));
     if (lane == 0 && d.lse) d.lse[at] = sum == 0.f ? -INFINITY : (top + __log2f(sum)) * 0.6931471805599453f;
   }
+  if (!__any_sync(0xffffffffu, spoilt)) return;
+  // (behind the others, by the same warps: asked for as each row is joined, and in a call, it took 2 us more)
+  __syncwarp();
+#pragma unroll 1
+  for (int unit = blockIdx.x; unit < head.items * kShJoinUnits; unit += gridDim.x) {
+    const SharedItem item = p.items[unit / kShJoinUnits];
+    const int64_t first = div_costs(item.start + kShItemCost, head.size);
+    const int64_t last = item.start + item_cost(max(0, item.tiles - 1));
+    const int parts = (int)(div_costs(last, head.size) - first) + 1;
+    const int r = unit % kShJoinUnits * kShJoinRows + (threadIdx.x >> 5), row = item.block * kShRows + r;
+    if (row >= item.rows) continue;
+    int found = 0;
+    for (int k = lane; k < parts; k += 32)
+      found |= isnan(p.part_lse[k == 0 ? (int64_t)item.row + row : all + (first + k) * kShRows + r]);
+    if (__any_sync(0xffffffffu, found)) shared_row_alone(p, item.row + row);
+  }
 }
 
 namespace {
@@ -919,6 +1025,7 @@ size_t shared_layout(SharedParams& p) {
   };
   p.head = reinterpret_cast<SharedHead*>(take(sizeof(SharedHead)));
   p.items = reinterpret_cast<SharedItem*>(take((size_t)most_items(p) * sizeof(SharedItem)));
+  p.spoilt = reinterpret_cast<int*>(take((size_t)p.pairs * 8));
   const size_t parts = rows + (size_t)p.pairs * kShRows;
   p.part_lse = reinterpret_cast<float*>(take(parts * 4));
   p.part = reinterpret_cast<float*>(take(parts * kLat * 4));

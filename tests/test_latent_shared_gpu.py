@@ -145,6 +145,61 @@ def test_tables_about_as_wide_as_the_limit(more):
     _run(batch)
 
 
+def _others(batch, broken):
+    """Runs a batch in which a request's rows are not finite; checks the other requests."""
+    q, cache, table, lens, cu, prefix = batch
+    keep = [b for b in range(len(lens)) if b != broken]
+    lse = torch.full(q.shape[:3], NAN, device="cuda")
+    out = M.latent_decode_shared(q, cache, table, lens, cu, prefix, SCALE, lse=lse)
+    _check(out[keep], lse[keep], _reference(q[keep], cache, table[keep], lens[keep], SCALE), max(lens.tolist()))
+    assert get_status() == 0
+    return out, lse
+
+
+@pytest.mark.parametrize("value", [NAN, torch.inf, -torch.inf])
+@pytest.mark.parametrize("members,H,prefix,own", [([5], 16, 700, 300), ([24, 3], 32, 400, 100), ([9], 64, 128, 700),
+                                                  ([3], 16, 9000, 200), ([3, 40], 3, 300, 150)])
+def test_rows_that_are_not_finite_stay_with_their_request(members, H, prefix, own, value):
+    """Whole items and cut ones; a row near the start, the middle or the end of the broken request."""
+    n = sum(members)
+    for broken, at in ((0, 0), (1, own // 2), (2, own)):
+        batch = _batch(members, [prefix] * len(members), [1 + own + 7 * b % 60 for b in range(n)], 16, 1, H, seed=n + broken)
+        q, cache, table, lens = batch[:4]
+        at += prefix // 16 * 16 + 16  # (in a page of its own)
+        cache[table[broken, at // 16].long(), at % 16, 5] = value
+        out, lse = _others(batch, broken)
+        if value != value:  # (a row behind the length is never used)
+            seen = at < int(lens[broken])
+            assert (torch.isnan(out[broken]) == seen).all() and (torch.isnan(lse[broken]) == seen).all()
+
+
+def test_prefix_rows_that_are_not_finite_and_not_seen():
+    """A request that ends before the broken row of the prefix, and one without a token."""
+    batch = _batch([6], [600], [30] * 6, 16, 1, 32, seed=9)
+    q, cache, table, lens = batch[:4]
+    lens[2], lens[4] = 300, 0
+    cache[table[0, 400 // 16].long(), 400 % 16, 100] = NAN
+    lse = torch.empty(q.shape[:3], device="cuda")
+    out = M.latent_decode_shared(*batch, SCALE, lse=lse)
+    some = [2, 4]
+    _check(out[some], lse[some], _reference(q[some], cache, table[some], lens[some], SCALE), 300)
+    assert torch.isnan(out[[0, 1, 3, 5]]).all() and get_status() == 0
+
+
+@pytest.mark.parametrize("R", [2, 4])
+def test_new_rows_that_are_not_finite_and_not_seen_yet(R):
+    """The last new token's row is not finite: the ones before it do not see it."""
+    batch = _batch([7], [300], [40 + 50 * b for b in range(7)], 16, R, 24, seed=R)
+    q, cache, table, lens = batch[:4]
+    at = int(lens[3]) - 1
+    cache[table[3, at // 16].long(), at % 16] = NAN
+    lse = torch.empty(q.shape[:3], device="cuda")
+    out = M.latent_decode_shared(*batch, SCALE, lse=lse)
+    ref = [x[:, :-1] for x in _reference(q, cache, table, lens, SCALE)]
+    _check(out[:, :-1], lse[:, :-1], ref, int(lens.max()))
+    assert torch.isnan(out[3, -1]).all() and get_status() == 0
+
+
 @pytest.mark.parametrize("n", [12, 13])
 def test_rows_about_as_many_as_the_limit(n):
     """480 and 520 rows of 40 heads, in tables that hold little."""
