@@ -37,8 +37,8 @@
 //
 // Measured: 48 requests of three tokens behind two prefixes of 49152, 32 heads, 277 us or
 // 1.79 PFLOP/s, tensor pipe 86 % active; 256 requests of up to 512 own tokens behind 4096,
-// 32 heads, 73.5 us, of which 7 pass before a share's first scores (its plan 3.5, first
-// copies and first product); 24 prefixes of up to 8192, 16 heads, 80 us: a tile takes 3400
+// 32 heads, 74 us, of which 7 pass before a share's first scores (its plan 3.5, first
+// copies and first product); 24 prefixes of up to 8192, 16 heads, 81 us: a tile takes 3400
 // cycles, as most come from HBM, at 5 TB/s while there are any, and a piece's 128 KB of
 // fp32 output a CTA 4 to 6 us, the join 5.
 //
@@ -189,7 +189,7 @@ struct SharedPieces {
       leads = x == 0;
       // An item lies on the line from its last tile to its first: a share that ends one item and begins another
       // takes the one's first tiles, then the other's last, and so do the others at the same time (read from
-      // DRAM for 48 requests of three tokens behind two prefixes of 49152: 275 MB, the other way round 1010).
+      // DRAM for 48 requests of three tokens behind two prefixes of 49152: 285 MB, the other way round 1010).
       t0 = tiles - y;
       t1 = tiles - x;
       more = t0 < t1 || (tiles == 0 && start >= u0);  // (an item without tiles: rows that see nothing)
