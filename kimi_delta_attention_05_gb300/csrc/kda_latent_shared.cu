@@ -584,7 +584,7 @@ __global__ void __launch_bounds__(kShThreads, 1)
           }
           fence_proxy_async_smem();
           __syncwarp();
-          if (lane == 0) mbar_arrive_cluster(full);
+          if (lane == 0) mbar_release_shared_cluster(full);
         }
       }
     }
@@ -600,14 +600,21 @@ __global__ void __launch_bounds__(kShThreads, 1)
         __syncwarp();
         tc_fence_after();
       };
+      // what the second CTA's threads wrote to its shared memory is acquired at cluster scope (42 cycles)
+      auto ready_of_both = [&](int b, int n) {
+        wait(bar(b), (uint32_t)(n & 1));
+        mbar_try_wait_cluster(bar(b), (uint32_t)(n & 1));
+        __syncwarp();
+        tc_fence_after();
+      };
       int n = 0, q = 0;    // tiles whose scores are on the way, pieces
       bool fresh = false;  // the tile before is the first of its piece
       auto values = [&](int m, bool first) {
-        ready(kFP, m);
+        ready_of_both(kFP, m);
         const uint32_t more = first ? 0u : 1u;
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
-          ready(kFValues + h, m);
+          ready_of_both(kFValues + h, m);
           if (elect_one()) {
 #pragma unroll
             for (int ks = 0; ks < 4; ++ks)
@@ -744,9 +751,9 @@ __global__ void __launch_bounds__(kShThreads, 1)
         fence_proxy_async_smem();
         tc_fence_before();
         __syncwarp();
-        // (a plain arrival: the proxy fence orders the weights before it; one that releases at cluster scope took 1500
-        // to 2400 cycles)
-        if (lane == 0) mbar_arrive_cluster(lead(kFP));
+        // (the proxy fence orders the weights before the products' reads in this CTA, the release before the first CTA's
+        // thread that issues them; a release of all memory took 1700 to 2700 cycles, with copies in flight)
+        if (lane == 0) mbar_release_shared_cluster(lead(kFP));
       }
       // ---- the piece's rows ----
       wmax[quarter * 64 + r] = l;

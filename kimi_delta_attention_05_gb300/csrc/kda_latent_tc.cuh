@@ -205,12 +205,19 @@ __device__ __forceinline__ uint32_t map_rank(uint32_t addr, uint32_t rank) {
 // Arrivals at a barrier of either CTA.  For copies and tensor memory, whose
 // order the copy engine and the tcgen05 fences keep, the plain form: one with
 // cluster scope waits for everything this thread has written (900 cycles and
-// more).  mbar_release_cluster is for shared memory written by this thread.
+// more).  mbar_release_cluster is for shared memory written by this thread, and
+// mbar_release_shared_cluster too: it orders nothing but this CTA's shared memory,
+// and does not wait for the SM's other traffic, copies in flight among it.
 __device__ __forceinline__ void mbar_arrive_cluster(uint32_t bar) {
   asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];\n" ::"r"(bar) : "memory");
 }
 __device__ __forceinline__ void mbar_release_cluster(uint32_t bar) {
   asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];\n" ::"r"(bar) : "memory");
+}
+__device__ __forceinline__ void mbar_release_shared_cluster(uint32_t bar) {
+  asm volatile(
+      "fence.release.sync_restrict::shared::cta.cluster;\nmbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [%0];\n" ::"r"(bar)
+      : "memory");
 }
 __device__ __forceinline__ void mbar_expect_tx_cluster(uint32_t bar, uint32_t bytes) {
   asm volatile("mbarrier.arrive.expect_tx.shared::cluster.b64 _, [%0], %1;\n" ::"r"(bar), "r"(bytes) : "memory");

@@ -551,3 +551,24 @@ def test_samples_of_prompts_from_prompt_to_release():
     decode([each + 1] * prompts, lens0)
     left = G.latent_release(torch.arange(B, **I32), lens, table - 5, shares, page)
     assert int(left["count"]) + free.numel() == pages and not shares.any() and get_status() == 0
+
+
+def test_both_ctas_of_a_pair_hand_over_what_they_wrote():
+    """Weights and cleared rows lie in the shared memory of both CTAs of a pair and are read by products that one of them
+    issues: rows on both, many ends of requests (NaN behind them), maxima that move, calls on two streams at once.
+    Weights of the tile before, or rows that are not cleared yet, would give other bits in one call of many."""
+    a = _batch([30, 2], [1000, 300], [1 + 37 * b % 300 for b in range(32)], 16, 1, 32, seed=50, std=4.0)
+    b = _batch([9] * 8, [640] * 8, [3 + 29 * b % 200 for b in range(72)], 8, 3, 16, seed=51, std=4.0)
+    want = [_run(x) for x in (a, b)]
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    for s in streams:
+        s.wait_stream(torch.cuda.current_stream())
+    bad = torch.zeros(2, dtype=torch.int64, device="cuda")
+    for _ in range(300):
+        for k, (x, s) in enumerate(zip((a, b), streams)):
+            with torch.cuda.stream(s):
+                lse = torch.empty_like(want[k][1])
+                out = M.latent_decode_shared(*x, SCALE, lse=lse)
+                bad[k] += (out != want[k][0]).sum() + (lse != want[k][1]).sum()
+    torch.cuda.synchronize()
+    assert not bad.any() and all(get_status(s) == 0 for s in streams)
