@@ -599,6 +599,7 @@ extern "C" int kda_latent_decode_shared(const kda_latent_decode_shared_args* a, 
                                         void* stream) {
   const int rc = check_shared(a);
   if (rc != KDA_OK) return rc;
+  if (a->decode.B * a->decode.R * a->decode.H == 0) return KDA_OK;
   if (shares_little(a->decode)) return kda_latent_decode(&a->decode, workspace, workspace_bytes, stream);
   DecodeParams p = decode_params(&a->decode);
   if (!workspace || !al(workspace, 256) || workspace_bytes < shared_workspace_bytes(p, a->G)) return KDA_ERR_WORKSPACE;

@@ -143,3 +143,13 @@ def test_decode_shared_refuses_tensors_of_another_place():
     with pytest.raises(ValueError, match="CUDA"):
         t = torch.zeros(1, dtype=torch.int32)
         M.latent_decode_shared(torch.zeros(1, 1, 1, 576), t, t, t, t, t, 1.0)
+
+
+@pytest.mark.parametrize("max_pages", [0, 4, 40000])
+@pytest.mark.parametrize("B,R,H", [(2, 0, 16), (2, 1, 0), (2000, 0, 0), (0, 1, 32), (0, 0, 0)])
+def test_decode_shared_without_rows_is_nothing_whatever_the_table(B, R, H, max_pages):
+    """As kda_latent_decode: no workspace, no launch."""
+    d = M.kda_latent_decode_args(FAKE, _cache(), FAKE, max_pages, max_pages, FAKE, 0.07, FAKE, None, B, R, H)
+    a = M.kda_latent_decode_shared_args(d, FAKE, FAKE, 1)
+    assert M._library().kda_latent_decode_shared_workspace_bytes(ctypes.byref(a)) == 0
+    assert _call("decode", d, (None, 0)) == 0 and _call("decode_shared", a, (None, 0)) == 0
