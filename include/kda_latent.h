@@ -267,7 +267,8 @@ int kda_latent_prefill(const kda_latent_prefill_args *args, void *workspace, siz
  * NULL).  Whole pages are shared: their ids go into the child's row, their counts
  * up by one.  The rows of a last page that is not whole are copied into the next
  * page of free_pages (children in order).  Entries behind a child's last page are
- * left as they are; what a child's row held before has to be released first.
+ * left as they are; what a child's row held before has to be released first (its
+ * cached length is then 0).
  *
  *  parents, children, fork_lens : int32 [F].  No child twice, and none that is a
  *                parent in the same call; one parent may have many children
@@ -277,8 +278,8 @@ int kda_latent_prefill(const kda_latent_prefill_args *args, void *workspace, siz
  *  seq_lens    : int32 [B], out (another buffer than cached_lens): the children's
  *                tokens, else cached_lens
  *  pages_taken : int32 [1], out: entries of free_pages used (always the first ones)
- * Numbers of requests outside [0, B), lengths that do not fit, a child twice or as
- * parent set KDA_ERR_BAD_LENGTHS, too short a free_pages KDA_ERR_NO_PAGES, and
+ * Numbers of requests outside [0, B), lengths that do not fit, a child twice, as parent
+ * or with tokens set KDA_ERR_BAD_LENGTHS, too short a free_pages KDA_ERR_NO_PAGES, and
  * nothing is forked (seq_lens = cached_lens, pages_taken 0).  A page id outside the
  * cache sets KDA_ERR_BAD_PAGE; it is entered, but not counted or copied.
  */

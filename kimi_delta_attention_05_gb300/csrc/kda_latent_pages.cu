@@ -181,6 +181,7 @@ __global__ void __launch_bounds__(kCopyThreads) kda_latent_fork_kernel(const For
       continue;
     }
     if (atomicOr(&is_child[to >> 5], 1u << (to & 31)) >> (to & 31) & 1) bad = 1;  // twice
+    if (p.cached[to] != 0) bad = 1;                                                // holds pages, which would be lost
     const int held = p.cached[from], t = p.take ? p.take[f] : held;
     if (held < 0 || t < 0 || t > held || held > p.max_pages * p.page) {
       bad = 1;

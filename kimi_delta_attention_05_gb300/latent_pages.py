@@ -87,8 +87,8 @@ def latent_fork(parents, children, cached_lens, block_table, free_pages, shares,
     request ``parents[f]`` (int32 [F] each): whole pages are shared, the rows of a last
     page that is not whole are copied to the next page of free_pages.  block_table
     int32 [B, max_pages], shares int32 [num_pages] and cache are updated in place.
-    No child twice or as a parent; what its row held before has to be released
-    first.  Returns a dict of device tensors: seq_lens int32 [B] and pages_taken
+    No child twice, as a parent or with tokens: what its row held before has to be
+    released first.  Returns a dict of device tensors: seq_lens int32 [B] and pages_taken
     int32 [1].  Numbers and lengths that do not fit, or too few free pages, fork
     nothing and show in :func:`get_status` (18 / 19)."""
     dev, lens, table, stride, B, width = _requests(cached_lens, block_table, stream)

@@ -371,3 +371,23 @@ def test_a_captured_step_replayed_with_other_values():
         assert t["table"].tolist() == e["table"] and t["counts"].tolist() == e["shares"] and torch.equal(cache, want)
         assert c["page_map"].tolist() == e["page_map"]
     assert rng and get_status() == 0
+
+
+# ---- what would lose or overwrite pages ----
+
+@pytest.mark.parametrize("held", [1, 8, 24])
+def test_fork_over_a_request_that_holds_tokens_is_refused(held):
+    """Its pages would be held by nobody and free for nobody: they have to be released first."""
+    rows = [[0, 1, 2], [3, 4, 5], [-7, -7, -7]]
+    table, _ = _table(rows)
+    cache, big = _cache(9, 8)
+    before, counts = big.clone(), torch.zeros(9, **I32)
+    cached, free = [20, held, 0], torch.arange(6, 9, **I32)
+    p = G.latent_fork(_ints([0, 0]), _ints([2, 1]), _ints(cached), table, free, counts, cache)
+    assert get_status() == 18 and get_status() == 0
+    assert table.tolist() == rows and torch.equal(big, before) and not counts.any()
+    assert p["seq_lens"].tolist() == cached and p["pages_taken"].tolist() == [0]
+    # released, it is a child like any other
+    r = G.latent_release(_ints([1]), _ints(cached), table, counts, 8)
+    p = G.latent_fork(_ints([0, 0]), _ints([2, 1]), r["seq_lens"], table, free, counts, cache)
+    assert p["seq_lens"].tolist() == [20, 20, 20] and counts.tolist()[:2] == [2, 2] and get_status() == 0
