@@ -391,3 +391,109 @@ def test_fork_over_a_request_that_holds_tokens_is_refused(held):
     r = G.latent_release(_ints([1]), _ints(cached), table, counts, 8)
     p = G.latent_fork(_ints([0, 0]), _ints([2, 1]), r["seq_lens"], table, free, counts, cache)
     assert p["seq_lens"].tolist() == [20, 20, 20] and counts.tolist()[:2] == [2, 2] and get_status() == 0
+
+
+# ---- calls large enough for the forms that only they take ----
+
+@pytest.mark.parametrize("B,width,page", [(300, 200, 8), (40, 1000, 64), (16384, 3, 8)])
+@pytest.mark.parametrize("keep", [False, True])
+def test_release_of_many_entries(B, width, page, keep):
+    """More than 32768 entries: counted by a kernel of its own.  Rows in pairs that hold the same first pages."""
+    rng = random.Random(B + keep)
+    cached = [rng.randint(0, width * page) for _ in range(B)]
+    rows, at = [], 0
+    pages = sum(-(-c // page) for c in cached) + 7
+    ids, shares = list(range(pages)), [0] * pages
+    rng.shuffle(ids)
+    for b in range(B):
+        held = -(-cached[b] // page)
+        common = rng.randint(0, min(held, -(-cached[b - 1] // page))) if b % 2 else 0
+        row = rows[-1][:common] if common else []
+        for q in row:
+            shares[q] += 1
+        rows.append(row + ids[at:at + held - common] + [-7] * (width - held))
+        at += held - common
+    for n in (B, B * 9 // 10):
+        assert n * width > 32768
+        which = rng.sample(range(B), n)
+        _release(which, [rng.randint(0, cached[b]) for b in which] if keep else None, cached, rows, shares, page)
+
+
+def test_release_of_many_entries_refused_and_outside_the_cache():
+    width, B = 400, 100
+    table = torch.arange(B * width, **I32).view(B, width)
+    counts, lens = torch.zeros(B * width, **I32), torch.full((B,), 8 * width, **I32)
+    rows = torch.arange(B, **I32)
+    rows[70] = 3  # a row twice
+    p = G.latent_release(rows, lens, table, counts, 8)
+    assert get_status() == 18 and get_status() == 0 and not counts.any() and p["count"].item() == 0
+    assert (p["pages"] == -1).all() and torch.equal(p["seq_lens"], lens)
+    rows[70] = 70
+    table[99, 5], table[0, 0] = -2, B * width
+    p = G.latent_release(rows, lens, table, counts, 8)
+    assert get_status() == 20 and not counts.any() and p["count"].item() == B * width - 2
+    assert p["pages"][:3].tolist() == [1, 2, 3] and not p["seq_lens"].any()
+
+
+@pytest.mark.parametrize("pages", [65535, 65537, 131071, 131072, 131073, 262145, 300001])
+def test_release_of_caches_that_are_listed_in_rounds(pages):
+    """131072 pages a round: pages on both sides of every warp's, CTA's and round's run, few and many."""
+    rng = random.Random(pages)
+    near = sorted({x + d for x in range(0, pages + 1, 16384) for d in (-33, -1, 0, 1, 31, 32, 1023, 1024) if 0 <= x + d < pages})
+    for ids in (near, rng.sample(range(pages), 4000), list(range(pages - 9000, pages))):
+        ids = list(ids)
+        rng.shuffle(ids)
+        rows = [ids[:len(ids) // 2], ids[len(ids) // 2:]]
+        width = len(rows[1])
+        cached = [8 * len(r) for r in rows]
+        shares = [0] * pages
+        for q in rng.sample(ids, len(ids) // 3):  # held by others too
+            shares[q] = 1
+        _release([1, 0], None, cached, [r + [-7] * (width - len(r)) for r in rows], shares, 8)
+
+
+def test_compact_of_a_cache_of_many_pages():
+    """2.8 million pages (26 GB): a bit a page takes more shared memory than a kernel has by default; offsets past 32 bits."""
+    page, pages = 8, 2800000
+    rng = random.Random(4)
+    ids = rng.sample(range(pages), 900) + [pages - 1, pages - 2, 0, 5]
+    rng.shuffle(ids)
+    rows = [ids[:400], ids[400:]]
+    width = max(len(r) for r in rows)
+    cached, shares = [8 * len(r) - 3 for r in rows], [0] * pages
+    for q in ids[:50]:
+        shares[q] = 3
+    ref = L.compact(cached, [r + [-7] * (width - len(r)) for r in rows], shares, page)
+    cache = torch.empty((pages, page, 576), dtype=torch.bfloat16, device="cuda")
+    cache[_ints(ids).long()] = torch.randn((len(ids), page, 576), device="cuda").to(torch.bfloat16)
+    want = cache[_ints([src for _, src in ref["moves"]]).long()]
+    stay = [q for q in ids if q < len(ids)]
+    kept = cache[_ints(stay).long()]
+    table = _ints([r + [-7] * (width - len(r)) for r in rows])
+    p = G.latent_compact(_ints(cached), table, _ints(shares), cache)
+    assert p["block_table"].tolist() == ref["table"] and p["pages_used"].tolist() == ref["pages_used"] == [len(ids)]
+    assert p["shares"].tolist() == ref["shares"] and p["page_map"].tolist() == ref["page_map"]
+    assert torch.equal(cache[_ints([to for to, _ in ref["moves"]]).long()], want) and torch.equal(cache[_ints(stay).long()], kept)
+    assert get_status() == 0
+
+
+def test_fork_and_copy_past_32_bit_offsets():
+    """Pages behind element 2^31 (and byte 2^32) of the cache."""
+    page, pages = 64, 120000
+    cache = torch.empty((pages, page, 576), dtype=torch.bfloat16, device="cuda")
+    some = torch.randn((4, page, 576), device="cuda").to(torch.bfloat16)
+    far = [pages - 1, pages - 5, 70000, 3]
+    cache[_ints(far).long()] = some
+    table = _ints([[far[0], far[1]], [-7, -7], [-7, -7]])
+    counts = torch.zeros(pages, **I32)
+    p = G.latent_fork(_ints([0, 0]), _ints([1, 2]), _ints([100, 0, 0]), table, _ints([far[2], far[3]]), counts, cache, _ints([100, 30]))
+    assert p["pages_taken"].item() == 2 and table.tolist() == [far[:2], [far[0], far[2]], [far[3], -7]]
+    assert counts[far[0]] == 1 and int(counts.sum()) == 1
+    assert torch.equal(cache[far[2], :36], some[1, :36]) and torch.equal(cache[far[2], 36:], some[2, 36:])
+    assert torch.equal(cache[far[3], :30], some[0, :30]) and torch.equal(cache[far[3], 30:], some[3, 30:])
+    small = torch.randn((3, page, 576), device="cuda").to(torch.bfloat16)
+    before = small.clone()
+    G.latent_copy(cache, _ints([far[1], far[0]]), small, _ints([2, 0]))
+    assert torch.equal(small[2], some[1]) and torch.equal(small[0], some[0]) and torch.equal(small[1], before[1])
+    G.latent_copy(small, _ints([1, 2]), cache, _ints([pages - 2, 60000]))
+    assert torch.equal(cache[pages - 2], before[1]) and torch.equal(cache[60000], some[1]) and get_status() == 0
