@@ -130,7 +130,7 @@ def serve(requests=8, longest=700, steps=16, heads=8, width=512, seed=0, samples
     # ---- decoding ----
     one = torch.ones(n, dtype=torch.int32, device=dev)
     for _ in range(steps):
-        plan = latent_plan(cached, one, table, free, PAGE, n)
+        plan = latent_plan(cached, one, table, free, PAGE, n, shares=shares)
         cached = plan["seq_lens"]
         x = layers.kda(sample(n).view(n, 1, width), states)
         layers.store(x, plan["slot_map"], cache)

@@ -58,7 +58,7 @@ extern "C" {
 #define KDA_ERR_SCALE 16       /* scale is not a positive finite number */
 #define KDA_ERR_PAGE_SIZE 17   /* page_size is not a positive multiple of 8 */
 #define KDA_ERR_BAD_LENGTHS 18 /* (device status) a length is negative, or longer than its table, slots or pages allow;
-                                  or a request's number does not fit */
+                                  or would grow in a page that others hold; or a request's number does not fit */
 #define KDA_ERR_NO_PAGES 19    /* (device status) kda_latent_plan: too few free pages */
 #define KDA_ERR_BAD_PAGE 20    /* (device status) a page id or slot outside the cache */
 
@@ -77,8 +77,13 @@ extern "C" {
  *  slot_map    : int64 [T], out: cache slot (page * page_size + offset) of every
  *                packed new token; -1 behind the last one (T is a capacity)
  *  pages_taken : int32 [1], out: entries of free_pages used (always the first ones)
+ *  shares      : int32 [num_pages] or NULL: the holders of the cache's pages beyond the
+ *                first (see the calls on pages below).  Where given, a request with new
+ *                tokens whose last page is not whole has to be its only holder: a row that
+ *                kda_latent_release cut within a page of others does not write into theirs
  * If the lengths do not fit (a negative one, more than T new tokens, a request
- * beyond max_pages pages or 2^31 - 1 tokens: KDA_ERR_BAD_LENGTHS) or free_pages
+ * beyond max_pages pages or 2^31 - 1 tokens, new tokens for a page that others hold:
+ * KDA_ERR_BAD_LENGTHS) or free_pages
  * is too short (KDA_ERR_NO_PAGES), the status word is set and nothing is
  * planned: the table stays, seq_lens = cached_lens, cu_seqlens 0, slot_map -1,
  * pages_taken 0.  B is at most 16384.
@@ -93,6 +98,8 @@ typedef struct kda_latent_plan_args {
   int64_t *slot_map;
   int32_t *pages_taken;
   int64_t B, max_pages, num_free, page_size, T;
+  const int32_t *shares;
+  int64_t num_pages;             /* entries of shares */
 } kda_latent_plan_args;
 
 int kda_latent_plan(const kda_latent_plan_args *args, void *stream);
@@ -301,8 +308,9 @@ int kda_latent_fork(const kda_latent_fork_args *args, void *stream);
  * where keep_lens is NULL) and drops the pages behind them.  The count of a dropped
  * page goes down by one; pages whose last holder dropped them are listed.
  * A row that keeps part of a page which others hold must not grow from there: its
- * next tokens would be written into their page.  kda_latent_fork with fork_lens goes
- * on from any place, as it copies that part; the row itself is then released.
+ * next tokens would be written into their page (kda_latent_plan refuses it where it is
+ * given shares).  kda_latent_fork with fork_lens goes on from any place, as it copies
+ * that part; the row itself is then released.
  *
  *  rows, keep_lens : int32 [F]; no row twice
  *  block_table : int32 [B, max_pages], left as it is (a request's length says

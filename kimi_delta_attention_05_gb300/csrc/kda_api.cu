@@ -409,8 +409,8 @@ extern "C" const char* kda_error_string(int code) {
     case KDA_ERR_SCALE: return "scale must be positive and finite";
     case KDA_ERR_PAGE_SIZE: return "page_size must be a positive multiple of 8";
     case KDA_ERR_BAD_LENGTHS:
-      return "a request's length is negative or longer than its table, slots or pages allow, or its number does not fit "
-             "(device status)";
+      return "a request's length is negative or longer than its table, slots or pages allow, it would grow in a page that "
+             "others hold, or its number does not fit (device status)";
     case KDA_ERR_NO_PAGES: return "too few free pages for the requests' new tokens (device status)";
     case KDA_ERR_BAD_PAGE: return "a page id or slot lies outside the cache (device status)";
     default: return "unknown status code";

@@ -40,6 +40,8 @@ struct PlanParams {
   int B;
   int64_t max_pages, num_free, T;
   int page;
+  const int32_t* shares;  // [num_pages] or nullptr
+  int64_t num_pages;
   int* status;
 };
 
@@ -84,6 +86,10 @@ __global__ void __launch_bounds__(kPlanThreads) kda_latent_plan_kernel(const Pla
         n = 0;
       } else {
         need = pages - (c + P - 1) / P;
+        if (p.shares && n > 0 && c % P > 0) {  // (an entry that no CTA of this call writes)
+          const int64_t last = p.table[b * p.table_stride + c / P];
+          if (last >= 0 && last < p.num_pages && p.shares[last] > 0) bad = 1;
+        }
       }
     }
     const int64_t st = warp_scan(n, lane), sp = warp_scan(need, lane);
@@ -511,21 +517,22 @@ using namespace kda;
 extern "C" int kda_latent_plan(const kda_latent_plan_args* a, void* stream) {
   if (!a) return KDA_ERR_NULL_ARG;
   if (a->B < 0 || a->B > kMaxPlanRequests || a->max_pages < 0 || a->max_pages > INT32_MAX || a->num_free < 0 ||
-      a->num_free > INT32_MAX || a->T < 0 || a->T > INT32_MAX || a->table_stride < a->max_pages)
+      a->num_free > INT32_MAX || a->T < 0 || a->T > INT32_MAX || a->table_stride < a->max_pages ||
+      (a->shares && (a->num_pages < 0 || a->num_pages > INT32_MAX)))
     return KDA_ERR_SHAPE;
   if (a->page_size <= 0 || a->page_size % 8 || a->page_size > (1 << 24)) return KDA_ERR_PAGE_SIZE;
   if (!a->cu_seqlens || !a->pages_taken || (a->T > 0 && !a->slot_map) || (a->num_free > 0 && !a->free_pages) ||
       (a->B > 0 && (!a->cached_lens || !a->new_lens || !a->seq_lens || (a->max_pages > 0 && !a->block_table))))
     return KDA_ERR_NULL_ARG;
   if (!al(a->cached_lens, 4) || !al(a->new_lens, 4) || !al(a->block_table, 4) || !al(a->free_pages, 4) ||
-      !al(a->seq_lens, 4) || !al(a->cu_seqlens, 8) || !al(a->slot_map, 8) || !al(a->pages_taken, 4))
+      !al(a->seq_lens, 4) || !al(a->cu_seqlens, 8) || !al(a->slot_map, 8) || !al(a->pages_taken, 4) || !al(a->shares, 4))
     return KDA_ERR_ALIGNMENT;
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
   int* status = status_slot(s);
   if (!status) return KDA_ERR_LAUNCH;
   PlanParams p{a->cached_lens, a->new_lens, a->block_table, a->table_stride, a->free_pages, a->seq_lens,
                a->cu_seqlens, a->slot_map, a->pages_taken, (int)a->B, a->max_pages, a->num_free, a->T,
-               (int)a->page_size, status};
+               (int)a->page_size, a->shares, a->num_pages, status};
   const size_t smem = (size_t)(a->B + 1) * 8;
   if (smem > 40 * 1024) {
     static std::atomic<int> set[64];

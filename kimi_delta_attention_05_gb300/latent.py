@@ -31,7 +31,7 @@ class kda_latent_plan_args(ctypes.Structure):
     _fields_ = [("cached_lens", _P), ("new_lens", _P), ("block_table", _P), ("table_stride", _I),
                 ("free_pages", _P), ("seq_lens", _P), ("cu_seqlens", _P), ("slot_map", _P),
                 ("pages_taken", _P), ("B", _I), ("max_pages", _I), ("num_free", _I),
-                ("page_size", _I), ("T", _I)]
+                ("page_size", _I), ("T", _I), ("shares", _P), ("num_pages", _I)]
 
 
 class kda_latent_cache(ctypes.Structure):
@@ -191,7 +191,7 @@ def _cache_block(cache, device):
     return cache.data_ptr(), pages, page, page_stride, strides[1]
 
 
-def latent_plan(cached_lens, new_lens, block_table, free_pages, page_size, num_tokens, *, stream=None):
+def latent_plan(cached_lens, new_lens, block_table, free_pages, page_size, num_tokens, *, shares=None, stream=None):
     """Block tables and slot maps on the GPU from request lengths.
 
     cached_lens, new_lens int32 [B]; block_table int32 [B, max_pages], updated in
@@ -200,7 +200,9 @@ def latent_plan(cached_lens, new_lens, block_table, free_pages, page_size, num_t
     device tensors: seq_lens int32 [B], cu_seqlens int64 [B + 1], slot_map int64
     [num_tokens] (-1 behind the last token), pages_taken int32 [1].  Lengths that
     do not fit, or too few free pages, plan nothing and show in
-    :func:`get_status` (18 / 19)."""
+    :func:`get_status` (18 / 19).  With ``shares`` (int32 [num_pages], the holders of
+    pages beyond the first: :func:`latent_fork`), so do new tokens for a page that is
+    not whole and that other requests hold."""
     dev = _gpu(cached_lens, "cached_lens", stream)
     _on(cached_lens, _i32, 1, dev, "cached_lens")
     _on(new_lens, _i32, 1, dev, "new_lens")
@@ -214,13 +216,18 @@ def latent_plan(cached_lens, new_lens, block_table, free_pages, page_size, num_t
     if cached_lens.shape[0] != B or new_lens.shape[0] != B:
         raise ValueError("cached_lens, new_lens and block_table: one row a request")
     T = int(num_tokens)
+    counts, num_pages = 0, 0
+    if shares is not None:
+        _on(shares, _i32, 1, dev, "shares")
+        _dense(shares, "shares")
+        counts, num_pages = shares.data_ptr(), shares.shape[0]
     lens = _new(B, _i32, dev, stream)
     cu = _new(B + 1, _i64, dev, stream)
     slots = _new(max(T, 0), _i64, dev, stream)
     taken = _new(1, _i32, dev, stream)
     a = _plan_block(cached_lens.data_ptr(), new_lens.data_ptr(), block_table.data_ptr(), strides[0] if B > 1 else width,
                     free_pages.data_ptr(), lens.data_ptr(), cu.data_ptr(), slots.data_ptr(), taken.data_ptr(), B, width,
-                    free_pages.shape[0], int(page_size), T)
+                    free_pages.shape[0], int(page_size), T, counts, num_pages)
     rc = _library().kda_latent_plan(a, _handle(dev, stream))
     if rc != 0:
         _raise("kda_latent_plan", rc)

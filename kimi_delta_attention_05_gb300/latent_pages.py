@@ -125,7 +125,8 @@ def latent_release(rows, cached_lens, block_table, shares, page_size, keep_lens=
     int32 [num_pages] (those that nobody holds any more, ascending, and -1 behind
     them) and count int32 [1].  Rows and lengths that do not fit release nothing
     and show in :func:`get_status` (18).  A row that keeps part of a page that others
-    hold must not grow from there (:func:`latent_fork` with fork_lens copies that part)."""
+    hold must not grow from there (:func:`latent_plan` refuses it where it is given
+    shares; :func:`latent_fork` with fork_lens copies that part)."""
     dev, lens, table, stride, B, width = _requests(cached_lens, block_table, stream)
     at, F = _ints(rows, dev, "rows")
     keep = 0

@@ -153,3 +153,9 @@ def test_decode_shared_without_rows_is_nothing_whatever_the_table(B, R, H, max_p
     a = M.kda_latent_decode_shared_args(d, FAKE, FAKE, 1)
     assert M._library().kda_latent_decode_shared_workspace_bytes(ctypes.byref(a)) == 0
     assert _call("decode", d, (None, 0)) == 0 and _call("decode_shared", a, (None, 0)) == 0
+
+
+@pytest.mark.parametrize("over,code", [(dict(shares=FAKE + 2), 9), (dict(num_pages=-1), 3), (dict(num_pages=1 << 31), 3)])
+def test_plan_refuses_bad_shares(over, code):
+    a = M.kda_latent_plan_args(FAKE, FAKE, FAKE, 6, FAKE, FAKE, FAKE, FAKE, FAKE, 4, 6, 8, 64, 100, FAKE, 10)
+    assert _call("plan", _set(a, over)) == code

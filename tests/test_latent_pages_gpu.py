@@ -497,3 +497,43 @@ def test_fork_and_copy_past_32_bit_offsets():
     assert torch.equal(small[2], some[1]) and torch.equal(small[0], some[0]) and torch.equal(small[1], before[1])
     G.latent_copy(small, _ints([1, 2]), cache, _ints([pages - 2, 60000]))
     assert torch.equal(cache[pages - 2], before[1]) and torch.equal(cache[60000], some[1]) and get_status() == 0
+
+
+@pytest.mark.parametrize("B", [3, 700])
+def test_growth_in_a_page_that_others_hold_is_refused(B):
+    """A row cut within a page of others: its next token's slot would lie in their page."""
+    page, pages = 8, 3 * B + 9
+    rows = [[0, 1, 2, -7], [0, 1, 3, -7], [4, 5, 6, -7]] + [[7 + b, -7, -7, -7] for b in range(B - 3)]
+    cached = [20, 24, 24] + [3] * (B - 3)
+    shares = [1, 1] + [0] * (pages - 2)
+    table, counts, free = _ints(rows), _ints(shares), torch.arange(pages - B, pages, **I32)
+    lens, new = _ints(cached), torch.ones(B, **I32)
+    for keep, held in ((12, True), (16, False), (9, True), (24, False), (0, False)):
+        t, c = table.clone(), counts.clone()
+        r = G.latent_release(_ints([1]), lens, t, c, page, _ints([keep]))
+        before = t.clone()
+        p = M.latent_plan(r["seq_lens"], new, t, free, page, B, shares=c)
+        if held:
+            assert get_status() == 18 and get_status() == 0
+            assert torch.equal(t, before) and torch.equal(p["seq_lens"], r["seq_lens"])
+            assert (p["slot_map"] == -1).all() and not p["cu_seqlens"].any() and p["pages_taken"].item() == 0
+        else:
+            assert get_status() == 0 and torch.equal(p["seq_lens"], r["seq_lens"] + 1)
+            plain = M.latent_plan(r["seq_lens"], new, before, free, page, B)
+            assert torch.equal(t, before) and all(torch.equal(p[k], plain[k]) for k in p)
+        # a request without new tokens may keep such a part, and so may one whose others are gone
+        none = new.clone()
+        none[1] = 0
+        assert M.latent_plan(r["seq_lens"], none, t.clone(), free, page, B, shares=c)["seq_lens"][1] == keep
+        assert get_status() == 0
+        gone = G.latent_release(_ints([0]), r["seq_lens"], t, c, page)
+        p = M.latent_plan(gone["seq_lens"], new, t, free, page, B, shares=c)
+        assert get_status() == 0 and torch.equal(p["seq_lens"], gone["seq_lens"] + 1)
+
+
+def test_plan_with_shares_looks_at_no_page_outside_the_cache():
+    table = _ints([[0, 99], [-3, -7], [2, -7]])
+    p = M.latent_plan(_ints([12, 3, 8]), _ints([1, 1, 1]), table, _ints([5, 6]), 8, 3, shares=_ints([0, 0, 1, 0, 0, 0, 0]))
+    assert get_status() == 0 and p["seq_lens"].tolist() == [13, 4, 9] and p["pages_taken"].item() == 1
+    with pytest.raises(ValueError, match="shares"):
+        M.latent_plan(_ints([1]), _ints([1]), _ints([[0]]), _ints([1]), 8, 1, shares=torch.zeros(3, dtype=torch.int64, device="cuda"))
