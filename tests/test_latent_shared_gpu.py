@@ -572,3 +572,15 @@ def test_both_ctas_of_a_pair_hand_over_what_they_wrote():
                 bad[k] += (out != want[k][0]).sum() + (lse != want[k][1]).sum()
     torch.cuda.synchronize()
     assert not bad.any() and all(get_status(s) == 0 for s in streams)
+
+
+@pytest.mark.parametrize("R,H", [(5, 16), (9, 3), (33, 8), (130, 2), (300, 1)])
+def test_many_new_tokens(R, H):
+    """A request's rows fill several items, or its new tokens several tiles; requests that have fewer tokens than are new
+    (the first ones see none) or do not all see the prefix; the last group is behind a prefix that is longer than R."""
+    for prefix in ([0, 200], [128, 1000], [300, R]):
+        tails = [R, 1, R + 100, 2, 64, R + 3]
+        batch = _batch([3, 3], prefix, tails, 16, R, H, seed=R + H + prefix[1])
+        batch[3][1] = min(int(batch[3][1]), R // 2)
+        batch[3][5] = 0
+        _run(batch)
