@@ -192,7 +192,9 @@ int kda_latent_decode(const kda_latent_decode_args *args, void *workspace, size_
  * holds at most 2^30 tokens, and G is at most KDA_LATENT_SHARED_GROUPS.
  * Cached rows that are not finite touch no result of a request that does not see them
  * (such a call is slow: a request's tokens take part with weight 0 in the products of its
- * group's others, and what that spoils is computed anew).
+ * group's others, and what that spoils is computed anew).  A request's own rows have to be
+ * finite as in kda_latent_decode: whether one that is not reaches the new tokens before it
+ * depends on the form that a call takes.
  * What the cache holds behind a request's length is never used, whatever it is.
  * Parts are joined in fp32, so outputs have the error of kda_latent_decode's; they are
  * not bit for bit the same, but do not depend on anything but the arguments.

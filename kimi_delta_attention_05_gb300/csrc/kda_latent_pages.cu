@@ -241,7 +241,7 @@ __global__ void __launch_bounds__(kCopyThreads) kda_latent_fork_kernel(const For
 // the others' numbers over distributed shared memory: one launch, no workspace.  Eight
 // SMs take 2.5 cycles an atomic each, so calls with many entries have a kernel on all
 // SMs do the counts first.  16 rows of up to 64 pages 5.4 us; 256 rows of up to 1024,
-// 100000 pages, 28 us in one kernel and 17.4 in two; a million pages listed in 31 us.
+// 144127 pages, 28 us in one kernel and 17.9 in two; a million pages listed in 31 us.
 struct ReleaseParams {
   const int32_t *rows, *keep, *cached, *table;
   int64_t table_stride, max_pages;

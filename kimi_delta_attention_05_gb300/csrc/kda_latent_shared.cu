@@ -7,8 +7,9 @@
 // requests' rows see nothing.  So a cached row of the prefix crosses HBM once a
 // group and L2 once an item, and a request's own once: bound by the tensor cores (2 *
 // 1088 flops a query row and cached row of 1152 bytes) where many rows share, else by
-// HBM.  An own tile costs a whole one whatever the rows that see it, 1.1 us for 128
-// tokens on two SMs: less than HBM takes for them with all SMs at it.
+// HBM.  An own tile costs a whole one whatever the rows that see it and the tokens it
+// has, 1.1 us for up to 128 tokens on two SMs: less than HBM takes for 128 with all SMs
+// at it, more where a request has few tokens of its own.
 //
 // Products of a pair (cta_group::2, M = 128: 64 query rows a CTA, full rate):
 //   S [128 rows x 128 tokens] = Q (64 rows a CTA) . K^T (64 tokens a CTA)
@@ -35,10 +36,10 @@
 // Rows that are not finite: with weight 0 they make NaN of the O of rows that do not see
 // them, whose weights are finite; those rows are marked, and the join computes them anew.
 //
-// Measured: 48 requests of three tokens behind two prefixes of 49152, 32 heads, 277 us or
-// 1.79 PFLOP/s, tensor pipe 86 % active; 256 requests of up to 512 own tokens behind 4096,
+// Measured: 48 requests of three tokens behind two prefixes of 49152, 32 heads, 274 us or
+// 1.81 PFLOP/s, tensor pipe 86 % active; 256 requests of up to 512 own tokens behind 4096,
 // 32 heads, 74 us, of which 7 pass before a share's first scores (its plan 3.5, first
-// copies and first product); 24 prefixes of up to 8192, 16 heads, 81 us: a tile takes 3400
+// copies and first product); 24 prefixes of up to 8192, 16 heads, 82 us: a tile takes 3400
 // cycles, as most come from HBM, at 5 TB/s while there are any, and a piece's 128 KB of
 // fp32 output a CTA 4 to 6 us, the join 5.
 //
@@ -58,15 +59,18 @@ constexpr int kShTile = 128;       // cached rows of a tile
 constexpr int kShRows = 128;       // query rows of an item, a CTA pair's
 constexpr int kShThreads = 352, kShWarps = kShThreads / 32;
 constexpr int kShKeyWarp = 8, kShMmaWarp = 9, kShValueWarp = 10;
-// The line's costs: 4 a tile, and what an item's set-up and output take (8, 14 and 20 measured: 89.4, 88.2 and 87.6 us on
-// 24 prefixes of up to 8192); least cost of a share.  (A request's own tiles, which come from HBM, take longer than the
-// prefix's, but at 6 they made the shares less even: 95.8.)
+// The line's costs: 4 a tile, and what an item's set-up and output take (8, 12, 14, 16 and 20 measured: 82.8, 81.9, 81.6,
+// 82.1 and 82.4 us on 24 prefixes of up to 8192); least cost of a share.  (A request's own tiles, which come from HBM, take
+// longer than the prefix's, but at 6 they made the shares less even: 95.8 against 89.4 at 4, with an item's cost of 8 and
+// more fixed cost than now.)
 constexpr int kShTileCost = 4, kShItemCost = 16, kShLeast = 2 * kShTileCost;
 constexpr int kShWhole = 16;       // cost that cuts add, beside that which grows with the items
 constexpr float kShSlack = 8.0f;   // log2 growth of a maximum that is let pass
 
-// The join: CTAs an SM, rows of a CTA at a time, and how many such an item has (128 threads and 4 CTAs: 86.7 against 82.3 us
-// on 24 prefixes of up to 8192; a CTA for every 8 rows that an item could have, most of them empty: 83.1).
+// The join: CTAs of the grid an SM, rows of a CTA at a time, and how many such an item has.  Three CTAs are resident (80
+// registers), the fourth begins as another ends: 2, 3, 4 and 6 an SM took 85.5, 85.1, 82.0 and 82.0 us on 24 prefixes of up to
+// 8192, and 285, 280, 274 and 275 on 48 requests behind two of 49152.  (128 threads: 86.7 against 82.3; a CTA for every 8 rows
+// that an item could have, most of them empty: 83.1.)
 constexpr int kShJoinThreads = 256, kShJoinCtas = 4;
 constexpr int kShJoinRows = kShJoinThreads / 32, kShJoinUnits = kShRows / kShJoinRows;
 
